@@ -11,6 +11,7 @@
 #include <unordered_map>
 
 #include "dgt_gemm.h"
+#include "host.h"
 #include "launch.h"
 
 namespace dgt {
@@ -1090,6 +1091,51 @@ int run_gemm(int kind, int64_t M, int64_t N, int64_t K, const void* A, int64_t l
 }
 
 }  // namespace
+
+int begin_call(CallContext* out) {
+  const DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev, &out->dev);
+  if (st != GEMM_OK) return st;
+  out->sm_count = dev->sm_count;
+  out->status = dev->status_words;
+  out->epoch = g_epoch.fetch_add(1, std::memory_order_relaxed);
+  if (out->epoch == 0) out->epoch = g_epoch.fetch_add(1, std::memory_order_relaxed);
+  out->debug = g_debug_flags.load(std::memory_order_relaxed);
+  out->wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return GEMM_OK;
+}
+
+bool on_device(const void* ptr, int dev) { return is_device_memory(ptr, dev); }
+
+bool encode_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_bytes, uint64_t depth, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle swizzle) {
+  return encode_3d(m, dt, base, inner, outer, row_bytes, depth, mat_bytes, box_inner, box_outer, swizzle);
+}
+
+bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  thread_local TinyCache<7, CUtensorMap, 8> cache;
+  const uint64_t key[7] = {uint64_t(dt), uint64_t(reinterpret_cast<uintptr_t>(base)), inner, outer, row_bytes,
+                           (uint64_t(box_inner) << 32) | box_outer, uint64_t(swizzle)};
+  if (const CUtensorMap* hit = cache.find(key)) {
+    *m = *hit;
+    return true;
+  }
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  if (fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  cache.put(key, *m);
+  return true;
+}
+
+void count_launches(int n) { g_launches.fetch_add(uint64_t(n), std::memory_order_relaxed); }
 
 cudaError_t launch_pack(const PackSpec* specs, int n, cudaStream_t stream, int sm_count) {
   PackJob job[2] = {};
