@@ -1,0 +1,308 @@
+// Weighted sum of a token's rows and its gradient (gemm_combine,
+// gemm_combine_backward).
+//
+//   y[t] = residual[t] + sum_j w[t][j] z[slot[t][j]]
+//   dz[slot[t][j]] = w[t][j] dy[t];  dw[t][j] = dy[t] . z[slot[t][j]]
+//
+// Bound by HBM: each row of z is read (and of dz written) once, by slot, as
+// whole rows, so the gather costs no extra bytes. `tpt` threads take a token,
+// 16 bytes of its columns each (single elements where base, pitch or width
+// do not allow); up to eight rows' loads are in flight per thread before the
+// first is added, and they are added in the order of j.
+#include "elem.cuh"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace dgt {
+namespace {
+
+constexpr int kMaxK = 32;
+constexpr int kFlight = 8;  // rows of z a thread has in flight
+constexpr int kThreads = 256;
+
+struct CombineParams {
+  const void* z;
+  const int32_t* slots;
+  const float* weights;
+  const void* residual;
+  void* y;
+  long long ldz, ldr, ldy;
+  int tokens, cols, k, nslots;
+  int tpt, chunks;  // threads per token, column chunks (blocks) per group of tokens
+};
+
+template <int TYPE, int VEC>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p) {
+  using P = Pack<TYPE, VEC>;
+  using T = typename P::T;
+  grid_dependency_wait();
+  const int group = blockIdx.x / p.chunks, chunk = blockIdx.x - group * p.chunks;
+  const int per_block = kThreads / p.tpt;
+  const int token = group * per_block + threadIdx.x / p.tpt;
+  const int col = (chunk * p.tpt + threadIdx.x % p.tpt) * VEC;
+  if (token >= p.tokens || col >= p.cols) return;
+  const long long at = static_cast<long long>(token) * p.k;
+  const T* z = static_cast<const T*>(p.z);
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  P res;
+  res.zero();
+  if (p.residual != nullptr) res.load(static_cast<const T*>(p.residual) + token * p.ldr + col);
+  for (int j0 = 0; j0 < p.k; j0 += kFlight) {
+    P row[kFlight];
+    float w[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      row[j].zero();
+      w[j] = 0.0f;
+      if (j0 + j < p.k) {
+        const int s = p.slots[at + j0 + j];
+        w[j] = p.weights != nullptr ? p.weights[at + j0 + j] : 1.0f;
+        if (static_cast<uint32_t>(s) < static_cast<uint32_t>(p.nslots)) row[j].load(z + s * p.ldz + col);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j)
+      if (j0 + j < p.k) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] += w[j] * row[j].get(i);
+      }
+  }
+  P out;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) out.put(i, acc[i] + res.get(i));
+  out.store(static_cast<T*>(p.y) + token * p.ldy + col);
+  grid_launch_dependents();
+}
+
+struct CombineGradParams {
+  const void* dy;
+  const void* z;
+  const int32_t* slots;
+  const float* weights;
+  const int32_t* used;
+  void* dz;
+  float* dweights;
+  long long lddy, ldz, lddz;
+  int tokens, cols, k, nslots;
+  int tpt;  // threads per token, a power of two
+};
+
+// One group of tpt threads walks a token's columns, kFlight rows at a time:
+// dy stays in L1 between the passes of a token with more rows.
+template <int TYPE, int VEC>
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const CombineGradParams p) {
+  using P = Pack<TYPE, VEC>;
+  using T = typename P::T;
+  __shared__ float part[kThreads / 32][kFlight];
+  grid_dependency_wait();
+  const int tid = threadIdx.x % p.tpt, lane = threadIdx.x & 31;
+  const int per_block = kThreads / p.tpt;
+  const int token = blockIdx.x * per_block + threadIdx.x / p.tpt;
+  const bool in = token < p.tokens;
+  const long long at = static_cast<long long>(token) * p.k;
+  const T* z = static_cast<const T*>(p.z);
+  T* dz = static_cast<T*>(p.dz);
+  for (int j0 = 0; j0 < p.k; j0 += kFlight) {
+    int s[kFlight];
+    float w[kFlight], dot[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      s[j] = -1;
+      w[j] = 0.0f;
+      dot[j] = 0.0f;
+      if (in && j0 + j < p.k) {
+        s[j] = p.slots[at + j0 + j];
+        if (static_cast<uint32_t>(s[j]) >= static_cast<uint32_t>(p.nslots)) s[j] = -1;
+        w[j] = p.weights != nullptr ? p.weights[at + j0 + j] : 1.0f;
+      }
+    }
+    if (in) {
+      for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
+        P d;
+        d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
+        P row[kFlight];
+        if (p.dweights != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j) {
+            row[j].zero();
+            if (s[j] >= 0) row[j].load(z + s[j] * p.ldz + col);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          if (s[j] >= 0) {
+            P o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.put(i, w[j] * d.get(i));
+            o.store(dz + s[j] * p.lddz + col);
+          }
+        if (p.dweights != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j)
+            if (s[j] >= 0) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) dot[j] += d.get(i) * row[j].get(i);
+            }
+        }
+      }
+    }
+    if (p.dweights != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j)
+        for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+      if (p.tpt > 32) {
+        __syncthreads();  // the last pass has read part
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j) part[threadIdx.x >> 5][j] = dot[j];
+        }
+        __syncthreads();
+        if (tid < kFlight) {
+          float sum = 0.0f;
+          for (int i = 0; i < p.tpt >> 5; ++i) sum += part[(threadIdx.x >> 5) + i][tid];
+          if (in && j0 + tid < p.k) p.dweights[at + j0 + tid] = sum;
+        }
+      } else if (in && tid == 0) {
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          if (j0 + j < p.k) p.dweights[at + j0 + j] = dot[j];
+      }
+    }
+  }
+  // rows of dz that no pair owns
+  if (p.used != nullptr) {
+    const int used = max(*p.used, 0);
+    for (long long row = static_cast<long long>(used) + blockIdx.x; row < p.nslots; row += gridDim.x) {
+      P o;
+      o.zero();
+      for (int col = threadIdx.x * VEC; col < p.cols; col += kThreads * VEC) o.store(dz + row * p.lddz + col);
+    }
+  }
+  grid_launch_dependents();
+}
+
+bool bad_type(int type) { return type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F32; }
+bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
+bool bad_ld(int64_t ld, int64_t cols) { return ld < cols || ld > (int64_t(1) << 39); }
+bool wide(const void* p, int64_t ld, int es) {
+  return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * es)) % 16) == 0;
+}
+bool meet(const void* a, int64_t rows_a, int64_t ld_a, const void* b, int64_t rows_b, int64_t ld_b, int64_t cols, int es) {
+  if (a == nullptr || b == nullptr || rows_a == 0 || rows_b == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), a1 = a0 + uintptr_t(((rows_a - 1) * ld_a + cols) * es);
+  const uintptr_t b0 = reinterpret_cast<uintptr_t>(b), b1 = b0 + uintptr_t(((rows_b - 1) * ld_b + cols) * es);
+  return a0 < b1 && b0 < a1;
+}
+
+// Threads per token: a power of two covering its vectors, eight to a whole block.
+int threads_per_token(int64_t nvec) {
+  int t = 8;
+  while (t < kThreads && t < nvec) t *= 2;
+  return t;
+}
+
+constexpr int64_t kInt = (int64_t(1) << 31) - 1;
+
+}  // namespace
+}  // namespace dgt
+
+using namespace dgt;
+
+extern "C" {
+
+int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, int64_t ldz, int64_t nslots,
+                 const int32_t* slots, const float* weights, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                 void* stream) {
+  if (bad_type(type) || tokens < 0 || cols < 0 || nslots < 0 || k < 1 || k > kMaxK || tokens > kInt / k ||
+      cols > (kInt >> 8) || nslots > kInt)
+    return GEMM_ERR_INVALID_VALUE;
+  if (tokens == 0 || cols == 0) return GEMM_OK;
+  if ((nslots > 0 && (z == nullptr || bad_ld(ldz, cols))) || slots == nullptr || y == nullptr || bad_ld(ldy, cols) ||
+      (residual != nullptr && bad_ld(ldr, cols)))
+    return GEMM_ERR_INVALID_VALUE;
+  const int es = type_bytes(type);
+  if (misaligned(z, es) || misaligned(y, es) || misaligned(residual, es) || misaligned(slots, 4) ||
+      misaligned(weights, 4))
+    return GEMM_ERR_MISALIGNED;
+  if (meet(y, tokens, ldy, z, nslots, ldz, cols, es) ||
+      (!(y == residual && ldy == ldr) && meet(y, tokens, ldy, residual, tokens, ldr, cols, es)))
+    return GEMM_ERR_INVALID_VALUE;
+  CallContext ctx;
+  const int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[5] = {nslots > 0 ? z : nullptr, slots, y, weights, residual};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  const int v = 16 / es;
+  const bool vec = cols % v == 0 && (nslots == 0 || wide(z, ldz, es)) && wide(y, ldy, es) &&
+                   (residual == nullptr || wide(residual, ldr, es));
+  const int64_t nvec = vec ? cols / v : cols;
+  CombineParams p = {z, slots, weights, residual, y, (long long)ldz, (long long)ldr, (long long)ldy, int(tokens),
+                     int(cols), k, int(nslots), threads_per_token(nvec), 1};
+  p.chunks = int((nvec + p.tpt - 1) / p.tpt);
+  const int64_t groups = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt);
+  if (groups * p.chunks > kInt) return GEMM_ERR_INVALID_VALUE;
+  const int grid = int(groups * p.chunks);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (type == GEMM_TYPE_F16)
+    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_F16, 8>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_kernel<GEMM_TYPE_F16, 1>, grid, kThreads, 0, s, 1, p);
+  else if (type == GEMM_TYPE_BF16)
+    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_BF16, 8>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_kernel<GEMM_TYPE_BF16, 1>, grid, kThreads, 0, s, 1, p);
+  else
+    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_F32, 4>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_kernel<GEMM_TYPE_F32, 1>, grid, kThreads, 0, s, 1, p);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const void* dy, int64_t lddy, const void* z,
+                          int64_t ldz, int64_t nslots, const int32_t* slots, const float* weights,
+                          const int32_t* used, void* dz, int64_t lddz, float* dweights, void* stream) {
+  if (bad_type(type) || tokens < 0 || cols < 0 || nslots < 0 || k < 1 || k > kMaxK || tokens > kInt / k ||
+      cols > (kInt >> 8) || nslots > kInt)
+    return GEMM_ERR_INVALID_VALUE;
+  if (cols == 0 && dweights == nullptr) return GEMM_OK;
+  if (tokens == 0 && (nslots == 0 || used == nullptr)) return GEMM_OK;
+  if (tokens > 0 && (slots == nullptr || (cols > 0 && (dy == nullptr || bad_ld(lddy, cols)))))
+    return GEMM_ERR_INVALID_VALUE;
+  if (nslots > 0 && cols > 0 && (dz == nullptr || bad_ld(lddz, cols) || (dweights != nullptr && (z == nullptr || bad_ld(ldz, cols)))))
+    return GEMM_ERR_INVALID_VALUE;
+  const int es = type_bytes(type);
+  if (misaligned(z, es) || misaligned(dy, es) || misaligned(dz, es) || misaligned(slots, 4) ||
+      misaligned(weights, 4) || misaligned(used, 4) || misaligned(dweights, 4))
+    return GEMM_ERR_MISALIGNED;
+  if (cols > 0 && (meet(dz, nslots, lddz, dy, tokens, lddy, cols, es) || meet(dz, nslots, lddz, z, nslots, ldz, cols, es)))
+    return GEMM_ERR_INVALID_VALUE;
+  CallContext ctx;
+  const int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[7] = {dy, slots, nslots > 0 ? dz : nullptr, weights, used, dweights,
+                         dweights != nullptr && nslots > 0 ? z : nullptr};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  const int v = 16 / es;
+  const bool vec = cols % v == 0 && wide(dy, lddy, es) && wide(dz, lddz, es) && (dweights == nullptr || wide(z, ldz, es));
+  const int64_t nvec = vec ? cols / v : cols;
+  CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,
+                         int(tokens), int(cols), k, int(nslots), threads_per_token(nvec)};
+  const int64_t need = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt);
+  const int grid = int(need > 0 ? need : ctx.sm_count);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (type == GEMM_TYPE_F16)
+    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 8>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 1>, grid, kThreads, 0, s, 1, p);
+  else if (type == GEMM_TYPE_BF16)
+    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 8>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 1>, grid, kThreads, 0, s, 1, p);
+  else
+    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 4>, grid, kThreads, 0, s, 1, p)
+            : launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 1>, grid, kThreads, 0, s, 1, p);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,113 @@
+// Element access of the bandwidth-bound kernels (norm, combine): VEC elements
+// of a type at a time, held as fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "dgt_experts.h"
+
+namespace dgt {
+
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<GEMM_TYPE_F16> {
+  using T = __half;
+  static __device__ __forceinline__ float get(T v) { return __half2float(v); }
+  static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<GEMM_TYPE_BF16> {
+  using T = __nv_bfloat16;
+  static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<GEMM_TYPE_F32> {
+  using T = float;
+  static __device__ __forceinline__ float get(T v) { return v; }
+  static __device__ __forceinline__ T put(float v) { return v; }
+};
+
+inline int type_bytes(int type) { return type == GEMM_TYPE_F32 ? 4 : type == GEMM_TYPE_E4M3 ? 1 : 2; }
+
+// VEC consecutive elements as loaded: 16 bytes, or one element (VEC = 1).
+template <int TYPE, int VEC>
+struct Pack {
+  using E = Elem<TYPE>;
+  using T = typename E::T;
+  static_assert(VEC == 1 || VEC * sizeof(T) == 16, "16 bytes or one element");
+  alignas(VEC * sizeof(T)) T v[VEC];
+
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 1)
+      v[0] = *p;
+    else
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC == 1)
+      *p = v[0];
+    else
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = E::put(0.0f);
+  }
+  __device__ __forceinline__ float get(int i) const { return E::get(v[i]); }
+  __device__ __forceinline__ void put(int i, float x) { v[i] = E::put(x); }
+};
+
+// VEC values to E4M3 (round to nearest even, saturating; NaN stays NaN).
+template <int VEC>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[VEC]) {
+  if constexpr (VEC == 1) {
+    *p = __nv_cvt_float_to_fp8(x[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    uint32_t w[VEC / 4];
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i], x[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2], x[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+// Sum (or, of non-negative bit patterns, maximum) over the `tpr` consecutive
+// threads of a row (a power of two; each row's threads start at a multiple of
+// it). All threads of the block call it together; `red` holds a value per warp
+// and is not written again by the caller's next reduction (it alternates).
+__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
+  for (int d = (tpr < 32 ? tpr : 32) >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  if (tpr <= 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int warps = tpr >> 5, w0 = (threadIdx.x / tpr) * warps;
+  float s = (threadIdx.x & 31) < warps ? red[w0 + (threadIdx.x & 31)] : 0.0f;
+  return warp_sum(s);
+}
+__device__ __forceinline__ uint32_t row_max_bits(uint32_t v, int tpr, uint32_t* red) {
+  for (int d = (tpr < 32 ? tpr : 32) >> 1; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  if (tpr <= 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int warps = tpr >> 5, w0 = (threadIdx.x / tpr) * warps;
+  return __reduce_max_sync(0xFFFFFFFFu, (threadIdx.x & 31) < warps ? red[w0 + (threadIdx.x & 31)] : 0u);
+}
+
+}  // namespace dgt

@@ -1,0 +1,287 @@
+// C entry points of the grouped products (gemm_*_grouped) and of their weight
+// gradient (gemm_*_grouped_wgrad): argument checks, tensor maps, the choice of
+// kernel and the launch. The group sizes stay on the device.
+#include <cstring>
+
+#include "dgt_experts.h"
+#include "group_launch.h"
+
+namespace dgt {
+namespace {
+
+constexpr int64_t kIntLimit = (int64_t(1) << 31) - 1;
+constexpr int64_t kLdLimit = int64_t(1) << 39;
+
+bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
+
+// TMA reads rows whose base and pitch are 16-byte multiples.
+bool tma_rows(const void* p, int64_t ld, int es) { return !misaligned(p, 16) && (ld * es) % 16 == 0; }
+
+// Widest store (16, 8, 4 or 2 bytes) that base, row pitch and matrix stride of a 16-bit matrix allow.
+int store_granularity(const void* p, int64_t ld, int64_t stride) {
+  const uint64_t v = uint64_t(reinterpret_cast<uintptr_t>(p)) | uint64_t(ld * 2) | uint64_t(stride * 2);
+  int g = 16;
+  while (g > 2 && v % g != 0) g >>= 1;
+  return g;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+// Bytes from the first to the last element of a rows x cols matrix (of `count` of them, `stride` apart).
+Range range_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, int64_t count = 1, int64_t stride = 0) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + uintptr_t(((count - 1) * stride + (rows - 1) * ld + cols) * es)};
+}
+bool meet(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+CUtensorMapDataType map_type(int kind) {
+  return kind == KIND_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : kind == KIND_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                            : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
+
+void fill_common(const CallContext& ctx, GroupParams& p) {
+  p.g.status = ctx.status;
+  p.g.epoch = ctx.epoch;
+  p.g.debug = ctx.debug;
+  p.g.wait_limit_ns = ctx.wait_limit_ns;
+}
+
+// Tile rows per band: 8 row tiles of a group share each column tile's weights
+// while those are in L2.
+constexpr int kGroupRaster = 8;
+
+int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
+                int64_t a_rows, int64_t lda, const int32_t* rows, const void* W, int64_t ldw, int64_t stride_w, void* C,
+                int64_t ldc, int layout, const gemm_grouped_epilogue_t* epi, void* stream) {
+  const int es = kind == KIND_E4M3 ? 1 : 2;
+  if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
+      N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
+    return GEMM_ERR_INVALID_VALUE;
+  if (layout != GEMM_B_ROW_MAJOR && layout != GEMM_B_K_MAJOR) return GEMM_ERR_INVALID_VALUE;
+  if (kind == KIND_E4M3 && layout != GEMM_B_K_MAJOR) return GEMM_ERR_INVALID_VALUE;
+  const int act = epi != nullptr ? epi->activation : GEMM_ACT_NONE;
+  if (act < GEMM_ACT_NONE || act > GEMM_ACT_SILU_GATED) return GEMM_ERR_INVALID_VALUE;
+  const bool gated = act == GEMM_ACT_SILU_GATED;
+  if (gated && N % 2 != 0) return GEMM_ERR_INVALID_VALUE;
+  if (slots == 0 || N == 0) return GEMM_OK;
+  const int64_t out_cols = gated ? N / 2 : N;
+  if (offsets == nullptr || C == nullptr || ldc < out_cols || ldc > kLdLimit) return GEMM_ERR_INVALID_VALUE;
+  if (rows == nullptr && a_rows < slots) return GEMM_ERR_INVALID_VALUE;
+  const int64_t w_rows = layout == GEMM_B_ROW_MAJOR ? K : N, w_cols = layout == GEMM_B_ROW_MAJOR ? N : K;
+  if (K > 0) {
+    if (A == nullptr || W == nullptr || a_rows == 0 || lda < K || ldw < w_cols || lda > kLdLimit || ldw > kLdLimit ||
+        (groups > 1 && stride_w < (w_rows - 1) * ldw + w_cols) || stride_w < 0 || stride_w > kLdLimit)
+      return GEMM_ERR_INVALID_VALUE;
+  }
+  if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
+  const void* bias = epi != nullptr ? epi->bias : nullptr;
+  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
+      (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
+    return GEMM_ERR_MISALIGNED;
+  if (K > 0 && (!tma_rows(A, lda, es) || !tma_rows(W, ldw, es) || (groups > 1 && (stride_w * es) % 16 != 0)))
+    return GEMM_ERR_MISALIGNED;
+  // the value half of row-major weights is a TMA box of its own
+  if (K > 0 && gated && layout == GEMM_B_ROW_MAJOR && (out_cols * es) % 16 != 0) return GEMM_ERR_MISALIGNED;
+  const Range rc = range_of(C, slots, out_cols, ldc, 2);
+  if (K > 0 && (meet(rc, range_of(A, a_rows, K, lda, es)) ||
+                meet(rc, range_of(W, w_rows, w_cols, ldw, es, groups, groups > 1 ? stride_w : 0))))
+    return GEMM_ERR_INVALID_VALUE;
+
+  CallContext ctx;
+  int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  if (!on_device(C, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
+      (bias != nullptr && !on_device(bias, ctx.dev)) || (K > 0 && (!on_device(A, ctx.dev) || !on_device(W, ctx.dev))))
+    return GEMM_ERR_NOT_DEVICE_MEMORY;
+  if (epi != nullptr && ((epi->row_scale != nullptr && !on_device(epi->row_scale, ctx.dev)) ||
+                         (epi->col_scale != nullptr && !on_device(epi->col_scale, ctx.dev))))
+    return GEMM_ERR_NOT_DEVICE_MEMORY;
+  GroupLaunch L;
+  memset(&L, 0, sizeof(L));
+  GroupParams& p = L.p;
+  fill_common(ctx, p);
+  p.offsets = offsets;
+  p.groups = groups;
+  p.slots = int(slots);
+  p.rows = rows;
+  p.a_rows = int(a_rows);
+  p.row_scale = epi != nullptr ? epi->row_scale : nullptr;
+  p.col_scale = epi != nullptr ? epi->col_scale : nullptr;
+  p.g.alpha = epi != nullptr ? epi->alpha : 1.0f;
+  p.g.bias = bias;
+  p.g.act = act;
+  p.plain = !gated && act == GEMM_ACT_NONE && bias == nullptr && p.row_scale == nullptr && p.col_scale == nullptr &&
+            p.g.alpha == 1.0f;
+  p.out_cols = int(out_cols);
+  p.g.N = int(N);
+  p.g.K = int(K);
+  p.g.C = C;
+  p.g.ldc = ldc;
+  p.g.c_gran = store_granularity(C, ldc, 0);
+  p.g.c_tma = p.g.c_gran == 16;
+  p.g.num_kb = int((K * es + 127) / 128);
+  p.g.raster = kGroupRaster;
+  L.gated = gated;
+  L.dev = ctx.dev;
+  L.stream = static_cast<cudaStream_t>(stream);
+  // The host knows the slots and the groups, not the group sizes. A pair's 256-row tiles pay once an average
+  // group fills most of one.
+  const int64_t active = groups < slots ? groups : slots;
+  L.pair = slots / active >= 128;
+  const int out_bn = (L.pair ? kGroupPairN : kGroupSingleN) / (gated ? 2 : 1);
+  p.g.tiles_n = int((out_cols + out_bn - 1) / out_bn);
+  const int64_t tiles = (slots / (L.pair ? 256 : 128) + active + 1) * p.g.tiles_n;  // at most
+  const int64_t units = L.pair ? ctx.sm_count / 2 : ctx.sm_count;
+  L.grid = int((tiles < units ? tiles : units) * (L.pair ? 2 : 1));
+
+  const CUtensorMapDataType dt = map_type(kind);
+  const uint32_t bk = 128 / es;
+  if (K > 0) {
+    if (!encode_map_2d(&L.tmAg, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)) return GEMM_ERR_DRIVER;
+    const uint64_t mat = groups > 1 ? uint64_t(stride_w) * es : 0;
+    bool ok;
+    if (layout == GEMM_B_K_MAJOR) {
+      const uint32_t box = L.pair ? kGroupPairN / 2 : gated ? kGroupSingleN / 2 : kGroupSingleN;
+      ok = encode_map_3d(&L.tmB, dt, W, K, N, ldw * es, groups, mat, bk, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+      ok = encode_map_3d(&L.tmB, dt, W, N, K, ldw * es, groups, mat, 128 / es, bk, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (!ok) return GEMM_ERR_DRIVER;
+  }
+  if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, C, out_cols, slots, ldc * 2, 1, 0, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B))
+    return GEMM_ERR_DRIVER;
+  cudaError_t e;
+  const bool km = layout == GEMM_B_K_MAJOR;
+  if (kind == KIND_E4M3)
+    e = launch_group_e4m3_km(L);
+  else if (kind == KIND_BF16)
+    e = km ? launch_group_bf16_km(L) : launch_group_bf16_rm(L);
+  else
+    e = km ? launch_group_f16_km(L) : launch_group_f16_rm(L);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
+              int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
+              int64_t stride_dw, int layout, void* stream) {
+  if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
+      N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
+    return GEMM_ERR_INVALID_VALUE;
+  if (layout != GEMM_B_ROW_MAJOR && layout != GEMM_B_K_MAJOR) return GEMM_ERR_INVALID_VALUE;
+  if (N == 0 || K == 0) return GEMM_OK;
+  const bool km = layout == GEMM_B_K_MAJOR;
+  const int64_t out_rows = km ? N : K, out_cols = km ? K : N;
+  if (offsets == nullptr || dW == nullptr || lddw < out_cols || lddw > kLdLimit || stride_dw < 0 ||
+      stride_dw > kLdLimit || (groups > 1 && stride_dw < (out_rows - 1) * lddw + out_cols))
+    return GEMM_ERR_INVALID_VALUE;
+  if (slots > 0 && (A == nullptr || dC == nullptr || a_rows == 0 || lda < K || lddc < N || lda > kLdLimit ||
+                    lddc > kLdLimit || (rows == nullptr && a_rows < slots)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (((out_rows + 255) / 256) * ((out_cols + 255) / 256) > kIntLimit / groups) return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2)) return GEMM_ERR_MISALIGNED;
+  if (slots > 0 && (!tma_rows(A, lda, 2) || !tma_rows(dC, lddc, 2))) return GEMM_ERR_MISALIGNED;
+  const Range rw = range_of(dW, out_rows, out_cols, lddw, 2, groups, groups > 1 ? stride_dw : 0);
+  if (slots > 0 && (meet(rw, range_of(A, a_rows, K, lda, 2)) || meet(rw, range_of(dC, slots, N, lddc, 2))))
+    return GEMM_ERR_INVALID_VALUE;
+
+  CallContext ctx;
+  int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  if (!on_device(dW, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
+      (slots > 0 && (!on_device(A, ctx.dev) || !on_device(dC, ctx.dev))))
+    return GEMM_ERR_NOT_DEVICE_MEMORY;
+  GroupLaunch L;
+  memset(&L, 0, sizeof(L));
+  GroupParams& p = L.p;
+  fill_common(ctx, p);
+  p.offsets = offsets;
+  p.groups = groups;
+  p.slots = int(slots);
+  p.rows = rows;
+  p.a_rows = int(a_rows);
+  p.plain = 1;
+  p.out_rows = int(out_rows);
+  p.out_cols = int(out_cols);
+  p.g.C = dW;
+  p.g.ldc = lddw;
+  p.g.stride_c = groups > 1 ? stride_dw : 0;
+  p.g.c_gran = store_granularity(dW, lddw, p.g.stride_c);
+  p.g.c_tma = p.g.c_gran == 16;
+  p.g.raster = kGroupRaster;
+  p.g.tiles_m = int((out_rows + 255) / 256);
+  p.g.tiles_n = int((out_cols + 255) / 256);
+  // rows of A are gathered when the caller gives their numbers; dC is read by slot
+  p.gather_p = !km && rows != nullptr;
+  p.gather_q = km && rows != nullptr;
+  L.pair = true;
+  L.dev = ctx.dev;
+  L.stream = static_cast<cudaStream_t>(stream);
+  const int64_t tiles = int64_t(groups) * p.g.tiles_m * p.g.tiles_n;
+  const int64_t units = ctx.sm_count / 2;
+  L.grid = int(2 * (tiles < units ? tiles : units));
+  const CUtensorMapDataType dt = map_type(kind);
+  if (slots > 0) {
+    const void* P = km ? dC : A;
+    const void* Q = km ? A : dC;
+    const uint64_t ldp = uint64_t(km ? lddc : lda) * 2, ldq = uint64_t(km ? lda : lddc) * 2;
+    const uint64_t rp = km ? slots : a_rows, rq = km ? a_rows : slots;
+    bool ok = p.gather_p ? encode_map_2d(&L.tmAg, dt, P, out_rows, rp, ldp, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B)
+                         : encode_map_3d(&L.tmA, dt, P, out_rows, rp, ldp, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && (p.gather_q ? encode_map_2d(&L.tmBg, dt, Q, out_cols, rq, ldq, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B)
+                           : encode_map_3d(&L.tmB, dt, Q, out_cols, rq, ldq, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B));
+    if (!ok) return GEMM_ERR_DRIVER;
+  }
+  if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, dW, out_cols, out_rows, lddw * 2, groups,
+                                  uint64_t(p.g.stride_c) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return GEMM_ERR_DRIVER;
+  const cudaError_t e = kind == KIND_BF16 ? launch_group_bf16_wgrad(L) : launch_group_f16_wgrad(L);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace dgt
+
+extern "C" {
+
+int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
+                     int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
+                     int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
+                     void* stream) {
+  return dgt::run_grouped(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
+                          layout, epilogue, stream);
+}
+
+int gemm_bf16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
+                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
+                      int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
+                      void* stream) {
+  return dgt::run_grouped(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
+                          layout, epilogue, stream);
+}
+
+int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint8_t* A,
+                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint8_t* W, int64_t ldw,
+                      int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
+                      void* stream) {
+  return dgt::run_grouped(dgt::KIND_E4M3, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
+                          layout, epilogue, stream);
+}
+
+int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
+                           int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC, int64_t lddc,
+                           uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream) {
+  return dgt::run_wgrad(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
+                        stride_dw, layout, stream);
+}
+
+int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K,
+                            const uint16_t* A, int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC,
+                            int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream) {
+  return dgt::run_wgrad(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
+                        stride_dw, layout, stream);
+}
+
+}  // extern "C"

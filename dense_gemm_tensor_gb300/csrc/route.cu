@@ -1,0 +1,616 @@
+// Routing to experts: scores, choice, weights and the expert order
+// (gemm_route), and the gradient of the weights (gemm_route_backward).
+//
+// A warp takes a token: lane l holds the scores of experts l, l + 32, ... and
+// picks the k largest keys one after another (a warp maximum of the lanes'
+// best, then the winner's owner looks up its next best). The softmax
+// denominator is summed by halves -- within a lane, then across lanes 16, 8,
+// 4, 2, 1 apart -- which with zeros past the last expert is the order of any
+// power-of-two length, so the same logits give the same keys in every build
+// of the kernel.
+//
+// The expert order is a stable counting sort of the token-major pairs. A block
+// owns a run of tokens; its warps own consecutive pieces of the run's pairs
+// and rank them 32 at a time (match_any gives a pair's rank among equal
+// experts of the 32, a per-warp count per expert the rank before them). Few
+// tokens: one block does everything in one launch. More: the first launch
+// leaves each block's count per expert, and the second adds the counts of the
+// blocks before it and of the experts before its own.
+//
+// The bytes are few (one read of the logits); the time is the selection's
+// instructions and, for a serving step, launch latency.
+#include <math.h>
+
+#include "elem.cuh"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace dgt {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxK = 32;
+constexpr int kMaxBlocks = 152;      // of the two-launch form: one for each SM
+constexpr int kOneBlockTokens = 128;
+
+struct RouteParams {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int32_t* slots;
+  int32_t* rows;
+  int32_t* offsets;
+  int32_t* counts;  // two-launch form: blocks x experts
+  long long ld;
+  int type, tokens, experts, k, score, groups, kept, renormalize, per_block, blocks;
+  float scale;
+};
+
+__device__ __forceinline__ float load_logit(const void* p, int type, long long at) {
+  if (type == GEMM_TYPE_F32) return static_cast<const float*>(p)[at];
+  if (type == GEMM_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
+  return __half2float(static_cast<const __half*>(p)[at]);
+}
+
+// Order-preserving map of a float to an unsigned number (+-0 alike); 0 is below every number's image.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Sum of x[j] over all lanes and j by halves (see above).
+template <int NPL>
+__device__ __forceinline__ float halves_sum(const float (&e)[NPL]) {
+  float x[NPL];
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) x[j] = e[j];
+#pragma unroll
+  for (int w = NPL / 2; w > 0; w >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) x[j] = x[j] + x[j + w];
+  return warp_sum(x[0]);
+}
+
+// The scores of one token: lane l's s[j] is expert l + 32 j (0 past the last
+// one and for a logit of -inf); `there`: bit j set where the logit is above -inf.
+template <int NPL>
+__device__ __forceinline__ void token_scores(const void* logits, int type, long long base, int experts, int score,
+                                             int lane, float (&s)[NPL], uint32_t& there) {
+  float top = -INFINITY;
+  there = 0;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    const int e = lane + 32 * j;
+    s[j] = e < experts ? load_logit(logits, type, base + e) : -INFINITY;
+    if (!(s[j] == -INFINITY)) there |= 1u << j;
+    top = fmaxf(top, s[j]);
+  }
+  if (score == GEMM_SCORE_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) s[j] = (there >> j) & 1u ? 1.0f / (1.0f + expf(-s[j])) : 0.0f;
+    return;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) s[j] = (there >> j) & 1u ? expf(s[j] - top) : 0.0f;
+  const float z = halves_sum(s);
+  const float div = z == 0.0f ? 1.0f : z;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) s[j] = s[j] / div;
+}
+
+// Chooses one token's experts; lane i < k returns the i-th id (-1: none) and its weight.
+template <int NPL>
+__device__ __forceinline__ void route_token(const RouteParams& p, int token, int lane, int& id, float& weight) {
+  float s[NPL];
+  uint32_t there;
+  token_scores<NPL>(p.logits, p.type, token * p.ld, p.experts, p.score, lane, s, there);
+  float key[NPL];
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    const int e = lane + 32 * j;
+    key[j] = -INFINITY;
+    if ((there >> j) & 1u) {
+      const float v = p.bias != nullptr ? s[j] + p.bias[e] : s[j];
+      nan = nan || s[j] != s[j];
+      if (v == v) key[j] = v;
+    }
+  }
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  uint32_t kept = 0xFFFFFFFFu;
+  const int per = p.experts / p.groups;
+  if (p.groups > 1) {
+    float mine = 0.0f;  // lane g: group g's key
+    for (int g = 0; g < p.groups; ++g) {
+      float a = -INFINITY, b = -INFINITY;  // the two largest keys
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        const int e = lane + 32 * j;
+        if (e >= g * per && e < (g + 1) * per) {
+          b = fmaxf(b, fminf(a, key[j]));
+          a = fmaxf(a, key[j]);
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        const float c = __shfl_xor_sync(0xFFFFFFFFu, a, d), f = __shfl_xor_sync(0xFFFFFFFFu, b, d);
+        b = fmaxf(fmaxf(b, f), fminf(a, c));
+        a = fmaxf(a, c);
+      }
+      if (lane == g) mine = per > 1 ? a + b : a;
+    }
+    uint32_t best = lane < p.groups ? order_bits(mine) : 0u;
+    kept = 0;
+    for (int i = 0; i < p.kept; ++i) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+      const int g = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+      kept |= 1u << g;
+      if (lane == g) best = 0;
+    }
+  }
+  uint32_t u[NPL];
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    u[j] = key[j] > -INFINITY ? order_bits(key[j]) : 0u;
+    if (p.groups > 1 && u[j] != 0 && !((kept >> ((lane + 32 * j) / per)) & 1u)) u[j] = 0;
+  }
+  id = -1;
+  weight = 0.0f;
+  for (int i = 0; i < p.k; ++i) {
+    uint32_t best = 0;
+    int at = 0;
+    float sc = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j)
+      if (u[j] > best) {
+        best = u[j];
+        at = j;
+        sc = s[j];
+      }
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (m == 0) break;  // no expert left
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == m);
+    int owner = __ffs(who) - 1;
+    if (who & (who - 1)) {  // equal keys: the lowest expert
+      const uint32_t e = best == m ? uint32_t(lane + 32 * at) : 0xFFFFFFFFu;
+      owner = int(__reduce_min_sync(0xFFFFFFFFu, e)) & 31;
+    }
+    const int won = __shfl_sync(0xFFFFFFFFu, lane + 32 * at, owner);
+    const float score = __shfl_sync(0xFFFFFFFFu, sc, owner);
+    if (lane == i) {
+      id = won;
+      weight = score;
+    }
+    if (lane == owner) {
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (j == at) u[j] = 0;
+    }
+  }
+  if (p.renormalize) weight = weight / (warp_sum(weight) + 1e-20f);
+  weight *= p.scale;
+  if (nan) weight = __int_as_float(0x7FC00000);
+}
+
+// Walks this warp's piece of the block's pairs in order, 32 at a time, and
+// calls use(pair, expert, rank) with each one's rank among the block's pairs of
+// its expert that this warp has seen, counted on top of hist[expert].
+template <class Use>
+__device__ __forceinline__ void rank_pairs(const int32_t* ids, long long first, int n, int warp, int warps, int lane,
+                                           int32_t* hist, Use use) {
+  const int piece = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const int end = min(n, (warp + 1) * piece);
+  for (int i0 = warp * piece; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const int e = i < end ? ids[first + i] : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    const int base = e >= 0 ? hist[e] : 0;
+    __syncwarp();
+    if (e >= 0 && before == 0) hist[e] = base + __popc(same);
+    __syncwarp();
+    use(first + i, i < end, e, base + before);
+  }
+}
+
+// Exclusive sum over the threads of the block; `sums` holds a value per warp.
+__device__ __forceinline__ int block_exclusive(int v, int32_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int at = incl - v;
+  for (int w = 0; w < warp; ++w) at += sums[w];
+  return at;
+}
+
+// Threads of a routing block: per-warp counts of all experts fit 32 KB.
+template <int NPL>
+constexpr int kRouteThreads = NPL <= 8 ? 1024 : NPL == 16 ? 512 : 256;
+
+// One-block form: chooses, then orders the pairs.
+// Two-launch form (p.blocks > 1): chooses and leaves the block's counts.
+template <int NPL>
+__global__ void __launch_bounds__(kRouteThreads<NPL>) route_kernel(const RouteParams p) {
+  constexpr int WARPS = kRouteThreads<NPL> / 32;
+  constexpr int E = 32 * NPL;
+  __shared__ int32_t hist[WARPS][E];
+  __shared__ int32_t sums[32];
+  __shared__ int32_t used;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < WARPS * E; i += blockDim.x) (&hist[0][0])[i] = 0;
+  grid_dependency_wait();
+  __syncthreads();
+  const int t0 = blockIdx.x * p.per_block;
+  const int t1 = min(p.tokens, t0 + p.per_block);
+  const bool alone = p.blocks == 1;
+  for (int t = t0 + warp; t < t1; t += WARPS) {
+    int id;
+    float w;
+    route_token<NPL>(p, t, lane, id, w);
+    if (lane < p.k) {
+      p.ids[static_cast<long long>(t) * p.k + lane] = id;
+      p.weights[static_cast<long long>(t) * p.k + lane] = w;
+      if (!alone && id >= 0) atomicAdd(&hist[0][id], 1);  // whole numbers: any order gives the same count
+    }
+  }
+  __syncthreads();
+  if (!alone) {
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
+      p.counts[static_cast<long long>(blockIdx.x) * p.experts + e] = hist[0][e];
+    grid_launch_dependents();
+    return;
+  }
+  const int n = (t1 - t0) * p.k;
+  rank_pairs(p.ids, 0, n, warp, WARPS, lane, hist[warp], [](long long, bool, int, int) {});
+  __syncthreads();
+  // counts per expert (thread e < experts; at most E <= blockDim.x * 4 experts)
+  constexpr int PER = (E + kRouteThreads<NPL> - 1) / kRouteThreads<NPL>;
+  int total[PER], sum = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = threadIdx.x * PER + q;
+    total[q] = 0;
+    if (e < E)
+      for (int w = 0; w < WARPS; ++w) {
+        const int c = hist[w][e];
+        hist[w][e] = total[q];
+        total[q] += c;
+      }
+    sum += total[q];
+  }
+  int at = block_exclusive(sum, sums);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = threadIdx.x * PER + q;
+    if (e < E)
+      for (int w = 0; w < WARPS; ++w) hist[w][e] += at;
+    if (e < p.experts) p.offsets[e] = at;
+    at += total[q];
+    if (e == p.experts - 1) p.offsets[p.experts] = used = at;
+  }
+  __syncthreads();
+  rank_pairs(p.ids, 0, n, warp, WARPS, lane, hist[warp], [&](long long i, bool in, int e, int rank) {
+    if (!in) return;
+    p.slots[i] = e >= 0 ? rank : -1;
+    if (e >= 0) p.rows[rank] = int(i / p.k);
+  });
+  for (int i = used + threadIdx.x; i < n; i += blockDim.x) p.rows[i] = -1;
+  grid_launch_dependents();
+}
+
+// Second launch of the two-launch form: block b places its pairs.
+__global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) {
+  extern __shared__ int32_t shared[];  // warps x experts counts, then totals and starts of the experts
+  __shared__ int32_t sums[32];
+  __shared__ int32_t used;
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* hist = shared;
+  int32_t* total = shared + warps * p.experts;
+  int32_t* start = total + p.experts;
+  for (int i = threadIdx.x; i < (warps + 2) * p.experts; i += blockDim.x) shared[i] = 0;
+  __syncthreads();
+  grid_dependency_wait();
+  // counts of all blocks and of those before this one: the threads split (block, expert) in whole rows
+  const int parts = max(1, int(blockDim.x) / p.experts);
+  for (int q = threadIdx.x; q < parts * p.experts; q += blockDim.x) {
+    const int e = q % p.experts, part = q / p.experts;
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int b = part; b < p.blocks; b += parts) {
+      const int c = __ldcg(p.counts + static_cast<long long>(b) * p.experts + e);
+      all += c;
+      before += b < int(blockIdx.x) ? c : 0;
+    }
+    atomicAdd(&total[e], all);
+    atomicAdd(&start[e], before);
+  }
+  const int t0 = blockIdx.x * p.per_block;
+  const int n = max(0, min(p.tokens, t0 + p.per_block) - t0) * p.k;
+  const long long first = static_cast<long long>(t0) * p.k;
+  rank_pairs(p.ids, first, n, warp, warps, lane, hist + warp * p.experts, [](long long, bool, int, int) {});
+  __syncthreads();
+  const int per = (p.experts + blockDim.x - 1) / blockDim.x;
+  int sum = 0;
+  for (int q = 0; q < per; ++q) {
+    const int e = threadIdx.x * per + q;
+    if (e < p.experts) sum += total[e];
+  }
+  int at = block_exclusive(sum, sums);
+  for (int q = 0; q < per; ++q) {
+    const int e = threadIdx.x * per + q;
+    if (e >= p.experts) break;
+    if (blockIdx.x == 0) p.offsets[e] = at;
+    int run = at + start[e];
+    for (int w = 0; w < warps; ++w) {
+      const int c = hist[w * p.experts + e];
+      hist[w * p.experts + e] = run;
+      run += c;
+    }
+    at += total[e];
+    if (e == p.experts - 1) {
+      if (blockIdx.x == 0) p.offsets[p.experts] = at;
+      used = at;
+    }
+  }
+  __syncthreads();
+  rank_pairs(p.ids, first, n, warp, warps, lane, hist + warp * p.experts, [&](long long i, bool in, int e, int rank) {
+    if (!in) return;
+    p.slots[i] = e >= 0 ? rank : -1;
+    if (e >= 0) p.rows[rank] = int(i / p.k);
+  });
+  const long long all = static_cast<long long>(p.tokens) * p.k;
+  for (long long i = used + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < all;
+       i += static_cast<long long>(gridDim.x) * blockDim.x)
+    p.rows[i] = -1;
+  grid_launch_dependents();
+}
+
+// dlogits of one token: the weights' gradient through the renormalisation,
+// then through the scores. With c = sum of the chosen scores + 1e-20 and
+// w_j = scale s_j / c: ds_j = (scale dw_j - sum_i dw_i w_i) / c; without
+// renormalisation ds_j = scale dw_j. Softmax: dl_e = s_e (ds_e - sum_i ds_i s_i)
+// (ds = 0 off the choice); sigmoid: dl_e = ds_e s_e (1 - s_e).
+template <int NPL>
+__global__ void __launch_bounds__(256) route_grad_kernel(const RouteParams p, const float* dweights, void* dlogits,
+                                                         long long ldd) {
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  for (long long t = (blockIdx.x * 256LL + threadIdx.x) >> 5; t < p.tokens; t += gridDim.x * 8LL) {
+    float s[NPL], ds[NPL];
+    uint32_t there;
+    token_scores<NPL>(p.logits, p.type, t * p.ld, p.experts, p.score, lane, s, there);
+    int id = -1;
+    float dw = 0.0f;
+    if (lane < p.k) {
+      id = p.ids[t * p.k + lane];
+      if (id >= p.experts) id = -1;
+      if (id >= 0) dw = dweights[t * p.k + lane] * p.scale;
+    }
+    float chosen = 0.0f;  // lane i: the score of the i-th choice
+    for (int i = 0; i < p.k; ++i) {
+      const int e = __shfl_sync(0xFFFFFFFFu, id, i);
+      float v = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        if (j == e >> 5) v = s[j];
+      v = __shfl_sync(0xFFFFFFFFu, v, e & 31);
+      if (lane == i && e >= 0) chosen = v;
+    }
+    float d = dw;
+    if (p.renormalize) {
+      const float c = warp_sum(chosen) + 1e-20f;
+      const float mean = warp_sum(dw * (chosen / c));
+      d = id >= 0 ? (dw - mean) / c : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) ds[j] = 0.0f;
+    for (int i = 0; i < p.k; ++i) {
+      const int e = __shfl_sync(0xFFFFFFFFu, id, i);
+      const float v = __shfl_sync(0xFFFFFFFFu, d, i);
+      if (e >= 0 && (e & 31) == lane) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+          if (j == e >> 5) ds[j] += v;
+      }
+    }
+    float dot = 0.0f;
+    if (p.score == GEMM_SCORE_SOFTMAX) {
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) dot += ds[j] * s[j];
+      dot = warp_sum(dot);
+    }
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      const int e = lane + 32 * j;
+      if (e >= p.experts) continue;
+      const float g = p.score == GEMM_SCORE_SOFTMAX ? s[j] * (ds[j] - dot) : ds[j] * s[j] * (1.0f - s[j]);
+      const long long at = t * ldd + e;
+      if (p.type == GEMM_TYPE_F32)
+        static_cast<float*>(dlogits)[at] = g;
+      else if (p.type == GEMM_TYPE_BF16)
+        static_cast<__nv_bfloat16*>(dlogits)[at] = __float2bfloat16_rn(g);
+      else
+        static_cast<__half*>(dlogits)[at] = __float2half_rn(g);
+    }
+  }
+  grid_launch_dependents();
+}
+
+bool bad_type(int type) { return type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F32; }
+bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
+
+// Registers of scores per lane: the smallest build that covers the experts.
+int scores_per_lane(int experts) {
+  int n = 1;
+  while (32 * n < experts) n *= 2;
+  return n;
+}
+
+// Blocks and tokens per block of gemm_route.
+void route_shape(int64_t tokens, int* blocks, int* per_block) {
+  if (tokens <= kOneBlockTokens) {
+    *blocks = 1;
+    *per_block = int(tokens);
+    return;
+  }
+  int64_t per = (tokens + kMaxBlocks - 1) / kMaxBlocks;
+  if (per < 32) per = 32;
+  *per_block = int(per);
+  *blocks = int((tokens + per - 1) / per);
+}
+
+int check_config(int64_t tokens, int experts, const gemm_route_config_t* c) {
+  if (c == nullptr || tokens < 0 || experts < 1 || experts > kMaxExperts || c->k < 1 || c->k > kMaxK ||
+      c->k > experts || (c->score != GEMM_SCORE_SOFTMAX && c->score != GEMM_SCORE_SIGMOID) ||
+      tokens > ((int64_t(1) << 31) - 1) / c->k)
+    return GEMM_ERR_INVALID_VALUE;
+  return GEMM_OK;
+}
+
+template <int NPL>
+cudaError_t launch_route(const RouteParams& p, cudaStream_t s) {
+  cudaError_t e = launch_dependent(route_kernel<NPL>, p.blocks, kRouteThreads<NPL>, 0, s, 1, p);
+  if (e != cudaSuccess || p.blocks == 1) return e;
+  // as many warps as let their counts stay within 32 KB
+  const int threads = kRouteThreads<NPL>;
+  const size_t smem = size_t(threads / 32 + 2) * size_t(p.experts) * sizeof(int32_t);
+  return launch_dependent(route_place_kernel, p.blocks, threads, smem, s, 1, p);
+}
+
+template <int NPL>
+cudaError_t launch_route_grad(const RouteParams& p, const float* dw, void* dl, long long ldd, int sms, cudaStream_t s) {
+  int64_t blocks = (int64_t(p.tokens) + 7) / 8;
+  if (blocks > int64_t(sms) * 8) blocks = int64_t(sms) * 8;
+  return launch_dependent(route_grad_kernel<NPL>, int(blocks), 256, 0, s, 1, p, dw, dl, ldd);
+}
+
+}  // namespace
+}  // namespace dgt
+
+using namespace dgt;
+
+extern "C" {
+
+int64_t gemm_route_workspace(int64_t tokens, int experts, int k) {
+  if (tokens <= 0 || experts < 1 || experts > kMaxExperts || k < 1) return 0;
+  int blocks, per;
+  route_shape(tokens, &blocks, &per);
+  return blocks > 1 ? int64_t(blocks) * experts * int64_t(sizeof(int32_t)) : 0;
+}
+
+int gemm_route(int type, int64_t tokens, int experts, const void* logits, int64_t ld, const float* bias,
+               const gemm_route_config_t* config, int32_t* ids, float* weights, int32_t* slots, int32_t* rows,
+               int32_t* offsets, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = check_config(tokens, experts, config);
+  if (st != GEMM_OK) return st;
+  if (bad_type(type) || config->groups < 1 || config->groups > 32 || experts % config->groups != 0 ||
+      config->kept_groups < 1 || config->kept_groups > config->groups ||
+      config->k > config->kept_groups * (experts / config->groups))
+    return GEMM_ERR_INVALID_VALUE;
+  if (offsets == nullptr || (tokens > 0 && (logits == nullptr || ids == nullptr || weights == nullptr ||
+                                            slots == nullptr || rows == nullptr || ld < experts ||
+                                            ld > (int64_t(1) << 39))))
+    return GEMM_ERR_INVALID_VALUE;
+  const int64_t need = gemm_route_workspace(tokens, experts, config->k);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(logits, type_bytes(type)) || misaligned(bias, 4) || misaligned(ids, 4) || misaligned(weights, 4) ||
+      misaligned(slots, 4) || misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(workspace, 16))
+    return GEMM_ERR_MISALIGNED;
+  CallContext ctx;
+  st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[8] = {offsets, tokens > 0 ? logits : nullptr, tokens > 0 ? ids : nullptr,
+                         tokens > 0 ? weights : nullptr, tokens > 0 ? slots : nullptr, tokens > 0 ? rows : nullptr,
+                         bias, need > 0 ? workspace : nullptr};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  RouteParams p = {};
+  p.logits = logits;
+  p.bias = bias;
+  p.ids = ids;
+  p.weights = weights;
+  p.slots = slots;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.counts = static_cast<int32_t*>(workspace);
+  p.ld = ld;
+  p.type = type;
+  p.tokens = int(tokens);
+  p.experts = experts;
+  p.k = config->k;
+  p.score = config->score;
+  p.groups = config->groups;
+  p.kept = config->kept_groups;
+  p.renormalize = config->renormalize != 0;
+  p.scale = config->scale;
+  route_shape(tokens, &p.blocks, &p.per_block);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (scores_per_lane(experts)) {
+    case 1: e = launch_route<1>(p, s); break;
+    case 2: e = launch_route<2>(p, s); break;
+    case 4: e = launch_route<4>(p, s); break;
+    case 8: e = launch_route<8>(p, s); break;
+    case 16: e = launch_route<16>(p, s); break;
+    default: e = launch_route<32>(p, s); break;
+  }
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int gemm_route_backward(int type, int64_t tokens, int experts, const void* logits, int64_t ld, const int32_t* ids,
+                        const float* dweights, const gemm_route_config_t* config, void* dlogits, int64_t ldd,
+                        void* stream) {
+  int st = check_config(tokens, experts, config);
+  if (st != GEMM_OK) return st;
+  if (bad_type(type)) return GEMM_ERR_INVALID_VALUE;
+  if (tokens == 0) return GEMM_OK;
+  if (logits == nullptr || ids == nullptr || dweights == nullptr || dlogits == nullptr || ld < experts ||
+      ldd < experts || ld > (int64_t(1) << 39) || ldd > (int64_t(1) << 39))
+    return GEMM_ERR_INVALID_VALUE;
+  const int es = type_bytes(type);
+  if (misaligned(logits, es) || misaligned(dlogits, es) || misaligned(ids, 4) || misaligned(dweights, 4))
+    return GEMM_ERR_MISALIGNED;
+  // dlogits may be the logits' own buffer and pitch (a warp reads its token before it writes it), or apart from it
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(logits), a1 = a0 + uintptr_t(((tokens - 1) * ld + experts) * es);
+  const uintptr_t b0 = reinterpret_cast<uintptr_t>(dlogits), b1 = b0 + uintptr_t(((tokens - 1) * ldd + experts) * es);
+  if (!(a0 == b0 && ld == ldd) && a0 < b1 && b0 < a1) return GEMM_ERR_INVALID_VALUE;
+  CallContext ctx;
+  st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[4] = {logits, ids, dweights, dlogits};
+  for (const void* q : ptrs)
+    if (!on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  RouteParams p = {};
+  p.logits = logits;
+  p.ids = const_cast<int32_t*>(ids);
+  p.ld = ld;
+  p.type = type;
+  p.tokens = int(tokens);
+  p.experts = experts;
+  p.k = config->k;
+  p.score = config->score;
+  p.renormalize = config->renormalize != 0;
+  p.scale = config->scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (scores_per_lane(experts)) {
+    case 1: e = launch_route_grad<1>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+    case 2: e = launch_route_grad<2>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+    case 4: e = launch_route_grad<4>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+    case 8: e = launch_route_grad<8>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+    case 16: e = launch_route_grad<16>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+    default: e = launch_route_grad<32>(p, dweights, dlogits, ldd, ctx.sm_count, s); break;
+  }
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // extern "C"
