@@ -48,13 +48,61 @@ void fill_common(const CallContext& ctx, GroupParams& p) {
   p.g.wait_limit_ns = ctx.wait_limit_ns;
 }
 
+// dst[s] = src[row(s)] for the slots in use: the rows of a gathered operand in
+// slot order, 16 bytes a lane (rows start on 16-byte boundaries; the last piece
+// of a row may run into its padding, which the pitch of dst holds). A warp takes
+// a row; bound by memory: one read of the rows (repeats of a token hit L2) and one
+// write, 134 MB of 4096 BF16 columns x 16384 slots in about 30 us.
+__global__ void __launch_bounds__(256) permute_rows_kernel(const uint8_t* src, long long ld, int a_rows,
+                                                           const int* rows, const int* offsets, int groups, int slots,
+                                                           uint8_t* dst, long long dst_ld, long long row_bytes) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int used = min(max(offsets[groups], 0), slots);
+  const int pieces = static_cast<int>((row_bytes + 15) / 16);
+  const int whole = static_cast<int>(row_bytes / 16);
+  for (long long s = blockIdx.x * 8LL + (threadIdx.x >> 5); s < used; s += gridDim.x * 8LL) {
+    const uint8_t* from = src + min(max(rows[s], 0), a_rows - 1) * ld;
+    uint8_t* to = dst + s * dst_ld;
+    int c = lane;
+    for (; c + 96 < whole; c += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (c + 32 * i) * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (c + 32 * i) * 16) = v[i];
+    }
+    for (; c < whole; c += 32) *reinterpret_cast<uint4*>(to + c * 16) = *reinterpret_cast<const uint4*>(from + c * 16);
+    if (whole < pieces && lane < int(row_bytes - whole * 16LL)) to[whole * 16 + lane] = from[whole * 16 + lane];
+  }
+  grid_launch_dependents();
+}
+
+// Row pitch in bytes of a gathered operand in slot order.
+int64_t permuted_pitch(int64_t K, int es) { return (K * es + 127) / 128 * 128; }
+
+int permute_rows(const CallContext& ctx, const void* A, int64_t a_rows, int64_t lda, const int32_t* rows,
+                 const int32_t* offsets, int groups, int64_t slots, int64_t K, int es, void* dst, cudaStream_t stream) {
+  const int64_t blocks = (slots + 7) / 8, most = int64_t(ctx.sm_count) * 8;
+  const cudaError_t e = launch_dependent(
+      permute_rows_kernel, int(blocks < most ? blocks : most), 256, 0, stream, 1, static_cast<const uint8_t*>(A),
+      (long long)(lda * es), int(a_rows), rows, offsets, groups, int(slots), static_cast<uint8_t*>(dst),
+      (long long)permuted_pitch(K, es), (long long)(K * es));
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+// The host knows the slots and the groups, not the group sizes. A pair's
+// 256-row tiles pay once an average group fills most of one.
+bool use_pair(int64_t slots, int64_t groups) { return slots / (groups < slots ? groups : slots) >= 128; }
+
 // Tile rows per band: 8 row tiles of a group share each column tile's weights
 // while those are in L2.
 constexpr int kGroupRaster = 8;
 
 int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
                 int64_t a_rows, int64_t lda, const int32_t* rows, const void* W, int64_t ldw, int64_t stride_w, void* C,
-                int64_t ldc, int layout, const gemm_grouped_epilogue_t* epi, void* stream) {
+                int64_t ldc, int layout, const gemm_grouped_epilogue_t* epi, void* workspace, int64_t workspace_bytes,
+                void* stream) {
   const int es = kind == KIND_E4M3 ? 1 : 2;
   if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
       N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
@@ -77,7 +125,10 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   }
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
   const void* bias = epi != nullptr ? epi->bias : nullptr;
+  if (rows == nullptr || K == 0) workspace = nullptr;
+  if (workspace != nullptr && workspace_bytes < slots * permuted_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
+      misaligned(workspace, 128) ||
       (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
     return GEMM_ERR_MISALIGNED;
   if (K > 0 && (!tma_rows(A, lda, es) || !tma_rows(W, ldw, es) || (groups > 1 && (stride_w * es) % 16 != 0)))
@@ -85,6 +136,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   // the value half of row-major weights is a TMA box of its own
   if (K > 0 && gated && layout == GEMM_B_ROW_MAJOR && (out_cols * es) % 16 != 0) return GEMM_ERR_MISALIGNED;
   const Range rc = range_of(C, slots, out_cols, ldc, 2);
+  if (workspace != nullptr && meet(rc, range_of(workspace, 1, workspace_bytes, 0, 1))) return GEMM_ERR_INVALID_VALUE;
   if (K > 0 && (meet(rc, range_of(A, a_rows, K, lda, es)) ||
                 meet(rc, range_of(W, w_rows, w_cols, ldw, es, groups, groups > 1 ? stride_w : 0))))
     return GEMM_ERR_INVALID_VALUE;
@@ -93,7 +145,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   int st = begin_call(&ctx);
   if (st != GEMM_OK) return st;
   if (!on_device(C, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
-      (bias != nullptr && !on_device(bias, ctx.dev)) || (K > 0 && (!on_device(A, ctx.dev) || !on_device(W, ctx.dev))))
+      (bias != nullptr && !on_device(bias, ctx.dev)) || (workspace != nullptr && !on_device(workspace, ctx.dev)) || (K > 0 && (!on_device(A, ctx.dev) || !on_device(W, ctx.dev))))
     return GEMM_ERR_NOT_DEVICE_MEMORY;
   if (epi != nullptr && ((epi->row_scale != nullptr && !on_device(epi->row_scale, ctx.dev)) ||
                          (epi->col_scale != nullptr && !on_device(epi->col_scale, ctx.dev))))
@@ -126,10 +178,8 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   L.gated = gated;
   L.dev = ctx.dev;
   L.stream = static_cast<cudaStream_t>(stream);
-  // The host knows the slots and the groups, not the group sizes. A pair's 256-row tiles pay once an average
-  // group fills most of one.
   const int64_t active = groups < slots ? groups : slots;
-  L.pair = slots / active >= 128;
+  L.pair = use_pair(slots, groups);
   const int out_bn = (L.pair ? kGroupPairN : kGroupSingleN) / (gated ? 2 : 1);
   p.g.tiles_n = int((out_cols + out_bn - 1) / out_bn);
   const int64_t tiles = (slots / (L.pair ? 256 : 128) + active + 1) * p.g.tiles_n;  // at most
@@ -139,7 +189,19 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   const CUtensorMapDataType dt = map_type(kind);
   const uint32_t bk = 128 / es;
   if (K > 0) {
-    if (!encode_map_2d(&L.tmAg, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)) return GEMM_ERR_DRIVER;
+    p.gather_a = rows != nullptr;
+    if (rows != nullptr && workspace != nullptr) {
+      st = permute_rows(ctx, A, a_rows, lda, rows, offsets, groups, slots, K, es, workspace, L.stream);
+      if (st != GEMM_OK) return st;
+      A = workspace;
+      lda = permuted_pitch(K, es) / es;
+      p.gather_a = 0;
+    }
+    const bool mapped =
+        p.gather_a ? encode_map_2d(&L.tmAg, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)
+                   : encode_map_3d(&L.tmA, dt, A, K, slots, lda * es, 1, 0, bk, L.pair ? 128 : 32,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!mapped) return GEMM_ERR_DRIVER;
     const uint64_t mat = groups > 1 ? uint64_t(stride_w) * es : 0;
     bool ok;
     if (layout == GEMM_B_K_MAJOR) {
@@ -166,7 +228,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
 
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
               int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
-              int64_t stride_dw, int layout, void* stream) {
+              int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream) {
   if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
       N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
     return GEMM_ERR_INVALID_VALUE;
@@ -181,7 +243,10 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
                     lddc > kLdLimit || (rows == nullptr && a_rows < slots)))
     return GEMM_ERR_INVALID_VALUE;
   if (((out_rows + 255) / 256) * ((out_cols + 255) / 256) > kIntLimit / groups) return GEMM_ERR_INVALID_VALUE;
-  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2)) return GEMM_ERR_MISALIGNED;
+  if (rows == nullptr || slots == 0) workspace = nullptr;
+  if (workspace != nullptr && workspace_bytes < slots * permuted_pitch(K, 2)) return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2) || misaligned(workspace, 128))
+    return GEMM_ERR_MISALIGNED;
   if (slots > 0 && (!tma_rows(A, lda, 2) || !tma_rows(dC, lddc, 2))) return GEMM_ERR_MISALIGNED;
   const Range rw = range_of(dW, out_rows, out_cols, lddw, 2, groups, groups > 1 ? stride_dw : 0);
   if (slots > 0 && (meet(rw, range_of(A, a_rows, K, lda, 2)) || meet(rw, range_of(dC, slots, N, lddc, 2))))
@@ -191,6 +256,7 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   int st = begin_call(&ctx);
   if (st != GEMM_OK) return st;
   if (!on_device(dW, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
+      (workspace != nullptr && !on_device(workspace, ctx.dev)) ||
       (slots > 0 && (!on_device(A, ctx.dev) || !on_device(dC, ctx.dev))))
     return GEMM_ERR_NOT_DEVICE_MEMORY;
   GroupLaunch L;
@@ -213,12 +279,21 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   p.g.raster = kGroupRaster;
   p.g.tiles_m = int((out_rows + 255) / 256);
   p.g.tiles_n = int((out_cols + 255) / 256);
-  // rows of A are gathered when the caller gives their numbers; dC is read by slot
-  p.gather_p = !km && rows != nullptr;
-  p.gather_q = km && rows != nullptr;
   L.pair = true;
   L.dev = ctx.dev;
   L.stream = static_cast<cudaStream_t>(stream);
+  // rows of A that the caller names are put in slot order first (gathered by TMA without a workspace); dC is read by slot
+  bool gather = rows != nullptr;
+  if (gather && slots > 0 && workspace != nullptr) {
+    st = permute_rows(ctx, A, a_rows, lda, rows, offsets, groups, slots, K, 2, workspace, L.stream);
+    if (st != GEMM_OK) return st;
+    A = workspace;
+    lda = permuted_pitch(K, 2) / 2;
+    a_rows = slots;
+    gather = false;
+  }
+  p.gather_p = !km && gather;
+  p.gather_q = km && gather;
   const int64_t tiles = int64_t(groups) * p.g.tiles_m * p.g.tiles_n;
   const int64_t units = ctx.sm_count / 2;
   L.grid = int(2 * (tiles < units ? tiles : units));
@@ -246,42 +321,53 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
 
 extern "C" {
 
+int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K) {
+  if (groups < 1 || slots <= 0 || K <= 0 || !dgt::use_pair(slots, groups)) return 0;
+  return slots * dgt::permuted_pitch(K, type == GEMM_TYPE_E4M3 ? 1 : 2);
+}
+
+int64_t gemm_grouped_wgrad_workspace(int64_t slots, int64_t K) {
+  return slots <= 0 || K <= 0 ? 0 : slots * dgt::permuted_pitch(K, 2);
+}
+
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
                      int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                     void* stream) {
+                     void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream);
 }
 
 int gemm_bf16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                       int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                      void* stream) {
+                      void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream);
 }
 
 int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint8_t* A,
                       int64_t a_rows, int64_t lda, const int32_t* rows, const uint8_t* W, int64_t ldw,
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                      void* stream) {
+                      void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_E4M3, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream);
 }
 
 int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                            int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC, int64_t lddc,
-                           uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream) {
+                           uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
   return dgt::run_wgrad(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
-                        stride_dw, layout, stream);
+                        stride_dw, layout, workspace, workspace_bytes, stream);
 }
 
 int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K,
                             const uint16_t* A, int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC,
-                            int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream) {
+                            int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
   return dgt::run_wgrad(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
-                        stride_dw, layout, stream);
+                        stride_dw, layout, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -13,11 +13,14 @@
 //     row-tile counts into shared memory once (one thread per few groups) and
 //     finds a work item's group by binary search, so the host never reads the
 //     group sizes and empty groups cost nothing but their table entry.
-//   * Rows are gathered by TMA (tile::gather4: four rows of 128 bytes an
-//     instruction, all 32 lanes of the producer warp issue one each), so the
-//     permuted copy of A (slots x K, written and read again) never exists, and a
-//     group's last tile fetches only the rows it has. A row past the group's
-//     end repeats the group's last row; its results are not stored.
+//   * Rows in slot order come by TMA boxes. Rows that the caller names are
+//     gathered by TMA (tile::gather4: four rows of 128 bytes an instruction,
+//     each lane of the producer warp issues one) where a group has few: an
+//     instruction costs about 75 cycles, so 128 rows of a slab take 2400, four
+//     times the MMA's 512, but a handful hides behind the weights' stream. For
+//     large groups the host first permutes the rows into the stream's scratch
+//     (one bandwidth-bound pass) and they are rows in slot order again. A group's
+//     last tile fetches only the rows it has.
 //   * The gradient contracts over a ragged number of rows. A group's last slab
 //     of 64 rows may run into the next group's rows; its loads complete on a
 //     barrier of their own, a sixth warp clears the rows past the end in shared
@@ -75,10 +78,11 @@ struct GroupParams {
   int a_rows;
   const float* row_scale;
   const float* col_scale;
+  int gather_a;  // product: rows of A by gather (else boxes by slot)
   int plain;     // the epilogue is the identity
   int out_cols;  // columns of C (or of dW)
   int out_rows;  // gradient: rows of dW
-  int gather_p, gather_q;  // gradient: the operand whose rows are gathered (else it is read by slot)
+  int gather_p, gather_q;  // gradient: the operand whose rows are gathered by TMA (else boxes by slot)
 };
 
 template <int KIND, int OPS, int BN_, bool PAIR, bool GATED>
@@ -113,6 +117,7 @@ struct GroupCfg {
   static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
   static constexpr int NUM_BARS = 4 * STAGES + 5;
   static constexpr int THREADS = WGRAD ? 224 : 192;
+  static constexpr int A_BOX_ROWS = PAIR ? 128 : 32;  // rows of A per box: one CTA's tile may hold few
   static_assert(BN % 64 == 0 && BN >= 64 && BN <= 256, "tile width");
   static_assert(B_KMAJOR || ES == 2, "8-bit operands are read K-major");
   static_assert(B_KMAJOR || BNH % BOXN == 0, "MN-major B comes in whole boxes");
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(224, 1)
     tail_slot[1] = 0;
     fence_mbar_init();
     if (!WGRAD && p.g.num_kb > 0) {
-      tma_prefetch_desc(&tmAg);
+      tma_prefetch_desc(p.gather_a ? &tmAg : &tmA);
       tma_prefetch_desc(&tmB);
     }
   }
@@ -399,10 +404,13 @@ __global__ void __launch_bounds__(224, 1)
           if (t.kbs == 0) continue;
           const int first = t.m0 + int(half) * Cf::BM;
           const int left = t.end - first;
-          quads = (min(max(left, 0), Cf::BM) + 3) >> 2;
-          tx = quads * 512 + Cf::B_BYTES;
-          if (PAIR && leader) tx += ((min(max(left - Cf::BM, 0), Cf::BM) + 3) >> 2) * 512 + Cf::B_BYTES;
-          if (lane < quads) {
+          // pieces of A this CTA loads: quads of gathered rows, or boxes
+          const int rows_per = p.gather_a ? 4 : Cf::A_BOX_ROWS;
+          auto pieces = [&](int rows) { return (min(max(rows, 0), Cf::BM) + rows_per - 1) / rows_per; };
+          quads = pieces(left);
+          tx = quads * rows_per * 128 + Cf::B_BYTES;
+          if (PAIR && leader) tx += pieces(left - Cf::BM) * rows_per * 128 + Cf::B_BYTES;
+          if (p.gather_a && lane < quads) {
             const int s = first + 4 * lane;
             r0 = gathered_row(p, s, t.end);
             r1 = gathered_row(p, s + 1, t.end);
@@ -452,10 +460,19 @@ __global__ void __launch_bounds__(224, 1)
             }
             __syncwarp();
             if (lane < quads) {
-              if constexpr (PAIR)
-                tma_gather4_pair(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
-              else
-                tma_gather4(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
+              const int x = kb * Cf::BK;
+              if (p.gather_a) {
+                if constexpr (PAIR)
+                  tma_gather4_pair(a_dst + lane * 512, &tmAg, fb, x, r0, r1, r2, r3);
+                else
+                  tma_gather4(a_dst + lane * 512, &tmAg, fb, x, r0, r1, r2, r3);
+              } else {
+                const int row = t.m0 + int(half) * Cf::BM + lane * Cf::A_BOX_ROWS;
+                if constexpr (PAIR)
+                  tma_load_3d_pair(a_dst + lane * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row, 0);
+                else
+                  tma_load_3d(a_dst + lane * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row, 0);
+              }
             }
           } else {
             const int s0 = t.begin + kb * Cf::BK;

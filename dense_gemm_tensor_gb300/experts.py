@@ -27,14 +27,15 @@ GEMM_ACT_SILU_GATED = 4
 # Every symbol the C header declares.
 EXPORTS = ("gemm_rmsnorm", "gemm_rmsnorm_backward", "gemm_rmsnorm_backward_workspace", "gemm_route",
            "gemm_route_workspace", "gemm_route_backward", "gemm_f16_grouped", "gemm_bf16_grouped",
-           "gemm_e4m3_grouped", "gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad", "gemm_combine",
-           "gemm_combine_backward")
+           "gemm_e4m3_grouped", "gemm_grouped_workspace", "gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad",
+           "gemm_grouped_wgrad_workspace", "gemm_combine", "gemm_combine_backward")
 
 ACTIVATIONS = {**gemm.ACTIVATIONS, "silu_gated": GEMM_ACT_SILU_GATED}
 SCORES = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
 
 _TYPE = {torch.float16: GEMM_TYPE_F16, torch.bfloat16: GEMM_TYPE_BF16, torch.float32: GEMM_TYPE_F32}
 _E4M3 = torch.float8_e4m3fn
+_GROUPED_TYPE = {torch.float16: GEMM_TYPE_F16, torch.bfloat16: GEMM_TYPE_BF16, _E4M3: GEMM_TYPE_E4M3}
 _GROUPED = {torch.float16: "gemm_f16_grouped", torch.bfloat16: "gemm_bf16_grouped", _E4M3: "gemm_e4m3_grouped"}
 
 
@@ -89,13 +90,14 @@ def _load():
         "gemm_combine_backward": [i, i64, i64, i, vp, i64, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp],
     }
     for name in _GROUPED.values():
-        sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64, i, epi, vp]
+        sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64, i, epi, vp, i64, vp]
     for name in ("gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad"):
-        sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, i, vp]
+        sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, i, vp, i64, vp]
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i
-    for name, args in (("gemm_rmsnorm_backward_workspace", [i64, i64]), ("gemm_route_workspace", [i64, i, i])):
+    for name, args in (("gemm_rmsnorm_backward_workspace", [i64, i64]), ("gemm_route_workspace", [i64, i, i]),
+                       ("gemm_grouped_workspace", [i, i, i64, i64]), ("gemm_grouped_wgrad_workspace", [i64, i64])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i64
     _lib = lib
@@ -338,22 +340,23 @@ def expert_matmul(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows:
     slots = A.shape[0] if rows is None else rows.numel()
     r = _vector(rows, "rows", torch.int32, slots) if rows is not None else None
     cols = N // 2 if act == GEMM_ACT_SILU_GATED else N
+    lib = _load()
+    need = lib.gemm_grouped_workspace(_GROUPED_TYPE[A.dtype], experts, slots, K) if rows is not None else 0
     s = gemm._raw_stream(stream, A.device.index)
-    if out is None:
-        with _on(stream):
+    ldc = _matrix(out, "out", out_dt, (slots, cols)) if out is not None else cols
+    with _on(stream):
+        if out is None:
             out = torch.empty((slots, cols), dtype=out_dt, device=A.device)
-        ldc = cols
-    else:
-        ldc = _matrix(out, "out", out_dt, (slots, cols))
+        ws = torch.empty((need,), dtype=torch.uint8, device=A.device) if need else None
     epi = None
     if act or alpha != 1.0 or a_scale is not None or w_scale is not None or bias is not None:
         epi = GroupedEpilogue(
             alpha, _vector(a_scale, "a_scale", torch.float32, A.shape[0]) if a_scale is not None else None,
             _vector(w_scale, "w_scale", torch.float32, experts * N) if w_scale is not None else None,
             _vector(bias, "bias", out_dt, experts * N) if bias is not None else None, act)
-    _check(getattr(_load(), name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r,
-                                  W.data_ptr() or None, ldw, stride_w, out.data_ptr() or None, ldc, layout, epi, s),
-           name)
+    _check(getattr(lib, name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r, W.data_ptr() or None,
+                              ldw, stride_w, out.data_ptr() or None, ldc, layout, epi, ws.data_ptr() if need else None,
+                              need, s), name)
     return out
 
 
@@ -375,16 +378,20 @@ def expert_weight_grad(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor,
     off = _vector(offsets, "offsets", torch.int32, experts + 1)
     r = _vector(rows, "rows", torch.int32, slots) if rows is not None else None
     shape = (experts, N, K) if layout == GEMM_B_K_MAJOR else (experts, K, N)
-    s = gemm._raw_stream(stream, A.device.index)
-    if out is None:
-        with _on(stream):
-            out = torch.empty(shape, dtype=A.dtype, device=A.device)
-    elif out.dtype != A.dtype or tuple(out.shape) != shape:
+    if out is not None and (out.dtype != A.dtype or tuple(out.shape) != shape):
         raise ValueError(f"out must be {shape[0]} x {shape[1]} x {shape[2]} of A's dtype")
+    lib = _load()
+    need = lib.gemm_grouped_wgrad_workspace(slots, K) if rows is not None else 0
+    s = gemm._raw_stream(stream, A.device.index)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=A.dtype, device=A.device)
+        ws = torch.empty((need,), dtype=torch.uint8, device=A.device) if need else None
     ldw, stride_w = _stack(out, "out")
     name = "gemm_f16_grouped_wgrad" if A.dtype == torch.float16 else "gemm_bf16_grouped_wgrad"
-    _check(getattr(_load(), name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r,
-                                  dC.data_ptr() or None, lddc, out.data_ptr() or None, ldw, stride_w, layout, s), name)
+    _check(getattr(lib, name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r,
+                              dC.data_ptr() or None, lddc, out.data_ptr() or None, ldw, stride_w, layout,
+                              ws.data_ptr() if need else None, need, s), name)
     return out
 
 

@@ -167,21 +167,28 @@ typedef struct gemm_grouped_epilogue {
  * layout flag the same call is the gradient of A: dA = dC . W_e^T, one row a
  * slot. epilogue NULL: C = A . W. 1 <= groups <= 1024; slots, N, K < 2^31;
  * K = 0 gives the epilogue of 0. Rows and bases of A and W and the matrix
- * stride must be 16-byte multiples (GEMM_ERR_MISALIGNED otherwise); C may
- * have any alignment that keeps its elements aligned.
+ * stride must be 16-byte multiples (GEMM_ERR_MISALIGNED otherwise), and with
+ * row-major W GEMM_ACT_SILU_GATED's second half must start on one; C may have
+ * any alignment that keeps its elements aligned.
+ *
+ * workspace, used with `rows` only: gemm_grouped_workspace bytes, 128-byte
+ * aligned, into which the rows are put in slot order first; NULL: they are
+ * gathered on the way to shared memory (the same results; slower where groups
+ * have many rows, which is where the size call asks for a workspace).
  */
+int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K);
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
                      int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                     void* stream);
+                     void* workspace, int64_t workspace_bytes, void* stream);
 int gemm_bf16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                       int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                      void* stream);
+                      void* workspace, int64_t workspace_bytes, void* stream);
 int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint8_t* A,
                       int64_t a_rows, int64_t lda, const int32_t* rows, const uint8_t* W, int64_t ldw,
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
-                      void* stream);
+                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Gradient of the grouped product's weights:
@@ -190,14 +197,18 @@ int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t
  * in fp32, rounded once to the operands' type; a group without slots gets
  * zeros. dC: slots x N. A, rows and dC as above (16-byte rows and bases); dW
  * may have any alignment that keeps its elements aligned, stride_dw at least
- * one matrix's extent.
+ * one matrix's extent. workspace: as above, of gemm_grouped_wgrad_workspace
+ * bytes.
  */
+int64_t gemm_grouped_wgrad_workspace(int64_t slots, int64_t K);
 int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                            int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC, int64_t lddc,
-                           uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream);
+                           uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
+                           int64_t workspace_bytes, void* stream);
 int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K,
                             const uint16_t* A, int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC,
-                            int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* stream);
+                            int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
+                            int64_t workspace_bytes, void* stream);
 
 /*
  * Weighted sum over a token's slots:

@@ -34,6 +34,10 @@ def test_workspace_sizes(lib):
     assert lib.gemm_route_workspace(128, 64, 8) == 0          # one block does it all
     assert lib.gemm_route_workspace(129, 64, 8) == 5 * 64 * 4  # five blocks of 32 tokens
     assert lib.gemm_route_workspace(1 << 20, 64, 8) == 152 * 64 * 4
+    assert lib.gemm_grouped_workspace(1, 4, 511, 64) == 0          # few rows a group: gathered on the way
+    assert lib.gemm_grouped_workspace(1, 4, 512, 65) == 512 * 256  # rows of 130 bytes, 128-byte pitch
+    assert lib.gemm_grouped_workspace(3, 4, 512, 65) == 512 * 128
+    assert lib.gemm_grouped_wgrad_workspace(3, 64) == 3 * 128 and lib.gemm_grouped_wgrad_workspace(0, 64) == 0
     assert lib.gemm_rmsnorm_backward_workspace(0, 64) == 0
     assert lib.gemm_rmsnorm_backward_workspace(3, 64) == 3 * 64 * 4
     assert lib.gemm_rmsnorm_backward_workspace(10 ** 6, 64) == 304 * 64 * 4
@@ -111,9 +115,10 @@ def test_route_backward_arguments(lib, kw, code):
 
 
 def _grouped(lib, name="gemm_bf16_grouped", groups=2, off=P, slots=4, N=8, K=8, A=2 * P, a_rows=4, lda=8, rows=None,
-             W=3 * P, ldw=8, sw=64, C=4 * P, ldc=8, layout=1, act=0, row_scale=None, col_scale=None, bias=None):
+             W=3 * P, ldw=8, sw=64, C=4 * P, ldc=8, layout=1, act=0, row_scale=None, col_scale=None, bias=None, ws=None, bytes=0):
     epi = experts.GroupedEpilogue(1.0, row_scale, col_scale, bias, act)
-    return getattr(lib, name)(groups, off, slots, N, K, A, a_rows, lda, rows, W, ldw, sw, C, ldc, layout, epi, None)
+    return getattr(lib, name)(groups, off, slots, N, K, A, a_rows, lda, rows, W, ldw, sw, C, ldc, layout, epi, ws, bytes,
+                              None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -128,6 +133,8 @@ def _grouped(lib, name="gemm_bf16_grouped", groups=2, off=P, slots=4, N=8, K=8, 
     (dict(bias=P + 1), MISALIGNED), (dict(row_scale=P + 2), MISALIGNED), (dict(col_scale=P + 2), MISALIGNED),
     (dict(act=4, N=24, ldw=24, sw=192, ldc=12, layout=0), MISALIGNED),  # the value half starts off a 16-byte boundary
     (dict(name="gemm_e4m3_grouped", lda=8), MISALIGNED),
+    (dict(rows=5 * P, ws=6 * P, bytes=4 * 128 - 1), INVALID), (dict(rows=5 * P, ws=4 * P, bytes=4 * 128), INVALID),
+    (dict(rows=5 * P, ws=6 * P + 16, bytes=4 * 128), MISALIGNED),
     (dict(slots=0, A=None, C=None), gemm.GEMM_OK), (dict(N=0), gemm.GEMM_OK),
 ])
 def test_grouped_arguments(lib, kw, code):
@@ -139,10 +146,11 @@ def test_grouped_arguments(lib, kw, code):
     (dict(dC=None), INVALID), (dict(dW=None), INVALID), (dict(a_rows=3), INVALID), (dict(lddc=0), INVALID),
     (dict(lddw=7), INVALID), (dict(sdw=56), INVALID), (dict(dW=2 * P), INVALID), (dict(lda=12), MISALIGNED),
     (dict(dC=3 * P + 8), MISALIGNED), (dict(dW=4 * P + 1), MISALIGNED), (dict(N=0), gemm.GEMM_OK),
+    (dict(rows=5 * P, ws=6 * P, bytes=4 * 128 - 1), INVALID),
 ])
 def test_weight_grad_arguments(lib, kw, code):
     a = dict(groups=2, off=P, slots=4, N=8, K=8, A=2 * P, a_rows=4, lda=8, rows=None, dC=3 * P, lddc=8, dW=4 * P,
-             lddw=8, sdw=64, layout=1) | kw
+             lddw=8, sdw=64, layout=1, ws=None, bytes=0) | kw
     assert lib.gemm_bf16_grouped_wgrad(*a.values(), None) == code
 
 
