@@ -399,18 +399,18 @@ __global__ void __launch_bounds__(224, 1)
       for (int w = unit; ok && w < work; w += nunits) {
         const GroupTile t = group_tile<Cf>(p, cum, w);
         int r0 = 0, r1 = 0, r2 = 0, r3 = 0;  // product: this lane's four rows of A
-        int quads = 0, tx = 0;
+        int pieces = 0, tx = 0;
         if constexpr (!WGRAD) {
           if (t.kbs == 0) continue;
           const int first = t.m0 + int(half) * Cf::BM;
           const int left = t.end - first;
           // pieces of A this CTA loads: quads of gathered rows, or boxes
           const int rows_per = p.gather_a ? 4 : Cf::A_BOX_ROWS;
-          auto pieces = [&](int rows) { return (min(max(rows, 0), Cf::BM) + rows_per - 1) / rows_per; };
-          quads = pieces(left);
-          tx = quads * rows_per * 128 + Cf::B_BYTES;
-          if (PAIR && leader) tx += pieces(left - Cf::BM) * rows_per * 128 + Cf::B_BYTES;
-          if (p.gather_a && lane < quads) {
+          auto count = [&](int rows) { return (min(max(rows, 0), Cf::BM) + rows_per - 1) / rows_per; };
+          pieces = count(left);
+          tx = pieces * rows_per * 128 + Cf::B_BYTES;
+          if (PAIR && leader) tx += count(left - Cf::BM) * rows_per * 128 + Cf::B_BYTES;
+          if (p.gather_a && lane < pieces) {
             const int s = first + 4 * lane;
             r0 = gathered_row(p, s, t.end);
             r1 = gathered_row(p, s + 1, t.end);
@@ -428,9 +428,21 @@ __global__ void __launch_bounds__(224, 1)
           const uint32_t b_dst = sB + s * Cf::B_BYTES;
           uint32_t fb = lead_full0 + 8 * s;
           if constexpr (!WGRAD) {
+            // (operands of the elected lane's loads are the same in every lane: the issue path wants them so)
+            const int row0 = t.m0 + int(half) * Cf::BM;
             if (elect_one()) {
               if (leader) mbar_arrive_expect_tx(full0 + 8 * s, tx);
               const int x = kb * Cf::BK;
+              if (!p.gather_a) {
+#pragma unroll
+                for (int j = 0; j < Cf::BM / Cf::A_BOX_ROWS; ++j)
+                  if (j < pieces) {
+                    if constexpr (PAIR)
+                      tma_load_3d_pair(a_dst + j * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row0 + j * Cf::A_BOX_ROWS, 0);
+                    else
+                      tma_load_3d(a_dst + j * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row0 + j * Cf::A_BOX_ROWS, 0);
+                  }
+              }
               if constexpr (Cf::B_KMAJOR) {
                 if constexpr (PAIR) {
                   const int n0 = GATED ? int(half) * (p.g.N / 2) + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH;
@@ -459,20 +471,11 @@ __global__ void __launch_bounds__(224, 1)
               }
             }
             __syncwarp();
-            if (lane < quads) {
-              const int x = kb * Cf::BK;
-              if (p.gather_a) {
-                if constexpr (PAIR)
-                  tma_gather4_pair(a_dst + lane * 512, &tmAg, fb, x, r0, r1, r2, r3);
-                else
-                  tma_gather4(a_dst + lane * 512, &tmAg, fb, x, r0, r1, r2, r3);
-              } else {
-                const int row = t.m0 + int(half) * Cf::BM + lane * Cf::A_BOX_ROWS;
-                if constexpr (PAIR)
-                  tma_load_3d_pair(a_dst + lane * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row, 0);
-                else
-                  tma_load_3d(a_dst + lane * Cf::A_BOX_ROWS * 128, &tmA, fb, x, row, 0);
-              }
+            if (p.gather_a && lane < pieces) {
+              if constexpr (PAIR)
+                tma_gather4_pair(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
+              else
+                tma_gather4(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
             }
           } else {
             const int s0 = t.begin + kb * Cf::BK;
@@ -485,49 +488,54 @@ __global__ void __launch_bounds__(224, 1)
               return min(max((cols - x0 + Cf::BOXN - 1) / Cf::BOXN, 0), most);
             };
             const int np = boxes_in(p0, p.out_rows, PB), nq = boxes_in(q0, p.out_cols, QB);
-            if (tail) {
-              // both operands of this CTA complete on its own barrier; the leader's
-              // full barrier has nothing to count
-              fb = tailf0 + 8 * s;
-              if (elect_one()) {
+            // A ragged slab: both operands of this CTA complete on its own barrier, and
+            // the leader's full barrier has nothing to count.
+            if (tail) fb = tailf0 + 8 * s;
+            const int peer = PAIR ? boxes_in(p0 + Cf::BM, p.out_rows, PB) + boxes_in(q0 + Cf::BNH, p.out_cols, QB) : 0;
+            if (elect_one()) {
+              if (tail) {
                 mbar_arrive_expect_tx(fb, (np + nq) * Cf::BOX_BYTES);
                 if (leader) mbar_arrive(full0 + 8 * s);
+              } else if (leader) {
+                mbar_arrive_expect_tx(full0 + 8 * s, (np + nq + peer) * Cf::BOX_BYTES);
               }
-              ++tails;
-            } else if (leader && elect_one()) {
-              const int peer = PAIR ? boxes_in(p0 + Cf::BM, p.out_rows, PB) + boxes_in(q0 + Cf::BNH, p.out_cols, QB) : 0;
-              mbar_arrive_expect_tx(full0 + 8 * s, (np + nq + peer) * Cf::BOX_BYTES);
+              if (PAIR && !tail) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j)
+                  if (!p.gather_p && j < np)
+                    tma_load_3d_pair(a_dst + j * Cf::BOX_BYTES, &tmA, fb, p0 + j * Cf::BOXN, s0, 0);
+#pragma unroll
+                for (int j = 0; j < QB; ++j)
+                  if (!p.gather_q && j < nq)
+                    tma_load_3d_pair(b_dst + j * Cf::BOX_BYTES, &tmB, fb, q0 + j * Cf::BOXN, s0, 0);
+              } else {
+#pragma unroll
+                for (int j = 0; j < PB; ++j)
+                  if (!p.gather_p && j < np) tma_load_3d(a_dst + j * Cf::BOX_BYTES, &tmA, fb, p0 + j * Cf::BOXN, s0, 0);
+#pragma unroll
+                for (int j = 0; j < QB; ++j)
+                  if (!p.gather_q && j < nq) tma_load_3d(b_dst + j * Cf::BOX_BYTES, &tmB, fb, q0 + j * Cf::BOXN, s0, 0);
+              }
             }
+            tails += tail ? 1 : 0;
             __syncwarp();
-            const int quad = lane & 15;
             if (p.gather_p || p.gather_q) {
+              // 16 quads of slots x the operand's boxes
+              const int quad = lane & 15;
               r0 = gathered_row(p, s0 + 4 * quad, t.end);
               r1 = gathered_row(p, s0 + 4 * quad + 1, t.end);
               r2 = gathered_row(p, s0 + 4 * quad + 2, t.end);
               r3 = gathered_row(p, s0 + 4 * quad + 3, t.end);
-            }
-            auto load = [&](uint32_t dst, const CUtensorMap& boxes, const CUtensorMap& gather, bool gathered, int x0,
-                            int nbox) {
-              if (gathered) {
-                for (int j = lane >> 4; j < nbox; j += 2) {
-                  const uint32_t d = dst + j * Cf::BOX_BYTES + quad * 512;
-                  if (PAIR && !tail)
-                    tma_gather4_pair(d, &gather, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
-                  else
-                    tma_gather4(d, &gather, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
-                }
-              } else if (elect_one()) {
-                for (int j = 0; j < nbox; ++j) {
-                  if (PAIR && !tail)
-                    tma_load_3d_pair(dst + j * Cf::BOX_BYTES, &boxes, fb, x0 + j * Cf::BOXN, s0, 0);
-                  else
-                    tma_load_3d(dst + j * Cf::BOX_BYTES, &boxes, fb, x0 + j * Cf::BOXN, s0, 0);
-                }
+              const uint32_t dst = (p.gather_p ? a_dst : b_dst) + quad * 512;
+              const CUtensorMap* map = p.gather_p ? &tmAg : &tmBg;
+              const int x0 = p.gather_p ? p0 : q0;
+              for (int j = lane >> 4; j < (p.gather_p ? np : nq); j += 2) {
+                if (PAIR && !tail)
+                  tma_gather4_pair(dst + j * Cf::BOX_BYTES, map, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
+                else
+                  tma_gather4(dst + j * Cf::BOX_BYTES, map, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
               }
-              __syncwarp();
-            };
-            load(a_dst, tmA, tmAg, p.gather_p != 0, p0, np);
-            load(b_dst, tmB, tmBg, p.gather_q != 0, q0, nq);
+            }
           }
           __syncwarp();
         }
