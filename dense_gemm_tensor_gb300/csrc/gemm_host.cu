@@ -341,16 +341,17 @@ struct TinyCache {
 
 // 3-D tiled tensor map: x innermost (contiguous), y rows `row_bytes` apart, z
 // matrices of a batch `mat_bytes` apart (depth 1 for one product, whose z is
-// always 0). Boxes are box_inner x box_outer x 1. Encoded maps are cached per
+// always 0). Boxes are box_inner x box_outer x box_depth. Encoded maps are cached per
 // thread (a map is a pure function of these arguments).
 bool encode_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                uint64_t row_bytes, uint64_t depth, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  thread_local TinyCache<9, CUtensorMap, 16> cache;
+               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, uint32_t box_depth = 1) {
+  thread_local TinyCache<10, CUtensorMap, 16> cache;
   if (depth == 1) mat_bytes = row_bytes * outer;  // never stepped; a stride that spans the matrix
   if (mat_bytes == 0 || mat_bytes % 16 != 0 || mat_bytes >= (uint64_t(1) << 40)) return false;
-  const uint64_t key[9] = {uint64_t(dt), uint64_t(reinterpret_cast<uintptr_t>(base)), inner, outer, row_bytes,
-                           depth, mat_bytes, (uint64_t(box_inner) << 32) | box_outer, uint64_t(swizzle)};
+  const uint64_t key[10] = {uint64_t(dt), uint64_t(reinterpret_cast<uintptr_t>(base)), inner, outer, row_bytes,
+                            depth, mat_bytes, (uint64_t(box_inner) << 32) | box_outer, uint64_t(swizzle),
+                            uint64_t(box_depth)};
   if (const CUtensorMap* hit = cache.find(key)) {
     *m = *hit;
     return true;
@@ -359,7 +360,7 @@ bool encode_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_
   if (!fn) return false;
   cuuint64_t dims[3] = {inner, outer, depth};
   cuuint64_t strides[2] = {row_bytes, mat_bytes};
-  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t box[3] = {box_inner, box_outer, box_depth};
   cuuint32_t estr[3] = {1, 1, 1};
   if (fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -1109,8 +1110,8 @@ bool on_device(const void* ptr, int dev) { return is_device_memory(ptr, dev); }
 
 bool encode_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint64_t depth, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_outer,
-                   CUtensorMapSwizzle swizzle) {
-  return encode_3d(m, dt, base, inner, outer, row_bytes, depth, mat_bytes, box_inner, box_outer, swizzle);
+                   CUtensorMapSwizzle swizzle, uint32_t box_depth) {
+  return encode_3d(m, dt, base, inner, outer, row_bytes, depth, mat_bytes, box_inner, box_outer, swizzle, box_depth);
 }
 
 bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,

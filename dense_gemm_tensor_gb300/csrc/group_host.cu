@@ -48,46 +48,84 @@ void fill_common(const CallContext& ctx, GroupParams& p) {
   p.g.wait_limit_ns = ctx.wait_limit_ns;
 }
 
-// dst[s] = src[row(s)] for the slots in use: the rows of a gathered operand in
-// slot order, 16 bytes a lane (rows start on 16-byte boundaries; the last piece
-// of a row may run into its padding, which the pitch of dst holds). A warp takes
-// a row; bound by memory: one read of the rows (repeats of a token hit L2) and one
-// write, 134 MB of 4096 BF16 columns x 16384 slots in about 30 us.
-__global__ void __launch_bounds__(256) permute_rows_kernel(const uint8_t* src, long long ld, int a_rows,
-                                                           const int* rows, const int* offsets, int groups, int slots,
-                                                           uint8_t* dst, long long dst_ld, long long row_bytes) {
+// Copies of rows into the workspace ahead of a grouped kernel, a warp a row,
+// 16 bytes a lane (rows start on 16-byte boundaries; bytes of the destination's
+// pitch past the row are zero):
+//   * `order`: the gathered operand's rows in slot order, order[s] = a[row(s)]
+//   * `slab_a`, `slab_c` (the weights' gradient): the last slab of 64 slots of
+//     every group whose count is not a multiple of 64, zeros past its end
+// Bound by memory: one read of the rows (repeats of a token hit L2) and one
+// write; 16384 slots of 4096 BF16 columns (134 MB written) take about 45 us.
+struct StageRows {
+  const uint8_t* a;
+  const uint8_t* c;
+  const int* rows;
+  const int* offsets;
+  uint8_t* order;
+  uint8_t* slab_a;
+  uint8_t* slab_c;
+  long long ld_a, ld_c, pitch_a, pitch_c, bytes_a, bytes_c;
+  int a_rows, groups, slots;
+};
+
+constexpr int kSlab = 64;
+
+__device__ __forceinline__ void stage_row(const uint8_t* from, long long bytes, uint8_t* to, long long pitch,
+                                          int lane) {
+  const int pieces = static_cast<int>(pitch / 16);
+  const int whole = from != nullptr ? static_cast<int>(bytes / 16) : 0;
+  int c = lane;
+  for (; c + 96 < whole; c += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (c + 32 * i) * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (c + 32 * i) * 16) = v[i];
+  }
+  for (; c < pieces; c += 32) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (c < whole) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from + c * 16);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if (from != nullptr && c == whole) {
+      for (int i = 0; i < int(bytes - whole * 16LL); ++i) w[i >> 2] |= uint32_t(from[c * 16 + i]) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint4*>(to + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int used = min(max(offsets[groups], 0), slots);
-  const int pieces = static_cast<int>((row_bytes + 15) / 16);
-  const int whole = static_cast<int>(row_bytes / 16);
-  for (long long s = blockIdx.x * 8LL + (threadIdx.x >> 5); s < used; s += gridDim.x * 8LL) {
-    const uint8_t* from = src + min(max(rows[s], 0), a_rows - 1) * ld;
-    uint8_t* to = dst + s * dst_ld;
-    int c = lane;
-    for (; c + 96 < whole; c += 128) {
-      uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (c + 32 * i) * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (c + 32 * i) * 16) = v[i];
+  auto start = [&](int e) { return e <= 0 ? 0 : min(max(p.offsets[e], 0), p.slots); };
+  auto row = [&](int s) { return min(max(p.rows != nullptr ? p.rows[s] : s, 0), p.a_rows - 1); };
+  const long long used = p.order != nullptr ? start(p.groups) : 0;
+  const long long tasks = used + (p.slab_a != nullptr ? 2LL * p.groups * kSlab : 0);
+  for (long long t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < tasks; t += gridDim.x * 8LL) {
+    if (t < used) {
+      stage_row(p.a + row(int(t)) * p.ld_a, p.bytes_a, p.order + t * p.pitch_a, p.pitch_a, lane);
+      continue;
     }
-    for (; c < whole; c += 32) *reinterpret_cast<uint4*>(to + c * 16) = *reinterpret_cast<const uint4*>(from + c * 16);
-    if (whole < pieces && lane < int(row_bytes - whole * 16LL)) to[whole * 16 + lane] = from[whole * 16 + lane];
+    const int q = int(t - used), e = q / (2 * kSlab), r = (q >> 1) % kSlab;
+    const int begin = start(e), end = max(begin, start(e + 1));
+    if ((end - begin) % kSlab == 0) continue;
+    const int s = begin + (end - begin) / kSlab * kSlab + r;
+    const long long at = static_cast<long long>(e) * kSlab + r;
+    if (q & 1)
+      stage_row(s < end ? p.a + row(s) * p.ld_a : nullptr, p.bytes_a, p.slab_a + at * p.pitch_a, p.pitch_a, lane);
+    else
+      stage_row(s < end ? p.c + s * p.ld_c : nullptr, p.bytes_c, p.slab_c + at * p.pitch_c, p.pitch_c, lane);
   }
   grid_launch_dependents();
 }
 
-// Row pitch in bytes of a gathered operand in slot order.
-int64_t permuted_pitch(int64_t K, int es) { return (K * es + 127) / 128 * 128; }
+// Row pitch in bytes of staged rows: whole 128-byte lines.
+int64_t staged_pitch(int64_t cols, int es) { return (cols * es + 127) / 128 * 128; }
 
-int permute_rows(const CallContext& ctx, const void* A, int64_t a_rows, int64_t lda, const int32_t* rows,
-                 const int32_t* offsets, int groups, int64_t slots, int64_t K, int es, void* dst, cudaStream_t stream) {
-  const int64_t blocks = (slots + 7) / 8, most = int64_t(ctx.sm_count) * 8;
-  const cudaError_t e = launch_dependent(
-      permute_rows_kernel, int(blocks < most ? blocks : most), 256, 0, stream, 1, static_cast<const uint8_t*>(A),
-      (long long)(lda * es), int(a_rows), rows, offsets, groups, int(slots), static_cast<uint8_t*>(dst),
-      (long long)permuted_pitch(K, es), (long long)(K * es));
+int stage_rows(const CallContext& ctx, const StageRows& p, cudaStream_t stream) {
+  const int64_t rows = (p.order != nullptr ? p.slots : 0) + (p.slab_a != nullptr ? 2 * int64_t(p.groups) * kSlab : 0);
+  const int64_t blocks = (rows + 7) / 8, most = int64_t(ctx.sm_count) * 8;
+  const cudaError_t e = launch_dependent(stage_rows_kernel, int(blocks < most ? blocks : most), 256, 0, stream, 1, p);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -126,7 +164,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
   const void* bias = epi != nullptr ? epi->bias : nullptr;
   if (rows == nullptr || K == 0) workspace = nullptr;
-  if (workspace != nullptr && workspace_bytes < slots * permuted_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;
+  if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
       misaligned(workspace, 128) ||
       (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
@@ -191,14 +229,25 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if (K > 0) {
     p.gather_a = rows != nullptr;
     if (rows != nullptr && workspace != nullptr) {
-      st = permute_rows(ctx, A, a_rows, lda, rows, offsets, groups, slots, K, es, workspace, L.stream);
+      StageRows q = {};
+      q.a = static_cast<const uint8_t*>(A);
+      q.ld_a = lda * es;
+      q.bytes_a = K * es;
+      q.pitch_a = staged_pitch(K, es);
+      q.a_rows = int(a_rows);
+      q.rows = rows;
+      q.offsets = offsets;
+      q.groups = groups;
+      q.slots = int(slots);
+      q.order = static_cast<uint8_t*>(workspace);
+      st = stage_rows(ctx, q, L.stream);
       if (st != GEMM_OK) return st;
       A = workspace;
-      lda = permuted_pitch(K, es) / es;
+      lda = staged_pitch(K, es) / es;
       p.gather_a = 0;
     }
     const bool mapped =
-        p.gather_a ? encode_map_2d(&L.tmAg, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)
+        p.gather_a ? encode_map_2d(&L.tmA2, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)
                    : encode_map_3d(&L.tmA, dt, A, K, slots, lda * es, 1, 0, bk, L.pair ? 128 : 32,
                                    CU_TENSOR_MAP_SWIZZLE_128B);
     if (!mapped) return GEMM_ERR_DRIVER;
@@ -212,8 +261,8 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
     }
     if (!ok) return GEMM_ERR_DRIVER;
   }
-  if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, C, out_cols, slots, ldc * 2, 1, 0, 32, 32,
-                                  CU_TENSOR_MAP_SWIZZLE_64B))
+  if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, C, out_cols, slots, ldc * 2, 1, 0, 64, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_ERR_DRIVER;
   cudaError_t e;
   const bool km = layout == GEMM_B_K_MAJOR;
@@ -224,6 +273,10 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   else
     e = km ? launch_group_f16_km(L) : launch_group_f16_rm(L);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int64_t wgrad_workspace(int64_t groups, int64_t slots, int64_t N, int64_t K, bool gathered) {
+  return groups * kSlab * (staged_pitch(N, 2) + staged_pitch(K, 2)) + (gathered ? slots * staged_pitch(K, 2) : 0);
 }
 
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
@@ -243,12 +296,15 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
                     lddc > kLdLimit || (rows == nullptr && a_rows < slots)))
     return GEMM_ERR_INVALID_VALUE;
   if (((out_rows + 255) / 256) * ((out_cols + 255) / 256) > kIntLimit / groups) return GEMM_ERR_INVALID_VALUE;
-  if (rows == nullptr || slots == 0) workspace = nullptr;
-  if (workspace != nullptr && workspace_bytes < slots * permuted_pitch(K, 2)) return GEMM_ERR_INVALID_VALUE;
+  if (slots == 0) workspace = nullptr;
+  if (slots > 0 && (workspace == nullptr ||
+                    workspace_bytes < wgrad_workspace(groups, slots, N, K, rows != nullptr)))
+    return GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2) || misaligned(workspace, 128))
     return GEMM_ERR_MISALIGNED;
   if (slots > 0 && (!tma_rows(A, lda, 2) || !tma_rows(dC, lddc, 2))) return GEMM_ERR_MISALIGNED;
   const Range rw = range_of(dW, out_rows, out_cols, lddw, 2, groups, groups > 1 ? stride_dw : 0);
+  if (workspace != nullptr && meet(rw, range_of(workspace, 1, workspace_bytes, 0, 1))) return GEMM_ERR_INVALID_VALUE;
   if (slots > 0 && (meet(rw, range_of(A, a_rows, K, lda, 2)) || meet(rw, range_of(dC, slots, N, lddc, 2))))
     return GEMM_ERR_INVALID_VALUE;
 
@@ -282,35 +338,54 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   L.pair = true;
   L.dev = ctx.dev;
   L.stream = static_cast<cudaStream_t>(stream);
-  // rows of A that the caller names are put in slot order first (gathered by TMA without a workspace); dC is read by slot
-  bool gather = rows != nullptr;
-  if (gather && slots > 0 && workspace != nullptr) {
-    st = permute_rows(ctx, A, a_rows, lda, rows, offsets, groups, slots, K, 2, workspace, L.stream);
-    if (st != GEMM_OK) return st;
-    A = workspace;
-    lda = permuted_pitch(K, 2) / 2;
-    a_rows = slots;
-    gather = false;
-  }
-  p.gather_p = !km && gather;
-  p.gather_q = km && gather;
   const int64_t tiles = int64_t(groups) * p.g.tiles_m * p.g.tiles_n;
   const int64_t units = ctx.sm_count / 2;
   L.grid = int(2 * (tiles < units ? tiles : units));
   const CUtensorMapDataType dt = map_type(kind);
   if (slots > 0) {
-    const void* P = km ? dC : A;
-    const void* Q = km ? A : dC;
-    const uint64_t ldp = uint64_t(km ? lddc : lda) * 2, ldq = uint64_t(km ? lda : lddc) * 2;
-    const uint64_t rp = km ? slots : a_rows, rq = km ? a_rows : slots;
-    bool ok = p.gather_p ? encode_map_2d(&L.tmAg, dt, P, out_rows, rp, ldp, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B)
-                         : encode_map_3d(&L.tmA, dt, P, out_rows, rp, ldp, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-    ok = ok && (p.gather_q ? encode_map_2d(&L.tmBg, dt, Q, out_cols, rq, ldq, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B)
-                           : encode_map_3d(&L.tmB, dt, Q, out_cols, rq, ldq, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B));
+    // workspace: the groups' ragged slabs of dC and of A, then A's rows in slot order where the caller names them
+    StageRows q = {};
+    q.a = static_cast<const uint8_t*>(A);
+    q.c = static_cast<const uint8_t*>(dC);
+    q.ld_a = lda * 2;
+    q.ld_c = lddc * 2;
+    q.bytes_a = K * 2;
+    q.bytes_c = N * 2;
+    q.pitch_a = staged_pitch(K, 2);
+    q.pitch_c = staged_pitch(N, 2);
+    q.a_rows = int(a_rows);
+    q.rows = rows;
+    q.offsets = offsets;
+    q.groups = groups;
+    q.slots = int(slots);
+    q.slab_c = static_cast<uint8_t*>(workspace);
+    q.slab_a = q.slab_c + int64_t(groups) * kSlab * q.pitch_c;
+    if (rows != nullptr) {
+      q.order = q.slab_a + int64_t(groups) * kSlab * q.pitch_a;
+      A = q.order;
+      lda = q.pitch_a / 2;
+    }
+    st = stage_rows(ctx, q, L.stream);
+    if (st != GEMM_OK) return st;
+    // rows x cols with rows `ld` apart: 64-column blocks as the outer coordinate, two to a box, where the columns are
+    // whole blocks (a block past the row's end would be memory past the matrix); else boxes of one block
+    auto operand = [&](CUtensorMap* m, const void* base, int64_t cols, int64_t nrows, int64_t ld_bytes, int* wide) {
+      *wide = cols % 64 == 0;
+      return *wide ? encode_map_3d(m, dt, base, 64, nrows, ld_bytes, cols / 64, 128, 64, kSlab, CU_TENSOR_MAP_SWIZZLE_128B, 2)
+                   : encode_map_3d(m, dt, base, cols, nrows, ld_bytes, 1, 0, 64, kSlab, CU_TENSOR_MAP_SWIZZLE_128B, 1);
+    };
+    auto slabs = [&](CUtensorMap* m, const void* base, int64_t pitch) {
+      return encode_map_3d(m, dt, base, 64, int64_t(groups) * kSlab, pitch, pitch / 128, 128, 64, kSlab,
+                           CU_TENSOR_MAP_SWIZZLE_128B, 2);
+    };
+    const bool ok = operand(km ? &L.tmA : &L.tmB, dC, N, slots, lddc * 2, km ? &p.wide_p : &p.wide_q) &&
+                    operand(km ? &L.tmB : &L.tmA, A, K, slots, lda * 2, km ? &p.wide_q : &p.wide_p) &&
+                    slabs(km ? &L.tmA2 : &L.tmB2, q.slab_c, q.pitch_c) &&
+                    slabs(km ? &L.tmB2 : &L.tmA2, q.slab_a, q.pitch_a);
     if (!ok) return GEMM_ERR_DRIVER;
   }
   if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, dW, out_cols, out_rows, lddw * 2, groups,
-                                  uint64_t(p.g.stride_c) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+                                  uint64_t(p.g.stride_c) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_ERR_DRIVER;
   const cudaError_t e = kind == KIND_BF16 ? launch_group_bf16_wgrad(L) : launch_group_f16_wgrad(L);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
@@ -323,11 +398,11 @@ extern "C" {
 
 int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K) {
   if (groups < 1 || slots <= 0 || K <= 0 || !dgt::use_pair(slots, groups)) return 0;
-  return slots * dgt::permuted_pitch(K, type == GEMM_TYPE_E4M3 ? 1 : 2);
+  return slots * dgt::staged_pitch(K, type == GEMM_TYPE_E4M3 ? 1 : 2);
 }
 
-int64_t gemm_grouped_wgrad_workspace(int64_t slots, int64_t K) {
-  return slots <= 0 || K <= 0 ? 0 : slots * dgt::permuted_pitch(K, 2);
+int64_t gemm_grouped_wgrad_workspace(int groups, int64_t slots, int64_t N, int64_t K, int gathered) {
+  return groups < 1 || slots <= 0 || N <= 0 || K <= 0 ? 0 : dgt::wgrad_workspace(groups, slots, N, K, gathered != 0);
 }
 
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,

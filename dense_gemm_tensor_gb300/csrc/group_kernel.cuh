@@ -9,10 +9,10 @@
 // issues tcgen05.mma, four epilogue warps per CTA, fp32 accumulators double
 // buffered in tensor memory -- with the three things a ragged group needs:
 //
-//   * Tiles come from the offsets on the device. Each CTA scans the groups'
-//     row-tile counts into shared memory once (one thread per few groups) and
-//     finds a work item's group by binary search, so the host never reads the
-//     group sizes and empty groups cost nothing but their table entry.
+//   * Tiles come from the offsets on the device, so the host never reads the
+//     group sizes. A scheduler warp holds the tile counts of 32 groups at a time
+//     (a lane each), finds a work item's group by ballot and hands the tiles to
+//     the other warps through a ring in shared memory; empty groups cost nothing.
 //   * Rows in slot order come by TMA boxes. Rows that the caller names are
 //     gathered by TMA (tile::gather4: four rows of 128 bytes an instruction,
 //     each lane of the producer warp issues one) where a group has few: an
@@ -22,10 +22,13 @@
 //     (one bandwidth-bound pass) and they are rows in slot order again. A group's
 //     last tile fetches only the rows it has.
 //   * The gradient contracts over a ragged number of rows. A group's last slab
-//     of 64 rows may run into the next group's rows; its loads complete on a
-//     barrier of their own, a sixth warp clears the rows past the end in shared
-//     memory (both operands: an infinity or NaN of another group times zero
-//     would be a NaN), and only then may the MMA read the stage.
+//     of 64 slots may run into the next group's rows, and an infinity or NaN of
+//     another group times zero would be a NaN; so a small kernel first writes
+//     every group's last slab, zero padded, to the workspace, and the producer
+//     loads that one from there.
+//   * The tiles are many and their k-loops short (1024 rows an expert are 16
+//     slabs of the gradient), so the epilogue has to keep up: eight warps, each
+//     storing 64 columns of its 32 rows with one TMA store.
 //
 // PAIR: a CTA pair (cta_group::2) computes a 256 x BN tile, each CTA loading
 // 128 rows of A and half of the B columns; else one CTA computes 128 x BN.
@@ -59,6 +62,9 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void* tmap,
 }
 
 constexpr int kMaxGroups = 1024;
+constexpr int kGroupThreads = 384;  // warps 0-3 and 8-11 epilogue, 4 producer, 5 MMA, 6 idle, 7 scheduler
+constexpr int kGroupEpiWarps = 8;
+constexpr int kTileRing = 4;        // tiles the scheduler is ahead
 
 // Operand arrangements.
 enum : int {
@@ -82,7 +88,7 @@ struct GroupParams {
   int plain;     // the epilogue is the identity
   int out_cols;  // columns of C (or of dW)
   int out_rows;  // gradient: rows of dW
-  int gather_p, gather_q;  // gradient: the operand whose rows are gathered by TMA (else boxes by slot)
+  int wide_p, wide_q;  // gradient: an operand's map has 64-column blocks as its outer coordinate (two blocks a box)
 };
 
 template <int KIND, int OPS, int BN_, bool PAIR, bool GATED>
@@ -107,22 +113,23 @@ struct GroupCfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SMEM_LIMIT = 232448;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int TABLE_BYTES = WGRAD ? 0 : ((kMaxGroups + 2) * 4 + 127) / 128 * 128;
-  static constexpr int FIXED = 1024 /*align slack*/ + BAR_BYTES + TABLE_BYTES;
-  static constexpr int STAGES_FIT = (SMEM_LIMIT - FIXED - EPI_BYTES) / STAGE_BYTES;
+  static constexpr int EPI_TILE = 32 * 128;                // one warp's 32 rows x 64 columns of a 16-bit C
+  static constexpr int EPI_STAGING = kGroupEpiWarps * EPI_TILE;
+  static constexpr int FIXED = 1024 /*align slack*/ + BAR_BYTES + EPI_STAGING;
+  static constexpr int STAGES_FIT = (SMEM_LIMIT - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-  static constexpr int EPI_BUFS = epi_bufs_for(SMEM_LIMIT, FIXED + STAGES * STAGE_BYTES);
-  static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES + EPI_BUFS * EPI_BYTES;
+  static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
   static constexpr int ACC_COLS = BN;
   static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
-  static constexpr int NUM_BARS = 4 * STAGES + 5;
-  static constexpr int THREADS = WGRAD ? 224 : 192;
+  static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * kTileRing;
   static constexpr int A_BOX_ROWS = PAIR ? 128 : 32;  // rows of A per box: one CTA's tile may hold few
   static_assert(BN % 64 == 0 && BN >= 64 && BN <= 256, "tile width");
   static_assert(B_KMAJOR || ES == 2, "8-bit operands are read K-major");
   static_assert(B_KMAJOR || BNH % BOXN == 0, "MN-major B comes in whole boxes");
   static_assert(!GATED || B_KMAJOR || PAIR || (BN / 2) % BOXN == 0, "each half is whole boxes");
-  static_assert(NUM_BARS * 8 + 64 <= BAR_BYTES, "barrier area");
+  static_assert(OUT_BN % 64 == 0, "an epilogue warp stores 64 columns at a time");
+  static_assert(NUM_BARS * 8 + 32 + kTileRing * 32 <= BAR_BYTES, "barrier area");
+  static_assert(!WGRAD || (ES == 2 && BM == 2 * BOXN && BNH == 2 * BOXN), "two 64-column blocks of each operand per CTA");
   static_assert(STAGES >= 4 && SMEM_BYTES <= SMEM_LIMIT, "shared memory");
   static constexpr uint32_t IDESC = (1u << 4) | (KindTraits<KIND>::fmt << 7) | (KindTraits<KIND>::fmt << 10) |
                                     ((WGRAD ? 1u : 0u) << 15) | ((B_KMAJOR ? 0u : 1u) << 16) |
@@ -131,7 +138,7 @@ struct GroupCfg {
 
 // A work item: group, first accumulator row and the rows' end (slots of the
 // product, rows of dW for the gradient), tile column, slots of the group
-// [begin, end) and k-slabs.
+// [begin, end) and k-slabs (-1: no more work).
 struct GroupTile {
   int e, m0, row_end, nb, begin, end, kbs;
 };
@@ -155,35 +162,27 @@ __device__ __forceinline__ void band_place(int r, int raster, int tiles_m, int t
   mb = first + (q - nb * rows);
 }
 
-template <class Cf>
-__device__ __forceinline__ GroupTile group_tile(const GroupParams& p, const int* cum, int w) {
+// The next tile of the ring, handed out by the scheduler: `n` counts this
+// warp's tiles. All lanes return the same; kbs is -1 after the last one and
+// when the launch was aborted. Warp-collective.
+__device__ __forceinline__ GroupTile next_tile(const GemmParams& g, uint32_t schf0, uint32_t sche0, uint32_t ring, int n,
+                                               uint32_t role) {
+  const int s = n % kTileRing;
   GroupTile t;
-  int mb;
-  if constexpr (Cf::WGRAD) {
-    const int per = p.g.tiles_m * p.g.tiles_n;
-    t.e = w / per;
-    band_place(w - t.e * per, p.g.raster, p.g.tiles_m, p.g.tiles_n, mb, t.nb);
-    t.begin = group_start(p, t.e);
-    t.end = max(t.begin, group_start(p, t.e + 1));
-    t.m0 = mb * Cf::BMT;
-    t.row_end = p.out_rows;
-    t.kbs = (t.end - t.begin + Cf::BK - 1) / Cf::BK;
-  } else {
-    const int q = w / p.g.tiles_n;
-    int lo = 0, hi = p.groups;  // the last group with cum <= q (group `groups`: the slots past the last group)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cum[mid] <= q) lo = mid;
-      else hi = mid - 1;
-    }
-    t.e = lo;
-    band_place(w - cum[lo] * p.g.tiles_n, p.g.raster, cum[lo + 1] - cum[lo], p.g.tiles_n, mb, t.nb);
-    t.begin = group_start(p, lo);
-    t.end = lo < p.groups ? max(t.begin, group_start(p, lo + 1)) : p.slots;
-    t.m0 = t.begin + mb * Cf::BMT;
-    t.row_end = t.end;
-    t.kbs = lo < p.groups ? p.g.num_kb : 0;
-  }
+  t.kbs = -1;
+  if (!warp_wait_phase(g, schf0 + 8 * s, (n / kTileRing) & 1, role)) return t;
+  __syncwarp();
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(t.e), "=r"(t.m0), "=r"(t.row_end), "=r"(t.nb)
+               : "r"(ring + 32 * s)
+               : "memory");
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+               : "=r"(t.begin), "=r"(t.end)
+               : "r"(ring + 32 * s + 16)
+               : "memory");
+  t.kbs = static_cast<int>(ld_shared_u32(ring + 32 * s + 24));
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(sche0 + 8 * s);
   return t;
 }
 
@@ -195,14 +194,20 @@ __device__ __forceinline__ int gathered_row(const GroupParams& p, int s, int end
   return min(max(r, 0), p.a_rows - 1);
 }
 
-// Writes the staged 32 x 64-byte tile to C[row0 .., col0 ..] of matrix z:
-// rows before row_end and columns before p.out_cols only. TMA stores whole
-// 32-row pieces (it clips at the tensor's end, not at a group's, so a piece
-// that crosses the group's end is stored row by row).
+// An epilogue warp's staging tile: 32 rows of 128 bytes in the layout of
+// TMA's 128-byte swizzle; 16-byte chunk j of row r sits at r * 128 + ((j ^ (r mod 8)) * 16).
+__device__ __forceinline__ uint32_t stage_chunk(uint32_t stage, int r, int j) {
+  return stage + static_cast<uint32_t>(r * 128) + (static_cast<uint32_t>(j ^ (r & 7)) << 4);
+}
+
+// Writes the staged 32 x 64 tile to C[row0 .., col0 ..] of matrix z: rows
+// before row_end and columns before p.out_cols only. TMA stores whole 32-row
+// pieces (CLIP: it clips at the tensor's end; a group's end it does not know, so
+// a piece that crosses it is stored row by row).
 template <bool CLIP>
 __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensorMap* tmC, uint32_t stage, int lane,
                                             int row0, int row_end, int col0, int z) {
-  const bool full_cols = col0 + 32 <= p.out_cols;
+  const bool full_cols = col0 + 64 <= p.out_cols;
   if (p.g.c_tma && full_cols && (CLIP ? row0 < row_end : row0 + 32 <= row_end)) {
     fence_proxy_async_smem();
     __syncwarp();
@@ -214,27 +219,36 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
   }
   __syncwarp();
   uint16_t* base = static_cast<uint16_t*>(p.g.C) + z * p.g.stride_c + col0;
-  if (p.g.c_gran >= 8 && full_cols) {
-    const int l = lane & 7;
+  if (p.g.c_gran == 16) {
+    // 8 lanes a row, 16 bytes a lane; the last lane of a ragged row element by element
+    const int l = lane & 7, cols = p.out_cols - col0 - 8 * l;
 #pragma unroll
     for (int rr = 0; rr < 32; rr += 4) {
       const int r = rr + (lane >> 3);
-      uint32_t lo, hi;
-      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                   : "=r"(lo), "=r"(hi)
-                   : "r"(epi_chunk_addr(stage, r, l >> 1) + ((l & 1) << 3))
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(stage_chunk(stage, r, l))
                    : "memory");
-      if (row0 + r < row_end)
-        *reinterpret_cast<uint2*>(base + static_cast<long long>(row0 + r) * p.g.ldc + l * 4) = make_uint2(lo, hi);
+      if (row0 + r < row_end) {
+        uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 8 * l;
+        if (cols >= 8) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            if (k < cols) dst[k] = static_cast<uint16_t>(k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu);
+        }
+      }
     }
   } else {
-    const int l = lane & 15, col = col0 + 2 * l;
+    // a row at a time, two columns a lane
+    const int col = col0 + 2 * lane;
 #pragma unroll 4
-    for (int rr = 0; rr < 32; rr += 2) {
-      const int r = rr + (lane >> 4);
-      const uint32_t v = ld_shared_u32(epi_chunk_addr(stage, r, l >> 2) + ((l & 3) << 2));
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t v = ld_shared_u32(stage_chunk(stage, r, lane >> 2) + ((lane & 3) << 2));
       if (row0 + r < row_end && col < p.out_cols) {
-        uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 2 * l;
+        uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 2 * lane;
         if (p.g.c_gran >= 4 && col + 1 < p.out_cols) {
           *reinterpret_cast<uint32_t*>(dst) = v;
         } else {
@@ -247,9 +261,17 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
   __syncwarp();
 }
 
+template <bool PAIR>
+__device__ __forceinline__ void wgrad_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (PAIR)
+    tma_load_3d_pair(dst, map, bar, x, y, z);
+  else
+    tma_load_3d(dst, map, bar, x, y, z);
+}
+
 // The scaled and biased pre-activation of 32 accumulator columns from
 // column `col` of group e: v = scale * col_scale[col] * acc + bias[col]. Each
-// lane loads one column's scale and bias; shuffles hand them to every lane.
+// lane loads one column's scale and bias, and shuffles hand them to every lane.
 template <int KIND>
 __device__ __forceinline__ void group_scale(const GroupParams& p, int e, int col, int lane, float scale,
                                             const uint32_t (&r)[32], float (&v)[32]) {
@@ -276,9 +298,9 @@ __device__ __forceinline__ void group_scale(const GroupParams& p, int e, int col
 }
 
 template <int KIND, int OPS, int BN, bool PAIR, bool GATED>
-__global__ void __launch_bounds__(224, 1)
-    group_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAg,
-                 const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBg,
+__global__ void __launch_bounds__(kGroupThreads, 1)
+    group_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+                 const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GroupParams p) {
   using Cf = GroupCfg<KIND, OPS, BN, PAIR, GATED>;
   constexpr int S = Cf::STAGES;
@@ -291,21 +313,18 @@ __global__ void __launch_bounds__(224, 1)
   const uint32_t sA = sbase;
   const uint32_t sB = sbase + S * Cf::A_BYTES;
   const uint32_t sE = sbase + S * Cf::STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sptr + S * Cf::STAGE_BYTES + Cf::EPI_BUFS * EPI_BYTES);
-  int* cum = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + Cf::BAR_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sptr + S * Cf::STAGE_BYTES + Cf::EPI_STAGING);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * S;
   const uint32_t accf0 = empty0 + 8 * S;
   const uint32_t acce0 = accf0 + 16;
   const uint32_t drain_bar = acce0 + 16;
-  const uint32_t tailf0 = drain_bar + 8;   // gradient: a stage's ragged slab has landed in this CTA
-  const uint32_t tailok0 = tailf0 + 8 * S; // gradient (leader): both CTAs have cleared its rows past the end
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(bars + Cf::NUM_BARS);
-  volatile int* issued_slot = reinterpret_cast<volatile int*>(bars + Cf::NUM_BARS) + 1;
+  const uint32_t schf0 = drain_bar + 8;  // tile ring: entry written, entry read by every warp that takes tiles
+  const uint32_t sche0 = schf0 + 8 * kTileRing;
+  const uint32_t ring = (sche0 + 8 * kTileRing + 15u) & ~15u;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + (ring - sbase) + 32 * kTileRing);
+  volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot) + 1;
   volatile int* consumed_slot = issued_slot + 1;
-  volatile int* ok_slot = issued_slot + 2;    // [2]
-  volatile int* tail_slot = issued_slot + 4;  // ragged slabs issued, and seen landed
-  int* warp_sums = reinterpret_cast<int*>(bars + Cf::NUM_BARS) + 8;  // [8]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -318,21 +337,22 @@ __global__ void __launch_bounds__(224, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(tailf0 + 8 * s, 1);
-      mbar_init(tailok0 + 8 * s, Cf::CTAS);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
-      mbar_init(acce0 + 8 * b, 4 * Cf::CTAS);
+      mbar_init(acce0 + 8 * b, kGroupEpiWarps * Cf::CTAS);
+    }
+    for (int i = 0; i < kTileRing; ++i) {
+      mbar_init(schf0 + 8 * i, 1);
+      // every warp that takes tiles: epilogue, producer, the leader's MMA warp
+      mbar_init(sche0 + 8 * i, kGroupEpiWarps + 1 + (leader ? 1 : 0));
     }
     mbar_init(drain_bar, 1);
     *issued_slot = 0;
     *consumed_slot = 0;
-    tail_slot[0] = 0;
-    tail_slot[1] = 0;
     fence_mbar_init();
     if (!WGRAD && p.g.num_kb > 0) {
-      tma_prefetch_desc(p.gather_a ? &tmAg : &tmA);
+      tma_prefetch_desc(p.gather_a ? &tmA2 : &tmA);
       tma_prefetch_desc(&tmB);
     }
   }
@@ -348,56 +368,21 @@ __global__ void __launch_bounds__(224, 1)
   }
   // set-up done; from here on memory that earlier kernels wrote is read
   grid_dependency_wait();
-  if constexpr (!WGRAD) {
-    // row tiles of each group, and of the slots past the last one, summed in group order
-    const int n = p.groups + 1;
-    const int per = (n + Cf::THREADS - 1) / Cf::THREADS;  // at most 6
-    const int e0 = threadIdx.x * per;
-    int cnt[6];
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      const int e = e0 + i;
-      cnt[i] = 0;
-      if (i < per && e < n) {
-        const int b = group_start(p, e);
-        const int z = e < p.groups ? group_start(p, e + 1) : p.slots;
-        cnt[i] = z > b ? (z - b + Cf::BMT - 1) / Cf::BMT : 0;
-      }
-      sum += cnt[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      if (i < per && e0 + i < n) cum[e0 + i] = at;
-      at += cnt[i];
-    }
-    if (threadIdx.x == Cf::THREADS - 1) cum[n] = at;
-  }
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // barriers of both CTAs initialised before any remote signal
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int work = WGRAD ? p.groups * p.g.tiles_m * p.g.tiles_n : cum[p.groups + 1] * p.g.tiles_n;
 
   if (warp == 4) {
     // ---------------------------------------------------------------- TMA producer (every CTA)
     if (!(p.g.debug & DEBUG_STALL_PRODUCER)) {
-      int it = 0, tails = 0;
+      int it = 0;
       bool ok = true;
       const uint32_t lead_full0 = PAIR ? mapa_shared(full0, 0) : full0;
-      for (int w = unit; ok && w < work; w += nunits) {
-        const GroupTile t = group_tile<Cf>(p, cum, w);
+      for (int n = 0; ok; ++n) {
+        const GroupTile t = next_tile(p.g, schf0, sche0, ring, n, ROLE_PRODUCER | (0x80u << 8));
+        if (t.kbs < 0) break;
         int r0 = 0, r1 = 0, r2 = 0, r3 = 0;  // product: this lane's four rows of A
         int pieces = 0, tx = 0;
         if constexpr (!WGRAD) {
@@ -426,7 +411,7 @@ __global__ void __launch_bounds__(224, 1)
           }
           const uint32_t a_dst = sA + s * Cf::A_BYTES;
           const uint32_t b_dst = sB + s * Cf::B_BYTES;
-          uint32_t fb = lead_full0 + 8 * s;
+          const uint32_t fb = lead_full0 + 8 * s;
           if constexpr (!WGRAD) {
             // (operands of the elected lane's loads are the same in every lane: the issue path wants them so)
             const int row0 = t.m0 + int(half) * Cf::BM;
@@ -473,87 +458,49 @@ __global__ void __launch_bounds__(224, 1)
             __syncwarp();
             if (p.gather_a && lane < pieces) {
               if constexpr (PAIR)
-                tma_gather4_pair(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
+                tma_gather4_pair(a_dst + lane * 512, &tmA2, fb, kb * Cf::BK, r0, r1, r2, r3);
               else
-                tma_gather4(a_dst + lane * 512, &tmAg, fb, kb * Cf::BK, r0, r1, r2, r3);
+                tma_gather4(a_dst + lane * 512, &tmA2, fb, kb * Cf::BK, r0, r1, r2, r3);
             }
           } else {
+            // the group's last slab, where ragged, comes from its zero-padded copy: 64 rows for each group
             const int s0 = t.begin + kb * Cf::BK;
-            const bool tail = s0 + Cf::BK > t.end;
-            // boxes of each operand that start inside it (the columns of the others are not stored)
-            const int p0 = t.m0 + int(half) * Cf::BM;
-            const int q0 = t.nb * BN + int(half) * Cf::BNH;
-            constexpr int PB = Cf::BM / Cf::BOXN, QB = Cf::BNH / Cf::BOXN;
-            auto boxes_in = [](int x0, int cols, int most) {
-              return min(max((cols - x0 + Cf::BOXN - 1) / Cf::BOXN, 0), most);
-            };
-            const int np = boxes_in(p0, p.out_rows, PB), nq = boxes_in(q0, p.out_cols, QB);
-            // A ragged slab: both operands of this CTA complete on its own barrier, and
-            // the leader's full barrier has nothing to count.
-            if (tail) fb = tailf0 + 8 * s;
-            const int peer = PAIR ? boxes_in(p0 + Cf::BM, p.out_rows, PB) + boxes_in(q0 + Cf::BNH, p.out_cols, QB) : 0;
+            const bool ragged = s0 + Cf::BK > t.end;
+            const int y = ragged ? t.e * Cf::BK : s0;
+            const CUtensorMap* map_p = ragged ? &tmA2 : &tmA;
+            const CUtensorMap* map_q = ragged ? &tmB2 : &tmB;
+            const bool wide_p = ragged || p.wide_p, wide_q = ragged || p.wide_q;
+            const int p0 = t.m0 + int(half) * Cf::BM, q0 = t.nb * BN + int(half) * Cf::BNH;
             if (elect_one()) {
-              if (tail) {
-                mbar_arrive_expect_tx(fb, (np + nq) * Cf::BOX_BYTES);
-                if (leader) mbar_arrive(full0 + 8 * s);
-              } else if (leader) {
-                mbar_arrive_expect_tx(full0 + 8 * s, (np + nq + peer) * Cf::BOX_BYTES);
-              }
-              if (PAIR && !tail) {
-#pragma unroll
-                for (int j = 0; j < PB; ++j)
-                  if (!p.gather_p && j < np)
-                    tma_load_3d_pair(a_dst + j * Cf::BOX_BYTES, &tmA, fb, p0 + j * Cf::BOXN, s0, 0);
-#pragma unroll
-                for (int j = 0; j < QB; ++j)
-                  if (!p.gather_q && j < nq)
-                    tma_load_3d_pair(b_dst + j * Cf::BOX_BYTES, &tmB, fb, q0 + j * Cf::BOXN, s0, 0);
+              if (leader) mbar_arrive_expect_tx(full0 + 8 * s, Cf::CTAS * Cf::STAGE_BYTES);
+              if (wide_p) {
+                wgrad_load<PAIR>(a_dst, map_p, fb, 0, y, p0 / Cf::BOXN);
               } else {
-#pragma unroll
-                for (int j = 0; j < PB; ++j)
-                  if (!p.gather_p && j < np) tma_load_3d(a_dst + j * Cf::BOX_BYTES, &tmA, fb, p0 + j * Cf::BOXN, s0, 0);
-#pragma unroll
-                for (int j = 0; j < QB; ++j)
-                  if (!p.gather_q && j < nq) tma_load_3d(b_dst + j * Cf::BOX_BYTES, &tmB, fb, q0 + j * Cf::BOXN, s0, 0);
+                wgrad_load<PAIR>(a_dst, map_p, fb, p0, y, 0);
+                wgrad_load<PAIR>(a_dst + Cf::BOX_BYTES, map_p, fb, p0 + Cf::BOXN, y, 0);
               }
-            }
-            tails += tail ? 1 : 0;
-            __syncwarp();
-            if (p.gather_p || p.gather_q) {
-              // 16 quads of slots x the operand's boxes
-              const int quad = lane & 15;
-              r0 = gathered_row(p, s0 + 4 * quad, t.end);
-              r1 = gathered_row(p, s0 + 4 * quad + 1, t.end);
-              r2 = gathered_row(p, s0 + 4 * quad + 2, t.end);
-              r3 = gathered_row(p, s0 + 4 * quad + 3, t.end);
-              const uint32_t dst = (p.gather_p ? a_dst : b_dst) + quad * 512;
-              const CUtensorMap* map = p.gather_p ? &tmAg : &tmBg;
-              const int x0 = p.gather_p ? p0 : q0;
-              for (int j = lane >> 4; j < (p.gather_p ? np : nq); j += 2) {
-                if (PAIR && !tail)
-                  tma_gather4_pair(dst + j * Cf::BOX_BYTES, map, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
-                else
-                  tma_gather4(dst + j * Cf::BOX_BYTES, map, fb, x0 + j * Cf::BOXN, r0, r1, r2, r3);
+              if (wide_q) {
+                wgrad_load<PAIR>(b_dst, map_q, fb, 0, y, q0 / Cf::BOXN);
+              } else {
+                wgrad_load<PAIR>(b_dst, map_q, fb, q0, y, 0);
+                wgrad_load<PAIR>(b_dst + Cf::BOX_BYTES, map_q, fb, q0 + Cf::BOXN, y, 0);
               }
             }
           }
           __syncwarp();
         }
       }
-      if (lane == 0) {
-        *issued_slot = it;
-        tail_slot[0] = tails;
-      }
+      if (lane == 0) *issued_slot = it;
     }
     grid_launch_dependents();
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA issuer (the pair's leader)
     if (leader) {
       int it = 0, tc = 0;
-      uint32_t tail_ph = 0;  // parity of each stage's next ragged slab
       bool ok = true;
-      for (int w = unit; ok && w < work; w += nunits) {
-        const GroupTile t = group_tile<Cf>(p, cum, w);
+      for (int n = 0; ok; ++n) {
+        const GroupTile t = next_tile(p.g, schf0, sche0, ring, n, ROLE_MMA | (0x81u << 8));
+        if (t.kbs < 0) break;
         if (t.kbs == 0) continue;
         const int b = tc & 1;
         if (!warp_wait_phase(p.g, acce0 + 8 * b, ((tc >> 1) & 1) ^ 1, ROLE_MMA | (0x80u << 8))) break;
@@ -562,12 +509,10 @@ __global__ void __launch_bounds__(224, 1)
         const uint32_t d = tmem + b * Cf::ACC_COLS;
         for (int kb = 0; kb < t.kbs; ++kb, ++it) {
           const int s = it % S;
-          ok = warp_wait_phase(p.g, full0 + 8 * s, (it / S) & 1, ROLE_MMA | (s << 8));
-          if (WGRAD && ok && t.begin + (kb + 1) * Cf::BK > t.end) {
-            ok = warp_wait_phase(p.g, tailok0 + 8 * s, (tail_ph >> s) & 1u, ROLE_MMA | ((0x40u + s) << 8));
-            tail_ph ^= 1u << s;
+          if (!warp_wait_phase(p.g, full0 + 8 * s, (it / S) & 1, ROLE_MMA | (s << 8))) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
           tc_fence_after();
           const uint32_t a_addr = sA + s * Cf::A_BYTES;
           const uint32_t b_addr = sB + s * Cf::B_BYTES;
@@ -615,81 +560,91 @@ __global__ void __launch_bounds__(224, 1)
       if (lane == 0) wait_phase_drain(p.g, drain_bar, 0);
       __syncwarp();
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || warp >= 8) {
     // ---------------------------------------------------------------- epilogue (every CTA)
+    // warps q and q + 8 read tensor-memory lanes 32 q ..; the first takes 64-column pieces 0, 2, ..., the second 1, 3, ...
+    const int q = warp & 3, set = warp >> 3;
+    const uint32_t stage = sE + static_cast<uint32_t>((set * 4 + q) * Cf::EPI_TILE);
     int tc = 0;
-    EpiRing ring{sE + static_cast<uint32_t>(warp * Cf::EPI_BUFS * EPI_WARP_BYTES), Cf::EPI_BUFS, 0,
-                 sE + static_cast<uint32_t>(Cf::EPI_BUFS * EPI_BYTES)};
-    for (int w = unit; w < work; w += nunits) {
-      const GroupTile t = group_tile<Cf>(p, cum, w);
+    for (int n = 0;; ++n) {
+      const GroupTile t = next_tile(p.g, schf0, sche0, ring, n, ROLE_EPILOGUE | (0x80u << 8));
+      if (t.kbs < 0) break;
       const int b = tc & 1;
       if (t.kbs > 0) {
-        // the four warps take every decision together: thread 0 waits, the barrier publishes the outcome
-        if (threadIdx.x == 0)
-          ok_slot[b] = wait_phase(p.g, accf0 + 8 * b, (tc >> 1) & 1, ROLE_EPILOGUE | (b << 8)) ? 1 : 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (!ok_slot[b]) break;
+        if (!warp_wait_phase(p.g, accf0 + 8 * b, (tc >> 1) & 1, ROLE_EPILOGUE | (b << 8))) break;
         ++tc;
         tc_fence_after();
       }
-      const int row0 = t.m0 + int(half) * Cf::BM + warp * 32;
+      const int row0 = t.m0 + int(half) * Cf::BM + q * 32;
       const int col0 = t.nb * Cf::OUT_BN;
       const int z = WGRAD ? t.e : 0;
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * Cf::ACC_COLS;
-      const int ncols = min(Cf::OUT_BN, p.out_cols - col0);
-      const int nchunks = row0 < t.row_end && ncols > 0 ? (ncols + 31) / 32 : 0;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * Cf::ACC_COLS;
       const bool null_group = !WGRAD && t.e >= p.groups;
+      const bool convert_only = WGRAD || p.plain || null_group;
       float scale = p.g.alpha;
       if (!WGRAD && p.row_scale != nullptr && !null_group && row0 + lane < t.end)
         scale *= p.row_scale[gathered_row(p, row0 + lane, t.end)];
-      auto store = [&](int c, const uint32_t(&words)[16]) {
-        const uint32_t stage = epi_acquire(p.g, lane, ring);
-        epi_put_row(stage, lane, words);
-        group_flush<WGRAD>(p, &tmC, stage, lane, row0, t.row_end, col0 + c * 32, z);
-      };
-      auto emit = [&](int c, const uint32_t(&r)[32], const uint32_t(&r2)[32]) {
-        uint32_t words[16];
-        if (WGRAD || p.plain || null_group) {
+      if (row0 < t.row_end) {
+        for (int c = set * 64; c < Cf::OUT_BN && col0 + c < p.out_cols; c += 128) {
+          uint32_t acc[2][32];
+          if (t.kbs == 0) {
+            // nothing was accumulated (K = 0, an empty group's gradient, the slots past the last group)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) words[j] = pack2<KindTraits<KIND>::out>(r[2 * j], r[2 * j + 1]);
-        } else {
-          float v[32];
-          group_scale<KIND>(p, t.e, col0 + c * 32, lane, scale, r, v);
-          if constexpr (GATED) {
-            float u[32];
-            group_scale<KIND>(p, t.e, p.g.N / 2 + col0 + c * 32, lane, scale, r2, u);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = v[k] / (1.0f + expf(-v[k])) * u[k];
-          } else {
-            epi_activate(v, p.g.act);
+            for (int k = 0; k < 32; ++k) acc[0][k] = acc[1][k] = 0u;
           }
+          uint32_t words[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            words[j] = pack2<KindTraits<KIND>::out>(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
-        }
-        store(c, words);
-      };
-      if (t.kbs == 0) {
-        // nothing was accumulated (K = 0, an empty group's gradient, the slots past the last group)
-        uint32_t zero[32];
+          for (int h = 0; h < 2; ++h) {
+            const int cc = c + 32 * h;
+            if (t.kbs > 0) {
+              __syncwarp();
+              if constexpr (GATED) {
+                tmem_ld_32x32b_x32(taddr + cc, acc[0]);
+                tmem_ld_32x32b_x32(taddr + BN / 2 + cc, acc[1]);
+                tmem_wait_ld_into(acc[0]);
+                tmem_wait_ld_into(acc[1]);
+              } else if (h == 0) {
+                tmem_ld_32x32b_x32(taddr + cc, acc[0]);
+                tmem_ld_32x32b_x32(taddr + cc + 32, acc[1]);
+                tmem_wait_ld_into(acc[0]);
+                tmem_wait_ld_into(acc[1]);
+              }
+            }
+            const uint32_t(&r)[32] = GATED ? acc[0] : acc[h];
+            if (convert_only) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) zero[k] = 0u;
-        for (int c = 0; c < nchunks; ++c) emit(c, zero, zero);
-        continue;
-      }
-      if constexpr (GATED) {
-        for (int c = 0; c < nchunks; ++c) {
-          uint32_t ra[32], rb[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(taddr + c * 32, ra);
-          tmem_ld_32x32b_x32(taddr + BN / 2 + c * 32, rb);
-          tmem_wait_ld_into(ra);
-          tmem_wait_ld_into(rb);
-          emit(c, ra, rb);
+              for (int j = 0; j < 16; ++j) words[j] = pack2<KindTraits<KIND>::out>(r[2 * j], r[2 * j + 1]);
+            } else {
+              float v[32];
+              group_scale<KIND>(p, t.e, col0 + cc, lane, scale, r, v);
+              if constexpr (GATED) {
+                // silu(g) u with the hardware's exponential and reciprocal: both are within a few 2^-22 of
+                // the value, far inside the 2^-9 to which the result is rounded next
+                float u[32];
+                group_scale<KIND>(p, t.e, p.g.N / 2 + col0 + cc, lane, scale, acc[1], u);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __fdividef(v[k], 1.0f + __expf(-v[k])) * u[k];
+              } else {
+                epi_activate(v, p.g.act);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                words[j] = pack2<KindTraits<KIND>::out>(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
+            }
+            if (h == 0) {
+              // the tile's last TMA store has read it
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4(stage_chunk(stage, lane, 4 * h + j), words[4 * j], words[4 * j + 1], words[4 * j + 2],
+                           words[4 * j + 3]);
+          }
+          group_flush<WGRAD>(p, &tmC, stage, lane, row0, t.row_end, col0 + c, z);
         }
-      } else if (nchunks > 0) {
-        for_each_acc_chunk(taddr, nchunks, [&](int c, const uint32_t(&r)[32]) { emit(c, r, r); });
       }
+      if (t.kbs == 0) continue;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -701,42 +656,77 @@ __global__ void __launch_bounds__(224, 1)
     }
     if (lane == 0) bulk_wait_read_all();
     __syncwarp();
-  } else if (WGRAD && warp == 6) {
-    // ---------------------------------------------------------------- ragged slabs (every CTA)
-    int it = 0, seen = 0;
-    uint32_t ph = 0;
+  } else if (warp == 7) {
+    // ---------------------------------------------------------------- scheduler (every CTA)
+    int n = 0;
+    auto push = [&](const GroupTile& t) {
+      const int s = n % kTileRing;
+      const bool ok = warp_wait_phase(p.g, sche0 + 8 * s, ((n / kTileRing) & 1) ^ 1, ROLE_PRODUCER | (0x90u << 8));
+      if (ok && lane == 0) {
+        st_shared_v4(ring + 32 * s, t.e, t.m0, t.row_end, t.nb);
+        st_shared_v4(ring + 32 * s + 16, t.begin, t.end, t.kbs, 0);
+        mbar_arrive(schf0 + 8 * s);
+      }
+      ++n;
+      return ok;
+    };
+    GroupTile t;
     bool ok = true;
-    for (int w = unit; ok && w < work; w += nunits) {
-      const GroupTile t = group_tile<Cf>(p, cum, w);
-      if (t.kbs == 0) continue;
-      const int valid = t.end - t.begin - (t.kbs - 1) * Cf::BK;
-      it += t.kbs;
-      if (valid == Cf::BK) continue;
-      const int s = (it - 1) % S;
-      if (!warp_wait_phase(p.g, tailf0 + 8 * s, (ph >> s) & 1u, ROLE_COPY | (s << 8))) {
-        ok = false;
-        break;
+    if constexpr (WGRAD) {
+      const int per = p.g.tiles_m * p.g.tiles_n, work = p.groups * per;
+      for (int w = unit; ok && w < work; w += nunits) {
+        int mb;
+        t.e = w / per;
+        band_place(w - t.e * per, p.g.raster, p.g.tiles_m, p.g.tiles_n, mb, t.nb);
+        t.begin = group_start(p, t.e);
+        t.end = max(t.begin, group_start(p, t.e + 1));
+        t.m0 = mb * Cf::BMT;
+        t.row_end = p.out_rows;
+        t.kbs = (t.end - t.begin + Cf::BK - 1) / Cf::BK;
+        ok = push(t);
       }
-      ph ^= 1u << s;
-      ++seen;
-      // clear rows [valid, BK) of every 128-byte-wide box (a whole row: the swizzle permutes within it)
-      constexpr int NBOX = Cf::BM / Cf::BOXN + Cf::BNH / Cf::BOXN;
+    } else {
+      // lane l: group base + l's slots and row tiles (group `groups`: the slots past the last one), and the tiles up
+      // to and with it, counted from `before`
+      int base = 0, before = 0, first = 0, last = 0, count = 0, incl = 0;
+      auto load = [&]() {
+        const int e = base + lane;
+        first = e <= p.groups ? group_start(p, e) : p.slots;
+        last = e < p.groups ? max(first, group_start(p, e + 1)) : p.slots;
+        count = incl = (last - first + Cf::BMT - 1) / Cf::BMT;
 #pragma unroll
-      for (int j = 0; j < NBOX; ++j) {
-        const uint32_t box = j < Cf::BM / Cf::BOXN ? sA + s * Cf::A_BYTES + j * Cf::BOX_BYTES
-                                                   : sB + s * Cf::B_BYTES + (j - Cf::BM / Cf::BOXN) * Cf::BOX_BYTES;
-        for (int r = valid + (lane >> 3); r < Cf::BK; r += 4) st_shared_v4(box + r * 128 + (lane & 7) * 16, 0, 0, 0, 0);
-      }
-      asm volatile("fence.proxy.async;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_cluster(mapa_shared(tailok0 + 8 * s, 0));
-        else
-          mbar_arrive(tailok0 + 8 * s);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+          if (lane >= d) incl += o;
+        }
+      };
+      load();
+      for (int w = unit; ok; w += nunits) {
+        const int tile = w / p.g.tiles_n;  // row tile, were each column of tiles to be walked alone
+        int sum = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        while (tile >= before + sum && base + 32 <= p.groups) {
+          before += sum;
+          base += 32;
+          load();
+          sum = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (tile >= before + sum) break;
+        const int l = __ffs(__ballot_sync(0xFFFFFFFFu, incl > tile - before)) - 1;
+        const int tiles_m = __shfl_sync(0xFFFFFFFFu, count, l);
+        const int tiles_before = before + __shfl_sync(0xFFFFFFFFu, incl, l) - tiles_m;
+        int mb;
+        band_place(w - tiles_before * p.g.tiles_n, p.g.raster, tiles_m, p.g.tiles_n, mb, t.nb);
+        t.e = base + l;
+        t.begin = __shfl_sync(0xFFFFFFFFu, first, l);
+        t.end = __shfl_sync(0xFFFFFFFFu, last, l);
+        t.m0 = t.begin + mb * Cf::BMT;
+        t.row_end = t.end;
+        t.kbs = t.e < p.groups ? p.g.num_kb : 0;
+        ok = push(t);
       }
     }
-    if (lane == 0) tail_slot[1] = seen;
+    t.kbs = -1;
+    if (ok) push(t);
   }
 
   // ------------------------------------------------------------------ teardown
@@ -748,19 +738,6 @@ __global__ void __launch_bounds__(224, 1)
     const int issued = *issued_slot;
     for (int j = *consumed_slot; j < issued; ++j)
       if (!wait_phase_drain(p.g, full0 + 8 * (j % S), (j / S) & 1)) break;
-  }
-  if (WGRAD && threadIdx.x == 32 && tail_slot[1] < tail_slot[0]) {
-    // the unseen ragged slabs are the last ones, at most one a stage: walk the work again and wait for them
-    int it = 0, n = 0;
-    uint32_t ph = 0;
-    for (int w = unit; n < tail_slot[0] && w < work; w += nunits) {
-      const GroupTile t = group_tile<Cf>(p, cum, w);
-      it += t.kbs;
-      if (t.kbs == 0 || (t.end - t.begin) % Cf::BK == 0) continue;
-      const int s = (it - 1) % S;
-      if (n++ >= tail_slot[1] && !wait_phase_drain(p.g, tailf0 + 8 * s, (ph >> s) & 1u)) break;
-      ph ^= 1u << s;
-    }
   }
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still signal it

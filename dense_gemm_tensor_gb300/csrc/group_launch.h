@@ -8,8 +8,8 @@
 namespace dgt {
 
 struct GroupLaunch {
-  CUtensorMap tmA, tmAg;  // the MMA's A operand: boxes (gradient), gathered rows
-  CUtensorMap tmB, tmBg;  // its B operand: boxes, gathered rows (gradient)
+  CUtensorMap tmA, tmA2;  // the MMA's A operand: boxes; gathered rows (product) or the groups' ragged slabs (gradient)
+  CUtensorMap tmB, tmB2;  // its B operand: boxes; ragged slabs (gradient)
   CUtensorMap tmC;        // valid when p.g.c_tma
   GroupParams p;
   bool pair, gated;
@@ -37,7 +37,7 @@ cudaError_t launch_group_variant(const GroupLaunch& L) {
     if (e != cudaSuccess) return e;
     if (L.dev < 64) __atomic_store_n(&configured[L.dev], 1, __ATOMIC_RELEASE);
   }
-  return launch_dependent(kern, L.grid, Cf::THREADS, Cf::SMEM_BYTES, L.stream, Cf::CTAS, L.tmA, L.tmAg, L.tmB, L.tmBg,
+  return launch_dependent(kern, L.grid, kGroupThreads, Cf::SMEM_BYTES, L.stream, Cf::CTAS, L.tmA, L.tmA2, L.tmB, L.tmB2,
                           L.tmC, L.p);
 }
 

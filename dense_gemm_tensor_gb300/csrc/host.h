@@ -26,11 +26,12 @@ int begin_call(CallContext* out);
 // Device (or managed) memory of the current device `dev`?
 bool on_device(const void* ptr, int dev);
 
-// Tiled tensor maps with x innermost; box box_inner x box_outer (x 1). 3-D: z
-// matrices mat_bytes apart. 2-D: rows only (the form row gathers take).
+// Tiled tensor maps with x innermost; box box_inner x box_outer. 3-D: z
+// matrices mat_bytes apart, box_depth of them to a box. 2-D: rows only (the
+// form row gathers take).
 bool encode_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint64_t depth, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_outer,
-                   CUtensorMapSwizzle swizzle);
+                   CUtensorMapSwizzle swizzle, uint32_t box_depth = 1);
 bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 

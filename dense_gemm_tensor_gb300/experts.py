@@ -97,7 +97,8 @@ def _load():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i
     for name, args in (("gemm_rmsnorm_backward_workspace", [i64, i64]), ("gemm_route_workspace", [i64, i, i]),
-                       ("gemm_grouped_workspace", [i, i, i64, i64]), ("gemm_grouped_wgrad_workspace", [i64, i64])):
+                       ("gemm_grouped_workspace", [i, i, i64, i64]),
+                       ("gemm_grouped_wgrad_workspace", [i, i64, i64, i64, i])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i64
     _lib = lib
@@ -381,7 +382,7 @@ def expert_weight_grad(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor,
     if out is not None and (out.dtype != A.dtype or tuple(out.shape) != shape):
         raise ValueError(f"out must be {shape[0]} x {shape[1]} x {shape[2]} of A's dtype")
     lib = _load()
-    need = lib.gemm_grouped_wgrad_workspace(slots, K) if rows is not None else 0
+    need = lib.gemm_grouped_wgrad_workspace(experts, slots, N, K, int(rows is not None))
     s = gemm._raw_stream(stream, A.device.index)
     with _on(stream):
         if out is None:

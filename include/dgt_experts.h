@@ -197,10 +197,11 @@ int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t
  * in fp32, rounded once to the operands' type; a group without slots gets
  * zeros. dC: slots x N. A, rows and dC as above (16-byte rows and bases); dW
  * may have any alignment that keeps its elements aligned, stride_dw at least
- * one matrix's extent. workspace: as above, of gemm_grouped_wgrad_workspace
- * bytes.
+ * one matrix's extent. workspace: gemm_grouped_wgrad_workspace bytes (`gathered`:
+ * `rows` is given), 128-byte aligned, for the groups' last, partly filled slabs
+ * and, with `rows`, A's rows in slot order.
  */
-int64_t gemm_grouped_wgrad_workspace(int64_t slots, int64_t K);
+int64_t gemm_grouped_wgrad_workspace(int groups, int64_t slots, int64_t N, int64_t K, int gathered);
 int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                            int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC, int64_t lddc,
                            uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,

@@ -37,7 +37,10 @@ def test_workspace_sizes(lib):
     assert lib.gemm_grouped_workspace(1, 4, 511, 64) == 0          # few rows a group: gathered on the way
     assert lib.gemm_grouped_workspace(1, 4, 512, 65) == 512 * 256  # rows of 130 bytes, 128-byte pitch
     assert lib.gemm_grouped_workspace(3, 4, 512, 65) == 512 * 128
-    assert lib.gemm_grouped_wgrad_workspace(3, 64) == 3 * 128 and lib.gemm_grouped_wgrad_workspace(0, 64) == 0
+    # a slab of 64 rows of dC and of A for each group, and the rows of A in slot order
+    assert lib.gemm_grouped_wgrad_workspace(2, 3, 65, 64, 0) == 2 * 64 * (256 + 128)
+    assert lib.gemm_grouped_wgrad_workspace(2, 3, 65, 64, 1) == 2 * 64 * (256 + 128) + 3 * 128
+    assert lib.gemm_grouped_wgrad_workspace(2, 0, 65, 64, 1) == 0
     assert lib.gemm_rmsnorm_backward_workspace(0, 64) == 0
     assert lib.gemm_rmsnorm_backward_workspace(3, 64) == 3 * 64 * 4
     assert lib.gemm_rmsnorm_backward_workspace(10 ** 6, 64) == 304 * 64 * 4
@@ -146,11 +149,12 @@ def test_grouped_arguments(lib, kw, code):
     (dict(dC=None), INVALID), (dict(dW=None), INVALID), (dict(a_rows=3), INVALID), (dict(lddc=0), INVALID),
     (dict(lddw=7), INVALID), (dict(sdw=56), INVALID), (dict(dW=2 * P), INVALID), (dict(lda=12), MISALIGNED),
     (dict(dC=3 * P + 8), MISALIGNED), (dict(dW=4 * P + 1), MISALIGNED), (dict(N=0), gemm.GEMM_OK),
-    (dict(rows=5 * P, ws=6 * P, bytes=4 * 128 - 1), INVALID),
+    (dict(ws=None), INVALID), (dict(bytes=2 * 64 * 256 - 1), INVALID), (dict(rows=5 * P), INVALID),
+    (dict(ws=4 * P, bytes=2 * 64 * 256), INVALID), (dict(ws=7 * P + 64), MISALIGNED),
 ])
 def test_weight_grad_arguments(lib, kw, code):
     a = dict(groups=2, off=P, slots=4, N=8, K=8, A=2 * P, a_rows=4, lda=8, rows=None, dC=3 * P, lddc=8, dW=4 * P,
-             lddw=8, sdw=64, layout=1, ws=None, bytes=0) | kw
+             lddw=8, sdw=64, layout=1, ws=7 * P, bytes=2 * 64 * 256) | kw
     assert lib.gemm_bf16_grouped_wgrad(*a.values(), None) == code
 
 
