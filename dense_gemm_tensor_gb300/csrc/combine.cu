@@ -8,7 +8,10 @@
 // whole rows, so the gather costs no extra bytes. `tpt` threads take a token,
 // 16 bytes of its columns each (single elements where base, pitch or width
 // do not allow); up to eight rows' loads are in flight per thread before the
-// first is added, and they are added in the order of j.
+// first is added, and they are added in the order of j. The blocks stay on
+// their SMs and walk the tokens: a token's slots are loaded while the rows of
+// the one before are on their way, so that one memory latency, not two, stands
+// between a block and its rows.
 #include "elem.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -28,51 +31,81 @@ struct CombineParams {
   void* y;
   long long ldz, ldr, ldy;
   int tokens, cols, k, nslots;
-  int tpt, chunks;  // threads per token, column chunks (blocks) per group of tokens
+  int tpt, chunks;      // threads per token, column chunks per group of tokens
+  long long work;       // groups of tokens x chunks
+};
+
+// Slots j0 .. j0 + kFlight - 1 of a token (-1: none) and their weights.
+struct Picks {
+  int s[kFlight];
+  float w[kFlight];
+
+  __device__ __forceinline__ void load(const int32_t* slots, const float* weights, long long token, int k, int j0,
+                                       int nslots, bool in) {
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      s[j] = -1;
+      w[j] = 0.0f;
+      if (in && j0 + j < k) {
+        const long long at = token * k + j0 + j;
+        s[j] = slots[at];
+        if (static_cast<uint32_t>(s[j]) >= static_cast<uint32_t>(nslots)) s[j] = -1;
+        w[j] = weights != nullptr ? weights[at] : 1.0f;
+      }
+    }
+  }
 };
 
 template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(kThreads, 3) combine_kernel(const CombineParams p) {
   using P = Pack<TYPE, VEC>;
   using T = typename P::T;
   grid_dependency_wait();
-  const int group = blockIdx.x / p.chunks, chunk = blockIdx.x - group * p.chunks;
-  const int per_block = kThreads / p.tpt;
-  const int token = group * per_block + threadIdx.x / p.tpt;
-  const int col = (chunk * p.tpt + threadIdx.x % p.tpt) * VEC;
-  if (token >= p.tokens || col >= p.cols) return;
-  const long long at = static_cast<long long>(token) * p.k;
+  const int per_block = kThreads / p.tpt, sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const T* z = static_cast<const T*>(p.z);
-  float acc[VEC];
+  long long u = blockIdx.x;
+  long long token = u / p.chunks * per_block + sub;
+  Picks now;
+  now.load(p.slots, p.weights, token, p.k, 0, p.nslots, u < p.work && token < p.tokens);
+  for (; u < p.work; u += gridDim.x) {
+    const long long next = (u + gridDim.x) / p.chunks * per_block + sub;
+    const int col = (int(u % p.chunks) * p.tpt + tid) * VEC;
+    const bool in = token < p.tokens && col < p.cols;
+    float acc[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-  P res;
-  res.zero();
-  if (p.residual != nullptr) res.load(static_cast<const T*>(p.residual) + token * p.ldr + col);
-  for (int j0 = 0; j0 < p.k; j0 += kFlight) {
-    P row[kFlight];
-    float w[kFlight];
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    P res;
+    res.zero();
+    if (p.residual != nullptr && in) res.stream(static_cast<const T*>(p.residual) + token * p.ldr + col);
+    Picks ahead;
+    for (int j0 = 0; j0 < p.k; j0 += kFlight) {
+      P row[kFlight];
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
-      row[j].zero();
-      w[j] = 0.0f;
-      if (j0 + j < p.k) {
-        const int s = p.slots[at + j0 + j];
-        w[j] = p.weights != nullptr ? p.weights[at + j0 + j] : 1.0f;
-        if (static_cast<uint32_t>(s) < static_cast<uint32_t>(p.nslots)) row[j].load(z + s * p.ldz + col);
+      for (int j = 0; j < kFlight; ++j) {
+        row[j].zero();
+        if (in && now.s[j] >= 0) row[j].stream(z + now.s[j] * p.ldz + col);
       }
+      // the next slots: this token's, or the next one's
+      const bool last = j0 + kFlight >= p.k;
+      ahead.load(p.slots, p.weights, last ? next : token, p.k, last ? 0 : j0 + kFlight, p.nslots,
+                 last ? u + gridDim.x < p.work && next < p.tokens : token < p.tokens);
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j)
+        if (j0 + j < p.k) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = fmaf(now.w[j], row[j].get(i), acc[i]);
+        }
+      now = ahead;
     }
+    if (in) {
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j)
-      if (j0 + j < p.k) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] += w[j] * row[j].get(i);
-      }
+      for (int i = 0; i < VEC; ++i) acc[i] += res.get(i);
+      P out;
+      out.set(acc);
+      out.store(static_cast<T*>(p.y) + token * p.ldy + col);
+    }
+    token = next;
   }
-  P out;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) out.put(i, acc[i] + res.get(i));
-  out.store(static_cast<T*>(p.y) + token * p.ldy + col);
   grid_launch_dependents();
 }
 
@@ -92,83 +125,86 @@ struct CombineGradParams {
 // One group of tpt threads walks a token's columns, kFlight rows at a time:
 // dy stays in L1 between the passes of a token with more rows.
 template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const CombineGradParams p) {
+__global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const CombineGradParams p) {
   using P = Pack<TYPE, VEC>;
   using T = typename P::T;
-  __shared__ float part[kThreads / 32][kFlight];
+  __shared__ float part[2][kThreads / 32][kFlight];
   grid_dependency_wait();
-  const int tid = threadIdx.x % p.tpt, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt, lane = threadIdx.x & 31;
   const int per_block = kThreads / p.tpt;
-  const int token = blockIdx.x * per_block + threadIdx.x / p.tpt;
-  const bool in = token < p.tokens;
-  const long long at = static_cast<long long>(token) * p.k;
   const T* z = static_cast<const T*>(p.z);
   T* dz = static_cast<T*>(p.dz);
-  for (int j0 = 0; j0 < p.k; j0 += kFlight) {
-    int s[kFlight];
-    float w[kFlight], dot[kFlight];
+  const long long step = static_cast<long long>(gridDim.x) * per_block;
+  long long token = static_cast<long long>(blockIdx.x) * per_block + sub;
+  int turn = 0;
+  Picks now;
+  now.load(p.slots, p.weights, token, p.k, 0, p.nslots, token < p.tokens);
+  for (long long first = static_cast<long long>(blockIdx.x) * per_block; first < p.tokens; first += step, token += step) {
+    const bool in = token < p.tokens;
+    for (int j0 = 0; j0 < p.k; j0 += kFlight, turn ^= 1) {
+      float dot[kFlight];
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
-      s[j] = -1;
-      w[j] = 0.0f;
-      dot[j] = 0.0f;
-      if (in && j0 + j < p.k) {
-        s[j] = p.slots[at + j0 + j];
-        if (static_cast<uint32_t>(s[j]) >= static_cast<uint32_t>(p.nslots)) s[j] = -1;
-        w[j] = p.weights != nullptr ? p.weights[at + j0 + j] : 1.0f;
-      }
-    }
-    if (in) {
-      for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
-        P d;
-        d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
-        P row[kFlight];
-        if (p.dweights != nullptr) {
+      for (int j = 0; j < kFlight; ++j) dot[j] = 0.0f;
+      const bool last = j0 + kFlight >= p.k;
+      Picks ahead;
+      ahead.load(p.slots, p.weights, last ? token + step : token, p.k, last ? 0 : j0 + kFlight, p.nslots,
+                 last ? token + step < p.tokens : in);
+      if (in) {
+        for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
+          P d;
+          d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
+          P row[kFlight];
+          if (p.dweights != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kFlight; ++j) {
-            row[j].zero();
-            if (s[j] >= 0) row[j].load(z + s[j] * p.ldz + col);
+            for (int j = 0; j < kFlight; ++j) {
+              row[j].zero();
+              if (now.s[j] >= 0) row[j].stream(z + now.s[j] * p.ldz + col);
+            }
           }
-        }
-#pragma unroll
-        for (int j = 0; j < kFlight; ++j)
-          if (s[j] >= 0) {
-            P o;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o.put(i, w[j] * d.get(i));
-            o.store(dz + s[j] * p.lddz + col);
-          }
-        if (p.dweights != nullptr) {
 #pragma unroll
           for (int j = 0; j < kFlight; ++j)
-            if (s[j] >= 0) {
+            if (now.s[j] >= 0) {
+              float o[VEC];
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) dot[j] += d.get(i) * row[j].get(i);
+              for (int i = 0; i < VEC; ++i) o[i] = now.w[j] * d.get(i);
+              P out;
+              out.set(o);
+              out.store(dz + now.s[j] * p.lddz + col);
             }
+          if (p.dweights != nullptr) {
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j)
+              if (now.s[j] >= 0) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) dot[j] = fmaf(d.get(i), row[j].get(i), dot[j]);
+              }
+          }
         }
       }
-    }
-    if (p.dweights != nullptr) {
-#pragma unroll
-      for (int j = 0; j < kFlight; ++j)
-        for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
-      if (p.tpt > 32) {
-        __syncthreads();  // the last pass has read part
-        if (lane == 0) {
-#pragma unroll
-          for (int j = 0; j < kFlight; ++j) part[threadIdx.x >> 5][j] = dot[j];
-        }
-        __syncthreads();
-        if (tid < kFlight) {
-          float sum = 0.0f;
-          for (int i = 0; i < p.tpt >> 5; ++i) sum += part[(threadIdx.x >> 5) + i][tid];
-          if (in && j0 + tid < p.k) p.dweights[at + j0 + tid] = sum;
-        }
-      } else if (in && tid == 0) {
+      if (p.dweights != nullptr) {
 #pragma unroll
         for (int j = 0; j < kFlight; ++j)
-          if (j0 + j < p.k) p.dweights[at + j0 + j] = dot[j];
+          for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1)
+            dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+        if (p.tpt > 32) {
+          // (the two halves of `part` alternate: one barrier a pass is enough)
+          if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
+          }
+          __syncthreads();
+          if (tid < kFlight) {
+            float sum = 0.0f;
+            for (int i = 0; i < p.tpt >> 5; ++i) sum += part[turn][(threadIdx.x >> 5) + i][tid];
+            if (in && j0 + tid < p.k) p.dweights[token * p.k + j0 + tid] = sum;
+          }
+        } else if (in && tid == 0) {
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j)
+            if (j0 + j < p.k) p.dweights[token * p.k + j0 + j] = dot[j];
+        }
       }
+      now = ahead;
     }
   }
   // rows of dz that no pair owns
@@ -240,11 +276,11 @@ int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, i
                    (residual == nullptr || wide(residual, ldr, es));
   const int64_t nvec = vec ? cols / v : cols;
   CombineParams p = {z, slots, weights, residual, y, (long long)ldz, (long long)ldr, (long long)ldy, int(tokens),
-                     int(cols), k, int(nslots), threads_per_token(nvec), 1};
+                     int(cols), k, int(nslots), threads_per_token(nvec), 1, 0};
   p.chunks = int((nvec + p.tpt - 1) / p.tpt);
-  const int64_t groups = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt);
-  if (groups * p.chunks > kInt) return GEMM_ERR_INVALID_VALUE;
-  const int grid = int(groups * p.chunks);
+  p.work = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt) * p.chunks;
+  const int64_t most = int64_t(ctx.sm_count) * 3;  // resident at once
+  const int grid = int(p.work < most ? p.work : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == GEMM_TYPE_F16)
@@ -290,7 +326,8 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
   CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,
                          int(tokens), int(cols), k, int(nslots), threads_per_token(nvec)};
   const int64_t need = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt);
-  const int grid = int(need > 0 ? need : ctx.sm_count);
+  const int64_t most = int64_t(ctx.sm_count) * 3;  // resident at once
+  const int grid = int(need > 0 && need < most ? need : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == GEMM_TYPE_F16)

@@ -48,6 +48,19 @@ struct Pack {
     else
       *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
   }
+  // a load of data that is read once: it leaves L1 to what is read again
+  __device__ __forceinline__ void stream(const T* p) {
+    if constexpr (VEC == 1) {
+      v[0] = *p;
+    } else {
+      uint4 q;
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                   : "l"(p)
+                   : "memory");
+      *reinterpret_cast<uint4*>(v) = q;
+    }
+  }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (VEC == 1)
       *p = v[0];
@@ -55,11 +68,35 @@ struct Pack {
       *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
   }
   __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = E::put(0.0f);
+    if constexpr (VEC == 1)
+      v[0] = E::put(0.0f);
+    else
+      *reinterpret_cast<uint4*>(v) = make_uint4(0u, 0u, 0u, 0u);
   }
-  __device__ __forceinline__ float get(int i) const { return E::get(v[i]); }
-  __device__ __forceinline__ void put(int i, float x) { v[i] = E::put(x); }
+  // Element i as fp32 (bfloat16 is the upper half of an fp32: a shift or a mask of its word).
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (TYPE == GEMM_TYPE_BF16 && VEC > 1) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i >> 1];
+      return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+    } else {
+      return E::get(v[i]);
+    }
+  }
+  // All elements from fp32, rounded to nearest even, two at a time.
+  __device__ __forceinline__ void set(const float (&x)[VEC]) {
+    if constexpr (VEC == 1 || TYPE == GEMM_TYPE_F32) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = E::put(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) {
+        if constexpr (TYPE == GEMM_TYPE_BF16)
+          *reinterpret_cast<__nv_bfloat162*>(v + i) = __floats2bfloat162_rn(x[i], x[i + 1]);
+        else
+          *reinterpret_cast<__half2*>(v + i) = __floats2half2_rn(x[i], x[i + 1]);
+      }
+    }
+  }
 };
 
 // VEC values to E4M3 (round to nearest even, saturating; NaN stays NaN).

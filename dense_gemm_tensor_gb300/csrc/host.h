@@ -58,8 +58,9 @@ cudaError_t launch_dependent(void (*kern)(P...), int grid, int block, size_t sme
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  const cudaError_t launched = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+  const cudaError_t last = cudaGetLastError();  // also clears a refused launch's error for the next call
+  const cudaError_t e = launched != cudaSuccess ? launched : last;
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

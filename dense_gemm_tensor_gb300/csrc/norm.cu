@@ -5,11 +5,20 @@
 //   dx = r (g - xhat mean(g xhat)) + dh,  g = dy w, xhat = h r;  dw = sum over rows of dy xhat
 //
 // Both are bound by HBM: each matrix is read or written once. A row stays in
-// the registers of the `tpr` threads that own it (EPT elements each at most)
-// between the reductions and the output, so nothing is read twice; a thread
-// owns the same columns of every row it meets, so the weights are loaded once
-// and dw accumulates in registers. 16-byte accesses where base, pitch and
-// width allow, single elements otherwise.
+// the registers of the `tpr` threads that own it (at most 64 bytes each)
+// between the reductions and the output, so nothing is read twice. While a row
+// is reduced and stored its threads load nothing, so several blocks share an SM:
+// 64 registers a thread let 1024 threads keep two matrices' loads in flight.
+//
+// Three ways to reach memory:
+//   ALIGNED  rows start on 16-byte boundaries and hold whole 16-byte pieces
+//   FLAT     every matrix is contiguous, from a 16-byte boundary, with rows of
+//            any width: a row is the 16-byte pieces of the flat array that meet
+//            it, and its first and last ones are partly other rows' (those two
+//            go element by element). Weights, and the gradient's dw, are then at
+//            another offset in every row: they sit in shared memory, element c
+//            at (c mod VEC, c / VEC), where the lanes' accesses do not collide.
+//   SINGLE   anything else: one element at a time
 #include "elem.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -17,9 +26,110 @@
 namespace dgt {
 namespace {
 
-constexpr int kMaxThreads = 512;       // of a block whose threads hold more than 8 elements of a row
-constexpr int64_t kMaxCols = 16384;    // 32 elements for each of them
+enum { ALIGNED = 0, FLAT = 1, SINGLE = 2 };
+
+constexpr int64_t kMaxCols = 16384;
+constexpr int64_t kMaxFlatCols = 11000;  // a FLAT row meets one piece more, and its weights (and dw) fit shared memory
 constexpr float kE4M3Max = 448.0f;
+
+// Elements a thread holds of a row: 8 (few rows, for their latency), or 64 bytes' worth; single elements take a
+// register each, so 16 of them.
+template <int TYPE, int MODE>
+constexpr int kFullEpt = MODE == SINGLE ? 16 : 64 / int(sizeof(typename Elem<TYPE>::T));
+// Threads of a block: 16384 columns' worth.
+template <int TYPE, int EPT>
+constexpr int kNormThreads = EPT == 8 ? 1024 : int(kMaxCols) / EPT;
+
+// A row as the thread's pieces: piece i holds columns lo(i) .. lo(i) + VEC - 1.
+template <int MODE, int VEC>
+struct Row {
+  int tid, tpr, cols, shift;
+
+  __device__ __forceinline__ Row(int tid_, int tpr_, int cols_) : tid(tid_), tpr(tpr_), cols(cols_), shift(0) {}
+  // FLAT: the row's first piece starts `shift` elements before it
+  __device__ __forceinline__ void at(long long row) {
+    if constexpr (MODE == FLAT) shift = static_cast<int>((row * cols) % VEC);
+  }
+  __device__ __forceinline__ int lo(int i) const { return (i * tpr + tid) * VEC - shift; }
+  __device__ __forceinline__ bool whole(int i) const {
+    return MODE == FLAT ? lo(i) >= 0 && lo(i) + VEC <= cols : lo(i) < cols;
+  }
+  // index of column lo(i) + j in shared memory
+  __device__ __forceinline__ int place(int i, int j) const {
+    const int c = lo(i) + j;
+    return (c % VEC) * ((cols + VEC - 1) / VEC) + c / VEC;
+  }
+  template <int TYPE>
+  __device__ __forceinline__ void load(Pack<TYPE, VEC>& v, const void* base, long long row, long long ld, int i,
+                                       bool in) const {
+    using T = typename Pack<TYPE, VEC>::T;
+    v.zero();
+    if (!in) return;
+    const T* p = static_cast<const T*>(base) + row * ld;
+    if (whole(i)) {
+      v.stream(p + lo(i));
+    } else if constexpr (MODE == FLAT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (lo(i) + j >= 0 && lo(i) + j < cols) v.v[j] = p[lo(i) + j];
+    }
+  }
+  template <int TYPE>
+  __device__ __forceinline__ void store(const Pack<TYPE, VEC>& v, void* base, long long row, long long ld, int i,
+                                        bool in) const {
+    using T = typename Pack<TYPE, VEC>::T;
+    if (!in) return;
+    T* p = static_cast<T*>(base) + row * ld;
+    if (whole(i)) {
+      v.store(p + lo(i));
+    } else if constexpr (MODE == FLAT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (lo(i) + j >= 0 && lo(i) + j < cols) p[lo(i) + j] = v.v[j];
+    }
+  }
+  __device__ __forceinline__ void store_q8(const float (&x)[VEC], void* base, long long row, long long ld, int i,
+                                           bool in) const {
+    if (!in) return;
+    uint8_t* p = static_cast<uint8_t*>(base) + row * ld;
+    if (whole(i)) {
+      store_e4m3<VEC>(p + lo(i), x);
+    } else if constexpr (MODE == FLAT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (lo(i) + j >= 0 && lo(i) + j < cols) p[lo(i) + j] = __nv_cvt_float_to_fp8(x[j], __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+};
+
+// Column weights of piece i as fp32: from memory (L1 holds them), or from shared memory (FLAT).
+template <int MODE, int TYPE, int VEC>
+__device__ __forceinline__ void load_weights(float (&w)[VEC], const Row<MODE, VEC>& r, const void* weight,
+                                             const typename Elem<TYPE>::T* shared, int i) {
+  using E = Elem<TYPE>;
+  if constexpr (MODE == FLAT) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = r.lo(i) + j;
+      w[j] = c >= 0 && c < r.cols ? E::get(shared[r.place(i, j)]) : 0.0f;
+    }
+  } else {
+    Pack<TYPE, VEC> v;
+    v.zero();
+    if (r.whole(i)) v.load(static_cast<const typename E::T*>(weight) + r.lo(i));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = v.get(j);
+  }
+}
+
+// FLAT: the weights in shared memory, in place()'s order.
+template <int TYPE, int VEC>
+__device__ __forceinline__ void stage_weights(typename Elem<TYPE>::T* shared, const void* weight, int cols) {
+  const int per = (cols + VEC - 1) / VEC;
+  for (int c = threadIdx.x; c < cols; c += blockDim.x)
+    shared[(c % VEC) * per + c / VEC] = static_cast<const typename Elem<TYPE>::T*>(weight)[c];
+  __syncthreads();
+}
 
 struct NormParams {
   const void* x;
@@ -34,47 +144,40 @@ struct NormParams {
   float eps;
 };
 
-template <int TYPE, int VEC, int EPT, bool Q8>
-__global__ void __launch_bounds__(EPT == 8 ? 1024 : kMaxThreads) rmsnorm_kernel(const NormParams p) {
+template <int TYPE, int MODE, int EPT, bool Q8>
+__global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EPT> == 512 ? 2 : 1)
+    rmsnorm_kernel(const NormParams p) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = MODE == SINGLE ? 1 : 16 / sizeof(T);
   using P = Pack<TYPE, VEC>;
-  using T = typename P::T;
   constexpr int NV = EPT / VEC;
   __shared__ float red[2][2][32];
-  const int tid = threadIdx.x % p.tpr;
-  const int per_block = blockDim.x / p.tpr;
-  const int nvec = p.cols / VEC;
+  extern __shared__ uint4 dynamic[];
+  T* shared_w = reinterpret_cast<T*>(dynamic);
+  const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
+  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
   grid_dependency_wait();
-  P w[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    w[i].zero();
-    if (i * p.tpr + tid < nvec) w[i].load(static_cast<const T*>(p.weight) + (i * p.tpr + tid) * VEC);
-  }
+  if constexpr (MODE == FLAT) stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
   int turn = 0;
   for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows;
        r0 += static_cast<long long>(gridDim.x) * per_block, turn ^= 1) {
-    const long long row = r0 + threadIdx.x / p.tpr;
+    const long long row = r0 + sub;
     const bool in = row < p.rows;
+    r.at(row);
     P h[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      h[i].zero();
-      if (in && i * p.tpr + tid < nvec) h[i].load(static_cast<const T*>(p.x) + row * p.ldx + (i * p.tpr + tid) * VEC);
-    }
+    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in);
     if (p.residual != nullptr) {
       P a[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        a[i].zero();
-        if (in && i * p.tpr + tid < nvec)
-          a[i].load(static_cast<const T*>(p.residual) + row * p.ldr + (i * p.tpr + tid) * VEC);
-      }
+      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        float x[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i].put(j, h[i].get(j) + a[i].get(j));
-        if (p.h != nullptr && in && i * p.tpr + tid < nvec)
-          h[i].store(static_cast<T*>(p.h) + row * p.ldh + (i * p.tpr + tid) * VEC);
+        for (int j = 0; j < VEC; ++j) x[j] = h[i].get(j) + a[i].get(j);
+        h[i].set(x);
+        if (p.h != nullptr) r.store(h[i], p.h, row, p.ldh, i, in);
       }
     }
     float ss = 0.0f;
@@ -84,38 +187,49 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : kMaxThreads) rmsnorm_kernel(
       for (int j = 0; j < VEC; ++j) ss += h[i].get(j) * h[i].get(j);
     ss = row_sum(ss, p.tpr, red[turn][0]);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
-    if (p.rstd != nullptr && in && tid == 0) p.rstd[row] = rstd;
+    if (p.rstd != nullptr && in && r.tid == 0) p.rstd[row] = rstd;
     if constexpr (!Q8) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        float w[VEC];
+        load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
         P o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o.put(j, h[i].get(j) * rstd * w[i].get(j));
-        if (in && i * p.tpr + tid < nvec) o.store(static_cast<T*>(p.y) + row * p.ldy + (i * p.tpr + tid) * VEC);
+        for (int j = 0; j < VEC; ++j) w[j] = h[i].get(j) * rstd * w[j];
+        o.set(w);
+        r.store(o, p.y, row, p.ldy, i, in);
       }
     } else {
       // |y| compared by bit pattern: a NaN is above every number and reaches the scale
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        float w[VEC];
+        load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          top = max(top, __float_as_uint(h[i].get(j) * rstd * w[i].get(j)) & 0x7FFFFFFFu);
+        for (int j = 0; j < VEC; ++j) top = max(top, __float_as_uint(h[i].get(j) * rstd * w[j]) & 0x7FFFFFFFu);
+      }
       const float amax = __uint_as_float(row_max_bits(top, p.tpr, reinterpret_cast<uint32_t*>(red[turn][1])));
       const float scale = (amax < 1e-12f ? 1e-12f : amax) / kE4M3Max;
       const float inv = 1.0f / scale;
-      if (in && tid == 0) p.scale[row] = scale;
+      if (in && r.tid == 0) p.scale[row] = scale;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float o[VEC];
+        float w[VEC];
+        load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = h[i].get(j) * rstd * w[i].get(j) * inv;
-        if (in && i * p.tpr + tid < nvec)
-          store_e4m3<VEC>(static_cast<uint8_t*>(p.y) + row * p.ldy + (i * p.tpr + tid) * VEC, o);
+        for (int j = 0; j < VEC; ++j) w[j] = h[i].get(j) * rstd * w[j] * inv;
+        r.store_q8(w, p.y, row, p.ldy, i, in);
       }
     }
   }
   grid_launch_dependents();
+}
+
+constexpr int kGradEpt = 16;  // elements of a row per thread of the gradient
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 struct NormGradParams {
@@ -130,136 +244,217 @@ struct NormGradParams {
   int rows, cols, tpr;
 };
 
-template <int TYPE, int VEC, int EPT>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_grad_kernel(const NormGradParams p) {
+// A thread owns the same columns of every row (ALIGNED, SINGLE) and adds dw up
+// in registers; FLAT rows move against the threads, and dw is in shared memory,
+// where a column meets one thread a row and the rows' reductions separate them.
+// ALIGNED with AHEAD: each thread copies its pieces of the next row to its own
+// places in shared memory (cp.async) before it works on this one, so that loads
+// are in flight during the reduction and the stores, and nothing but the thread
+// itself waits for them. (Without: 8192 x 4096 BF16 took 60-73 us.)
+template <int TYPE, int MODE, bool AHEAD>
+__global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kernel(const NormGradParams p) {
+  constexpr int EPT = kGradEpt;
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = MODE == SINGLE ? 1 : 16 / sizeof(T);
   using P = Pack<TYPE, VEC>;
-  using T = typename P::T;
   constexpr int NV = EPT / VEC;
   __shared__ float red[2][32];
-  extern __shared__ float sums[];  // (rows of the block - 1) x cols
-  const int tid = threadIdx.x % p.tpr, sub = threadIdx.x / p.tpr;
-  const int per_block = blockDim.x / p.tpr;
-  const int nvec = p.cols / VEC;
+  extern __shared__ uint4 dynamic[];
+  // ALIGNED, SINGLE: (rows of the block - 1) x cols partial sums; FLAT: dw of each row of the block, then the weights
+  float* sums = reinterpret_cast<float*>(dynamic);
+  const int places = (p.cols + VEC - 1) / VEC * VEC;
+  const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
+  T* shared_w = reinterpret_cast<T*>(sums + per_block * places);
+  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const int streams = p.dh != nullptr ? 3 : 2;
+  const long long step = static_cast<long long>(gridDim.x) * per_block;
+  // AHEAD: piece i of stream m of stage s
+  auto cell = [&](int s, int m, int i) { return dynamic + ((s * streams + m) * NV + i) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](long long row, int s) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (r.whole(i)) {
+          copy16(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i));
+          copy16(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i));
+          if (streams == 3) copy16(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i));
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   grid_dependency_wait();
-  P w[NV];
-  float dw[NV][VEC];
+  if constexpr (AHEAD) fetch(static_cast<long long>(blockIdx.x) * per_block + sub, 0);
+  float dw[MODE == FLAT ? 1 : NV][VEC];
+  if constexpr (MODE == FLAT) {
+    for (int i = threadIdx.x; i < per_block * places; i += blockDim.x) sums[i] = 0.0f;
+    stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    w[i].zero();
-    if (i * p.tpr + tid < nvec) w[i].load(static_cast<const T*>(p.weight) + (i * p.tpr + tid) * VEC);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
+      for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
   }
   int turn = 0;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows;
-       r0 += static_cast<long long>(gridDim.x) * per_block, turn ^= 1) {
+  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows; r0 += step, turn ^= 1) {
     const long long row = r0 + sub;
     const bool in = row < p.rows;
+    r.at(row);
     P h[NV], dy[NV], dh[NV];
+    if constexpr (AHEAD) {
+      fetch(row + step, turn ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row's pieces have landed
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      h[i].zero();
-      dy[i].zero();
-      dh[i].zero();
-      const int at = (i * p.tpr + tid) * VEC;
-      if (in && i * p.tpr + tid < nvec) {
-        h[i].load(static_cast<const T*>(p.h) + row * p.ldh + at);
-        dy[i].load(static_cast<const T*>(p.dy) + row * p.lddy + at);
-        if (p.dh != nullptr) dh[i].load(static_cast<const T*>(p.dh) + row * p.lddh + at);
+      for (int i = 0; i < NV; ++i) {
+        h[i].zero();
+        dy[i].zero();
+        dh[i].zero();
+        if (in && r.whole(i)) {
+          h[i].load(reinterpret_cast<const T*>(cell(turn, 0, i)));
+          dy[i].load(reinterpret_cast<const T*>(cell(turn, 1, i)));
+          if (streams == 3) dh[i].load(reinterpret_cast<const T*>(cell(turn, 2, i)));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        r.load(h[i], p.h, row, p.ldh, i, in);
+        r.load(dy[i], p.dy, row, p.lddy, i, in);
+      }
+      if (p.dh != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dh[i].zero();
       }
     }
+    // with the row's rstd taken out of the sums: mean(g xhat) = rstd * mean(g h), dw += (dy rstd) h,
+    // dx = rstd g - (rstd^3 mean(g h)) h + dh
     const float rstd = in ? p.rstd[row] : 0.0f;
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float w[VEC];
+      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float xhat = h[i].get(j) * rstd, d = dy[i].get(j);
-        dot += d * w[i].get(j) * xhat;
-        dw[i][j] += d * xhat;
-      }
-    const float mean = row_sum(dot, p.tpr, red[turn]) / static_cast<float>(p.cols);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      P o;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        o.put(j, rstd * (dy[i].get(j) * w[i].get(j) - h[i].get(j) * rstd * mean) + dh[i].get(j));
-      if (in && i * p.tpr + tid < nvec) o.store(static_cast<T*>(p.dx) + row * p.lddx + (i * p.tpr + tid) * VEC);
-    }
-  }
-  // the block's sum over its rows, in row order
-  if (per_block > 1) {
-    __syncthreads();
-    if (sub > 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (i * p.tpr + tid < nvec) sums[(sub - 1) * p.cols + (i * p.tpr + tid) * VEC + j] = dw[i][j];
-    }
-    __syncthreads();
-    if (sub == 0) {
-      for (int s = 0; s + 1 < per_block; ++s)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (i * p.tpr + tid < nvec) dw[i][j] += sums[s * p.cols + (i * p.tpr + tid) * VEC + j];
-    }
-  }
-  if (sub == 0) {
-    float* out = p.partial + static_cast<long long>(blockIdx.x) * p.cols;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * p.tpr + tid < nvec) {
-        if constexpr (VEC == 1) {
-          out[i * p.tpr + tid] = dw[i][0];
+        const float hv = h[i].get(j), d = dy[i].get(j);
+        dot = fmaf(d * w[j], hv, dot);
+        if constexpr (MODE == FLAT) {
+          const int c = r.lo(i) + j;
+          if (in && c >= 0 && c < p.cols) sums[sub * places + r.place(i, j)] += d * rstd * hv;
         } else {
-#pragma unroll
-          for (int j = 0; j < VEC; j += 4)
-            *reinterpret_cast<float4*>(out + (i * p.tpr + tid) * VEC + j) =
-                make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+          dw[i][j] = fmaf(d * rstd, hv, dw[i][j]);
         }
       }
+    }
+    const float back = rstd * rstd * rstd * (row_sum(dot, p.tpr, red[turn]) / static_cast<float>(p.cols));
+    if (MODE == FLAT && p.tpr <= 32) __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float w[VEC];
+      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      P o;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = fmaf(dy[i].get(j) * w[j], rstd, fmaf(h[i].get(j), -back, dh[i].get(j)));
+      o.set(w);
+      r.store(o, p.dx, row, p.lddx, i, in);
+    }
+  }
+  if constexpr (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float* out = p.partial + static_cast<long long>(blockIdx.x) * p.cols;
+  if constexpr (MODE == FLAT) {
+    __syncthreads();
+    const int per = places / VEC;
+    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+      float s = 0.0f;
+      for (int i = 0; i < per_block; ++i) s += sums[i * places + (c % VEC) * per + c / VEC];
+      out[c] = s;
+    }
+  } else {
+    // the block's sum over its rows, in row order
+    if (per_block > 1) {
+      __syncthreads();
+      if (sub > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (r.whole(i)) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sums[(sub - 1) * p.cols + r.lo(i) + j] = dw[i][j];
+          }
+      }
+      __syncthreads();
+      if (sub == 0) {
+        for (int s = 0; s + 1 < per_block; ++s)
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (r.whole(i)) {
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) dw[i][j] += sums[s * p.cols + r.lo(i) + j];
+            }
+      }
+    }
+    if (sub == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (r.whole(i)) {
+          if constexpr (VEC == 1) {
+            out[r.lo(i)] = dw[i][0];
+          } else {
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4)
+              *reinterpret_cast<float4*>(out + r.lo(i) + j) =
+                  make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+          }
+        }
+    }
   }
   grid_launch_dependents();
 }
 
-// dw[j] = sum of the blocks' partial rows: 32 columns a block, eight threads a
-// column, each a fixed eighth of the rows.
+// dw[j] = sum of the blocks' partial rows: 32 columns a block, 32 threads a
+// column, each a fixed share of the rows, added in order of the threads.
 template <int TYPE>
-__global__ void __launch_bounds__(256) norm_weight_sum_kernel(const float* partial, int rows, int cols, void* dw) {
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* partial, int rows, int cols, void* dw) {
   using E = Elem<TYPE>;
-  __shared__ float part[8][33];
+  __shared__ float part[32][33];
   grid_dependency_wait();
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
   float s = 0.0f;
   if (col < cols) {
 #pragma unroll 8
-    for (int r = g; r < rows; r += 8) s += __ldcg(partial + static_cast<long long>(r) * cols + col);
+    for (int r = g; r < rows; r += 32) s += __ldcg(partial + static_cast<long long>(r) * cols + col);
   }
   part[g][c] = s;
   __syncthreads();
-  if (g == 0 && col < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += part[i][c];
-    static_cast<typename E::T*>(dw)[col] = E::put(s);
-  }
+  // warp g adds up column g of the block
+  s = warp_sum(part[c][g]);
+  const int mine = blockIdx.x * 32 + g;
+  if (c == 0 && mine < cols) static_cast<typename E::T*>(dw)[mine] = E::put(s);
   grid_launch_dependents();
 }
 
-// Blocks of the gradient: each leaves one partial row of dw, so there are no
-// more than two for each of a GB300's 152 SMs.
-constexpr int kGradBlocks = 304;
+// Blocks of the gradient, at most: each leaves one partial row of dw, which
+// costs a write and a read, so wide rows have about three for each of a GB300's
+// 152 SMs (what fits them at 64 registers) and narrow ones, whose blocks are
+// small, more.
+int grad_blocks(int64_t cols) { return cols <= 2048 ? 608 : 456; }
 
 bool aligned(const void* p, int64_t ld, int es, int to) {
   return ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * es)) % to) == 0;
 }
 
-// Threads that own a row of `cols` elements, `ept` each: whole warps.
-int threads_per_row(int64_t cols, int ept) { return int((cols + 32 * ept - 1) / (32 * ept) * 32); }
+// Threads that own a row of `cols` elements, `ept` each: whole warps. A FLAT row may meet one piece more.
+int threads_per_row(int64_t cols, int ept, int mode, int vec) {
+  const int64_t most = cols + (mode == FLAT ? vec : 0);
+  return int((most + 32 * ept - 1) / (32 * ept) * 32);
+}
+
+// A contiguous matrix from a `to`-byte boundary.
+bool flat(const void* p, int64_t ld, int64_t cols, int to) {
+  return ld == cols && reinterpret_cast<uintptr_t>(p) % to == 0;
+}
 
 bool bad_type(int type) { return type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F32; }
 bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
@@ -272,29 +467,47 @@ bool meet(const void* a, int64_t rows_a, int64_t cols_a, int64_t ld_a, int es_a,
   return a0 < b1 && b0 < a1;
 }
 
-template <int TYPE, int VEC, int EPT>
-cudaError_t launch_norm_ept(const NormParams& p, bool q8, int grid, int block, cudaStream_t s) {
-  return q8 ? launch_dependent(rmsnorm_kernel<TYPE, VEC, EPT, true>, grid, block, 0, s, 1, p)
-            : launch_dependent(rmsnorm_kernel<TYPE, VEC, EPT, false>, grid, block, 0, s, 1, p);
+template <int TYPE, int MODE, int EPT>
+cudaError_t launch_norm_mode(const NormParams& p, bool q8, int grid, int block, size_t smem, cudaStream_t s) {
+  return q8 ? launch_dependent(rmsnorm_kernel<TYPE, MODE, EPT, true>, grid, block, smem, s, 1, p)
+            : launch_dependent(rmsnorm_kernel<TYPE, MODE, EPT, false>, grid, block, smem, s, 1, p);
 }
 
 template <int TYPE>
-cudaError_t launch_norm(const NormParams& p, bool vec, int ept, bool q8, int grid, int block, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(typename Elem<TYPE>::T);
-  if (vec) return ept == 8 ? launch_norm_ept<TYPE, V, 8>(p, q8, grid, block, s)
-                           : launch_norm_ept<TYPE, V, 32>(p, q8, grid, block, s);
-  return ept == 8 ? launch_norm_ept<TYPE, 1, 8>(p, q8, grid, block, s)
-                  : launch_norm_ept<TYPE, 1, 32>(p, q8, grid, block, s);
+cudaError_t launch_norm(const NormParams& p, int mode, bool few, bool q8, int grid, int block, cudaStream_t s) {
+  const size_t smem = mode == FLAT ? size_t(p.cols + 8) * sizeof(typename Elem<TYPE>::T) : 0;
+  if (mode == ALIGNED)
+    return few ? launch_norm_mode<TYPE, ALIGNED, 8>(p, q8, grid, block, smem, s)
+               : launch_norm_mode<TYPE, ALIGNED, kFullEpt<TYPE, ALIGNED>>(p, q8, grid, block, smem, s);
+  if (mode == FLAT)
+    return few ? launch_norm_mode<TYPE, FLAT, 8>(p, q8, grid, block, smem, s)
+               : launch_norm_mode<TYPE, FLAT, kFullEpt<TYPE, FLAT>>(p, q8, grid, block, smem, s);
+  return few ? launch_norm_mode<TYPE, SINGLE, 8>(p, q8, grid, block, smem, s)
+             : launch_norm_mode<TYPE, SINGLE, kFullEpt<TYPE, SINGLE>>(p, q8, grid, block, smem, s);
 }
 
-template <int TYPE, int EPT>
-cudaError_t launch_norm_grad(const NormGradParams& p, bool vec, int grid, int block, void* dw, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(typename Elem<TYPE>::T);
-  const size_t smem = size_t(block / p.tpr - 1) * size_t(p.cols) * sizeof(float);
-  cudaError_t e = vec ? launch_dependent(rmsnorm_grad_kernel<TYPE, V, EPT>, grid, block, smem, s, 1, p)
-                      : launch_dependent(rmsnorm_grad_kernel<TYPE, 1, EPT>, grid, block, smem, s, 1, p);
+// Dynamic shared memory of the gradient's kernel.
+size_t grad_smem(const NormGradParams& p, int mode, bool ahead, int block, int es) {
+  if (mode == FLAT) return size_t(p.cols + 8) * (size_t(block / p.tpr) * sizeof(float) + es);
+  const size_t sums = size_t(block / p.tpr - 1) * size_t(p.cols) * sizeof(float);
+  const size_t stages = ahead ? size_t(2) * (p.dh != nullptr ? 3 : 2) * kGradEpt * es * size_t(block) : 0;
+  return sums > stages ? sums : stages;
+}
+
+template <int TYPE>
+cudaError_t launch_norm_grad(const NormGradParams& p, int mode, bool ahead, int grid, int block, void* dw,
+                             cudaStream_t s) {
+  const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
+  auto kern = mode == ALIGNED ? (ahead ? rmsnorm_grad_kernel<TYPE, ALIGNED, true> : rmsnorm_grad_kernel<TYPE, ALIGNED, false>)
+              : mode == FLAT  ? rmsnorm_grad_kernel<TYPE, FLAT, false>
+                              : rmsnorm_grad_kernel<TYPE, SINGLE, false>;
+  if (smem > 40 * 1024) {  // past what a launch may take unasked (48 KB, less the static arrays)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = launch_dependent(kern, grid, block, smem, s, 1, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(norm_weight_sum_kernel<TYPE>, (p.cols + 31) / 32, 256, 0, s, 1, p.partial, grid, p.cols, dw);
+  return launch_dependent(norm_weight_sum_kernel<TYPE>, (p.cols + 31) / 32, 1024, 0, s, 1, p.partial, grid, p.cols, dw);
 }
 
 }  // namespace
@@ -340,29 +553,36 @@ int gemm_rmsnorm(int type, int64_t rows, int64_t cols, const void* x, int64_t ld
   for (const void* q : ptrs)
     if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
   const int v = 16 / es;
-  const bool vec = cols % v == 0 && aligned(x, ldx, es, 16) && aligned(weight, 0, es, 16) &&
-                   (residual == nullptr || aligned(residual, ldr, es, 16)) && (h == nullptr || aligned(h, ldh, es, 16)) &&
-                   aligned(y, ldy, eo, v * eo);
+  int mode = SINGLE;
+  if (cols % v == 0 && aligned(x, ldx, es, 16) && aligned(weight, 0, es, 16) &&
+      (residual == nullptr || aligned(residual, ldr, es, 16)) && (h == nullptr || aligned(h, ldh, es, 16)) &&
+      aligned(y, ldy, eo, v * eo))
+    mode = ALIGNED;
+  else if (cols <= kMaxFlatCols && flat(x, ldx, cols, 16) && (residual == nullptr || flat(residual, ldr, cols, 16)) &&
+           (h == nullptr || flat(h, ldh, cols, 16)) && flat(y, ldy, cols, v * eo))
+    mode = FLAT;
   NormParams p = {x,   residual, weight, h,   y,         y_scale,   rstd, (long long)ldx, (long long)ldr,
                   (long long)ldh, (long long)ldy, int(rows), int(cols), 0, eps};
   // Eight elements a thread while the rows leave threads to spare (a row's latency is then one load of each
-  // matrix and two reductions), 32 once they fill the GPU (more loads in flight for each reduction).
-  const int ept = cols <= 8192 && rows * cols <= int64_t(ctx.sm_count) * 8192 ? 8 : 32;
-  p.tpr = threads_per_row(cols, ept);
-  const int block = p.tpr < 128 ? 128 / p.tpr * p.tpr : p.tpr;
+  // matrix and two reductions), 64 bytes once they fill the GPU (more loads in flight for each reduction).
+  const bool few = cols <= 8000 && rows * cols <= int64_t(ctx.sm_count) * 8192;
+  p.tpr = threads_per_row(cols, few ? 8 : mode == SINGLE ? 16 : 64 / es, mode, v);
+  // FLAT blocks stage the weights, so they are few and take many rows
+  const int least = mode == FLAT && !few ? 512 : 128;
+  const int block = p.tpr < least ? least / p.tpr * p.tpr : p.tpr;
   const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
-  const int64_t most = int64_t(ctx.sm_count) * (2048 / block);
+  const int64_t most = int64_t(ctx.sm_count) * (mode == FLAT ? 1024 / block + 1 : 2048 / block);
   const int grid = int(need < most ? need : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_norm<GEMM_TYPE_F16>(p, vec, ept, q8, grid, block, s)
-                        : type == GEMM_TYPE_BF16 ? launch_norm<GEMM_TYPE_BF16>(p, vec, ept, q8, grid, block, s)
-                                                 : launch_norm<GEMM_TYPE_F32>(p, vec, ept, q8, grid, block, s);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_norm<GEMM_TYPE_F16>(p, mode, few, q8, grid, block, s)
+                        : type == GEMM_TYPE_BF16 ? launch_norm<GEMM_TYPE_BF16>(p, mode, few, q8, grid, block, s)
+                                                 : launch_norm<GEMM_TYPE_F32>(p, mode, few, q8, grid, block, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
 int64_t gemm_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || cols > kMaxCols) return 0;
-  return (rows < kGradBlocks ? rows : kGradBlocks) * cols * int64_t(sizeof(float));
+  return (rows < grad_blocks(cols) ? rows : grad_blocks(cols)) * cols * int64_t(sizeof(float));
 }
 
 int gemm_rmsnorm_backward(int type, int64_t rows, int64_t cols, const void* dy, int64_t lddy, const void* h,
@@ -402,25 +622,23 @@ int gemm_rmsnorm_backward(int type, int64_t rows, int64_t cols, const void* dy, 
   for (const void* q : ptrs)
     if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
   const int v = 16 / es;
-  const bool vec = cols % v == 0 && aligned(dy, lddy, es, 16) && aligned(h, ldh, es, 16) &&
-                   aligned(weight, 0, es, 16) && aligned(dx, lddx, es, 16) && (dh == nullptr || aligned(dh, lddh, es, 16));
+  int mode = SINGLE;
+  if (cols % v == 0 && aligned(dy, lddy, es, 16) && aligned(h, ldh, es, 16) && aligned(weight, 0, es, 16) &&
+      aligned(dx, lddx, es, 16) && (dh == nullptr || aligned(dh, lddh, es, 16)))
+    mode = ALIGNED;
+  else if (cols <= kMaxFlatCols && flat(dy, lddy, cols, 16) && flat(h, ldh, cols, 16) && flat(dx, lddx, cols, 16) &&
+           (dh == nullptr || flat(dh, lddh, cols, 16)))
+    mode = FLAT;
   NormGradParams p = {dy, h, weight, rstd, dh, dx, static_cast<float*>(workspace), (long long)lddy, (long long)ldh,
                       (long long)lddh, (long long)lddx, int(rows), int(cols), 0};
-  const int ept = cols <= kMaxThreads * 16 ? 16 : 32;
-  p.tpr = threads_per_row(cols, ept);
-  const int block = p.tpr < 256 ? 256 / p.tpr * p.tpr : p.tpr;
+  p.tpr = threads_per_row(cols, kGradEpt, mode, v);
+  const int block = p.tpr >= 256 ? p.tpr : 256 / p.tpr * p.tpr;
+  const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= 200 * 1024;
   const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
-  const int grid = int(need < kGradBlocks ? need : kGradBlocks);
-  cudaError_t e;
-  if (type == GEMM_TYPE_F16)
-    e = ept == 16 ? launch_norm_grad<GEMM_TYPE_F16, 16>(p, vec, grid, block, dw, s)
-                  : launch_norm_grad<GEMM_TYPE_F16, 32>(p, vec, grid, block, dw, s);
-  else if (type == GEMM_TYPE_BF16)
-    e = ept == 16 ? launch_norm_grad<GEMM_TYPE_BF16, 16>(p, vec, grid, block, dw, s)
-                  : launch_norm_grad<GEMM_TYPE_BF16, 32>(p, vec, grid, block, dw, s);
-  else
-    e = ept == 16 ? launch_norm_grad<GEMM_TYPE_F32, 16>(p, vec, grid, block, dw, s)
-                  : launch_norm_grad<GEMM_TYPE_F32, 32>(p, vec, grid, block, dw, s);
+  const int grid = int(need < grad_blocks(cols) ? need : grad_blocks(cols));
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_norm_grad<GEMM_TYPE_F16>(p, mode, ahead, grid, block, dw, s)
+                        : type == GEMM_TYPE_BF16 ? launch_norm_grad<GEMM_TYPE_BF16>(p, mode, ahead, grid, block, dw, s)
+                                                 : launch_norm_grad<GEMM_TYPE_F32>(p, mode, ahead, grid, block, dw, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

@@ -1,21 +1,22 @@
 // Routing to experts: scores, choice, weights and the expert order
 // (gemm_route), and the gradient of the weights (gemm_route_backward).
 //
-// A warp takes a token: lane l holds the scores of experts l, l + 32, ... and
-// picks the k largest keys one after another (a warp maximum of the lanes'
-// best, then the winner's owner looks up its next best). The softmax
-// denominator is summed by halves -- within a lane, then across lanes 16, 8,
-// 4, 2, 1 apart -- which with zeros past the last expert is the order of any
-// power-of-two length, so the same logits give the same keys in every build
+// A warp takes a token: lane l holds the scores of experts l, l + 32, ..., sorts
+// its keys (up to eight of them) and the warp takes the k largest one after
+// another: a warp maximum of the lanes' heads, whose owner moves its list up. The
+// softmax denominator is summed by halves -- within a lane, then across lanes
+// 16, 8, 4, 2, 1 apart -- which with zeros past the last expert is the order of
+// any power-of-two length, so the same logits give the same keys in every build
 // of the kernel.
 //
-// The expert order is a stable counting sort of the token-major pairs. A block
-// owns a run of tokens; its warps own consecutive pieces of the run's pairs
-// and rank them 32 at a time (match_any gives a pair's rank among equal
-// experts of the 32, a per-warp count per expert the rank before them). Few
-// tokens: one block does everything in one launch. More: the first launch
-// leaves each block's count per expert, and the second adds the counts of the
-// blocks before it and of the experts before its own.
+// The expert order is a stable counting sort of the token-major pairs. Up to 32
+// tokens: one block does everything in one launch, and with up to 256 pairs
+// each thread counts its pair's place directly. More: the first launch leaves
+// each block's count per expert, and in the second a block adds the counts of
+// the blocks before it and of the experts before its own; its warps own
+// consecutive pieces of its pairs and rank them 32 at a time (match_any gives a
+// pair's rank among equal experts of the 32, a per-warp count per expert the
+// rank before them).
 //
 // The bytes are few (one read of the logits); the time is the selection's
 // instructions and, for a serving step, launch latency.
@@ -31,7 +32,10 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxK = 32;
 constexpr int kMaxBlocks = 152;      // of the two-launch form: one for each SM
-constexpr int kOneBlockTokens = 128;
+constexpr int kOneBlockTokens = 32;  // a warp each; more go to several blocks (128 tokens of 64 experts: 13.8 us in one)
+constexpr int kPairsPerWarp = 64;    // of the ranking: fewer warps mean fewer counts to add up
+constexpr int kDirectPairs = 256;    // pairs up to which each counts its place itself
+constexpr int kStagedPairs = 2048;   // pairs of a block whose experts are ranked from shared memory
 
 struct RouteParams {
   const void* logits;
@@ -59,6 +63,10 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float order_value(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+
 // Sum of x[j] over all lanes and j by halves (see above).
 template <int NPL>
 __device__ __forceinline__ float halves_sum(const float (&e)[NPL]) {
@@ -72,12 +80,18 @@ __device__ __forceinline__ float halves_sum(const float (&e)[NPL]) {
   return warp_sum(x[0]);
 }
 
+// The score of one logit above -inf, from the token's largest logit and its softmax denominator.
+__device__ __forceinline__ float one_score(float l, int score, float top, float div) {
+  return score == GEMM_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / div;
+}
+
 // The scores of one token: lane l's s[j] is expert l + 32 j (0 past the last
 // one and for a logit of -inf); `there`: bit j set where the logit is above -inf.
 template <int NPL>
 __device__ __forceinline__ void token_scores(const void* logits, int type, long long base, int experts, int score,
-                                             int lane, float (&s)[NPL], uint32_t& there) {
-  float top = -INFINITY;
+                                             int lane, float (&s)[NPL], uint32_t& there, float& top, float& div) {
+  top = -INFINITY;
+  div = 1.0f;
   there = 0;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) {
@@ -88,7 +102,7 @@ __device__ __forceinline__ void token_scores(const void* logits, int type, long 
   }
   if (score == GEMM_SCORE_SIGMOID) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) s[j] = (there >> j) & 1u ? 1.0f / (1.0f + expf(-s[j])) : 0.0f;
+    for (int j = 0; j < NPL; ++j) s[j] = (there >> j) & 1u ? one_score(s[j], score, top, div) : 0.0f;
     return;
   }
 #pragma unroll
@@ -96,123 +110,180 @@ __device__ __forceinline__ void token_scores(const void* logits, int type, long 
 #pragma unroll
   for (int j = 0; j < NPL; ++j) s[j] = (there >> j) & 1u ? expf(s[j] - top) : 0.0f;
   const float z = halves_sum(s);
-  const float div = z == 0.0f ? 1.0f : z;
+  div = z == 0.0f ? 1.0f : z;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) s[j] = s[j] / div;
+}
+
+// The warp's largest of the lanes' candidates (key `best` of expert `e`; 0: none) goes to the lowest expert; returns its
+// lane, or -1 if there is none, and the expert.
+__device__ __forceinline__ int take_largest(uint32_t best, int e, int& won) {
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+  if (m == 0) return -1;
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == m);
+  int owner = __ffs(who) - 1;
+  if (who & (who - 1)) owner = int(__reduce_min_sync(0xFFFFFFFFu, best == m ? uint32_t(e) : 0xFFFFFFFFu)) & 31;
+  won = __shfl_sync(0xFFFFFFFFu, e, owner);
+  return owner;
 }
 
 // Chooses one token's experts; lane i < k returns the i-th id (-1: none) and its weight.
 template <int NPL>
 __device__ __forceinline__ void route_token(const RouteParams& p, int token, int lane, int& id, float& weight) {
-  float s[NPL];
-  uint32_t there;
-  token_scores<NPL>(p.logits, p.type, token * p.ld, p.experts, p.score, lane, s, there);
-  float key[NPL];
+  const long long base = token * p.ld;
+  float top, div;
+  uint32_t u[NPL];  // the keys' order; 0: out
   bool nan = false;
+  uint32_t kept = 0xFFFFFFFFu;
+  const int per = p.experts / p.groups;
+  {
+    float key[NPL];
+    uint32_t there;
+    token_scores<NPL>(p.logits, p.type, base, p.experts, p.score, lane, key, there, top, div);
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = lane + 32 * j;
-    key[j] = -INFINITY;
-    if ((there >> j) & 1u) {
-      const float v = p.bias != nullptr ? s[j] + p.bias[e] : s[j];
-      nan = nan || s[j] != s[j];
-      if (v == v) key[j] = v;
+    for (int j = 0; j < NPL; ++j) {
+      float v = -INFINITY;
+      if ((there >> j) & 1u) {
+        v = p.bias != nullptr ? key[j] + p.bias[lane + 32 * j] : key[j];
+        nan = nan || key[j] != key[j];
+        if (v != v) v = -INFINITY;
+      }
+      key[j] = v;
+    }
+    if (p.groups > 1) {
+      // lane g gets group g's key: the sum of its two largest
+      float mine = -INFINITY;
+      if (per % 32 == 0) {
+        // groups of whole rows of 32: the two largest of each row over the lanes, then of the group's rows
+        float first = -INFINITY, second = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+          const uint32_t o = order_bits(key[j]);
+          const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, o);
+          const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, o == m1)) - 1;
+          const uint32_t m2 = __reduce_max_sync(0xFFFFFFFFu, lane == owner ? 0u : o);
+          const float a = order_value(m1), b = order_value(m2);
+          if (32 * j / per == lane) {
+            second = fmaxf(fmaxf(second, b), fminf(first, a));
+            first = fmaxf(first, a);
+          }
+        }
+        mine = first + second;
+      } else {
+        for (int g = 0; g < p.groups; ++g) {
+          float a = -INFINITY, b = -INFINITY;  // this lane's two largest keys of the group
+#pragma unroll
+          for (int j = 0; j < NPL; ++j)
+            if (lane + 32 * j >= g * per && lane + 32 * j < (g + 1) * per) {
+              b = fmaxf(b, fminf(a, key[j]));
+              a = fmaxf(a, key[j]);
+            }
+          // the largest of all lanes; its (first) owner puts its second one forward
+          const uint32_t ua = order_bits(a);
+          const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, ua);
+          const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, ua == m1)) - 1;
+          const uint32_t m2 = __reduce_max_sync(0xFFFFFFFFu, lane == owner ? order_bits(b) : ua);
+          if (lane == g) mine = per > 1 ? order_value(m1) + order_value(m2) : order_value(m1);
+        }
+      }
+      uint32_t best = lane < p.groups ? order_bits(mine) : 0u;
+      kept = 0;
+      for (int i = 0; i < p.kept; ++i) {
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+        const int g = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+        kept |= 1u << g;
+        if (lane == g) best = 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      u[j] = key[j] > -INFINITY ? order_bits(key[j]) : 0u;
+      if (p.groups > 1 && !((kept >> ((lane + 32 * j) / per)) & 1u)) u[j] = 0;
     }
   }
   nan = __any_sync(0xFFFFFFFFu, nan);
-  uint32_t kept = 0xFFFFFFFFu;
-  const int per = p.experts / p.groups;
-  if (p.groups > 1) {
-    float mine = 0.0f;  // lane g: group g's key
-    for (int g = 0; g < p.groups; ++g) {
-      float a = -INFINITY, b = -INFINITY;  // the two largest keys
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        const int e = lane + 32 * j;
-        if (e >= g * per && e < (g + 1) * per) {
-          b = fmaxf(b, fminf(a, key[j]));
-          a = fmaxf(a, key[j]);
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const float c = __shfl_xor_sync(0xFFFFFFFFu, a, d), f = __shfl_xor_sync(0xFFFFFFFFu, b, d);
-        b = fmaxf(fmaxf(b, f), fminf(a, c));
-        a = fmaxf(a, c);
-      }
-      if (lane == g) mine = per > 1 ? a + b : a;
-    }
-    uint32_t best = lane < p.groups ? order_bits(mine) : 0u;
-    kept = 0;
-    for (int i = 0; i < p.kept; ++i) {
-      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-      const int g = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-      kept |= 1u << g;
-      if (lane == g) best = 0;
-    }
-  }
-  uint32_t u[NPL];
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    u[j] = key[j] > -INFINITY ? order_bits(key[j]) : 0u;
-    if (p.groups > 1 && u[j] != 0 && !((kept >> ((lane + 32 * j) / per)) & 1u)) u[j] = 0;
-  }
   id = -1;
-  weight = 0.0f;
-  for (int i = 0; i < p.k; ++i) {
-    uint32_t best = 0;
-    int at = 0;
-    float sc = 0.0f;
+  if constexpr (NPL <= 8) {
+    // in descending order, equal keys as they are (the lower expert first)
+    int e[NPL];
 #pragma unroll
-    for (int j = 0; j < NPL; ++j)
-      if (u[j] > best) {
-        best = u[j];
-        at = j;
-        sc = s[j];
+    for (int j = 0; j < NPL; ++j) e[j] = lane + 32 * j;
+#pragma unroll
+    for (int a = NPL - 1; a > 0; --a)
+#pragma unroll
+      for (int j = 0; j < a; ++j) {
+        const bool swap = u[j + 1] > u[j];
+        const uint32_t hi = max(u[j], u[j + 1]), lo = min(u[j], u[j + 1]);
+        const int eh = swap ? e[j + 1] : e[j], el = swap ? e[j] : e[j + 1];
+        u[j] = hi;
+        u[j + 1] = lo;
+        e[j] = eh;
+        e[j + 1] = el;
       }
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (m == 0) break;  // no expert left
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == m);
-    int owner = __ffs(who) - 1;
-    if (who & (who - 1)) {  // equal keys: the lowest expert
-      const uint32_t e = best == m ? uint32_t(lane + 32 * at) : 0xFFFFFFFFu;
-      owner = int(__reduce_min_sync(0xFFFFFFFFu, e)) & 31;
+    for (int i = 0; i < p.k; ++i) {
+      int won;
+      const int owner = take_largest(u[0], e[0], won);
+      if (owner < 0) break;
+      if (lane == i) id = won;
+      if (lane == owner) {
+#pragma unroll
+        for (int j = 0; j + 1 < NPL; ++j) {
+          u[j] = u[j + 1];
+          e[j] = e[j + 1];
+        }
+        u[NPL - 1] = 0;
+      }
     }
-    const int won = __shfl_sync(0xFFFFFFFFu, lane + 32 * at, owner);
-    const float score = __shfl_sync(0xFFFFFFFFu, sc, owner);
-    if (lane == i) {
-      id = won;
-      weight = score;
-    }
-    if (lane == owner) {
+  } else {
+    for (int i = 0; i < p.k; ++i) {
+      uint32_t best = 0;
+      int at = 0, won;
 #pragma unroll
       for (int j = 0; j < NPL; ++j)
-        if (j == at) u[j] = 0;
+        if (u[j] > best) {
+          best = u[j];
+          at = j;
+        }
+      const int owner = take_largest(best, lane + 32 * at, won);
+      if (owner < 0) break;
+      if (lane == i) id = won;
+      if (lane == owner) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+          if (j == at) u[j] = 0;
+      }
     }
   }
+  // the chosen scores, from their logits once more (the same operations, so the same bits)
+  weight = id >= 0 ? one_score(load_logit(p.logits, p.type, base + id), p.score, top, div) : 0.0f;
   if (p.renormalize) weight = weight / (warp_sum(weight) + 1e-20f);
   weight *= p.scale;
   if (nan) weight = __int_as_float(0x7FC00000);
 }
 
-// Walks this warp's piece of the block's pairs in order, 32 at a time, and
-// calls use(pair, expert, rank) with each one's rank among the block's pairs of
-// its expert that this warp has seen, counted on top of hist[expert].
+__device__ __forceinline__ int ranking_warps(int n, int most) {
+  return min(most, max(1, (n + kPairsPerWarp - 1) / kPairsPerWarp));
+}
+
+// Walks this warp's piece of the block's n pairs in order, 32 at a time, and
+// calls use(i, expert, rank) with each one's rank among the block's pairs of
+// its expert that this warp has seen, counted on top of hist[expert]. `staged`
+// holds the pairs' experts (-1: none), or `ids` does.
 template <class Use>
-__device__ __forceinline__ void rank_pairs(const int32_t* ids, long long first, int n, int warp, int warps, int lane,
-                                           int32_t* hist, Use use) {
+__device__ __forceinline__ void rank_pairs(const int16_t* staged, const int32_t* ids, int n, int warp, int warps,
+                                           int lane, int32_t* hist, Use use) {
   const int piece = ((n + warps - 1) / warps + 31) / 32 * 32;
-  const int end = min(n, (warp + 1) * piece);
+  const int end = warp < warps ? min(n, (warp + 1) * piece) : 0;
   for (int i0 = warp * piece; i0 < end; i0 += 32) {
     const int i = i0 + lane;
-    const int e = i < end ? ids[first + i] : -1;
+    const int e = i >= end ? -1 : staged != nullptr ? staged[i] : ids[i];
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     const int before = __popc(same & ((1u << lane) - 1u));
     const int base = e >= 0 ? hist[e] : 0;
     __syncwarp();
     if (e >= 0 && before == 0) hist[e] = base + __popc(same);
     __syncwarp();
-    use(first + i, i < end, e, base + before);
+    if (i < end) use(i, e, base + before);
   }
 }
 
@@ -227,39 +298,50 @@ __device__ __forceinline__ int block_exclusive(int v, int32_t* sums) {
   }
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  int at = incl - v;
-  for (int w = 0; w < warp; ++w) at += sums[w];
-  return at;
+  int before = lane < int(blockDim.x >> 5) ? sums[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+    if (lane >= d) before += o;
+  }
+  return incl - v + (warp > 0 ? __shfl_sync(0xFFFFFFFFu, before, warp - 1) : 0);
 }
 
 // Threads of a routing block: per-warp counts of all experts fit 32 KB.
+constexpr int kLeastThreads = 256;
 template <int NPL>
 constexpr int kRouteThreads = NPL <= 8 ? 1024 : NPL == 16 ? 512 : 256;
 
 // One-block form: chooses, then orders the pairs.
 // Two-launch form (p.blocks > 1): chooses and leaves the block's counts.
 template <int NPL>
-__global__ void __launch_bounds__(kRouteThreads<NPL>) route_kernel(const RouteParams p) {
-  constexpr int WARPS = kRouteThreads<NPL> / 32;
+__global__ void __launch_bounds__(kRouteThreads<NPL>, 1) route_kernel(const RouteParams p) {
+  constexpr int WARPS = kRouteThreads<NPL> / 32;  // at most
   constexpr int E = 32 * NPL;
+  const int warps = blockDim.x >> 5;
   __shared__ int32_t hist[WARPS][E];
+  __shared__ __align__(16) int16_t staged[kOneBlockTokens * kMaxK];
   __shared__ int32_t sums[32];
   __shared__ int32_t used;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < WARPS * E; i += blockDim.x) (&hist[0][0])[i] = 0;
+  const bool alone = p.blocks == 1;
+  const int ranking = alone ? ranking_warps(p.tokens * p.k, warps) : 1;
+  for (int i = threadIdx.x; i < ranking * E; i += blockDim.x) (&hist[0][0])[i] = 0;
   grid_dependency_wait();
   __syncthreads();
   const int t0 = blockIdx.x * p.per_block;
   const int t1 = min(p.tokens, t0 + p.per_block);
-  const bool alone = p.blocks == 1;
-  for (int t = t0 + warp; t < t1; t += WARPS) {
+  for (int t = t0 + warp; t < t1; t += warps) {
     int id;
     float w;
     route_token<NPL>(p, t, lane, id, w);
     if (lane < p.k) {
       p.ids[static_cast<long long>(t) * p.k + lane] = id;
       p.weights[static_cast<long long>(t) * p.k + lane] = w;
-      if (!alone && id >= 0) atomicAdd(&hist[0][id], 1);  // whole numbers: any order gives the same count
+      if (alone)
+        staged[t * p.k + lane] = static_cast<int16_t>(id);
+      else if (id >= 0)
+        atomicAdd(&hist[0][id], 1);  // whole numbers: any order gives the same count
     }
   }
   __syncthreads();
@@ -270,17 +352,47 @@ __global__ void __launch_bounds__(kRouteThreads<NPL>) route_kernel(const RoutePa
     return;
   }
   const int n = (t1 - t0) * p.k;
-  rank_pairs(p.ids, 0, n, warp, WARPS, lane, hist[warp], [](long long, bool, int, int) {});
+  if (n <= kDirectPairs) {
+    // place of pair i: the pairs of lower experts, and its own expert's before it; offset of expert e: the pairs of
+    // lower experts (e = experts: all)
+    for (int q = threadIdx.x; q < n + p.experts + 1; q += blockDim.x) {
+      const int e = q < n ? staged[q] : q - n;
+      const int self = q < n ? q : 0;
+      int below = 0, before = 0;
+      for (int i = 0; i < n; i += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(staged + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const int o = static_cast<int16_t>(h & 1 ? w[h >> 1] >> 16 : w[h >> 1] & 0xFFFFu);
+          below += i + h < n && o >= 0 && o < e;
+          before += i + h < self && o == e;
+        }
+      }
+      if (q >= n) {
+        p.offsets[e] = below;
+      } else {
+        p.slots[q] = e >= 0 ? below + before : -1;
+        if (e >= 0) p.rows[below + before] = q / p.k;
+      }
+      if (q == n + p.experts) used = below;
+    }
+    __syncthreads();
+    for (int i = used + threadIdx.x; i < n; i += blockDim.x) p.rows[i] = -1;
+    grid_launch_dependents();
+    return;
+  }
+  rank_pairs(staged, nullptr, n, warp, ranking, lane, hist[warp], [](int, int, int) {});
   __syncthreads();
-  // counts per expert (thread e < experts; at most E <= blockDim.x * 4 experts)
-  constexpr int PER = (E + kRouteThreads<NPL> - 1) / kRouteThreads<NPL>;
+  // counts per expert
+  constexpr int PER = (E + kLeastThreads - 1) / kLeastThreads;
   int total[PER], sum = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = threadIdx.x * PER + q;
     total[q] = 0;
     if (e < E)
-      for (int w = 0; w < WARPS; ++w) {
+      for (int w = 0; w < ranking; ++w) {
         const int c = hist[w][e];
         hist[w][e] = total[q];
         total[q] += c;
@@ -292,27 +404,30 @@ __global__ void __launch_bounds__(kRouteThreads<NPL>) route_kernel(const RoutePa
   for (int q = 0; q < PER; ++q) {
     const int e = threadIdx.x * PER + q;
     if (e < E)
-      for (int w = 0; w < WARPS; ++w) hist[w][e] += at;
+      for (int w = 0; w < ranking; ++w) hist[w][e] += at;
     if (e < p.experts) p.offsets[e] = at;
     at += total[q];
     if (e == p.experts - 1) p.offsets[p.experts] = used = at;
   }
   __syncthreads();
-  rank_pairs(p.ids, 0, n, warp, WARPS, lane, hist[warp], [&](long long i, bool in, int e, int rank) {
-    if (!in) return;
+  rank_pairs(staged, nullptr, n, warp, ranking, lane, hist[warp], [&](int i, int e, int rank) {
     p.slots[i] = e >= 0 ? rank : -1;
-    if (e >= 0) p.rows[rank] = int(i / p.k);
+    if (e >= 0) p.rows[rank] = i / p.k;
   });
   for (int i = used + threadIdx.x; i < n; i += blockDim.x) p.rows[i] = -1;
   grid_launch_dependents();
 }
 
 // Second launch of the two-launch form: block b places its pairs.
-__global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(1024, 1) route_place_kernel(const RouteParams p) {
   extern __shared__ int32_t shared[];  // warps x experts counts, then totals and starts of the experts
+  __shared__ int16_t pairs[kStagedPairs];
   __shared__ int32_t sums[32];
   __shared__ int32_t used;
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * p.per_block;
+  const int n = max(0, min(p.tokens, t0 + p.per_block) - t0) * p.k;
+  const int warps = ranking_warps(n, int(blockDim.x) >> 5);
   int32_t* hist = shared;
   int32_t* total = shared + warps * p.experts;
   int32_t* start = total + p.experts;
@@ -333,10 +448,13 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
     atomicAdd(&total[e], all);
     atomicAdd(&start[e], before);
   }
-  const int t0 = blockIdx.x * p.per_block;
-  const int n = max(0, min(p.tokens, t0 + p.per_block) - t0) * p.k;
   const long long first = static_cast<long long>(t0) * p.k;
-  rank_pairs(p.ids, first, n, warp, warps, lane, hist + warp * p.experts, [](long long, bool, int, int) {});
+  const int16_t* staged = n <= kStagedPairs ? pairs : nullptr;
+  if (staged != nullptr) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) pairs[i] = static_cast<int16_t>(p.ids[first + i]);
+    __syncthreads();
+  }
+  rank_pairs(staged, p.ids + first, n, warp, warps, lane, hist + warp * p.experts, [](int, int, int) {});
   __syncthreads();
   const int per = (p.experts + blockDim.x - 1) / blockDim.x;
   int sum = 0;
@@ -362,10 +480,9 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
     }
   }
   __syncthreads();
-  rank_pairs(p.ids, first, n, warp, warps, lane, hist + warp * p.experts, [&](long long i, bool in, int e, int rank) {
-    if (!in) return;
-    p.slots[i] = e >= 0 ? rank : -1;
-    if (e >= 0) p.rows[rank] = int(i / p.k);
+  rank_pairs(staged, p.ids + first, n, warp, warps, lane, hist + warp * p.experts, [&](int i, int e, int rank) {
+    p.slots[first + i] = e >= 0 ? rank : -1;
+    if (e >= 0) p.rows[rank] = t0 + i / p.k;
   });
   const long long all = static_cast<long long>(p.tokens) * p.k;
   for (long long i = used + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < all;
@@ -382,46 +499,42 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
 template <int NPL>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteParams p, const float* dweights, void* dlogits,
                                                          long long ldd) {
+  __shared__ float rows[8][32 * NPL];
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   for (long long t = (blockIdx.x * 256LL + threadIdx.x) >> 5; t < p.tokens; t += gridDim.x * 8LL) {
     float s[NPL], ds[NPL];
     uint32_t there;
-    token_scores<NPL>(p.logits, p.type, t * p.ld, p.experts, p.score, lane, s, there);
+    float top, div;
+    token_scores<NPL>(p.logits, p.type, t * p.ld, p.experts, p.score, lane, s, there, top, div);
     int id = -1;
     float dw = 0.0f;
     if (lane < p.k) {
       id = p.ids[t * p.k + lane];
-      if (id >= p.experts) id = -1;
+      if (id < 0 || id >= p.experts) id = -1;
       if (id >= 0) dw = dweights[t * p.k + lane] * p.scale;
     }
-    float chosen = 0.0f;  // lane i: the score of the i-th choice
-    for (int i = 0; i < p.k; ++i) {
-      const int e = __shfl_sync(0xFFFFFFFFu, id, i);
-      float v = 0.0f;
+    // the chosen scores, and their gradients, change lanes through the warp's row of shared memory
+    float* row = rows[threadIdx.x >> 5];
 #pragma unroll
-      for (int j = 0; j < NPL; ++j)
-        if (j == e >> 5) v = s[j];
-      v = __shfl_sync(0xFFFFFFFFu, v, e & 31);
-      if (lane == i && e >= 0) chosen = v;
-    }
+    for (int j = 0; j < NPL; ++j) row[lane + 32 * j] = s[j];
+    __syncwarp();
+    const float chosen = id >= 0 ? row[id] : 0.0f;  // lane i: the score of the i-th choice
     float d = dw;
     if (p.renormalize) {
       const float c = warp_sum(chosen) + 1e-20f;
       const float mean = warp_sum(dw * (chosen / c));
       d = id >= 0 ? (dw - mean) / c : 0.0f;
     }
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) ds[j] = 0.0f;
-    for (int i = 0; i < p.k; ++i) {
-      const int e = __shfl_sync(0xFFFFFFFFu, id, i);
-      const float v = __shfl_sync(0xFFFFFFFFu, d, i);
-      if (e >= 0 && (e & 31) == lane) {
+    for (int j = 0; j < NPL; ++j) row[lane + 32 * j] = 0.0f;
+    __syncwarp();
+    if (id >= 0) row[id] = d;  // a token's ids are distinct
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NPL; ++j)
-          if (j == e >> 5) ds[j] += v;
-      }
-    }
+    for (int j = 0; j < NPL; ++j) ds[j] = row[lane + 32 * j];
+    __syncwarp();
     float dot = 0.0f;
     if (p.score == GEMM_SCORE_SOFTMAX) {
 #pragma unroll
@@ -478,7 +591,10 @@ int check_config(int64_t tokens, int experts, const gemm_route_config_t* c) {
 
 template <int NPL>
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s) {
-  cudaError_t e = launch_dependent(route_kernel<NPL>, p.blocks, kRouteThreads<NPL>, 0, s, 1, p);
+  // one block: a warp for each token
+  const int most = kRouteThreads<NPL>, few = p.tokens * 32;
+  const int block = p.blocks > 1 || few > most ? most : few < kLeastThreads ? kLeastThreads : few;
+  cudaError_t e = launch_dependent(route_kernel<NPL>, p.blocks, block, 0, s, 1, p);
   if (e != cudaSuccess || p.blocks == 1) return e;
   // as many warps as let their counts stay within 32 KB
   const int threads = kRouteThreads<NPL>;

@@ -71,6 +71,7 @@ class Routing(NamedTuple):
 
 
 _lib = None
+_C = {}  # entry point -> bound C function, filled on first use
 
 
 def _load():
@@ -93,54 +94,56 @@ def _load():
         sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64, i, epi, vp, i64, vp]
     for name in ("gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad"):
         sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, i, vp, i64, vp]
-    for name, args in sig.items():
+    sizes = {"gemm_rmsnorm_backward_workspace": [i64, i64], "gemm_route_workspace": [i64, i, i],
+             "gemm_grouped_workspace": [i, i, i64, i64], "gemm_grouped_wgrad_workspace": [i, i64, i64, i64, i]}
+    for name, args in {**sig, **sizes}.items():
         fn = getattr(lib, name)
-        fn.argtypes, fn.restype = args, i
-    for name, args in (("gemm_rmsnorm_backward_workspace", [i64, i64]), ("gemm_route_workspace", [i64, i, i]),
-                       ("gemm_grouped_workspace", [i, i, i64, i64]),
-                       ("gemm_grouped_wgrad_workspace", [i, i64, i64, i64, i])):
-        fn = getattr(lib, name)
-        fn.argtypes, fn.restype = args, i64
+        fn.argtypes, fn.restype = args, i64 if name in sizes else i
+        _C[name] = fn
     _lib = lib
     return lib
 
 
-class _on:
-    """Makes ``stream`` current while a call allocates (so that the caching
-    allocator ties its tensors to the stream that uses them); nothing to do
-    for the current stream."""
-
-    def __new__(cls, stream):
-        return _NOTHING if stream is None else torch.cuda.stream(stream)
-
-
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
-def _check(code: int, name: str) -> None:
+def _call(name: str, *args) -> None:
+    """Calls one entry point; raises what it refuses."""
+    fn = _C.get(name)
+    if fn is None:
+        _load()
+        fn = _C[name]
+    code = fn(*args)
     if code != GEMM_OK:
         raise GemmError(code, name)
 
 
+def _size(name: str, *args) -> int:
+    if not _C:
+        _load()
+    return _C[name](*args)
+
+
+def _under(stream, fn, *args, **kw):
+    """fn under ``stream``, so that the caching allocator ties what it
+    allocates to the stream that uses it."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _stream(t: torch.Tensor) -> int:
+    return gemm._raw_stream(None, t.device.index)
+
+
 def _matrix(t: torch.Tensor, what: str, dtype=None, shape=None) -> int:
     """Checks a 2-D CUDA tensor with contiguous rows; its leading dimension."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
+    size = t.shape
+    if len(size) != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    rows, cols = size
+    if shape is not None and size != shape:
         raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride along its rows")
     if rows <= 1:
         return cols
@@ -149,9 +152,9 @@ def _matrix(t: torch.Tensor, what: str, dtype=None, shape=None) -> int:
     return s0
 
 
-def _vector(t: torch.Tensor, what: str, dtype, n: int) -> int:
-    """Checks a contiguous CUDA tensor of n elements; its address."""
-    if t.dtype != dtype:
+def _vector(t: torch.Tensor, what: str, dtype, n: int):
+    """Checks a contiguous CUDA tensor of n elements; its address (None if it has none)."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {n} elements")
@@ -177,29 +180,32 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     float8_e4m3fn: y then holds 8-bit rows and ``scale`` their scales (y * scale
     stands for the norm). ``h_out`` receives h (it may be ``x`` or
     ``residual``); without a residual h is x. ``rstd``: fp32, for the backward pass."""
-    code = _type(x, "x")
+    if stream is not None:
+        return _under(stream, rms_norm, x, weight, residual, eps=eps, out_dtype=out_dtype, h_out=h_out)
+    dt = x.dtype
+    code = _TYPE.get(dt)
+    if code is None:
+        raise TypeError("x must be float16, bfloat16 or float32")
     ldx = _matrix(x, "x")
     rows, cols = x.shape
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    if out_dtype != x.dtype and out_dtype != _E4M3:
+    q8 = out_dtype is _E4M3
+    if not q8 and out_dtype is not None and out_dtype is not dt:
         raise TypeError("out_dtype must be x's dtype or float8_e4m3fn")
-    w = _vector(weight, "weight", x.dtype, cols)
-    ldr = _matrix(residual, "residual", x.dtype, (rows, cols)) if residual is not None else 0
-    s = gemm._raw_stream(stream, x.device.index)
-    with _on(stream):
-        y = torch.empty((rows, cols), dtype=out_dtype, device=x.device)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        scale = torch.empty((rows,), dtype=torch.float32, device=x.device) if out_dtype == _E4M3 else None
-        if residual is None:
-            h, ldh = x, 0
+    w = _vector(weight, "weight", dt, cols)
+    dev = x.device
+    y = torch.empty((rows, cols), dtype=out_dtype or dt, device=dev)
+    rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    scale = torch.empty((rows,), dtype=torch.float32, device=dev) if q8 else None
+    h, ph, pr, ldh, ldr = x, None, None, 0, 0
+    if residual is not None:
+        ldr, pr = _matrix(residual, "residual", dt, x.shape), residual.data_ptr()
+        if h_out is None:
+            h, ldh = torch.empty((rows, cols), dtype=dt, device=dev), cols
         else:
-            h = h_out if h_out is not None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-            ldh = _matrix(h, "h_out", x.dtype, (rows, cols))
-    _check(_load().gemm_rmsnorm(
-        code, rows, cols, x.data_ptr() or None, ldx, residual.data_ptr() if residual is not None else None, ldr, w,
-        eps, h.data_ptr() if residual is not None else None, ldh, GEMM_TYPE_E4M3 if scale is not None else code,
-        y.data_ptr() or None, cols, scale.data_ptr() if scale is not None else None, rstd.data_ptr() or None, s),
-        "gemm_rmsnorm")
+            h, ldh = h_out, _matrix(h_out, "h_out", dt, x.shape)
+        ph = h.data_ptr()
+    _call("gemm_rmsnorm", code, rows, cols, x.data_ptr(), ldx, pr, ldr, w, eps, ph, ldh, GEMM_TYPE_E4M3 if q8 else code,
+          y.data_ptr(), cols, scale.data_ptr() if q8 else None, rstd.data_ptr(), gemm._raw_stream(None, dev.index))
     return Norm(y, h, rstd, scale)
 
 
@@ -207,23 +213,23 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
                       dh: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """(dx, dweight) of ``rms_norm``: dx is the gradient of x and of the
     residual alike; ``dh`` is the gradient that reaches h by the residual path."""
+    if stream is not None:
+        return _under(stream, rms_norm_backward, dy, h, weight, rstd, dh=dh)
+    dt = h.dtype
     code = _type(h, "h")
     ldh = _matrix(h, "h")
     rows, cols = h.shape
-    lddy = _matrix(dy, "dy", h.dtype, (rows, cols))
-    lddh = _matrix(dh, "dh", h.dtype, (rows, cols)) if dh is not None else 0
-    w, r = _vector(weight, "weight", h.dtype, cols), _vector(rstd, "rstd", torch.float32, rows)
-    lib = _load()
-    need = lib.gemm_rmsnorm_backward_workspace(rows, cols)
-    s = gemm._raw_stream(stream, h.device.index)
-    with _on(stream):
-        dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
-        dw = torch.empty((cols,), dtype=h.dtype, device=h.device)
-        ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=h.device)
-    _check(lib.gemm_rmsnorm_backward(
-        code, rows, cols, dy.data_ptr() or None, lddy, h.data_ptr() or None, ldh, w, r,
-        dh.data_ptr() if dh is not None else None, lddh, dx.data_ptr() or None, cols, dw.data_ptr() or None,
-        ws.data_ptr(), need, s), "gemm_rmsnorm_backward")
+    lddy = _matrix(dy, "dy", dt, h.shape)
+    lddh = _matrix(dh, "dh", dt, h.shape) if dh is not None else 0
+    w, r = _vector(weight, "weight", dt, cols), _vector(rstd, "rstd", torch.float32, rows)
+    need = _size("gemm_rmsnorm_backward_workspace", rows, cols)
+    dev = h.device
+    dx = torch.empty((rows, cols), dtype=dt, device=dev)
+    dw = torch.empty((cols,), dtype=dt, device=dev)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _call("gemm_rmsnorm_backward", code, rows, cols, dy.data_ptr(), lddy, h.data_ptr(), ldh, w, r,
+          dh.data_ptr() if dh is not None else None, lddh, dx.data_ptr(), cols, dw.data_ptr(), ws.data_ptr(), need,
+          _stream(h))
     return dx, dw
 
 
@@ -246,26 +252,25 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.T
     the weights are the chosen scores, renormalised to sum to 1 and times
     ``scale``. Ties go to the lowest expert; a logit of -inf takes its expert
     out (see the C header for the exact rules)."""
+    if stream is not None:
+        return _under(stream, route, logits, k, score=score, bias=bias, groups=groups, kept_groups=kept_groups,
+                      renormalize=renormalize, scale=scale)
     code = _type(logits, "logits")
     ld = _matrix(logits, "logits")
     tokens, experts = logits.shape
     cfg = _config(k, score, groups, kept_groups, renormalize, scale)
     b = _vector(bias, "bias", torch.float32, experts) if bias is not None else None
-    lib = _load()
-    need = lib.gemm_route_workspace(tokens, experts, int(k))
-    s = gemm._raw_stream(stream, logits.device.index)
-    k = max(int(k), 0)
-    with _on(stream):
-        dev = logits.device
-        ids = torch.empty((tokens, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
-        slots = torch.empty((tokens, k), dtype=torch.int32, device=dev)
-        rows = torch.empty((tokens * k,), dtype=torch.int32, device=dev)
-        offsets = torch.empty((experts + 1,), dtype=torch.int32, device=dev)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    _check(lib.gemm_route(code, tokens, experts, logits.data_ptr() or None, ld, b, cfg, ids.data_ptr() or None,
-                          weights.data_ptr() or None, slots.data_ptr() or None, rows.data_ptr() or None,
-                          offsets.data_ptr(), ws.data_ptr() if need else None, need, s), "gemm_route")
+    need = _size("gemm_route_workspace", tokens, experts, cfg.k)
+    k = max(cfg.k, 0)
+    dev, i32 = logits.device, torch.int32
+    ids = torch.empty((tokens, k), dtype=i32, device=dev)
+    weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+    slots = torch.empty((tokens, k), dtype=i32, device=dev)
+    rows = torch.empty((tokens * k,), dtype=i32, device=dev)
+    offsets = torch.empty((experts + 1,), dtype=i32, device=dev)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _call("gemm_route", code, tokens, experts, logits.data_ptr(), ld, b, cfg, ids.data_ptr(), weights.data_ptr(),
+          slots.data_ptr(), rows.data_ptr(), offsets.data_ptr(), ws.data_ptr() if need else None, need, _stream(logits))
     return Routing(ids, weights, slots, rows, offsets)
 
 
@@ -273,7 +278,9 @@ def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tens
                    renormalize: bool = True, scale: float = 1.0,
                    stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """dlogits (in the logits' dtype) from the weights' gradient, the logits and
-    the chosen ids; the choice itself is held fixed."""
+    the ids that ``route`` chose; the choice itself is held fixed."""
+    if stream is not None:
+        return _under(stream, route_backward, dweights, logits, ids, score=score, renormalize=renormalize, scale=scale)
     code = _type(logits, "logits")
     ld = _matrix(logits, "logits")
     tokens, experts = logits.shape
@@ -282,11 +289,9 @@ def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tens
     k = ids.shape[1]
     cfg = _config(k, score, 1, 1, renormalize, scale)
     i, d = _vector(ids, "ids", torch.int32, tokens * k), _vector(dweights, "dweights", torch.float32, tokens * k)
-    s = gemm._raw_stream(stream, logits.device.index)
-    with _on(stream):
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    _check(_load().gemm_route_backward(code, tokens, experts, logits.data_ptr() or None, ld, i, d, cfg,
-                                       out.data_ptr() or None, experts, s), "gemm_route_backward")
+    out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    _call("gemm_route_backward", code, tokens, experts, logits.data_ptr(), ld, i, d, cfg, out.data_ptr(), experts,
+          _stream(logits))
     return out
 
 
@@ -297,10 +302,11 @@ def _stack(t: torch.Tensor, what: str):
     if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{what} must be a 3-D CUDA tensor")
     g, r, c = t.shape
-    if c > 1 and t.stride(2) != 1:
+    s0, s1, s2 = t.stride()
+    if c > 1 and s2 != 1:
         raise ValueError(f"{what} must have unit stride along its rows")
-    ld = t.stride(1) if r > 1 else c
-    return ld, t.stride(0) if g > 1 else r * ld
+    ld = s1 if r > 1 else c
+    return ld, s0 if g > 1 else r * ld
 
 
 def expert_matmul(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None, *,
@@ -321,43 +327,48 @@ def expert_matmul(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows:
     ``gemm.matmul``'s, or "silu_gated" (W holds gate and value halves, C has
     N / 2 columns). Rows of C past offsets[-1] are zero. With the other layout
     flag the call is the gradient of A (a row per slot)."""
-    name = _GROUPED.get(A.dtype)
+    if stream is not None:
+        return _under(stream, expert_matmul, A, W, offsets, rows, layout=layout, out=out, alpha=alpha, a_scale=a_scale,
+                      w_scale=w_scale, bias=bias, activation=activation)
+    dt = A.dtype
+    name = _GROUPED.get(dt)
     if name is None:
         raise TypeError("A must be float16, bfloat16 or float8_e4m3fn")
-    if W.dtype != A.dtype:
+    if W.dtype is not dt:
         raise TypeError("A and W must have the same dtype")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(a for a in ACTIVATIONS if a)}")
     lda = _matrix(A, "A")
     ldw, stride_w = _stack(W, "W")
-    experts = W.shape[0]
-    K = A.shape[1]
-    N = W.shape[1] if layout == GEMM_B_K_MAJOR else W.shape[2]
-    if (W.shape[2] if layout == GEMM_B_K_MAJOR else W.shape[1]) != K:
+    experts, W1, W2 = W.shape
+    a_rows, K = A.shape
+    N, WK = (W1, W2) if layout == GEMM_B_K_MAJOR else (W2, W1)
+    if WK != K:
         raise ValueError("W's K dimension does not match A")
-    act = ACTIVATIONS[activation]
-    out_dt = torch.bfloat16 if A.dtype == _E4M3 else A.dtype
+    out_dt = torch.bfloat16 if dt is _E4M3 else dt
     off = _vector(offsets, "offsets", torch.int32, experts + 1)
-    slots = A.shape[0] if rows is None else rows.numel()
-    r = _vector(rows, "rows", torch.int32, slots) if rows is not None else None
+    dev = A.device
+    if rows is None:
+        slots, r, need = a_rows, None, 0
+    else:
+        slots = rows.numel()
+        r = _vector(rows, "rows", torch.int32, slots)
+        need = _size("gemm_grouped_workspace", _GROUPED_TYPE[dt], experts, slots, K)
     cols = N // 2 if act == GEMM_ACT_SILU_GATED else N
-    lib = _load()
-    need = lib.gemm_grouped_workspace(_GROUPED_TYPE[A.dtype], experts, slots, K) if rows is not None else 0
-    s = gemm._raw_stream(stream, A.device.index)
-    ldc = _matrix(out, "out", out_dt, (slots, cols)) if out is not None else cols
-    with _on(stream):
-        if out is None:
-            out = torch.empty((slots, cols), dtype=out_dt, device=A.device)
-        ws = torch.empty((need,), dtype=torch.uint8, device=A.device) if need else None
+    if out is None:
+        out, ldc = torch.empty((slots, cols), dtype=out_dt, device=dev), cols
+    else:
+        ldc = _matrix(out, "out", out_dt, (slots, cols))
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     epi = None
     if act or alpha != 1.0 or a_scale is not None or w_scale is not None or bias is not None:
         epi = GroupedEpilogue(
-            alpha, _vector(a_scale, "a_scale", torch.float32, A.shape[0]) if a_scale is not None else None,
+            alpha, _vector(a_scale, "a_scale", torch.float32, a_rows) if a_scale is not None else None,
             _vector(w_scale, "w_scale", torch.float32, experts * N) if w_scale is not None else None,
             _vector(bias, "bias", out_dt, experts * N) if bias is not None else None, act)
-    _check(getattr(lib, name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r, W.data_ptr() or None,
-                              ldw, stride_w, out.data_ptr() or None, ldc, layout, epi, ws.data_ptr() if need else None,
-                              need, s), name)
+    _call(name, experts, off, slots, N, K, A.data_ptr() or None, a_rows, lda, r, W.data_ptr() or None, ldw, stride_w,
+          out.data_ptr(), ldc, layout, epi, ws.data_ptr() if need else None, need, gemm._raw_stream(None, dev.index))
     return out
 
 
@@ -367,32 +378,32 @@ def expert_weight_grad(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor,
     """The gradient of ``expert_matmul``'s W (of its plain product) from
     ``dC`` (slots x N): experts x K x N for ``layout=GEMM_B_ROW_MAJOR``,
     experts x N x K for ``GEMM_B_K_MAJOR``; zeros for an expert without slots."""
-    if A.dtype not in (torch.float16, torch.bfloat16):
+    if stream is not None:
+        return _under(stream, expert_weight_grad, A, dC, offsets, rows, layout=layout, out=out)
+    dt = A.dtype
+    if dt not in (torch.float16, torch.bfloat16):
         raise TypeError("A must be float16 or bfloat16")
     lda = _matrix(A, "A")
-    slots = A.shape[0] if rows is None else rows.numel()
+    a_rows, K = A.shape
+    slots = a_rows if rows is None else rows.numel()
     if dC.dim() != 2 or dC.shape[0] != slots:
         raise ValueError("dC must have one row per slot")
-    lddc = _matrix(dC, "dC", A.dtype)
-    N, K = dC.shape[1], A.shape[1]
+    lddc = _matrix(dC, "dC", dt)
+    N = dC.shape[1]
     experts = offsets.numel() - 1
     off = _vector(offsets, "offsets", torch.int32, experts + 1)
     r = _vector(rows, "rows", torch.int32, slots) if rows is not None else None
     shape = (experts, N, K) if layout == GEMM_B_K_MAJOR else (experts, K, N)
-    if out is not None and (out.dtype != A.dtype or tuple(out.shape) != shape):
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=A.device)
+    elif out.dtype is not dt or tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape[0]} x {shape[1]} x {shape[2]} of A's dtype")
-    lib = _load()
-    need = lib.gemm_grouped_wgrad_workspace(experts, slots, N, K, int(rows is not None))
-    s = gemm._raw_stream(stream, A.device.index)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=A.dtype, device=A.device)
-        ws = torch.empty((need,), dtype=torch.uint8, device=A.device) if need else None
+    need = _size("gemm_grouped_wgrad_workspace", experts, slots, N, K, int(rows is not None))
+    ws = torch.empty((need,), dtype=torch.uint8, device=A.device) if need else None
     ldw, stride_w = _stack(out, "out")
-    name = "gemm_f16_grouped_wgrad" if A.dtype == torch.float16 else "gemm_bf16_grouped_wgrad"
-    _check(getattr(lib, name)(experts, off, slots, N, K, A.data_ptr() or None, A.shape[0], lda, r,
-                              dC.data_ptr() or None, lddc, out.data_ptr() or None, ldw, stride_w, layout,
-                              ws.data_ptr() if need else None, need, s), name)
+    _call("gemm_f16_grouped_wgrad" if dt is torch.float16 else "gemm_bf16_grouped_wgrad", experts, off, slots, N, K,
+          A.data_ptr() or None, a_rows, lda, r, dC.data_ptr() or None, lddc, out.data_ptr() or None, ldw, stride_w,
+          layout, ws.data_ptr() if need else None, need, _stream(A))
     return out
 
 
@@ -403,6 +414,9 @@ def combine(z: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None =
             stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """y[t] = residual[t] + sum_j weights[t][j] * z[slots[t][j]] (slots of -1
     add nothing; weights None: all 1). ``out`` may be ``residual``."""
+    if stream is not None:
+        return _under(stream, combine, z, slots, weights, residual=residual, out=out)
+    dt = z.dtype
     code = _type(z, "z")
     ldz = _matrix(z, "z")
     if slots.dim() != 2:
@@ -411,17 +425,13 @@ def combine(z: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None =
     nslots, cols = z.shape
     i = _vector(slots, "slots", torch.int32, tokens * k)
     w = _vector(weights, "weights", torch.float32, tokens * k) if weights is not None else None
-    ldr = _matrix(residual, "residual", z.dtype, (tokens, cols)) if residual is not None else 0
-    s = gemm._raw_stream(stream, z.device.index)
+    ldr = _matrix(residual, "residual", dt, (tokens, cols)) if residual is not None else 0
     if out is None:
-        with _on(stream):
-            out = torch.empty((tokens, cols), dtype=z.dtype, device=z.device)
-        ldy = cols
+        out, ldy = torch.empty((tokens, cols), dtype=dt, device=z.device), cols
     else:
-        ldy = _matrix(out, "out", z.dtype, (tokens, cols))
-    _check(_load().gemm_combine(code, tokens, cols, k, z.data_ptr() or None, ldz, nslots, i, w,
-                                residual.data_ptr() if residual is not None else None, ldr, out.data_ptr() or None,
-                                ldy, s), "gemm_combine")
+        ldy = _matrix(out, "out", dt, (tokens, cols))
+    _call("gemm_combine", code, tokens, cols, k, z.data_ptr(), ldz, nslots, i, w,
+          residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(), ldy, _stream(z))
     return out
 
 
@@ -430,24 +440,24 @@ def combine_backward(dy: torch.Tensor, z: torch.Tensor, slots: torch.Tensor, wei
     """(dz, dweights) of ``combine``. ``offsets`` (``Routing.offsets``): rows of
     dz past offsets[-1] are set to zero; without it every row of z must belong
     to a slot. dweights is None where weights is."""
+    if stream is not None:
+        return _under(stream, combine_backward, dy, z, slots, weights, offsets)
+    dt = z.dtype
     code = _type(z, "z")
     ldz = _matrix(z, "z")
     if slots.dim() != 2:
         raise ValueError("slots must be T x k")
     tokens, k = slots.shape
     nslots, cols = z.shape
-    lddy = _matrix(dy, "dy", z.dtype, (tokens, cols))
+    lddy = _matrix(dy, "dy", dt, (tokens, cols))
     i = _vector(slots, "slots", torch.int32, tokens * k)
     w = _vector(weights, "weights", torch.float32, tokens * k) if weights is not None else None
     used = None
     if offsets is not None:
-        used = _vector(offsets, "offsets", torch.int32, offsets.numel()) + 4 * (offsets.numel() - 1)
-    s = gemm._raw_stream(stream, z.device.index)
-    with _on(stream):
-        dz = torch.empty((nslots, cols), dtype=z.dtype, device=z.device)
-        dw = torch.empty((tokens, k), dtype=torch.float32, device=z.device) if weights is not None else None
-    _check(_load().gemm_combine_backward(code, tokens, cols, k, dy.data_ptr() or None, lddy, z.data_ptr() or None, ldz,
-                                         nslots, i, w, used, dz.data_ptr() or None, cols,
-                                         dw.data_ptr() or None if dw is not None else None, s),
-           "gemm_combine_backward")
+        n = offsets.numel()
+        used = _vector(offsets, "offsets", torch.int32, n) + 4 * (n - 1)
+    dz = torch.empty((nslots, cols), dtype=dt, device=z.device)
+    dw = torch.empty((tokens, k), dtype=torch.float32, device=z.device) if weights is not None else None
+    _call("gemm_combine_backward", code, tokens, cols, k, dy.data_ptr(), lddy, z.data_ptr(), ldz, nslots, i, w, used,
+          dz.data_ptr(), cols, dw.data_ptr() if dw is not None else None, _stream(z))
     return dz, dw

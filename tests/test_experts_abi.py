@@ -31,8 +31,8 @@ def test_header_declarations_match_binding(lib):
 
 def test_workspace_sizes(lib):
     assert lib.gemm_route_workspace(0, 8, 2) == 0
-    assert lib.gemm_route_workspace(128, 64, 8) == 0          # one block does it all
-    assert lib.gemm_route_workspace(129, 64, 8) == 5 * 64 * 4  # five blocks of 32 tokens
+    assert lib.gemm_route_workspace(32, 64, 8) == 0          # one block does it all
+    assert lib.gemm_route_workspace(33, 64, 8) == 2 * 64 * 4  # blocks of 32 tokens
     assert lib.gemm_route_workspace(1 << 20, 64, 8) == 152 * 64 * 4
     assert lib.gemm_grouped_workspace(1, 4, 511, 64) == 0          # few rows a group: gathered on the way
     assert lib.gemm_grouped_workspace(1, 4, 512, 65) == 512 * 256  # rows of 130 bytes, 128-byte pitch
@@ -43,7 +43,8 @@ def test_workspace_sizes(lib):
     assert lib.gemm_grouped_wgrad_workspace(2, 0, 65, 64, 1) == 0
     assert lib.gemm_rmsnorm_backward_workspace(0, 64) == 0
     assert lib.gemm_rmsnorm_backward_workspace(3, 64) == 3 * 64 * 4
-    assert lib.gemm_rmsnorm_backward_workspace(10 ** 6, 64) == 304 * 64 * 4
+    assert lib.gemm_rmsnorm_backward_workspace(10 ** 6, 64) == 608 * 64 * 4
+    assert lib.gemm_rmsnorm_backward_workspace(10 ** 6, 5000) == 456 * 5000 * 4
 
 
 def _norm(lib, type=1, rows=2, cols=8, x=P, ldx=8, res=None, ldr=8, w=2 * P, h=None, ldh=8, y_type=1, y=3 * P, ldy=8,

@@ -73,7 +73,7 @@ def _close(got, want, s, fmt, factor=1e-5):
 
 # ---------------------------------------------------------------- norm
 
-NORM_SHAPES = [(1, 1), (1, 7), (3, 64), (2, 1000), (5, 4096), (300, 264), (33, 5120), (4, 8200), (2, 16384), (700, 96)]
+NORM_SHAPES = [(1, 1), (1, 7), (3, 64), (2, 1000), (5, 4096), (300, 264), (33, 5120), (4, 8200), (2, 16384), (700, 96), (3, 16383), (1500, 99), (9, 8191), (40, 1023)]
 
 
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES)
