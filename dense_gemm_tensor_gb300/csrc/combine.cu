@@ -6,9 +6,10 @@
 //
 // Bound by HBM: each row of z is read (and of dz written) once, by slot, as
 // whole rows, so the gather costs no extra bytes. `tpt` threads take a token,
-// 16 bytes of its columns each (single elements where base, pitch or width
-// do not allow); up to eight rows' loads are in flight per thread before the
-// first is added, and they are added in the order of j. The blocks stay on
+// 16 bytes of its columns each; up to eight rows' loads are in flight per
+// thread before the first is added, and they are added in the order of j. Rows
+// that are not whole 16-byte pieces: contiguous matrices go by the pieces of
+// the flat arrays (the *_flat kernels), anything else by single elements. The blocks stay on
 // their SMs and walk the tokens: a token's slots are loaded while the rows of
 // the one before are on their way, so that one memory latency, not two, stands
 // between a block and its rows.
@@ -35,15 +36,16 @@ struct CombineParams {
   long long work;       // groups of tokens x chunks
 };
 
-// Slots j0 .. j0 + kFlight - 1 of a token (-1: none) and their weights.
+// Slots j0 .. j0 + N - 1 of a token (-1: none) and their weights.
+template <int N>
 struct Picks {
-  int s[kFlight];
-  float w[kFlight];
+  int s[N];
+  float w[N];
 
   __device__ __forceinline__ void load(const int32_t* slots, const float* weights, long long token, int k, int j0,
                                        int nslots, bool in) {
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
+    for (int j = 0; j < N; ++j) {
       s[j] = -1;
       w[j] = 0.0f;
       if (in && j0 + j < k) {
@@ -61,11 +63,11 @@ __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const CombineParam
   using P = Pack<TYPE, VEC>;
   using T = typename P::T;
   grid_dependency_wait();
-  const int per_block = kThreads / p.tpt, sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
+  const int per_block = blockDim.x / p.tpt, sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const T* z = static_cast<const T*>(p.z);
   long long u = blockIdx.x;
   long long token = u / p.chunks * per_block + sub;
-  Picks now;
+  Picks<kFlight> now;
   now.load(p.slots, p.weights, token, p.k, 0, p.nslots, u < p.work && token < p.tokens);
   for (; u < p.work; u += gridDim.x) {
     const long long next = (u + gridDim.x) / p.chunks * per_block + sub;
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const CombineParam
     P res;
     res.zero();
     if (p.residual != nullptr && in) res.stream(static_cast<const T*>(p.residual) + token * p.ldr + col);
-    Picks ahead;
+    Picks<kFlight> ahead;
     for (int j0 = 0; j0 < p.k; j0 += kFlight) {
       P row[kFlight];
 #pragma unroll
@@ -119,7 +121,7 @@ struct CombineGradParams {
   float* dweights;
   long long lddy, ldz, lddz;
   int tokens, cols, k, nslots;
-  int tpt;  // threads per token, a power of two
+  int tpt;  // threads per token: 8, 16 or whole warps
 };
 
 // One group of tpt threads walks a token's columns, kFlight rows at a time:
@@ -131,13 +133,13 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
   __shared__ float part[2][kThreads / 32][kFlight];
   grid_dependency_wait();
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt, lane = threadIdx.x & 31;
-  const int per_block = kThreads / p.tpt;
+  const int per_block = blockDim.x / p.tpt;
   const T* z = static_cast<const T*>(p.z);
   T* dz = static_cast<T*>(p.dz);
   const long long step = static_cast<long long>(gridDim.x) * per_block;
   long long token = static_cast<long long>(blockIdx.x) * per_block + sub;
   int turn = 0;
-  Picks now;
+  Picks<kFlight> now;
   now.load(p.slots, p.weights, token, p.k, 0, p.nslots, token < p.tokens);
   for (long long first = static_cast<long long>(blockIdx.x) * per_block; first < p.tokens; first += step, token += step) {
     const bool in = token < p.tokens;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
 #pragma unroll
       for (int j = 0; j < kFlight; ++j) dot[j] = 0.0f;
       const bool last = j0 + kFlight >= p.k;
-      Picks ahead;
+      Picks<kFlight> ahead;
       ahead.load(p.slots, p.weights, last ? token + step : token, p.k, last ? 0 : j0 + kFlight, p.nslots,
                  last ? token + step < p.tokens : in);
       if (in) {
@@ -213,8 +215,222 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
     for (long long row = static_cast<long long>(used) + blockIdx.x; row < p.nslots; row += gridDim.x) {
       P o;
       o.zero();
-      for (int col = threadIdx.x * VEC; col < p.cols; col += kThreads * VEC) o.store(dz + row * p.lddz + col);
+      for (int col = threadIdx.x * VEC; col < p.cols; col += blockDim.x * VEC) o.store(dz + row * p.lddz + col);
     }
+  }
+  grid_launch_dependents();
+}
+
+// VEC consecutive elements from element f >= 0 of a flat array that starts on a
+// 16-byte boundary: the two 16-byte pieces that hold them, shifted together.
+// They must lie inside the array; `whole` says that the second piece does too
+// (else element by element). f mod VEC is the same in all threads of a token.
+template <int TYPE, int VEC>
+__device__ __forceinline__ void load_across(Pack<TYPE, VEC>& out, const typename Elem<TYPE>::T* base, long long f,
+                                            long long total) {
+  const int m = static_cast<int>(f % VEC);
+  const long long a = f - m;
+  if (m == 0) {
+    out.load(base + a);
+    return;
+  }
+  if (a + 2 * VEC > total) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out.v[i] = base[f + i];
+    return;
+  }
+  const uint4 lo = *reinterpret_cast<const uint4*>(base + a);
+  const uint4 hi = *reinterpret_cast<const uint4*>(base + a + VEC);
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  constexpr int PER_WORD = VEC / 4;  // elements of a word
+  const int r = (m % PER_WORD) * (32 / PER_WORD);
+  uint32_t* o = reinterpret_cast<uint32_t*>(out.v);
+  switch (m / PER_WORD) {
+    case 0:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k], w[k + 1], r);
+      break;
+    case 1:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 1], w[k + 2], r);
+      break;
+    case 2:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 2], w[k + 3], r);
+      break;
+    default:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 3], w[k < 3 ? k + 4 : 7], r);
+      break;
+  }
+}
+
+constexpr int kFlatFlight = 4;  // rows in flight of the flat kernels: each is two pieces
+
+// combine over contiguous matrices whose rows are not whole pieces: a thread
+// takes a 16-byte piece of the flat y; the row's first and last pieces, partly
+// other rows', go element by element.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 3) combine_flat_kernel(const CombineParams p) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = 16 / sizeof(T);
+  using P = Pack<TYPE, VEC>;
+  grid_dependency_wait();
+  const int per_block = blockDim.x / p.tpt, sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
+  const T* z = static_cast<const T*>(p.z);
+  const T* res = static_cast<const T*>(p.residual);
+  T* y = static_cast<T*>(p.y);
+  const long long total = static_cast<long long>(p.nslots) * p.cols;
+  for (long long u = blockIdx.x; u < p.work; u += gridDim.x) {
+    const long long token = u / p.chunks * per_block + sub;
+    if (token >= p.tokens) continue;
+    const long long row = token * p.cols;
+    const int lo = (int(u % p.chunks) * p.tpt + tid) * VEC - static_cast<int>(row % VEC);
+    if (lo >= p.cols) continue;
+    const bool inside = lo >= 0 && lo + VEC <= p.cols;
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += kFlatFlight) {
+      Picks<kFlatFlight> pick;
+      pick.load(p.slots, p.weights, token, p.k, j0, p.nslots, true);
+      P v[kFlatFlight];
+#pragma unroll
+      for (int j = 0; j < kFlatFlight; ++j) {
+        v[j].zero();
+        if (pick.s[j] < 0) continue;
+        const long long f = static_cast<long long>(pick.s[j]) * p.cols + lo;
+        if (inside) {
+          load_across<TYPE, VEC>(v[j], z, f, total);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (lo + i >= 0 && lo + i < p.cols) v[j].v[i] = z[f + i];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kFlatFlight; ++j)
+        if (j0 + j < p.k) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = fmaf(pick.w[j], v[j].get(i), acc[i]);
+        }
+    }
+    if (inside) {
+      if (res != nullptr) {
+        P r;
+        r.load(res + row + lo);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] += r.get(i);
+      }
+      P out;
+      out.set(acc);
+      out.store(y + row + lo);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (lo + i >= 0 && lo + i < p.cols) {
+          if (res != nullptr) acc[i] += Elem<TYPE>::get(res[row + lo + i]);
+          y[row + lo + i] = Elem<TYPE>::put(acc[i]);
+        }
+    }
+  }
+  grid_launch_dependents();
+}
+
+// Its gradient: a thread takes 16-byte pieces of the flat z and dz (a row of
+// both starts at the same place), and dy, which lies otherwise, from L1.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 3) combine_grad_flat_kernel(const CombineGradParams p) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = 16 / sizeof(T);
+  using P = Pack<TYPE, VEC>;
+  __shared__ float part[2][kThreads / 32][kFlatFlight];
+  grid_dependency_wait();
+  const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt, lane = threadIdx.x & 31;
+  const int per_block = blockDim.x / p.tpt;
+  const T* z = static_cast<const T*>(p.z);
+  const T* dy = static_cast<const T*>(p.dy);
+  T* dz = static_cast<T*>(p.dz);
+  const long long total = static_cast<long long>(p.tokens) * p.cols;
+  const int pieces = (p.cols + VEC - 1) / VEC + 1;  // that a row meets at most
+  int turn = 0;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * per_block; t0 < p.tokens;
+       t0 += static_cast<long long>(gridDim.x) * per_block) {
+    const long long token = t0 + sub;
+    const bool in = token < p.tokens;
+    for (int j0 = 0; j0 < p.k; j0 += kFlatFlight, turn ^= 1) {
+      Picks<kFlatFlight> pick;
+      pick.load(p.slots, p.weights, token, p.k, j0, p.nslots, in);
+      float dot[kFlatFlight];
+#pragma unroll
+      for (int j = 0; j < kFlatFlight; ++j) dot[j] = 0.0f;
+      for (int c = tid; c < pieces; c += p.tpt) {
+        P v[kFlatFlight], d[kFlatFlight];
+#pragma unroll
+        for (int j = 0; j < kFlatFlight; ++j) {
+          if (pick.s[j] < 0) continue;
+          const long long row = static_cast<long long>(pick.s[j]) * p.cols;
+          const int lo = c * VEC - static_cast<int>(row % VEC);
+          if (lo < 0 || lo + VEC > p.cols) continue;
+          v[j].zero();
+          if (p.dweights != nullptr) v[j].stream(z + row + lo);
+          load_across<TYPE, VEC>(d[j], dy, token * p.cols + lo, total);
+        }
+#pragma unroll
+        for (int j = 0; j < kFlatFlight; ++j) {
+          if (pick.s[j] < 0) continue;
+          const long long row = static_cast<long long>(pick.s[j]) * p.cols;
+          const int lo = c * VEC - static_cast<int>(row % VEC);
+          if (lo >= 0 && lo + VEC <= p.cols) {
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              o[i] = pick.w[j] * d[j].get(i);
+              dot[j] = fmaf(d[j].get(i), v[j].get(i), dot[j]);
+            }
+            P out;
+            out.set(o);
+            out.store(dz + row + lo);
+          } else if (lo < p.cols) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              if (lo + i >= 0 && lo + i < p.cols) {
+                const float g = Elem<TYPE>::get(dy[token * p.cols + lo + i]);
+                if (p.dweights != nullptr) dot[j] = fmaf(g, Elem<TYPE>::get(z[row + lo + i]), dot[j]);
+                dz[row + lo + i] = Elem<TYPE>::put(pick.w[j] * g);
+              }
+          }
+        }
+      }
+      if (p.dweights != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kFlatFlight; ++j)
+          for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1)
+            dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+        if (p.tpt > 32) {
+          if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < kFlatFlight; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
+          }
+          __syncthreads();
+          if (tid < kFlatFlight) {
+            float sum = 0.0f;
+            for (int i = 0; i < p.tpt >> 5; ++i) sum += part[turn][(threadIdx.x >> 5) + i][tid];
+            if (in && j0 + tid < p.k) p.dweights[token * p.k + j0 + tid] = sum;
+          }
+        } else if (in && tid == 0) {
+#pragma unroll
+          for (int j = 0; j < kFlatFlight; ++j)
+            if (j0 + j < p.k) p.dweights[token * p.k + j0 + j] = dot[j];
+        }
+      }
+    }
+  }
+  if (p.used != nullptr) {
+    const long long first = static_cast<long long>(max(*p.used, 0)) * p.cols, end = static_cast<long long>(p.nslots) * p.cols;
+    for (long long i = first + blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < end;
+         i += static_cast<long long>(gridDim.x) * blockDim.x)
+      dz[i] = Elem<TYPE>::put(0.0f);
   }
   grid_launch_dependents();
 }
@@ -232,11 +448,12 @@ bool meet(const void* a, int64_t rows_a, int64_t ld_a, const void* b, int64_t ro
   return a0 < b1 && b0 < a1;
 }
 
-// Threads per token: a power of two covering its vectors, eight to a whole block.
+// Threads per token: 8, 16 or whole warps that cover its pieces in as few equal passes as 256 threads allow.
 int threads_per_token(int64_t nvec) {
-  int t = 8;
-  while (t < kThreads && t < nvec) t *= 2;
-  return t;
+  if (nvec <= 8) return 8;
+  if (nvec <= 16) return 16;
+  const int64_t passes = (nvec + kThreads - 1) / kThreads;
+  return int(((nvec + passes - 1) / passes + 31) / 32 * 32);
 }
 
 constexpr int64_t kInt = (int64_t(1) << 31) - 1;
@@ -274,24 +491,32 @@ int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, i
   const int v = 16 / es;
   const bool vec = cols % v == 0 && (nslots == 0 || wide(z, ldz, es)) && wide(y, ldy, es) &&
                    (residual == nullptr || wide(residual, ldr, es));
-  const int64_t nvec = vec ? cols / v : cols;
+  auto flat_matrix = [&](const void* m, int64_t ld) {
+    return m == nullptr || (ld == cols && reinterpret_cast<uintptr_t>(m) % 16 == 0);
+  };
+  const bool flat = !vec && cols >= v && flat_matrix(z, ldz) && flat_matrix(y, ldy) && flat_matrix(residual, ldr);
+  const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
   CombineParams p = {z, slots, weights, residual, y, (long long)ldz, (long long)ldr, (long long)ldy, int(tokens),
                      int(cols), k, int(nslots), threads_per_token(nvec), 1, 0};
   p.chunks = int((nvec + p.tpt - 1) / p.tpt);
-  p.work = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt) * p.chunks;
-  const int64_t most = int64_t(ctx.sm_count) * 3;  // resident at once
+  const int block = kThreads / p.tpt * p.tpt;
+  p.work = (tokens + block / p.tpt - 1) / (block / p.tpt) * p.chunks;
+  const int64_t most = int64_t(ctx.sm_count) * (3 * kThreads / block);  // resident at once
   const int grid = int(p.work < most ? p.work : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == GEMM_TYPE_F16)
-    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_F16, 8>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_kernel<GEMM_TYPE_F16, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_F16, 8>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_F16>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_kernel<GEMM_TYPE_F16, 1>, grid, block, 0, s, 1, p);
   else if (type == GEMM_TYPE_BF16)
-    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_BF16, 8>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_kernel<GEMM_TYPE_BF16, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_BF16, 8>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_BF16>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_kernel<GEMM_TYPE_BF16, 1>, grid, block, 0, s, 1, p);
   else
-    e = vec ? launch_dependent(combine_kernel<GEMM_TYPE_F32, 4>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_kernel<GEMM_TYPE_F32, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_F32, 4>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_F32>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_kernel<GEMM_TYPE_F32, 1>, grid, block, 0, s, 1, p);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -322,23 +547,30 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
     if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
   const int v = 16 / es;
   const bool vec = cols % v == 0 && wide(dy, lddy, es) && wide(dz, lddz, es) && (dweights == nullptr || wide(z, ldz, es));
-  const int64_t nvec = vec ? cols / v : cols;
+  auto flat_matrix = [&](const void* m, int64_t ld) { return ld == cols && reinterpret_cast<uintptr_t>(m) % 16 == 0; };
+  const bool flat = !vec && cols >= v && flat_matrix(dy, lddy) && flat_matrix(dz, lddz) &&
+                    (dweights == nullptr || flat_matrix(z, ldz));
+  const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
   CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,
                          int(tokens), int(cols), k, int(nslots), threads_per_token(nvec)};
-  const int64_t need = (tokens + kThreads / p.tpt - 1) / (kThreads / p.tpt);
-  const int64_t most = int64_t(ctx.sm_count) * 3;  // resident at once
-  const int grid = int(need > 0 && need < most ? need : most);
+  const int block = kThreads / p.tpt * p.tpt;
+  const int64_t need = (tokens + block / p.tpt - 1) / (block / p.tpt);
+  // a block for each group of tokens (blocks that stay and walk the tokens: 189 against 180 us at 8192 x 8 x 4096)
+  const int grid = int(need > 0 ? need : ctx.sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == GEMM_TYPE_F16)
-    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 8>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 8>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_F16>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 1>, grid, block, 0, s, 1, p);
   else if (type == GEMM_TYPE_BF16)
-    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 8>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 8>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_BF16>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 1>, grid, block, 0, s, 1, p);
   else
-    e = vec ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 4>, grid, kThreads, 0, s, 1, p)
-            : launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 1>, grid, kThreads, 0, s, 1, p);
+    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 4>, grid, block, 0, s, 1, p)
+        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_F32>, grid, block, 0, s, 1, p)
+               : launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 1>, grid, block, 0, s, 1, p);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

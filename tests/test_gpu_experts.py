@@ -172,7 +172,7 @@ def _check_order(r, ids, experts_n):
     assert np.array_equal(r.slots.cpu().numpy(), slots)
 
 
-ROUTES = [(1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (5, 64, 8, 8, 3), (128, 100, 7, 1, 1), (129, 33, 3, 1, 1), (200, 256, 8, 8, 4),
+ROUTES = [(32, 1024, 32, 1, 1), (20000, 16, 3, 1, 1), (33, 256, 8, 4, 2), (1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (5, 64, 8, 8, 3), (128, 100, 7, 1, 1), (129, 33, 3, 1, 1), (200, 256, 8, 8, 4),
           (700, 500, 20, 5, 2), (150, 1024, 32, 32, 5), (2000, 16, 2, 16, 5)]
 
 
@@ -453,7 +453,7 @@ def test_long_outputs():
 # ---------------------------------------------------------------- combine
 
 @pytest.mark.parametrize("tokens,cols,k", [(1, 1, 1), (1, 64, 3), (5, 100, 8), (33, 1000, 9), (300, 2048, 2), (7, 4104, 32),
-                                            (64, 24, 6)])
+                                            (64, 24, 6), (40, 1001, 5), (9, 2051, 2), (3, 4099, 8), (100, 13, 4)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("pad", [0, 1])
 def test_combine_and_backward(tokens, cols, k, dtype, pad):
