@@ -1,4 +1,5 @@
-"""Builds the CUDA library ``libdgt_gemm.so`` in-tree with nvcc for sm_103a.
+"""Builds the CUDA library ``libdgt_gemm.so`` in-tree with nvcc for sm_103a,
+and with g++ the compiled Python binding ``_experts.so``.
 
 The translation units compile in parallel into ``_build/`` and link into
 ``dense_gemm_tensor_gb300/libdgt_gemm.so`` (CUDA runtime linked statically, so
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdgt_gemm.so")
+# The compiled binding of the mixture-of-experts operators (a Python module; it
+# links torch and takes the library's entry points from the loaded library).
+BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")
+BINDING = os.path.join(PKG, "_experts.so")
 # The checked build: every range check in the kernels compiled in (DGT_CHECKED=1).
 LIB_CHECKED = os.path.join(PKG, "libdgt_gemm_checked.so")
 
@@ -48,6 +54,26 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _build_binding(force: bool = False) -> None:
+    deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cxx = shutil.which("g++") or "c++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc, "-I", INCLUDE, BINDING_SRC,
+           "-o", BINDING + ".tmp", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
@@ -60,6 +86,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     build, ``libdgt_gemm_checked.so``); returns its path."""
     lib = LIB_CHECKED if checked else LIB
     if not force and up_to_date(lib):
+        _build_binding()
         return lib
     bdir = os.path.join(BUILD, "checked") if checked else BUILD
     os.makedirs(bdir, exist_ok=True)
@@ -79,7 +106,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_build_binding, force)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = lib + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

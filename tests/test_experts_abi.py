@@ -212,4 +212,16 @@ def test_python_refusals():
     with pytest.raises(TypeError):
         experts.combine(torch.zeros(2, 4, dtype=torch.int32), i32.view(3, 1))
     with pytest.raises(ValueError):
-        experts._config(2, "tanh", 1, 1, True, 1.0)
+        experts.route(torch.zeros(2, 4), 2, score="tanh")
+    with pytest.raises(TypeError):
+        experts.rms_norm([1.0], f16[0])
+    with pytest.raises(TypeError):
+        experts.rms_norm(f16, f16[0], out_dtype=torch.float32)
+
+
+def test_binding_takes_every_argument():
+    ext = experts._binding()
+    with pytest.raises(TypeError):
+        ext.rms_norm(torch.zeros(2, 8))
+    with pytest.raises(ValueError):
+        ext.bind({})
