@@ -124,8 +124,11 @@ struct CombineGradParams {
   int tpt;  // threads per token: 8, 16 or whole warps
 };
 
-// One group of tpt threads walks a token's columns, kFlight rows at a time:
-// dy stays in L1 between the passes of a token with more rows.
+// A block for each few tokens; tpt threads walk a token's columns, kFlight rows
+// at a time (dy stays in L1 between the passes of a token with more rows). With
+// many tokens a thread takes several pieces of each row, so that the slots and
+// the dots' reductions cost it less (one piece each: 24 instructions an element,
+// 55 us for 4099 tokens x 6 x 2048 BF16).
 template <int TYPE, int VEC>
 __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const CombineGradParams p) {
   using P = Pack<TYPE, VEC>;
@@ -136,77 +139,70 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
   const int per_block = blockDim.x / p.tpt;
   const T* z = static_cast<const T*>(p.z);
   T* dz = static_cast<T*>(p.dz);
-  const long long step = static_cast<long long>(gridDim.x) * per_block;
-  long long token = static_cast<long long>(blockIdx.x) * per_block + sub;
+  const long long token = static_cast<long long>(blockIdx.x) * per_block + sub;
+  const bool in = token < p.tokens;
   int turn = 0;
-  Picks<kFlight> now;
-  now.load(p.slots, p.weights, token, p.k, 0, p.nslots, token < p.tokens);
-  for (long long first = static_cast<long long>(blockIdx.x) * per_block; first < p.tokens; first += step, token += step) {
-    const bool in = token < p.tokens;
-    for (int j0 = 0; j0 < p.k; j0 += kFlight, turn ^= 1) {
-      float dot[kFlight];
+  for (int j0 = 0; j0 < p.k; j0 += kFlight, turn ^= 1) {
+    Picks<kFlight> pick;
+    pick.load(p.slots, p.weights, token, p.k, j0, p.nslots, in);
+    float dot[kFlight];
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j) dot[j] = 0.0f;
-      const bool last = j0 + kFlight >= p.k;
-      Picks<kFlight> ahead;
-      ahead.load(p.slots, p.weights, last ? token + step : token, p.k, last ? 0 : j0 + kFlight, p.nslots,
-                 last ? token + step < p.tokens : in);
-      if (in) {
-        for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
-          P d;
-          d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
-          P row[kFlight];
-          if (p.dweights != nullptr) {
-#pragma unroll
-            for (int j = 0; j < kFlight; ++j) {
-              row[j].zero();
-              if (now.s[j] >= 0) row[j].stream(z + now.s[j] * p.ldz + col);
-            }
-          }
+    for (int j = 0; j < kFlight; ++j) dot[j] = 0.0f;
+    if (in) {
+      for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
+        P d;
+        d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
+        P row[kFlight];
+        if (p.dweights != nullptr) {
 #pragma unroll
           for (int j = 0; j < kFlight; ++j)
-            if (now.s[j] >= 0) {
-              float o[VEC];
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) o[i] = now.w[j] * d.get(i);
-              P out;
-              out.set(o);
-              out.store(dz + now.s[j] * p.lddz + col);
-            }
-          if (p.dweights != nullptr) {
-#pragma unroll
-            for (int j = 0; j < kFlight; ++j)
-              if (now.s[j] >= 0) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) dot[j] = fmaf(d.get(i), row[j].get(i), dot[j]);
-              }
-          }
+            if (pick.s[j] >= 0) row[j].stream(z + pick.s[j] * p.ldz + col);
         }
-      }
-      if (p.dweights != nullptr) {
+        float g[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) g[i] = d.get(i);
 #pragma unroll
         for (int j = 0; j < kFlight; ++j)
-          for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1)
-            dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
-        if (p.tpt > 32) {
-          // (the two halves of `part` alternate: one barrier a pass is enough)
-          if (lane == 0) {
+          if (pick.s[j] >= 0) {
+            float o[VEC];
 #pragma unroll
-            for (int j = 0; j < kFlight; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
+            for (int i = 0; i < VEC; ++i) o[i] = pick.w[j] * g[i];
+            P out;
+            out.set(o);
+            out.store(dz + pick.s[j] * p.lddz + col);
           }
-          __syncthreads();
-          if (tid < kFlight) {
-            float sum = 0.0f;
-            for (int i = 0; i < p.tpt >> 5; ++i) sum += part[turn][(threadIdx.x >> 5) + i][tid];
-            if (in && j0 + tid < p.k) p.dweights[token * p.k + j0 + tid] = sum;
-          }
-        } else if (in && tid == 0) {
+        if (p.dweights != nullptr) {
 #pragma unroll
           for (int j = 0; j < kFlight; ++j)
-            if (j0 + j < p.k) p.dweights[token * p.k + j0 + j] = dot[j];
+            if (pick.s[j] >= 0) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) dot[j] = fmaf(g[i], row[j].get(i), dot[j]);
+            }
         }
       }
-      now = ahead;
+    }
+    if (p.dweights != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j)
+        for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1)
+          dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+      if (p.tpt > 32) {
+        // (the two halves of `part` alternate: one barrier a pass is enough)
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
+        }
+        __syncthreads();
+        if (tid < kFlight) {
+          float sum = 0.0f;
+          for (int i = 0; i < p.tpt >> 5; ++i) sum += part[turn][(threadIdx.x >> 5) + i][tid];
+          if (in && j0 + tid < p.k) p.dweights[token * p.k + j0 + tid] = sum;
+        }
+      } else if (in && tid == 0) {
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          if (j0 + j < p.k) p.dweights[token * p.k + j0 + j] = dot[j];
+      }
     }
   }
   // rows of dz that no pair owns
@@ -221,10 +217,40 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
   grid_launch_dependents();
 }
 
+// 16 bytes from element s (0 .. VEC) of the 32 that w holds; VEC elements are 16
+// bytes. s is the same in every lane that calls this together.
+template <int VEC>
+__device__ __forceinline__ void shift_pieces(const uint32_t (&w)[8], int s, uint32_t* o) {
+  constexpr int PER_WORD = VEC / 4;  // elements of a word
+  const int r = (s % PER_WORD) * (32 / PER_WORD);
+  switch (s / PER_WORD) {
+    case 0:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k], w[k + 1], r);
+      break;
+    case 1:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 1], w[k + 2], r);
+      break;
+    case 2:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 2], w[k + 3], r);
+      break;
+    case 3:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 3], w[k < 3 ? k + 4 : 7], r);
+      break;
+    default:
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = w[k + 4];
+      break;
+  }
+}
+
 // VEC consecutive elements from element f >= 0 of a flat array that starts on a
-// 16-byte boundary: the two 16-byte pieces that hold them, shifted together.
-// They must lie inside the array; `whole` says that the second piece does too
-// (else element by element). f mod VEC is the same in all threads of a token.
+// 16-byte boundary: the two 16-byte pieces that hold them, shifted together
+// (element by element where the second piece would run past the array's
+// `total` elements). f mod VEC is the same in every lane that calls this together.
 template <int TYPE, int VEC>
 __device__ __forceinline__ void load_across(Pack<TYPE, VEC>& out, const typename Elem<TYPE>::T* base, long long f,
                                             long long total) {
@@ -242,27 +268,7 @@ __device__ __forceinline__ void load_across(Pack<TYPE, VEC>& out, const typename
   const uint4 lo = *reinterpret_cast<const uint4*>(base + a);
   const uint4 hi = *reinterpret_cast<const uint4*>(base + a + VEC);
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  constexpr int PER_WORD = VEC / 4;  // elements of a word
-  const int r = (m % PER_WORD) * (32 / PER_WORD);
-  uint32_t* o = reinterpret_cast<uint32_t*>(out.v);
-  switch (m / PER_WORD) {
-    case 0:
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k], w[k + 1], r);
-      break;
-    case 1:
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 1], w[k + 2], r);
-      break;
-    case 2:
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 2], w[k + 3], r);
-      break;
-    default:
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k + 3], w[k < 3 ? k + 4 : 7], r);
-      break;
-  }
+  shift_pieces<VEC>(w, m, reinterpret_cast<uint32_t*>(out.v));
 }
 
 constexpr int kFlatFlight = 4;  // rows in flight of the flat kernels: each is two pieces
@@ -291,29 +297,33 @@ __global__ void __launch_bounds__(kThreads, 3) combine_flat_kernel(const Combine
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += kFlatFlight) {
-      Picks<kFlatFlight> pick;
+    for (int j0 = 0; j0 < p.k; j0 += kFlight) {
+      Picks<kFlight> pick;
       pick.load(p.slots, p.weights, token, p.k, j0, p.nslots, true);
-      P v[kFlatFlight];
 #pragma unroll
-      for (int j = 0; j < kFlatFlight; ++j) {
-        v[j].zero();
-        if (pick.s[j] < 0) continue;
-        const long long f = static_cast<long long>(pick.s[j]) * p.cols + lo;
-        if (inside) {
-          load_across<TYPE, VEC>(v[j], z, f, total);
-        } else {
+      for (int h = 0; h < kFlight; h += kFlatFlight) {
+        if (j0 + h >= p.k) break;
+        P v[kFlatFlight];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (lo + i >= 0 && lo + i < p.cols) v[j].v[i] = z[f + i];
+        for (int j = 0; j < kFlatFlight; ++j) {
+          v[j].zero();
+          if (pick.s[h + j] < 0) continue;
+          const long long f = static_cast<long long>(pick.s[h + j]) * p.cols + lo;
+          if (inside) {
+            load_across<TYPE, VEC>(v[j], z, f, total);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              if (lo + i >= 0 && lo + i < p.cols) v[j].v[i] = z[f + i];
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kFlatFlight; ++j)
+          if (j0 + h + j < p.k) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] = fmaf(pick.w[h + j], v[j].get(i), acc[i]);
+          }
       }
-#pragma unroll
-      for (int j = 0; j < kFlatFlight; ++j)
-        if (j0 + j < p.k) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[i] = fmaf(pick.w[j], v[j].get(i), acc[i]);
-        }
     }
     if (inside) {
       if (res != nullptr) {
@@ -448,11 +458,12 @@ bool meet(const void* a, int64_t rows_a, int64_t ld_a, const void* b, int64_t ro
   return a0 < b1 && b0 < a1;
 }
 
-// Threads per token: 8, 16 or whole warps that cover its pieces in as few equal passes as 256 threads allow.
-int threads_per_token(int64_t nvec) {
+// Threads per token: 8, 16 or whole warps that cover its pieces in as few equal
+// passes as 256 threads allow, or in `passes` where that is more.
+int threads_per_token(int64_t nvec, int64_t passes = 1) {
   if (nvec <= 8) return 8;
   if (nvec <= 16) return 16;
-  const int64_t passes = (nvec + kThreads - 1) / kThreads;
+  if (passes < (nvec + kThreads - 1) / kThreads) passes = (nvec + kThreads - 1) / kThreads;
   return int(((nvec + passes - 1) / passes + 31) / 32 * 32);
 }
 
@@ -501,7 +512,8 @@ int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, i
   p.chunks = int((nvec + p.tpt - 1) / p.tpt);
   const int block = kThreads / p.tpt * p.tpt;
   p.work = (tokens + block / p.tpt - 1) / (block / p.tpt) * p.chunks;
-  const int64_t most = int64_t(ctx.sm_count) * (3 * kThreads / block);  // resident at once
+  // as many blocks as are resident at once; the flat kernel has nothing to load ahead and takes a block for each group
+  const int64_t most = flat ? kInt : int64_t(ctx.sm_count) * (3 * kThreads / block);
   const int grid = int(p.work < most ? p.work : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -551,11 +563,13 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
   const bool flat = !vec && cols >= v && flat_matrix(dy, lddy) && flat_matrix(dz, lddz) &&
                     (dweights == nullptr || flat_matrix(z, ldz));
   const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
+  // four pieces a thread once the tokens fill the GPU's threads that way
+  const int64_t passes = tokens * nvec >= int64_t(ctx.sm_count) * kThreads * 3 * 4 ? 4 : 1;
   CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,
-                         int(tokens), int(cols), k, int(nslots), threads_per_token(nvec)};
+                         int(tokens), int(cols), k, int(nslots), threads_per_token(nvec, passes)};
   const int block = kThreads / p.tpt * p.tpt;
   const int64_t need = (tokens + block / p.tpt - 1) / (block / p.tpt);
-  // a block for each group of tokens (blocks that stay and walk the tokens: 189 against 180 us at 8192 x 8 x 4096)
+  // a block for each few tokens
   const int grid = int(need > 0 ? need : ctx.sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
