@@ -82,6 +82,8 @@ struct Pack {
       return E::get(v[i]);
     }
   }
+  // Elements i and i + 1.
+  __device__ __forceinline__ float2 two(int i) const { return make_float2(get(i), get(i + 1)); }
   // All elements from fp32, rounded to nearest even, two at a time.
   __device__ __forceinline__ void set(const float (&x)[VEC]) {
     if constexpr (VEC == 1 || TYPE == GEMM_TYPE_F32) {
@@ -123,28 +125,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   return v;
-}
-
-// Sum (or, of non-negative bit patterns, maximum) over the `tpr` consecutive
-// threads of a row (a power of two; each row's threads start at a multiple of
-// it). All threads of the block call it together; `red` holds a value per warp
-// and is not written again by the caller's next reduction (it alternates).
-__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
-  for (int d = (tpr < 32 ? tpr : 32) >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if (tpr <= 32) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int warps = tpr >> 5, w0 = (threadIdx.x / tpr) * warps;
-  float s = (threadIdx.x & 31) < warps ? red[w0 + (threadIdx.x & 31)] : 0.0f;
-  return warp_sum(s);
-}
-__device__ __forceinline__ uint32_t row_max_bits(uint32_t v, int tpr, uint32_t* red) {
-  for (int d = (tpr < 32 ? tpr : 32) >> 1; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  if (tpr <= 32) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int warps = tpr >> 5, w0 = (threadIdx.x / tpr) * warps;
-  return __reduce_max_sync(0xFFFFFFFFu, (threadIdx.x & 31) < warps ? red[w0 + (threadIdx.x & 31)] : 0u);
 }
 
 }  // namespace dgt

@@ -131,6 +131,32 @@ __device__ __forceinline__ void stage_weights(typename Elem<TYPE>::T* shared, co
   __syncthreads();
 }
 
+// Reductions over the `warps` warps of a row, of which the first is the block's
+// warp w0. All threads of the block call them together; `red` holds a value per
+// warp and is not written again by the caller's next reduction (it alternates).
+struct RowWarps {
+  int warps, w0;
+  __device__ __forceinline__ RowWarps(int tpr, int sub) : warps(tpr >> 5), w0(sub * (tpr >> 5)) {}
+  __device__ __forceinline__ float sum(float v, float* red) const {
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(lane < warps ? red[w0 + lane] : 0.0f);
+  }
+  // the largest of non-negative bit patterns
+  __device__ __forceinline__ uint32_t max_bits(uint32_t v, float* red_) const {
+    uint32_t* red = reinterpret_cast<uint32_t*>(red_);
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xFFFFFFFFu, lane < warps ? red[w0 + lane] : 0u);
+  }
+};
+
 struct NormParams {
   const void* x;
   const void* residual;
@@ -156,6 +182,7 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
   T* shared_w = reinterpret_cast<T*>(dynamic);
   const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
   Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const RowWarps row_warps(p.tpr, sub);
   grid_dependency_wait();
   if constexpr (MODE == FLAT) stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
   int turn = 0;
@@ -185,7 +212,7 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss += h[i].get(j) * h[i].get(j);
-    ss = row_sum(ss, p.tpr, red[turn][0]);
+    ss = row_warps.sum(ss, red[turn][0]);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.cols) + p.eps);
     if (p.rstd != nullptr && in && r.tid == 0) p.rstd[row] = rstd;
     if constexpr (!Q8) {
@@ -209,7 +236,7 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
 #pragma unroll
         for (int j = 0; j < VEC; ++j) top = max(top, __float_as_uint(h[i].get(j) * rstd * w[j]) & 0x7FFFFFFFu);
       }
-      const float amax = __uint_as_float(row_max_bits(top, p.tpr, reinterpret_cast<uint32_t*>(red[turn][1])));
+      const float amax = __uint_as_float(row_warps.max_bits(top, red[turn][1]));
       const float scale = (amax < 1e-12f ? 1e-12f : amax) / kE4M3Max;
       const float inv = 1.0f / scale;
       if (in && r.tid == 0) p.scale[row] = scale;
@@ -250,7 +277,11 @@ struct NormGradParams {
 // ALIGNED with AHEAD: each thread copies its pieces of the next row to its own
 // places in shared memory (cp.async) before it works on this one, so that loads
 // are in flight during the reduction and the stores, and nothing but the thread
-// itself waits for them. (Without: 8192 x 4096 BF16 took 60-73 us.)
+// itself waits for them (without: 8192 x 4096 BF16 took 60-73 us). It reads a
+// piece from its place once for the sums and once for the output, so that
+// registers hold one piece at a time, and has the next row's rstd loaded: with
+// the row in registers the same took 58 us, 4097 x 5120 37.6 us. Now 51.7 us
+// (5.2 TB/s) and 34.7 us (4.8 TB/s), of which the second launch is 4 us.
 template <int TYPE, int MODE, bool AHEAD>
 __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kernel(const NormGradParams p) {
   constexpr int EPT = kGradEpt;
@@ -266,33 +297,42 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
   const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
   T* shared_w = reinterpret_cast<T*>(sums + per_block * places);
   Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
-  const int streams = p.dh != nullptr ? 3 : 2;
+  const RowWarps row_warps(p.tpr, sub);
   const long long step = static_cast<long long>(gridDim.x) * per_block;
-  // AHEAD: piece i of stream m of stage s
-  auto cell = [&](int s, int m, int i) { return dynamic + ((s * streams + m) * NV + i) * blockDim.x + threadIdx.x; };
+  // AHEAD: piece i of h, dy or dh (m = 0, 1, 2) of stage s
+  auto cell = [&](int s, int m, int i) { return dynamic + ((s * 3 + m) * NV + i) * blockDim.x + threadIdx.x; };
   auto fetch = [&](long long row, int s) {
-    if (row < p.rows) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (r.whole(i)) {
+    for (int i = 0; i < NV; ++i)
+      if (r.whole(i)) {
+        if (row < p.rows) {
           copy16(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i));
           copy16(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i));
-          if (streams == 3) copy16(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i));
+          if (p.dh != nullptr) copy16(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i));
+        } else if (per_block > 1) {  // a row past the last one counts as zeros
+          *cell(s, 0, i) = *cell(s, 1, i) = make_uint4(0u, 0u, 0u, 0u);
         }
-    }
+      }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  const long long start = static_cast<long long>(blockIdx.x) * per_block + sub;
   grid_dependency_wait();
-  if constexpr (AHEAD) fetch(static_cast<long long>(blockIdx.x) * per_block + sub, 0);
-  float dw[MODE == FLAT ? 1 : NV][VEC];
+  if constexpr (AHEAD) {
+    // zeros where no copy lands: past the last column, and dh where there is none
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      for (int c = 0; c < 6; ++c)
+        if (!r.whole(i) || (c % 3 == 2 && p.dh == nullptr)) *cell(c / 3, c % 3, i) = make_uint4(0u, 0u, 0u, 0u);
+    fetch(start, 0);
+  }
+  float rstd_ahead = AHEAD && start < p.rows ? p.rstd[start] : 0.0f;
+  float2 dw[MODE == FLAT ? 1 : EPT / 2];  // element e of the thread's EPT: half e & 1 of dw[e / 2]
   if constexpr (MODE == FLAT) {
     for (int i = threadIdx.x; i < per_block * places; i += blockDim.x) sums[i] = 0.0f;
     stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) dw[i][j] = 0.0f;
+    for (int e = 0; e < EPT / 2; ++e) dw[e] = make_float2(0.0f, 0.0f);
   }
   int turn = 0;
   for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows; r0 += step, turn ^= 1) {
@@ -303,17 +343,6 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
     if constexpr (AHEAD) {
       fetch(row + step, turn ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row's pieces have landed
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        h[i].zero();
-        dy[i].zero();
-        dh[i].zero();
-        if (in && r.whole(i)) {
-          h[i].load(reinterpret_cast<const T*>(cell(turn, 0, i)));
-          dy[i].load(reinterpret_cast<const T*>(cell(turn, 1, i)));
-          if (streams == 3) dh[i].load(reinterpret_cast<const T*>(cell(turn, 2, i)));
-        }
-      }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -328,35 +357,68 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
         for (int i = 0; i < NV; ++i) dh[i].zero();
       }
     }
+    // AHEAD: a piece from its place, once for each use: registers hold one piece at a time, not the row's
+    auto take = [&](P(&v)[NV], int m, int i) {
+      if constexpr (AHEAD) v[i].load(reinterpret_cast<const T*>(cell(turn, m, i)));
+    };
     // with the row's rstd taken out of the sums: mean(g xhat) = rstd * mean(g h), dw += (dy rstd) h,
-    // dx = rstd g - (rstd^3 mean(g h)) h + dh
-    const float rstd = in ? p.rstd[row] : 0.0f;
+    // dx = rstd g - (rstd^3 mean(g h)) h + dh; ALIGNED takes two elements to an instruction
+    const float rstd = AHEAD ? rstd_ahead : in ? p.rstd[row] : 0.0f;
+    if constexpr (AHEAD) rstd_ahead = row + step < p.rows ? p.rstd[row + step] : 0.0f;
+    float2 dots = make_float2(0.0f, 0.0f);  // ALIGNED
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float w[VEC];
       load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      take(h, 0, i);
+      take(dy, 1, i);
+      if constexpr (MODE == ALIGNED) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float hv = h[i].get(j), d = dy[i].get(j);
-        dot = fmaf(d * w[j], hv, dot);
-        if constexpr (MODE == FLAT) {
-          const int c = r.lo(i) + j;
-          if (in && c >= 0 && c < p.cols) sums[sub * places + r.place(i, j)] += d * rstd * hv;
-        } else {
-          dw[i][j] = fmaf(d * rstd, hv, dw[i][j]);
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 hv = h[i].two(j), d = dy[i].two(j);
+          dots = __ffma2_rn(__fmul2_rn(d, make_float2(w[j], w[j + 1])), hv, dots);
+          float2& sum = dw[(i * VEC + j) / 2];
+          sum = __ffma2_rn(__fmul2_rn(d, make_float2(rstd, rstd)), hv, sum);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float hv = h[i].get(j), d = dy[i].get(j);
+          dot = fmaf(d * w[j], hv, dot);
+          if constexpr (MODE == FLAT) {
+            const int c = r.lo(i) + j;
+            if (in && c >= 0 && c < p.cols) sums[sub * places + r.place(i, j)] += d * rstd * hv;
+          } else {
+            float& sum = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+            sum = fmaf(d * rstd, hv, sum);
+          }
         }
       }
     }
-    const float back = rstd * rstd * rstd * (row_sum(dot, p.tpr, red[turn]) / static_cast<float>(p.cols));
+    const float back = rstd * rstd * rstd * (row_warps.sum(MODE == ALIGNED ? dots.x + dots.y : dot, red[turn]) / static_cast<float>(p.cols));
     if (MODE == FLAT && p.tpr <= 32) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float w[VEC];
       load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      take(h, 0, i);
+      take(dy, 1, i);
+      take(dh, 2, i);
       P o;
+      if constexpr (MODE == ALIGNED) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) w[j] = fmaf(dy[i].get(j) * w[j], rstd, fmaf(h[i].get(j), -back, dh[i].get(j)));
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 g = __fmul2_rn(dy[i].two(j), make_float2(w[j], w[j + 1]));
+          const float2 v = __ffma2_rn(g, make_float2(rstd, rstd),
+                                      __ffma2_rn(h[i].two(j), make_float2(-back, -back), dh[i].two(j)));
+          w[j] = v.x;
+          w[j + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] = fmaf(dy[i].get(j) * w[j], rstd, fmaf(h[i].get(j), -back, dh[i].get(j)));
+      }
       o.set(w);
       r.store(o, p.dx, row, p.lddx, i, in);
     }
@@ -372,42 +434,32 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
       out[c] = s;
     }
   } else {
-    // the block's sum over its rows, in row order
+    // the block's sum over its rows, in row order; four columns a store
+    constexpr int RUN = VEC < 4 ? 1 : 4;
+    auto each = [&](auto use) {
+#pragma unroll
+      for (int e = 0; e < EPT; e += RUN)
+        if (r.whole(e / VEC)) use(r.lo(e / VEC) + e % VEC, e);
+    };
+    auto value = [&](int e) -> float& { return e & 1 ? dw[e / 2].y : dw[e / 2].x; };
+    auto store = [&](float* to, int e) {
+      if constexpr (RUN == 1)
+        *to = value(e);
+      else
+        *reinterpret_cast<float4*>(to) = make_float4(value(e), value(e + 1), value(e + 2), value(e + 3));
+    };
     if (per_block > 1) {
       __syncthreads();
-      if (sub > 0) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (r.whole(i)) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) sums[(sub - 1) * p.cols + r.lo(i) + j] = dw[i][j];
-          }
-      }
+      if (sub > 0) each([&](int c, int e) { store(sums + (sub - 1) * p.cols + c, e); });
       __syncthreads();
-      if (sub == 0) {
+      if (sub == 0)
         for (int s = 0; s + 1 < per_block; ++s)
+          each([&](int c, int e) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (r.whole(i)) {
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) dw[i][j] += sums[s * p.cols + r.lo(i) + j];
-            }
-      }
+            for (int k = 0; k < RUN; ++k) value(e + k) += sums[s * p.cols + c + k];
+          });
     }
-    if (sub == 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (r.whole(i)) {
-          if constexpr (VEC == 1) {
-            out[r.lo(i)] = dw[i][0];
-          } else {
-#pragma unroll
-            for (int j = 0; j < VEC; j += 4)
-              *reinterpret_cast<float4*>(out + r.lo(i) + j) =
-                  make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
-          }
-        }
-    }
+    if (sub == 0) each([&](int c, int e) { store(out + c, e); });
   }
   grid_launch_dependents();
 }
@@ -490,7 +542,7 @@ cudaError_t launch_norm(const NormParams& p, int mode, bool few, bool q8, int gr
 size_t grad_smem(const NormGradParams& p, int mode, bool ahead, int block, int es) {
   if (mode == FLAT) return size_t(p.cols + 8) * (size_t(block / p.tpr) * sizeof(float) + es);
   const size_t sums = size_t(block / p.tpr - 1) * size_t(p.cols) * sizeof(float);
-  const size_t stages = ahead ? size_t(2) * (p.dh != nullptr ? 3 : 2) * kGradEpt * es * size_t(block) : 0;
+  const size_t stages = ahead ? size_t(2 * 3) * kGradEpt * es * size_t(block) : 0;
   return sums > stages ? sums : stages;
 }
 
