@@ -37,6 +37,7 @@
 // stores silu(gate) * value, so the 2 x wider intermediate is never written.
 #pragma once
 
+#include "dgt_experts.h"
 #include "gemm_kernel.cuh"
 
 namespace dgt {
@@ -241,24 +242,75 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
         }
       }
     }
+  } else if (full_cols) {
+    // Rows of any 2-byte alignment: 8 lanes a row store the 16-byte pieces that lie whole in the row's 128 bytes,
+    // each shifted together from two staged chunks, and a lane each the eight columns around them.
+    const int l = lane & 7;
+#pragma unroll
+    for (int rr = 0; rr < 32; rr += 4) {
+      const int r = rr + (lane >> 3);
+      uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc;
+      const int m = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 7;  // columns past a 16-byte boundary
+      uint32_t w[8];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(stage_chunk(stage, r, l))
+                   : "memory");
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "r"(stage_chunk(stage, r, (l + 1) & 7))
+                   : "memory");
+      const int edge = l < 8 - m ? l : 56 + l;
+      const uint32_t one = ld_shared_u16(stage_chunk(stage, r, edge >> 3) + ((edge & 7) << 1));
+      if (row0 + r >= row_end) continue;
+      if (m == 0) {
+        *reinterpret_cast<uint4*>(dst + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+        continue;
+      }
+      // columns 8 l + 8 - m .. 8 l + 15 - m: element 8 - m of the two chunks
+      const int s = 8 - m, q = s >> 1, bits = (s & 1) * 16;
+      uint32_t a[6], b[5];
+#pragma unroll
+      for (int k = 0; k < 6; ++k) a[k] = q & 2 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) b[k] = q & 1 ? a[k + 1] : a[k];
+      if (l < 7)
+        *reinterpret_cast<uint4*>(dst + 8 * l + s) =
+            make_uint4(__funnelshift_r(b[0], b[1], bits), __funnelshift_r(b[1], b[2], bits),
+                       __funnelshift_r(b[2], b[3], bits), __funnelshift_r(b[3], b[4], bits));
+      dst[edge] = static_cast<uint16_t>(one);
+    }
   } else {
-    // a row at a time, two columns a lane
+    // the matrix's last columns: a row at a time, two columns a lane
     const int col = col0 + 2 * lane;
 #pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       const uint32_t v = ld_shared_u32(stage_chunk(stage, r, lane >> 2) + ((lane & 3) << 2));
       if (row0 + r < row_end && col < p.out_cols) {
         uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 2 * lane;
-        if (p.g.c_gran >= 4 && col + 1 < p.out_cols) {
-          *reinterpret_cast<uint32_t*>(dst) = v;
-        } else {
-          dst[0] = static_cast<uint16_t>(v & 0xFFFFu);
-          if (col + 1 < p.out_cols) dst[1] = static_cast<uint16_t>(v >> 16);
-        }
+        dst[0] = static_cast<uint16_t>(v & 0xFFFFu);
+        if (col + 1 < p.out_cols) dst[1] = static_cast<uint16_t>(v >> 16);
       }
     }
   }
   __syncwarp();
+}
+
+// The activation of every element. GELU's tanh form is v / (1 + exp(-2 u)) with
+// u = sqrt(2 / pi) (v + 0.044715 v^3); like the gated SiLU it takes the hardware's
+// exponential and reciprocal, both within a few 2^-22 of the value, far inside
+// the 2^-9 (2^-11) to which the result is rounded next (with tanhf the epilogue
+// of a 256-wide tile took about 15000 cycles).
+__device__ __forceinline__ void group_activate(float (&v)[32], int act) {
+  if (act == GEMM_ACT_GELU_TANH) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float u = 0.79788456080286536f * (v[k] + 0.044715f * v[k] * v[k] * v[k]);
+      v[k] = __fdividef(v[k], 1.0f + __expf(-2.0f * u));
+    }
+  } else {
+    epi_activate(v, act);
+  }
 }
 
 template <bool PAIR>
@@ -618,14 +670,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
               float v[32];
               group_scale<KIND>(p, t.e, col0 + cc, lane, scale, r, v);
               if constexpr (GATED) {
-                // silu(g) u with the hardware's exponential and reciprocal: both are within a few 2^-22 of
-                // the value, far inside the 2^-9 to which the result is rounded next
                 float u[32];
                 group_scale<KIND>(p, t.e, p.g.N / 2 + col0 + cc, lane, scale, acc[1], u);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = __fdividef(v[k], 1.0f + __expf(-v[k])) * u[k];
               } else {
-                epi_activate(v, p.g.act);
+                group_activate(v, p.g.act);
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j)
