@@ -17,6 +17,11 @@ bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p
 // TMA reads rows whose base and pitch are 16-byte multiples.
 bool tma_rows(const void* p, int64_t ld, int es) { return !misaligned(p, 16) && (ld * es) % 16 == 0; }
 
+// The pitch of a matrix of one row says nothing: any is as good as the next 16-byte multiple.
+int64_t row_pitch(int64_t rows, int64_t cols, int64_t ld, int es) {
+  return rows == 1 && ld >= cols ? (cols * es + 15) / 16 * 16 / es : ld;
+}
+
 // Widest store (16, 8, 4 or 2 bytes) that base, row pitch and matrix stride of a 16-bit matrix allow.
 int store_granularity(const void* p, int64_t ld, int64_t stride) {
   const uint64_t v = uint64_t(reinterpret_cast<uintptr_t>(p)) | uint64_t(ld * 2) | uint64_t(stride * 2);
@@ -162,6 +167,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
       return GEMM_ERR_INVALID_VALUE;
   }
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
+  lda = row_pitch(a_rows, K, lda, es);
   const void* bias = epi != nullptr ? epi->bias : nullptr;
   if (rows == nullptr || K == 0) workspace = nullptr;
   if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;
@@ -296,6 +302,8 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
                     lddc > kLdLimit || (rows == nullptr && a_rows < slots)))
     return GEMM_ERR_INVALID_VALUE;
   if (((out_rows + 255) / 256) * ((out_cols + 255) / 256) > kIntLimit / groups) return GEMM_ERR_INVALID_VALUE;
+  lda = row_pitch(a_rows, K, lda, 2);
+  lddc = row_pitch(slots, N, lddc, 2);
   if (slots == 0) workspace = nullptr;
   if (slots > 0 && (workspace == nullptr ||
                     workspace_bytes < wgrad_workspace(groups, slots, N, K, rows != nullptr)))

@@ -309,6 +309,25 @@ def test_expert_matmul(tokens, E, k, K, N, dtype, layout, gather):
     assert torch.all(buf[:, N:] == 7.0) and torch.all(buf[tokens * k:] == 7.0)
 
 
+# few slots and a long contraction; all of them in one group, or spread; one slot is a matrix of one row
+@pytest.mark.parametrize("slots", [1, 31, 32, 33])
+@pytest.mark.parametrize("E", [1, 7])
+@pytest.mark.parametrize("dtype,layout", [("bf16", 0), ("bf16", 1), ("f16", 0), ("f16", 1), ("e4m3", 1)])
+@pytest.mark.parametrize("gather", [True, False])
+def test_expert_matmul_of_few_slots(slots, E, dtype, layout, gather):
+    K, N = 2056, 208  # (row-major halves start on 16 bytes)
+    _, _, rows, offsets = _routing(slots, E, 1, 41)
+    a, w = _normal((slots, K), dtype, 42), _normal((E, N, K) if layout else (E, K, N), dtype, 43)
+    r, off = _dev_order(rows, offsets)
+    args = (_pitch16(a), _pitch16(w), off, r if gather else None)
+    c, s = ox.grouped(_np(a.float()), _np(w.float()), offsets, rows if gather else None, layout)
+    _accept(experts.expert_matmul(*args, layout=layout), c, s, dtype)
+    g, v = 1e-2 * c[:, :N // 2], 1e-2 * c[:, N // 2:]
+    s, silu = 1e-2 * s, g / (1 + np.exp(-g))
+    C = experts.expert_matmul(*args, layout=layout, alpha=1e-2, activation="silu_gated")
+    _accept(C, silu * v, 1.1 * s[:, :N // 2] * (np.abs(v) + 1e-3 * s[:, N // 2:]) + np.abs(silu) * s[:, N // 2:], dtype)
+
+
 def _epilogue(c, s, act, lip):
     return {"none": lambda x: x, "relu": oracle.relu, "gelu": oracle.gelu, "gelu_tanh": oracle.gelu_tanh}[act](c), s * lip
 
