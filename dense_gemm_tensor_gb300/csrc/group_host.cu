@@ -134,9 +134,20 @@ int stage_rows(const CallContext& ctx, const StageRows& p, cudaStream_t stream) 
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-// The host knows the slots and the groups, not the group sizes. A pair's
-// 256-row tiles pay once an average group fills most of one.
-bool use_pair(int64_t slots, int64_t groups) { return slots / (groups < slots ? groups : slots) >= 128; }
+// The host knows the slots and the groups, not the group sizes, so its rules go by
+// an average group.
+int64_t average_group(int64_t slots, int64_t groups) { return slots / (groups < slots ? groups : slots); }
+
+// Named rows are put in slot order first from 16 rows a group on. 16 groups,
+// 4096 x 4096 BF16, gathered on the way / staged: groups of 8 rows 92.6 / 93.9 us,
+// 16 rows 104.7 / 98.4, 32 rows 138 / 99, 96 rows 351 / 115.
+bool use_staging(int64_t slots, int64_t groups) { return average_group(slots, groups) >= 16; }
+
+// A pair's 256-row tiles pay once an average group fills one CTA's 128 rows.
+// 16 groups, 4096 x 4096 BF16, one CTA / a pair: groups of 64 rows 93 / 106 us,
+// 96 rows 108 / 110, 128 rows 123 / 107, 256 rows 188 / 150; 64 groups, 2048 x 4096
+// row-major: 96 rows 191 / 198, 128 rows 231 / 216.
+bool use_pair(int64_t slots, int64_t groups) { return average_group(slots, groups) >= 128; }
 
 // Tile rows per band: 8 row tiles of a group share each column tile's weights
 // while those are in L2.
@@ -405,7 +416,7 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
 extern "C" {
 
 int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K) {
-  if (groups < 1 || slots <= 0 || K <= 0 || !dgt::use_pair(slots, groups)) return 0;
+  if (groups < 1 || slots <= 0 || K <= 0 || !dgt::use_staging(slots, groups)) return 0;
   return slots * dgt::staged_pitch(K, type == GEMM_TYPE_E4M3 ? 1 : 2);
 }
 

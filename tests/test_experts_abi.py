@@ -34,7 +34,7 @@ def test_workspace_sizes(lib):
     assert lib.gemm_route_workspace(32, 64, 8) == 0          # one block does it all
     assert lib.gemm_route_workspace(33, 64, 8) == 2 * 64 * 4  # blocks of 32 tokens
     assert lib.gemm_route_workspace(1 << 20, 64, 8) == 152 * 64 * 4
-    assert lib.gemm_grouped_workspace(1, 4, 511, 64) == 0          # few rows a group: gathered on the way
+    assert lib.gemm_grouped_workspace(1, 4, 63, 64) == 0           # few rows a group: gathered on the way
     assert lib.gemm_grouped_workspace(1, 4, 512, 65) == 512 * 256  # rows of 130 bytes, 128-byte pitch
     assert lib.gemm_grouped_workspace(3, 4, 512, 65) == 512 * 128
     # a slab of 64 rows of dC and of A for each group, and the rows of A in slot order
