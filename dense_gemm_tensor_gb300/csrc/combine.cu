@@ -6,7 +6,7 @@
 //
 // Bound by HBM: each row of z is read (and of dz written) once, by slot, as
 // whole rows, so the gather costs no extra bytes. `tpt` threads take a token,
-// 16 bytes of its columns each; up to eight rows' loads are in flight per
+// one or more 16-byte pieces of its columns each; up to eight loads of rows are in flight per
 // thread before the first is added, and they are added in the order of j. Rows
 // that are not whole 16-byte pieces: contiguous matrices go by the pieces of
 // the flat arrays (the *_flat kernels), anything else by single elements. The blocks stay on
@@ -58,54 +58,78 @@ struct Picks {
   }
 };
 
-template <int TYPE, int VEC>
+// PIECES of a row a thread, with a token's FLIGHT rows of each in flight: eight
+// loads a thread whatever k is (k <= FLIGHT where a thread has several pieces).
+// 8192 tokens x k x 4096 BF16 with a residual, one piece a thread against several:
+// k 1 79.6 us and 29.2, k 2 83.3 and 40.3 (6.7 TB/s), k 4 90.5 and 61.0.
+template <int TYPE, int VEC, int FLIGHT, int PIECES>
 __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const CombineParams p) {
   using P = Pack<TYPE, VEC>;
   using T = typename P::T;
   grid_dependency_wait();
   const int per_block = blockDim.x / p.tpt, sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt;
   const T* z = static_cast<const T*>(p.z);
+  auto group = [&](long long u) { return p.chunks == 1 ? u : u / p.chunks; };
   long long u = blockIdx.x;
-  long long token = u / p.chunks * per_block + sub;
-  Picks<kFlight> now;
+  long long token = group(u) * per_block + sub;
+  Picks<FLIGHT> now;
   now.load(p.slots, p.weights, token, p.k, 0, p.nslots, u < p.work && token < p.tokens);
   for (; u < p.work; u += gridDim.x) {
-    const long long next = (u + gridDim.x) / p.chunks * per_block + sub;
-    const int col = (int(u % p.chunks) * p.tpt + tid) * VEC;
-    const bool in = token < p.tokens && col < p.cols;
+    const long long next = group(u + gridDim.x) * per_block + sub;
+    const int chunk = p.chunks == 1 ? 0 : int(u % p.chunks);
+    const int col0 = (chunk * PIECES * p.tpt + tid) * VEC, step = p.tpt * VEC;
+    const bool here = token < p.tokens;
+    P res[PIECES];
     float acc[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-    P res;
-    res.zero();
-    if (p.residual != nullptr && in) res.stream(static_cast<const T*>(p.residual) + token * p.ldr + col);
-    Picks<kFlight> ahead;
-    for (int j0 = 0; j0 < p.k; j0 += kFlight) {
-      P row[kFlight];
-#pragma unroll
-      for (int j = 0; j < kFlight; ++j) {
-        row[j].zero();
-        if (in && now.s[j] >= 0) row[j].stream(z + now.s[j] * p.ldz + col);
-      }
-      // the next slots: this token's, or the next one's
-      const bool last = j0 + kFlight >= p.k;
-      ahead.load(p.slots, p.weights, last ? next : token, p.k, last ? 0 : j0 + kFlight, p.nslots,
-                 last ? u + gridDim.x < p.work && next < p.tokens : token < p.tokens);
-#pragma unroll
-      for (int j = 0; j < kFlight; ++j)
-        if (j0 + j < p.k) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[i] = fmaf(now.w[j], row[j].get(i), acc[i]);
-        }
-      now = ahead;
+    for (int q = 0; q < PIECES; ++q) {
+      res[q].zero();
+      if (p.residual != nullptr && here && col0 + q * step < p.cols)
+        res[q].stream(static_cast<const T*>(p.residual) + token * p.ldr + col0 + q * step);
     }
-    if (in) {
+    auto finish = [&](int q) {
+      if (!here || col0 + q * step >= p.cols) return;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += res.get(i);
+      for (int i = 0; i < VEC; ++i) acc[i] += res[q].get(i);
       P out;
       out.set(acc);
-      out.store(static_cast<T*>(p.y) + token * p.ldy + col);
+      out.store(static_cast<T*>(p.y) + token * p.ldy + col0 + q * step);
+    };
+    if constexpr (PIECES == 1) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     }
+    Picks<FLIGHT> ahead;
+    for (int j0 = 0; j0 < (PIECES == 1 ? p.k : 1); j0 += FLIGHT) {
+      P row[PIECES][FLIGHT];
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j) {
+          row[q][j].zero();
+          if (here && col0 + q * step < p.cols && now.s[j] >= 0) row[q][j].stream(z + now.s[j] * p.ldz + col0 + q * step);
+        }
+      // the next slots: this token's, or the next one's
+      const bool last = j0 + FLIGHT >= p.k;
+      ahead.load(p.slots, p.weights, last ? next : token, p.k, last ? 0 : j0 + FLIGHT, p.nslots,
+                 last ? u + gridDim.x < p.work && next < p.tokens : here);
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) {
+        if constexpr (PIECES > 1) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j)
+          if (j0 + j < p.k) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] = fmaf(now.w[j], row[q][j].get(i), acc[i]);
+          }
+        if constexpr (PIECES > 1) finish(q);
+      }
+      now = ahead;
+    }
+    if constexpr (PIECES == 1) finish(0);
     token = next;
   }
   grid_launch_dependents();
@@ -128,12 +152,14 @@ struct CombineGradParams {
 // at a time (dy stays in L1 between the passes of a token with more rows). With
 // many tokens a thread takes several pieces of each row, so that the slots and
 // the dots' reductions cost it less (one piece each: 24 instructions an element,
-// 55 us for 4099 tokens x 6 x 2048 BF16).
-template <int TYPE, int VEC>
+// 55 us for 4099 tokens x 6 x 2048 BF16, 41.7 now), and where k is small PIECES of
+// them at once, so that eight loads are in flight as well: 8192 tokens x k x 4096
+// BF16, one and several at once: k 1 68.8 us and 40.3, k 2 80.9 and 54.4 (6.2 TB/s), k 4 107 and 92.7.
+template <int TYPE, int VEC, int FLIGHT, int PIECES>
 __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const CombineGradParams p) {
   using P = Pack<TYPE, VEC>;
   using T = typename P::T;
-  __shared__ float part[2][kThreads / 32][kFlight];
+  __shared__ float part[2][kThreads / 32][FLIGHT];
   grid_dependency_wait();
   const int sub = threadIdx.x / p.tpt, tid = threadIdx.x - sub * p.tpt, lane = threadIdx.x & 31;
   const int per_block = blockDim.x / p.tpt;
@@ -142,65 +168,74 @@ __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const Combine
   const long long token = static_cast<long long>(blockIdx.x) * per_block + sub;
   const bool in = token < p.tokens;
   int turn = 0;
-  for (int j0 = 0; j0 < p.k; j0 += kFlight, turn ^= 1) {
-    Picks<kFlight> pick;
+  for (int j0 = 0; j0 < p.k; j0 += FLIGHT, turn ^= 1) {
+    Picks<FLIGHT> pick;
     pick.load(p.slots, p.weights, token, p.k, j0, p.nslots, in);
-    float dot[kFlight];
+    float dot[FLIGHT];
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) dot[j] = 0.0f;
+    for (int j = 0; j < FLIGHT; ++j) dot[j] = 0.0f;
     if (in) {
-      for (int col = tid * VEC; col < p.cols; col += p.tpt * VEC) {
-        P d;
-        d.load(static_cast<const T*>(p.dy) + token * p.lddy + col);
-        P row[kFlight];
+      const int step = p.tpt * VEC;
+      for (int col0 = tid * VEC; col0 < p.cols; col0 += PIECES * step) {
+        P d[PIECES], row[PIECES][FLIGHT];
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q)
+          if (col0 + q * step < p.cols) d[q].load(static_cast<const T*>(p.dy) + token * p.lddy + col0 + q * step);
         if (p.dweights != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kFlight; ++j)
-            if (pick.s[j] >= 0) row[j].stream(z + pick.s[j] * p.ldz + col);
+          for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j)
+              if (pick.s[j] >= 0 && col0 + q * step < p.cols) row[q][j].stream(z + pick.s[j] * p.ldz + col0 + q * step);
         }
-        float g[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) g[i] = d.get(i);
+        for (int q = 0; q < PIECES; ++q) {
+          const int col = col0 + q * step;
+          if (col >= p.cols) continue;
+          float g[VEC];
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j)
-          if (pick.s[j] >= 0) {
-            float o[VEC];
+          for (int i = 0; i < VEC; ++i) g[i] = d[q].get(i);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = pick.w[j] * g[i];
-            P out;
-            out.set(o);
-            out.store(dz + pick.s[j] * p.lddz + col);
-          }
-        if (p.dweights != nullptr) {
-#pragma unroll
-          for (int j = 0; j < kFlight; ++j)
+          for (int j = 0; j < FLIGHT; ++j)
             if (pick.s[j] >= 0) {
+              float o[VEC];
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) dot[j] = fmaf(g[i], row[j].get(i), dot[j]);
+              for (int i = 0; i < VEC; ++i) o[i] = pick.w[j] * g[i];
+              P out;
+              out.set(o);
+              out.store(dz + pick.s[j] * p.lddz + col);
             }
+          if (p.dweights != nullptr) {
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j)
+              if (pick.s[j] >= 0) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) dot[j] = fmaf(g[i], row[q][j].get(i), dot[j]);
+              }
+          }
         }
       }
     }
     if (p.dweights != nullptr) {
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j)
+      for (int j = 0; j < FLIGHT; ++j)
         for (int d = (p.tpt < 32 ? p.tpt : 32) >> 1; d > 0; d >>= 1)
           dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
       if (p.tpt > 32) {
         // (the two halves of `part` alternate: one barrier a pass is enough)
         if (lane == 0) {
 #pragma unroll
-          for (int j = 0; j < kFlight; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
+          for (int j = 0; j < FLIGHT; ++j) part[turn][threadIdx.x >> 5][j] = dot[j];
         }
         __syncthreads();
-        if (tid < kFlight) {
+        if (tid < FLIGHT) {
           float sum = 0.0f;
           for (int i = 0; i < p.tpt >> 5; ++i) sum += part[turn][(threadIdx.x >> 5) + i][tid];
           if (in && j0 + tid < p.k) p.dweights[token * p.k + j0 + tid] = sum;
         }
       } else if (in && tid == 0) {
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j)
+        for (int j = 0; j < FLIGHT; ++j)
           if (j0 + j < p.k) p.dweights[token * p.k + j0 + j] = dot[j];
       }
     }
@@ -469,6 +504,34 @@ int threads_per_token(int64_t nvec, int64_t passes = 1) {
 
 constexpr int64_t kInt = (int64_t(1) << 31) - 1;
 
+// Pieces of a row a thread takes at once: one, or what makes eight loads with the token's k rows, where the tokens
+// are enough to fill the GPU's threads that way.
+int pieces_at_once(const CallContext& ctx, bool vec, int k, int64_t tokens, int64_t nvec) {
+  const int pieces = k <= 2 ? 4 : k <= 4 ? 2 : 1;
+  return vec && tokens * nvec >= int64_t(ctx.sm_count) * kThreads * 3 * pieces ? pieces : 1;
+}
+
+template <int TYPE>
+cudaError_t launch_combine(const CombineParams& p, bool vec, bool flat, int pieces, int grid, int block, cudaStream_t s) {
+  constexpr int VEC = 16 / int(sizeof(typename Elem<TYPE>::T));
+  if (flat) return launch_dependent(combine_flat_kernel<TYPE>, grid, block, 0, s, 1, p);
+  if (!vec) return launch_dependent(combine_kernel<TYPE, 1, kFlight, 1>, grid, block, 0, s, 1, p);
+  return pieces == 4   ? launch_dependent(combine_kernel<TYPE, VEC, kFlight / 4, 4>, grid, block, 0, s, 1, p)
+         : pieces == 2 ? launch_dependent(combine_kernel<TYPE, VEC, kFlight / 2, 2>, grid, block, 0, s, 1, p)
+                       : launch_dependent(combine_kernel<TYPE, VEC, kFlight, 1>, grid, block, 0, s, 1, p);
+}
+
+template <int TYPE>
+cudaError_t launch_combine_grad(const CombineGradParams& p, bool vec, bool flat, int pieces, int grid, int block,
+                                cudaStream_t s) {
+  constexpr int VEC = 16 / int(sizeof(typename Elem<TYPE>::T));
+  if (flat) return launch_dependent(combine_grad_flat_kernel<TYPE>, grid, block, 0, s, 1, p);
+  if (!vec) return launch_dependent(combine_grad_kernel<TYPE, 1, kFlight, 1>, grid, block, 0, s, 1, p);
+  return pieces == 4   ? launch_dependent(combine_grad_kernel<TYPE, VEC, kFlight / 4, 4>, grid, block, 0, s, 1, p)
+         : pieces == 2 ? launch_dependent(combine_grad_kernel<TYPE, VEC, kFlight / 2, 2>, grid, block, 0, s, 1, p)
+                       : launch_dependent(combine_grad_kernel<TYPE, VEC, kFlight, 1>, grid, block, 0, s, 1, p);
+}
+
 }  // namespace
 }  // namespace dgt
 
@@ -507,28 +570,19 @@ int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, i
   };
   const bool flat = !vec && cols >= v && flat_matrix(z, ldz) && flat_matrix(y, ldy) && flat_matrix(residual, ldr);
   const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
+  const int pieces = pieces_at_once(ctx, vec, k, tokens, nvec);
   CombineParams p = {z, slots, weights, residual, y, (long long)ldz, (long long)ldr, (long long)ldy, int(tokens),
-                     int(cols), k, int(nslots), threads_per_token(nvec), 1, 0};
-  p.chunks = int((nvec + p.tpt - 1) / p.tpt);
+                     int(cols), k, int(nslots), threads_per_token(nvec, pieces), 1, 0};
+  p.chunks = int((nvec + int64_t(p.tpt) * pieces - 1) / (int64_t(p.tpt) * pieces));
   const int block = kThreads / p.tpt * p.tpt;
   p.work = (tokens + block / p.tpt - 1) / (block / p.tpt) * p.chunks;
   // as many blocks as are resident at once; the flat kernel has nothing to load ahead and takes a block for each group
   const int64_t most = flat ? kInt : int64_t(ctx.sm_count) * (3 * kThreads / block);
   const int grid = int(p.work < most ? p.work : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (type == GEMM_TYPE_F16)
-    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_F16, 8>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_F16>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_kernel<GEMM_TYPE_F16, 1>, grid, block, 0, s, 1, p);
-  else if (type == GEMM_TYPE_BF16)
-    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_BF16, 8>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_BF16>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_kernel<GEMM_TYPE_BF16, 1>, grid, block, 0, s, 1, p);
-  else
-    e = vec    ? launch_dependent(combine_kernel<GEMM_TYPE_F32, 4>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_flat_kernel<GEMM_TYPE_F32>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_kernel<GEMM_TYPE_F32, 1>, grid, block, 0, s, 1, p);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_combine<GEMM_TYPE_F16>(p, vec, flat, pieces, grid, block, s)
+                        : type == GEMM_TYPE_BF16 ? launch_combine<GEMM_TYPE_BF16>(p, vec, flat, pieces, grid, block, s)
+                                                 : launch_combine<GEMM_TYPE_F32>(p, vec, flat, pieces, grid, block, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -565,6 +619,7 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
   const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
   // four pieces a thread once the tokens fill the GPU's threads that way
   const int64_t passes = tokens * nvec >= int64_t(ctx.sm_count) * kThreads * 3 * 4 ? 4 : 1;
+  const int pieces = pieces_at_once(ctx, vec, k, tokens, nvec);
   CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,
                          int(tokens), int(cols), k, int(nslots), threads_per_token(nvec, passes)};
   const int block = kThreads / p.tpt * p.tpt;
@@ -572,19 +627,9 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
   // a block for each few tokens
   const int grid = int(need > 0 ? need : ctx.sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (type == GEMM_TYPE_F16)
-    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 8>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_F16>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_grad_kernel<GEMM_TYPE_F16, 1>, grid, block, 0, s, 1, p);
-  else if (type == GEMM_TYPE_BF16)
-    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 8>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_BF16>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_grad_kernel<GEMM_TYPE_BF16, 1>, grid, block, 0, s, 1, p);
-  else
-    e = vec    ? launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 4>, grid, block, 0, s, 1, p)
-        : flat ? launch_dependent(combine_grad_flat_kernel<GEMM_TYPE_F32>, grid, block, 0, s, 1, p)
-               : launch_dependent(combine_grad_kernel<GEMM_TYPE_F32, 1>, grid, block, 0, s, 1, p);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_combine_grad<GEMM_TYPE_F16>(p, vec, flat, pieces, grid, block, s)
+                        : type == GEMM_TYPE_BF16 ? launch_combine_grad<GEMM_TYPE_BF16>(p, vec, flat, pieces, grid, block, s)
+                                                 : launch_combine_grad<GEMM_TYPE_F32>(p, vec, flat, pieces, grid, block, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

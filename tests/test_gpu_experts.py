@@ -476,6 +476,18 @@ def test_long_outputs():
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("pad", [0, 1])
 def test_combine_and_backward(tokens, cols, k, dtype, pad):
+    _combine_and_backward(tokens, cols, k, dtype, pad)
+
+
+# enough tokens for a thread to take several pieces of each row, by the number of experts a token
+@pytest.mark.parametrize("tokens,cols,k", [(1901, 2056, 1), (1901, 2056, 2), (1901, 2056, 3), (1901, 2056, 4), (471, 8200, 2),
+                                            (4801, 264, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_combine_and_backward_of_many_tokens(tokens, cols, k, dtype):
+    _combine_and_backward(tokens, cols, k, dtype, 0)
+
+
+def _combine_and_backward(tokens, cols, k, dtype, pad):
     E = max(k, 3)
     _, slots, rows, offsets = _routing(tokens, E, k, 81, unused=tokens // 4)
     z, w = _normal((tokens * k, cols), dtype, 82), torch.rand((tokens, k), generator=_gen(83))
