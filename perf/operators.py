@@ -96,9 +96,7 @@ def _draw(rng):
                  gather=rng.random() < 0.7)
         c["k"] = rng.randint(1, min(4, c["experts"]))
         c["K"] = _log(rng, 128, 4096)
-        c["N"] = _log(rng, 128, 4096)
-        if act == "silu_gated":  # two halves; in row-major weights the second starts on a 16-byte boundary
-            c["N"] = 2 * _log(rng, 64, 2048) if c["layout"] == 1 else 16 * _log(rng, 8, 256)
+        c["N"] = 2 * _log(rng, 64, 2048) if act == "silu_gated" else _log(rng, 128, 4096)
         return c
     if op == "experts_grad":
         c = dict(op=op, tokens=_log(rng, 16, 8192), experts=_log(rng, 2, 16), K=_log(rng, 128, 4096),
