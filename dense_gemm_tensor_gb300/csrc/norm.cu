@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
     auto take = [&](P(&v)[NV], int m, int i) {
       if constexpr (AHEAD) v[i].load(reinterpret_cast<const T*>(cell(turn, m, i)));
     };
-    // with the row's rstd taken out of the sums: mean(g xhat) = rstd * mean(g h), dw += (dy rstd) h,
-    // dx = rstd g - (rstd^3 mean(g h)) h + dh; ALIGNED takes two elements to an instruction
+    // xhat = h rstd is formed first, and dx = rstd g - (rstd mean(g xhat)) xhat + dh: every factor stays of the size of
+    // dy or of dx. (rstd^3 mean(g h) would leave fp32 for rows of 1e13 and above, or of 1e-13 with a tiny eps.)
+    // ALIGNED takes two elements to an instruction.
     const float rstd = AHEAD ? rstd_ahead : in ? p.rstd[row] : 0.0f;
     if constexpr (AHEAD) rstd_ahead = row + step < p.rows ? p.rstd[row + step] : 0.0f;
     float2 dots = make_float2(0.0f, 0.0f);  // ALIGNED
@@ -376,27 +377,27 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
       if constexpr (MODE == ALIGNED) {
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
-          const float2 hv = h[i].two(j), d = dy[i].two(j);
-          dots = __ffma2_rn(__fmul2_rn(d, make_float2(w[j], w[j + 1])), hv, dots);
+          const float2 xhat = __fmul2_rn(h[i].two(j), make_float2(rstd, rstd)), d = dy[i].two(j);
+          dots = __ffma2_rn(__fmul2_rn(d, make_float2(w[j], w[j + 1])), xhat, dots);
           float2& sum = dw[(i * VEC + j) / 2];
-          sum = __ffma2_rn(__fmul2_rn(d, make_float2(rstd, rstd)), hv, sum);
+          sum = __ffma2_rn(d, xhat, sum);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float hv = h[i].get(j), d = dy[i].get(j);
-          dot = fmaf(d * w[j], hv, dot);
+          const float xhat = h[i].get(j) * rstd, d = dy[i].get(j);
+          dot = fmaf(d * w[j], xhat, dot);
           if constexpr (MODE == FLAT) {
             const int c = r.lo(i) + j;
-            if (in && c >= 0 && c < p.cols) sums[sub * places + r.place(i, j)] += d * rstd * hv;
+            if (in && c >= 0 && c < p.cols) sums[sub * places + r.place(i, j)] += d * xhat;
           } else {
             float& sum = i & 1 ? dw[i / 2].y : dw[i / 2].x;
-            sum = fmaf(d * rstd, hv, sum);
+            sum = fmaf(d, xhat, sum);
           }
         }
       }
     }
-    const float back = rstd * rstd * rstd * (row_warps.sum(MODE == ALIGNED ? dots.x + dots.y : dot, red[turn]) / static_cast<float>(p.cols));
+    const float back = rstd * (row_warps.sum(MODE == ALIGNED ? dots.x + dots.y : dot, red[turn]) / static_cast<float>(p.cols));
     if (MODE == FLAT && p.tpr <= 32) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -410,14 +411,14 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) rmsnorm_grad_kern
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
           const float2 g = __fmul2_rn(dy[i].two(j), make_float2(w[j], w[j + 1]));
-          const float2 v = __ffma2_rn(g, make_float2(rstd, rstd),
-                                      __ffma2_rn(h[i].two(j), make_float2(-back, -back), dh[i].two(j)));
+          const float2 xhat = __fmul2_rn(h[i].two(j), make_float2(rstd, rstd));
+          const float2 v = __ffma2_rn(g, make_float2(rstd, rstd), __ffma2_rn(xhat, make_float2(-back, -back), dh[i].two(j)));
           w[j] = v.x;
           w[j + 1] = v.y;
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = fmaf(dy[i].get(j) * w[j], rstd, fmaf(h[i].get(j), -back, dh[i].get(j)));
+        for (int j = 0; j < VEC; ++j) w[j] = fmaf(dy[i].get(j) * w[j], rstd, fmaf(h[i].get(j) * rstd, -back, dh[i].get(j)));
       }
       o.set(w);
       r.store(o, p.dx, row, p.lddx, i, in);
