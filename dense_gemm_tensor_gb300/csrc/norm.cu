@@ -547,18 +547,33 @@ size_t grad_smem(const NormGradParams& p, int mode, bool ahead, int block, int e
   return sums > stages ? sums : stages;
 }
 
+// Most dynamic shared memory that a launch of the gradient takes: AHEAD goes up to here, and a FLAT row of
+// kMaxFlatCols has 86 KB.
+constexpr size_t kGradSmem = 200 * 1024;
+
+// Launches one build of the gradient's kernel. Its limit is a property of the kernel, not of the launch, so it is set
+// once, to the most that any launch takes: other host threads may be launching it with other sizes.
+template <int TYPE, int MODE, bool AHEAD>
+cudaError_t launch_norm_grad_mode(const NormGradParams& p, int dev, int grid, int block, size_t smem, cudaStream_t s) {
+  static int configured[64] = {};
+  auto kern = rmsnorm_grad_kernel<TYPE, MODE, AHEAD>;
+  if (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGradSmem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+  }
+  return launch_dependent(kern, grid, block, smem, s, 1, p);
+}
+
 template <int TYPE>
-cudaError_t launch_norm_grad(const NormGradParams& p, int mode, bool ahead, int grid, int block, void* dw,
+cudaError_t launch_norm_grad(const NormGradParams& p, int mode, bool ahead, int dev, int grid, int block, void* dw,
                              cudaStream_t s) {
   const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
-  auto kern = mode == ALIGNED ? (ahead ? rmsnorm_grad_kernel<TYPE, ALIGNED, true> : rmsnorm_grad_kernel<TYPE, ALIGNED, false>)
-              : mode == FLAT  ? rmsnorm_grad_kernel<TYPE, FLAT, false>
-                              : rmsnorm_grad_kernel<TYPE, SINGLE, false>;
-  if (smem > 40 * 1024) {  // past what a launch may take unasked (48 KB, less the static arrays)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e = launch_dependent(kern, grid, block, smem, s, 1, p);
+  const cudaError_t e = mode == ALIGNED
+                            ? (ahead ? launch_norm_grad_mode<TYPE, ALIGNED, true>(p, dev, grid, block, smem, s)
+                                     : launch_norm_grad_mode<TYPE, ALIGNED, false>(p, dev, grid, block, smem, s))
+                        : mode == FLAT ? launch_norm_grad_mode<TYPE, FLAT, false>(p, dev, grid, block, smem, s)
+                                       : launch_norm_grad_mode<TYPE, SINGLE, false>(p, dev, grid, block, smem, s);
   if (e != cudaSuccess) return e;
   return launch_dependent(norm_weight_sum_kernel<TYPE>, (p.cols + 31) / 32, 1024, 0, s, 1, p.partial, grid, p.cols, dw);
 }
@@ -686,12 +701,12 @@ int gemm_rmsnorm_backward(int type, int64_t rows, int64_t cols, const void* dy, 
                       (long long)lddh, (long long)lddx, int(rows), int(cols), 0};
   p.tpr = threads_per_row(cols, kGradEpt, mode, v);
   const int block = p.tpr >= 256 ? p.tpr : 256 / p.tpr * p.tpr;
-  const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= 200 * 1024;
+  const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= kGradSmem;
   const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
   const int grid = int(need < grad_blocks(cols) ? need : grad_blocks(cols));
-  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_norm_grad<GEMM_TYPE_F16>(p, mode, ahead, grid, block, dw, s)
-                        : type == GEMM_TYPE_BF16 ? launch_norm_grad<GEMM_TYPE_BF16>(p, mode, ahead, grid, block, dw, s)
-                                                 : launch_norm_grad<GEMM_TYPE_F32>(p, mode, ahead, grid, block, dw, s);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_norm_grad<GEMM_TYPE_F16>(p, mode, ahead, ctx.dev, grid, block, dw, s)
+                        : type == GEMM_TYPE_BF16 ? launch_norm_grad<GEMM_TYPE_BF16>(p, mode, ahead, ctx.dev, grid, block, dw, s)
+                                                 : launch_norm_grad<GEMM_TYPE_F32>(p, mode, ahead, ctx.dev, grid, block, dw, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

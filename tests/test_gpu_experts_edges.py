@@ -4,6 +4,8 @@ operands of any width. Each case against the float64 oracle (oracle/experts.py);
 tolerances as in test_gpu_experts.py where none is given.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -73,3 +75,42 @@ def test_rms_norm_backward_of_large_and_small_rows(rows, cols, pad, dtype, size)
     g, xh, r = np.abs(_np(dy) * _np(w)), np.abs(_np(h) * _np(rstd)[:, None]), _np(rstd)[:, None]
     _close(dx, want_x, r * (g + xh * (g * xh).mean(1, keepdims=True)), dtype)
     _close(dw, want_w, (np.abs(_np(dy)) * xh).sum(0), dtype)
+
+
+def test_rms_norm_backward_from_several_threads():
+    """The C call from host threads at once, each on its own stream, with widths that take different shared memory."""
+    lib = experts._load()
+    widths = [4096, 8192, 6144, 2731]
+    cases, errors = [], []
+    for i, cols in enumerate(widths):
+        t = [_normal((64, cols), "bf16", 10 * i + j).cuda() for j in range(3)]
+        w = _normal((cols,), "bf16", 10 * i + 4).cuda()
+        rstd = torch.rsqrt(t[1].float().square().mean(1) + 1e-6)
+        cases.append((cols, *t, w, rstd, experts.rms_norm_backward(t[0], t[1], w, rstd, dh=t[2])))
+    torch.cuda.synchronize()
+
+    def work(case):
+        cols, dy, h, dh, w, rstd, want = case
+        try:
+            torch.cuda.set_device(0)
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                dx, dw = torch.empty_like(h), torch.empty_like(w)
+                need = lib.gemm_rmsnorm_backward_workspace(64, cols)
+                ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+                args = (1, 64, cols, dy.data_ptr(), cols, h.data_ptr(), cols, w.data_ptr(), rstd.data_ptr(), dh.data_ptr(),
+                        cols, dx.data_ptr(), cols, dw.data_ptr(), ws.data_ptr(), need, s.cuda_stream)
+                codes = [lib.gemm_rmsnorm_backward(*args) for _ in range(400)]
+            s.synchronize()
+            assert codes == [gemm.GEMM_OK] * len(codes), (cols, [c for c in codes if c][:3])
+            assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    for _ in range(3):
+        threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert not errors, errors
