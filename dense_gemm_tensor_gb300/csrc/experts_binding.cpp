@@ -404,10 +404,12 @@ PyObject* combine_backward(PyObject* const* a) {
     if (off.numel() < 1) value_error("offsets must not be empty");
     used = vector<int32_t>(off, "offsets", at::kInt, off.numel()) + off.numel() - 1;
   }
-  Tensor dz = make({nslots, cols}, z, dt), dw = w != nullptr ? make({tokens, k}, z, at::kFloat) : Tensor();
+  // (by the argument, not by w: the address of no weights is null too)
+  const bool weighted = a[3] != Py_None;
+  Tensor dz = make({nslots, cols}, z, dt), dw = weighted ? make({tokens, k}, z, at::kFloat) : Tensor();
   const int st = entry.c.combine_backward(code, tokens, cols, static_cast<int>(k > 1 << 20 ? 1 << 20 : k), dy.data_ptr(),
                                           lddy, z.data_ptr(), ldz, nslots, i, w, used, dz.data_ptr(), cols,
-                                          w != nullptr ? static_cast<float*>(dw.data_ptr()) : nullptr, stream_of(z));
+                                          weighted ? static_cast<float*>(dw.data_ptr()) : nullptr, stream_of(z));
   return st != GEMM_OK ? PyLong_FromLong(st) : tuple_of(dz, dw);
 }
 

@@ -114,3 +114,28 @@ def test_rms_norm_backward_from_several_threads():
         for t in threads:
             t.join()
     assert not errors, errors
+
+
+# ---------------------------------------------------------------- no tokens
+
+def test_combine_backward_of_no_tokens():
+    z = torch.ones(4, 16, device="cuda", dtype=torch.bfloat16)
+    slots, w = torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    dz, dw = experts.combine_backward(z[:0], z, slots, w, off)
+    assert torch.all(dz == 0) and dw.shape == (0, 2) and dw.dtype == torch.float32
+    dz, dw = experts.combine_backward(z[:0], z, slots, None, off)
+    assert torch.all(dz == 0) and dw is None
+
+
+def test_block_of_no_tokens():
+    from dense_gemm_tensor_gb300 import moe
+    block = moe.MoeBlock.random(128, 64, 4, 2, torch.bfloat16)
+    x = torch.zeros(0, 128, device="cuda", dtype=torch.bfloat16)
+    assert block.serve(x, x).shape == (0, 128)
+    y, saved = block.forward(x, x)
+    assert y.shape == (0, 128)
+    grads = block.backward(y, saved)
+    assert grads.x.shape == (0, 128)
+    for g, p in zip(grads[1:], (block.norm, block.router, block.up, block.down)):
+        assert g.shape == p.shape and torch.all(g == 0)
