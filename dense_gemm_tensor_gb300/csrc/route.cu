@@ -345,6 +345,13 @@ constexpr int kLeastThreads = 256;
 template <int NPL>
 constexpr int kRouteThreads = NPL <= 8 ? 1024 : NPL == 16 ? 512 : 256;  // by the registers of a lane's scores
 
+// Tokens of the block: [first, first + the result). (first + per_block may pass 2^31 in the last block.)
+__device__ __forceinline__ int block_tokens(const RouteParams& p, int& first) {
+  const long long at = static_cast<long long>(blockIdx.x) * p.per_block, left = p.tokens - at;
+  first = static_cast<int>(at);
+  return static_cast<int>(left < p.per_block ? (left < 0 ? 0 : left) : p.per_block);
+}
+
 // One-block form: chooses, then orders the pairs.
 // Two-launch form (p.blocks > 1): chooses and leaves the block's counts.
 template <int NPL>
@@ -358,9 +365,10 @@ __global__ void __launch_bounds__(kRouteThreads<NPL>, 1) route_kernel(const Rout
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
   grid_dependency_wait();
   __syncthreads();
-  const int t0 = blockIdx.x * p.per_block;
-  const int t1 = min(p.tokens, t0 + p.per_block);
-  for (int t = t0 + warp; t < t1; t += warps) {
+  int t0;
+  const int tokens = block_tokens(p, t0);
+  for (int i = warp; i < tokens; i += warps) {
+    const int t = t0 + i;
     int id;
     float w;
     route_token<NPL>(p, t, lane, id, w);
@@ -390,8 +398,8 @@ __global__ void __launch_bounds__(1024, 1) route_place_kernel(const RouteParams 
   __shared__ uint32_t masks[kMaskWords];
   __shared__ int32_t all[kMaxExperts], before[kMaxExperts];
   __shared__ int32_t sums[32], total;
-  const int t0 = blockIdx.x * p.per_block;
-  const int n = max(0, min(p.tokens, t0 + p.per_block) - t0) * p.k;
+  int t0;
+  const int n = block_tokens(p, t0) * p.k;
   const long long first = static_cast<long long>(t0) * p.k;
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) all[e] = before[e] = 0;
   __syncthreads();
@@ -521,8 +529,8 @@ int check_config(int64_t tokens, int experts, const gemm_route_config_t* c) {
 template <int NPL>
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s) {
   // one block: a warp for each token
-  const int most = kRouteThreads<NPL>, few = p.tokens * 32;
-  const int block = p.blocks > 1 || few > most ? most : few < kLeastThreads ? kLeastThreads : few;
+  const int most = kRouteThreads<NPL>, few = p.blocks > 1 ? most : p.tokens * 32;
+  const int block = few > most ? most : few < kLeastThreads ? kLeastThreads : few;
   cudaError_t e = launch_dependent(route_kernel<NPL>, p.blocks, block, 0, s, 1, p);
   if (e != cudaSuccess || p.blocks == 1) return e;
   return launch_dependent(route_place_kernel, p.blocks, 1024, 0, s, 1, p);

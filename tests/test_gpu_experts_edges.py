@@ -139,3 +139,24 @@ def test_block_of_no_tokens():
     assert grads.x.shape == (0, 128)
     for g, p in zip(grads[1:], (block.norm, block.router, block.up, block.down)):
         assert g.shape == p.shape and torch.all(g == 0)
+
+
+# ---------------------------------------------------------------- numbers at the ends of their ranges
+
+def test_routing_of_the_most_tokens():
+    """tokens * k just below 2^31, whose last block of tokens ends past it."""
+    tokens = (1 << 31) - 1
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("takes 60 GB")
+    logits = torch.zeros(tokens, 1, dtype=torch.float16, device="cuda")
+    logits[-1] = -float("inf")
+    r = experts.route(logits, 1)
+    assert r.offsets.tolist() == [0, tokens - 1]
+    for lo in range(0, tokens, 1 << 28):
+        hi = min(tokens, lo + (1 << 28))
+        for got, last in ((r.slots[lo:hi, 0], -1), (r.rows[lo:hi], -1)):
+            want = torch.arange(lo, hi, dtype=torch.int32, device="cuda")
+            if hi == tokens:
+                want[-1] = last
+            assert torch.equal(got, want)
+    assert int(r.ids[-1]) == -1 and not bool(r.ids[:-1].any()) and float(r.weights[-1]) == 0
