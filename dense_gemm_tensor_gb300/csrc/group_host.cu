@@ -171,6 +171,8 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   const int64_t out_cols = gated ? N / 2 : N;
   if (offsets == nullptr || C == nullptr || ldc < out_cols || ldc > kLdLimit) return GEMM_ERR_INVALID_VALUE;
   if (rows == nullptr && a_rows < slots) return GEMM_ERR_INVALID_VALUE;
+  // (with K = 0 rows of A may be named that it does not have: nothing of them is read but their scales)
+  if (a_rows == 0 && epi != nullptr && epi->row_scale != nullptr) return GEMM_ERR_INVALID_VALUE;
   const int64_t w_rows = layout == GEMM_B_ROW_MAJOR ? K : N, w_cols = layout == GEMM_B_ROW_MAJOR ? N : K;
   if (K > 0) {
     if (A == nullptr || W == nullptr || a_rows == 0 || lda < K || ldw < w_cols || lda > kLdLimit || ldw > kLdLimit ||
