@@ -181,6 +181,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   }
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
   lda = row_pitch(a_rows, K, lda, es);
+  ldw = row_pitch(w_rows, w_cols, ldw, es);
   const void* bias = epi != nullptr ? epi->bias : nullptr;
   if (rows == nullptr || K == 0) workspace = nullptr;
   if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;

@@ -167,8 +167,8 @@ typedef struct gemm_grouped_epilogue {
  * layout flag the same call is the gradient of A: dA = dC . W_e^T, one row a
  * slot. epilogue NULL: C = A . W. 1 <= groups <= 1024; slots, N, K < 2^31;
  * K = 0 gives the epilogue of 0. Rows and bases of A and W and the matrix
- * stride must be 16-byte multiples (GEMM_ERR_MISALIGNED otherwise; an A of one
- * row may have any pitch), and with row-major W GEMM_ACT_SILU_GATED's second
+ * stride must be 16-byte multiples (GEMM_ERR_MISALIGNED otherwise; an A or a W_e
+ * of one row may have any pitch), and with row-major W GEMM_ACT_SILU_GATED's second
  * half must start on one; C may have any alignment that keeps its elements
  * aligned.
  *

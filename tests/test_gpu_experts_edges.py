@@ -141,6 +141,54 @@ def test_block_of_no_tokens():
         assert g.shape == p.shape and torch.all(g == 0)
 
 
+# ---------------------------------------------------------------- operands of any width
+
+def _routing(tokens, E, k, seed, empty=(), unused=0):
+    rng = np.random.default_rng(seed)
+    open_ = [e for e in range(E) if e not in empty]
+    ids = np.stack([rng.permutation(open_)[:k] for _ in range(tokens)])
+    if unused:
+        ids[-unused:] = -1
+    return (ids, *ox.order(ids, E))
+
+
+def _dev_order(rows, offsets):
+    return torch.from_numpy(rows).int().cuda(), torch.from_numpy(offsets).int().cuda()
+
+
+def _pitch16(t):
+    """A CUDA view whose rows sit a multiple of 16 bytes apart (NaN in the gaps)."""
+    per = 16 // t.element_size()
+    full = -(-t.shape[-1] // per) * per
+    if t.dtype == torch.float8_e4m3fn:
+        buf = torch.full((*t.shape[:-1], full), 0x7F, dtype=torch.uint8).view(t.dtype)
+    else:
+        buf = torch.full((*t.shape[:-1], full), float("nan"), dtype=t.dtype)
+    buf[..., :t.shape[-1]] = t
+    return buf.cuda()[..., :t.shape[-1]]
+
+
+def _accept(got, ref, s, dtype):
+    res = oracle.check(_np(got).reshape(-1, got.shape[-1]), ref.reshape(-1, ref.shape[-1]), s.reshape(-1, s.shape[-1]),
+                       "bf16" if dtype == "e4m3" else dtype)
+    assert res["ok"], res
+
+
+KINDS = [("bf16", 0), ("bf16", 1), ("f16", 0), ("f16", 1), ("e4m3", 1)]
+
+
+@pytest.mark.parametrize("K,N", [(67, 1), (1, 67), (1, 1)])
+@pytest.mark.parametrize("dtype,layout", KINDS)
+def test_weights_of_one_row(K, N, dtype, layout):
+    """The pitch of a weight matrix of one row says nothing; the matrices start 16-byte multiples apart."""
+    _, _, rows, offsets = _routing(20, 3, 2, 1)
+    a, w = _normal((20, K), dtype, 2), _normal((3, N, K) if layout else (3, K, N), dtype, 3)
+    r, off = _dev_order(rows, offsets)
+    C = experts.expert_matmul(_pitch16(a), _pitch16(w), off, r, layout=layout)
+    c, s = ox.grouped(_np(a.float()), _np(w.float()), offsets, rows, layout)
+    _accept(C, c, s, dtype)
+
+
 # ---------------------------------------------------------------- numbers at the ends of their ranges
 
 def test_routing_of_the_most_tokens():
