@@ -37,18 +37,18 @@ struct Entries {
   decltype(&gemm_f16_grouped) f16_grouped;
   decltype(&gemm_bf16_grouped) bf16_grouped;
   decltype(&gemm_e4m3_grouped) e4m3_grouped;
-  decltype(&gemm_grouped_workspace) grouped_workspace;
+  decltype(&gemm_grouped_rows_workspace) grouped_rows_workspace;
   decltype(&gemm_f16_grouped_wgrad) f16_grouped_wgrad;
   decltype(&gemm_bf16_grouped_wgrad) bf16_grouped_wgrad;
-  decltype(&gemm_grouped_wgrad_workspace) grouped_wgrad_workspace;
+  decltype(&gemm_grouped_wgrad_rows_workspace) grouped_wgrad_rows_workspace;
   decltype(&gemm_combine) combine;
   decltype(&gemm_combine_backward) combine_backward;
 };
 constexpr const char* kNames[] = {
     "gemm_rmsnorm",          "gemm_rmsnorm_backward", "gemm_rmsnorm_backward_workspace", "gemm_route",
     "gemm_route_workspace",  "gemm_route_backward",   "gemm_f16_grouped",                "gemm_bf16_grouped",
-    "gemm_e4m3_grouped",     "gemm_grouped_workspace", "gemm_f16_grouped_wgrad",         "gemm_bf16_grouped_wgrad",
-    "gemm_grouped_wgrad_workspace", "gemm_combine",   "gemm_combine_backward"};
+    "gemm_e4m3_grouped",     "gemm_grouped_rows_workspace", "gemm_f16_grouped_wgrad",         "gemm_bf16_grouped_wgrad",
+    "gemm_grouped_wgrad_rows_workspace", "gemm_combine",   "gemm_combine_backward"};
 constexpr int kEntries = sizeof(kNames) / sizeof(kNames[0]);
 static_assert(sizeof(Entries) == kEntries * sizeof(void*), "one address for each name");
 union {
@@ -277,14 +277,14 @@ PyObject* expert_matmul(PyObject* const* a) {
   const at::ScalarType out_dt = code == GEMM_TYPE_E4M3 ? at::kBFloat16 : dt;
   const int32_t* offsets = vector<int32_t>(tensor(a[2], "offsets"), "offsets", at::kInt, experts + 1);
   const int e = experts > (1 << 30) ? 1 << 30 : static_cast<int>(experts);
-  int64_t slots = a_rows, need = 0;
+  int64_t slots = a_rows;
   const int32_t* rows = nullptr;
   if (a[3] != Py_None) {
     const Tensor& r = tensor(a[3], "rows");
     slots = r.numel();
     rows = vector<int32_t>(r, "rows", at::kInt, slots);
-    need = entry.c.grouped_workspace(code, e, slots, K);
   }
+  const int64_t need = entry.c.grouped_rows_workspace(code, e, slots, K, a_rows, lda, rows != nullptr);
   const int act = static_cast<int>(whole(a[10]));
   const int64_t cols = act == GEMM_ACT_SILU_GATED ? N / 2 : N;
   Tensor out;
@@ -349,7 +349,7 @@ PyObject* expert_weight_grad(PyObject* const* a) {
     out = make({experts < 0 ? 0 : experts, r0, r1}, A, dt);
   }
   const Stack w = stack(out, "out");
-  const int64_t need = entry.c.grouped_wgrad_workspace(e, slots, N, K, rows != nullptr);
+  const int64_t need = entry.c.grouped_wgrad_rows_workspace(e, slots, N, K, a_rows, lda, rows != nullptr, lddc);
   Tensor ws = scratch(need, A);
   const auto fn = dt == at::kHalf ? entry.c.f16_grouped_wgrad : entry.c.bf16_grouped_wgrad;
   const int st = fn(e, offsets, slots, N, K, static_cast<const uint16_t*>(A.data_ptr()), a_rows, lda, rows,

@@ -14,8 +14,8 @@ constexpr int64_t kLdLimit = int64_t(1) << 39;
 
 bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
 
-// TMA reads rows whose base and pitch are 16-byte multiples.
-bool tma_rows(const void* p, int64_t ld, int es) { return !misaligned(p, 16) && (ld * es) % 16 == 0; }
+// TMA reads rows whose base and pitch are 16-byte multiples: rows of another pitch are copied first.
+bool odd_pitch(int64_t ld, int es) { return (ld * es) % 16 != 0; }
 
 // The pitch of a matrix of one row says nothing: any is as good as the next 16-byte multiple.
 int64_t row_pitch(int64_t rows, int64_t cols, int64_t ld, int es) {
@@ -54,9 +54,10 @@ void fill_common(const CallContext& ctx, GroupParams& p) {
 }
 
 // Copies of rows into the workspace ahead of a grouped kernel, a warp a row,
-// 16 bytes a lane (rows start on 16-byte boundaries; bytes of the destination's
-// pitch past the row are zero):
+// 16 bytes a lane (the matrices start on 16-byte boundaries, their rows anywhere;
+// bytes of the destination's pitch past the row are zero):
 //   * `order`: the gathered operand's rows in slot order, order[s] = a[row(s)]
+//   * `order_c`: the other operand's rows c[s], where their pitch is not TMA's
 //   * `slab_a`, `slab_c` (the weights' gradient): the last slab of 64 slots of
 //     every group whose count is not a multiple of 64, zeros past its end
 // Bound by memory: one read of the rows (repeats of a token hit L2) and one
@@ -67,6 +68,7 @@ struct StageRows {
   const int* rows;
   const int* offsets;
   uint8_t* order;
+  uint8_t* order_c;
   uint8_t* slab_a;
   uint8_t* slab_c;
   long long ld_a, ld_c, pitch_a, pitch_c, bytes_a, bytes_c;
@@ -75,8 +77,43 @@ struct StageRows {
 
 constexpr int kSlab = 64;
 
+// A row that starts m bytes past a 16-byte boundary: each piece is shifted
+// together from the two aligned ones that hold it, as long as the second lies
+// whole in the row; the last pieces go byte by byte.
+__device__ __forceinline__ void stage_shifted_row(const uint8_t* from, int m, long long bytes, uint8_t* to,
+                                                  long long pitch, int lane) {
+  const int pieces = static_cast<int>(pitch / 16), whole = static_cast<int>((m + bytes) / 16) - 1;
+  const uint8_t* base = from - m;  // in the matrix, which starts on a boundary
+#pragma unroll 2
+  for (int c = lane; c < pieces; c += 32) {
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (c < whole) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(base + c * 16LL);
+      const uint4 hi = *reinterpret_cast<const uint4*>(base + c * 16LL + 16);
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      uint32_t a[6], b[5];
+#pragma unroll
+      for (int k = 0; k < 6; ++k) a[k] = m & 8 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) b[k] = m & 4 ? a[k + 1] : a[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(b[k], b[k + 1], (m & 3) * 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c * 16LL + i < bytes) o[i >> 2] |= uint32_t(from[c * 16LL + i]) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint4*>(to + c * 16LL) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 __device__ __forceinline__ void stage_row(const uint8_t* from, long long bytes, uint8_t* to, long long pitch,
                                           int lane) {
+  const int m = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
+  if (m != 0) {
+    stage_shifted_row(from, m, bytes, to, pitch, lane);
+    return;
+  }
   const int pieces = static_cast<int>(pitch / 16);
   const int whole = from != nullptr ? static_cast<int>(bytes / 16) : 0;
   int c = lane;
@@ -104,11 +141,17 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
   const int lane = threadIdx.x & 31;
   auto start = [&](int e) { return e <= 0 ? 0 : min(max(p.offsets[e], 0), p.slots); };
   auto row = [&](int s) { return min(max(p.rows != nullptr ? p.rows[s] : s, 0), p.a_rows - 1); };
-  const long long used = p.order != nullptr ? start(p.groups) : 0;
+  const long long rows_a = p.order != nullptr ? start(p.groups) : 0;
+  const long long used = rows_a + (p.order_c != nullptr ? start(p.groups) : 0);
   const long long tasks = used + (p.slab_a != nullptr ? 2LL * p.groups * kSlab : 0);
   for (long long t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < tasks; t += gridDim.x * 8LL) {
-    if (t < used) {
+    if (t < rows_a) {
       stage_row(p.a + row(int(t)) * p.ld_a, p.bytes_a, p.order + t * p.pitch_a, p.pitch_a, lane);
+      continue;
+    }
+    if (t < used) {
+      const long long s = t - rows_a;
+      stage_row(p.c + s * p.ld_c, p.bytes_c, p.order_c + s * p.pitch_c, p.pitch_c, lane);
       continue;
     }
     const int q = int(t - used), e = q / (2 * kSlab), r = (q >> 1) % kSlab;
@@ -128,7 +171,8 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
 int64_t staged_pitch(int64_t cols, int es) { return (cols * es + 127) / 128 * 128; }
 
 int stage_rows(const CallContext& ctx, const StageRows& p, cudaStream_t stream) {
-  const int64_t rows = (p.order != nullptr ? p.slots : 0) + (p.slab_a != nullptr ? 2 * int64_t(p.groups) * kSlab : 0);
+  const int64_t rows = (p.order != nullptr ? p.slots : 0) + (p.order_c != nullptr ? p.slots : 0) +
+                       (p.slab_a != nullptr ? 2 * int64_t(p.groups) * kSlab : 0);
   const int64_t blocks = (rows + 7) / 8, most = int64_t(ctx.sm_count) * 8;
   const cudaError_t e = launch_dependent(stage_rows_kernel, int(blocks < most ? blocks : most), 256, 0, stream, 1, p);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
@@ -152,6 +196,13 @@ bool use_pair(int64_t slots, int64_t groups) { return average_group(slots, group
 // Tile rows per band: 8 row tiles of a group share each column tile's weights
 // while those are in L2.
 constexpr int kGroupRaster = 8;
+
+// Bytes of the workspace for A's rows in slot order: those with names from 16 a group on, and all of a pitch that is
+// not TMA's.
+int64_t rows_workspace(int es, int64_t groups, int64_t slots, int64_t K, int64_t a_rows, int64_t lda, bool gathered) {
+  const bool copied = odd_pitch(row_pitch(a_rows, K, lda, es), es) || (gathered && use_staging(slots, groups));
+  return copied ? slots * staged_pitch(K, es) : 0;
+}
 
 int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
                 int64_t a_rows, int64_t lda, const int32_t* rows, const void* W, int64_t ldw, int64_t stride_w, void* C,
@@ -183,13 +234,16 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   lda = row_pitch(a_rows, K, lda, es);
   ldw = row_pitch(w_rows, w_cols, ldw, es);
   const void* bias = epi != nullptr ? epi->bias : nullptr;
-  if (rows == nullptr || K == 0) workspace = nullptr;
-  if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es)) return GEMM_ERR_INVALID_VALUE;
+  const bool odd_a = K > 0 && odd_pitch(lda, es);
+  if ((rows == nullptr && !odd_a) || K == 0) workspace = nullptr;
+  if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es))
+    return odd_a ? GEMM_ERR_MISALIGNED : GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
       misaligned(workspace, 128) ||
       (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
     return GEMM_ERR_MISALIGNED;
-  if (K > 0 && (!tma_rows(A, lda, es) || !tma_rows(W, ldw, es) || (groups > 1 && (stride_w * es) % 16 != 0)))
+  if (K > 0 && (misaligned(A, 16) || (odd_a && workspace == nullptr) || misaligned(W, 16) || odd_pitch(ldw, es) ||
+                (groups > 1 && (stride_w * es) % 16 != 0)))
     return GEMM_ERR_MISALIGNED;
   // the value half of row-major weights is a TMA box of its own
   if (K > 0 && gated && layout == GEMM_B_ROW_MAJOR && (out_cols * es) % 16 != 0) return GEMM_ERR_MISALIGNED;
@@ -248,7 +302,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   const uint32_t bk = 128 / es;
   if (K > 0) {
     p.gather_a = rows != nullptr;
-    if (rows != nullptr && workspace != nullptr) {
+    if (workspace != nullptr) {
       StageRows q = {};
       q.a = static_cast<const uint8_t*>(A);
       q.ld_a = lda * es;
@@ -295,8 +349,10 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-int64_t wgrad_workspace(int64_t groups, int64_t slots, int64_t N, int64_t K, bool gathered) {
-  return groups * kSlab * (staged_pitch(N, 2) + staged_pitch(K, 2)) + (gathered ? slots * staged_pitch(K, 2) : 0);
+// The slabs, and the rows of A and of dC that are copied whole.
+int64_t wgrad_workspace(int64_t groups, int64_t slots, int64_t N, int64_t K, bool copy_a, bool copy_c = false) {
+  return groups * kSlab * (staged_pitch(N, 2) + staged_pitch(K, 2)) + (copy_a ? slots * staged_pitch(K, 2) : 0) +
+         (copy_c ? slots * staged_pitch(N, 2) : 0);
 }
 
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
@@ -324,7 +380,10 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
     return GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2) || misaligned(workspace, 128))
     return GEMM_ERR_MISALIGNED;
-  if (slots > 0 && (!tma_rows(A, lda, 2) || !tma_rows(dC, lddc, 2))) return GEMM_ERR_MISALIGNED;
+  const bool copy_a = rows != nullptr || odd_pitch(lda, 2), copy_c = odd_pitch(lddc, 2);
+  if (slots > 0 && (misaligned(A, 16) || misaligned(dC, 16) ||
+                    workspace_bytes < wgrad_workspace(groups, slots, N, K, copy_a, copy_c)))
+    return GEMM_ERR_MISALIGNED;
   const Range rw = range_of(dW, out_rows, out_cols, lddw, 2, groups, groups > 1 ? stride_dw : 0);
   if (workspace != nullptr && meet(rw, range_of(workspace, 1, workspace_bytes, 0, 1))) return GEMM_ERR_INVALID_VALUE;
   if (slots > 0 && (meet(rw, range_of(A, a_rows, K, lda, 2)) || meet(rw, range_of(dC, slots, N, lddc, 2))))
@@ -365,7 +424,8 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   L.grid = int(2 * (tiles < units ? tiles : units));
   const CUtensorMapDataType dt = map_type(kind);
   if (slots > 0) {
-    // workspace: the groups' ragged slabs of dC and of A, then A's rows in slot order where the caller names them
+    // workspace: the groups' ragged slabs of dC and of A, then A's rows in slot order where the caller names them or
+    // their pitch is not TMA's, then dC's rows where theirs is not
     StageRows q = {};
     q.a = static_cast<const uint8_t*>(A);
     q.c = static_cast<const uint8_t*>(dC);
@@ -382,10 +442,17 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
     q.slots = int(slots);
     q.slab_c = static_cast<uint8_t*>(workspace);
     q.slab_a = q.slab_c + int64_t(groups) * kSlab * q.pitch_c;
-    if (rows != nullptr) {
-      q.order = q.slab_a + int64_t(groups) * kSlab * q.pitch_a;
+    uint8_t* next = q.slab_a + int64_t(groups) * kSlab * q.pitch_a;
+    if (copy_a) {
+      q.order = next;
+      next += slots * q.pitch_a;
       A = q.order;
       lda = q.pitch_a / 2;
+    }
+    if (copy_c) {
+      q.order_c = next;
+      dC = q.order_c;
+      lddc = q.pitch_c / 2;
     }
     st = stage_rows(ctx, q, L.stream);
     if (st != GEMM_OK) return st;
@@ -425,6 +492,20 @@ int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K) {
 
 int64_t gemm_grouped_wgrad_workspace(int groups, int64_t slots, int64_t N, int64_t K, int gathered) {
   return groups < 1 || slots <= 0 || N <= 0 || K <= 0 ? 0 : dgt::wgrad_workspace(groups, slots, N, K, gathered != 0);
+}
+
+int64_t gemm_grouped_rows_workspace(int type, int groups, int64_t slots, int64_t K, int64_t a_rows, int64_t lda,
+                                    int gathered) {
+  if (groups < 1 || slots <= 0 || K <= 0) return 0;
+  return dgt::rows_workspace(type == GEMM_TYPE_E4M3 ? 1 : 2, groups, slots, K, a_rows, lda, gathered != 0);
+}
+
+int64_t gemm_grouped_wgrad_rows_workspace(int groups, int64_t slots, int64_t N, int64_t K, int64_t a_rows, int64_t lda,
+                                          int gathered, int64_t lddc) {
+  if (groups < 1 || slots <= 0 || N <= 0 || K <= 0) return 0;
+  return dgt::wgrad_workspace(groups, slots, N, K,
+                              gathered != 0 || dgt::odd_pitch(dgt::row_pitch(a_rows, K, lda, 2), 2),
+                              dgt::odd_pitch(dgt::row_pitch(slots, N, lddc, 2), 2));
 }
 
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,

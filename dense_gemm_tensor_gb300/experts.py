@@ -28,7 +28,8 @@ GEMM_ACT_SILU_GATED = 4
 EXPORTS = ("gemm_rmsnorm", "gemm_rmsnorm_backward", "gemm_rmsnorm_backward_workspace", "gemm_route",
            "gemm_route_workspace", "gemm_route_backward", "gemm_f16_grouped", "gemm_bf16_grouped",
            "gemm_e4m3_grouped", "gemm_grouped_workspace", "gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad",
-           "gemm_grouped_wgrad_workspace", "gemm_combine", "gemm_combine_backward")
+           "gemm_grouped_wgrad_workspace", "gemm_grouped_rows_workspace", "gemm_grouped_wgrad_rows_workspace",
+           "gemm_combine", "gemm_combine_backward")
 
 ACTIVATIONS = {**gemm.ACTIVATIONS, "silu_gated": GEMM_ACT_SILU_GATED}
 SCORES = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
@@ -92,7 +93,9 @@ def _load():
     for name in ("gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad"):
         sig[name] = [i, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, i, vp, i64, vp]
     sizes = {"gemm_rmsnorm_backward_workspace": [i64, i64], "gemm_route_workspace": [i64, i, i],
-             "gemm_grouped_workspace": [i, i, i64, i64], "gemm_grouped_wgrad_workspace": [i, i64, i64, i64, i]}
+             "gemm_grouped_workspace": [i, i, i64, i64], "gemm_grouped_wgrad_workspace": [i, i64, i64, i64, i],
+             "gemm_grouped_rows_workspace": [i, i, i64, i64, i64, i64, i],
+             "gemm_grouped_wgrad_rows_workspace": [i, i64, i64, i64, i64, i64, i, i64]}
     for name, args in {**sig, **sizes}.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i64 if name in sizes else i

@@ -166,17 +166,22 @@ typedef struct gemm_grouped_epilogue {
  * `slots` are set to zero. `rows` NULL needs a_rows >= slots. With the other
  * layout flag the same call is the gradient of A: dA = dC . W_e^T, one row a
  * slot. epilogue NULL: C = A . W. 1 <= groups <= 1024; slots, N, K < 2^31;
- * K = 0 gives the epilogue of 0. Rows and bases of A and W and the matrix
- * stride must be 16-byte multiples (GEMM_ERR_MISALIGNED otherwise; an A or a W_e
- * of one row may have any pitch), and with row-major W GEMM_ACT_SILU_GATED's second
- * half must start on one; C may have any alignment that keeps its elements
- * aligned.
+ * K = 0 gives the epilogue of 0 (an A of no rows takes no row_scale then). A and
+ * W must start on 16-byte boundaries, and W's rows and the matrix stride must be
+ * 16-byte multiples (GEMM_ERR_MISALIGNED otherwise; a W_e of one row may have any
+ * pitch), and with row-major W GEMM_ACT_SILU_GATED's second half must start on
+ * one; C may have any alignment that keeps its elements aligned.
  *
- * workspace, used with `rows` only: gemm_grouped_workspace bytes, 128-byte
- * aligned, into which the rows are put in slot order first; NULL: they are
- * gathered on the way to shared memory (the same results; slower where groups
- * have many rows, which is where the size call asks for a workspace).
+ * workspace: gemm_grouped_rows_workspace bytes, 128-byte aligned, into which A's
+ * rows are put in slot order first: rows of a pitch that is not a multiple of 16
+ * bytes (GEMM_ERR_MISALIGNED without it; an A of one row may have any pitch), and
+ * with `rows` those of groups that have many rows on average. Without it (NULL)
+ * named rows are gathered on the way to shared memory (the same results; slower
+ * where groups have many rows). gemm_grouped_workspace: the same for A with rows
+ * of 16-byte multiples and `rows`.
  */
+int64_t gemm_grouped_rows_workspace(int type, int groups, int64_t slots, int64_t K, int64_t a_rows, int64_t lda,
+                                    int gathered);
 int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K);
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,
@@ -196,12 +201,16 @@ int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t
  *   layout GEMM_B_K_MAJOR:   dW_e (N x K) = sum over the group's s of dC[s]^T A[row(s)]
  *   layout GEMM_B_ROW_MAJOR: dW_e (K x N) = sum over the group's s of A[row(s)]^T dC[s]
  * in fp32, rounded once to the operands' type; a group without slots gets
- * zeros. dC: slots x N. A, rows and dC as above (16-byte rows and bases); dW
+ * zeros. dC: slots x N. A, rows and dC as above (from 16-byte boundaries); dW
  * may have any alignment that keeps its elements aligned, stride_dw at least
- * one matrix's extent. workspace: gemm_grouped_wgrad_workspace bytes (`gathered`:
- * `rows` is given), 128-byte aligned, for the groups' last, partly filled slabs
- * and, with `rows`, A's rows in slot order.
+ * one matrix's extent. workspace: gemm_grouped_wgrad_rows_workspace bytes
+ * (`gathered`: `rows` is given), 128-byte aligned, for the groups' last, partly
+ * filled slabs, for A's rows in slot order with `rows` or a pitch that is not a
+ * multiple of 16 bytes, and for dC's rows with such a pitch.
+ * gemm_grouped_wgrad_workspace: the same for pitches that are.
  */
+int64_t gemm_grouped_wgrad_rows_workspace(int groups, int64_t slots, int64_t N, int64_t K, int64_t a_rows, int64_t lda,
+                                          int gathered, int64_t lddc);
 int64_t gemm_grouped_wgrad_workspace(int groups, int64_t slots, int64_t N, int64_t K, int gathered);
 int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                            int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* dC, int64_t lddc,

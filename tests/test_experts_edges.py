@@ -26,3 +26,32 @@ def test_row_scales_of_a_matrix_without_rows(lib):
     """Slots that name rows of an A of no rows have no scale to read, whatever K is."""
     for K in (0, 8):
         assert _grouped(lib, K=K, A=None, a_rows=0, rows=5 * P, row_scale=6 * P) == INVALID
+
+
+def test_workspace_of_rows_of_any_pitch(lib):
+    rows, grad = lib.gemm_grouped_rows_workspace, lib.gemm_grouped_wgrad_rows_workspace
+    for gathered in (0, 1):
+        assert rows(1, 4, 5, 65, 5, 65, gathered) == 5 * 256      # rows of 130 bytes are copied at a 128-byte pitch
+        assert rows(3, 4, 5, 65, 5, 65, gathered) == 5 * 128
+        assert rows(1, 4, 5, 65, 1, 65, gathered) == 0            # the pitch of one row says nothing
+        assert rows(1, 4, 5, 65, 5, 72, gathered) == 0            # rows of 144 bytes are read where they are
+        assert rows(1, 4, 0, 65, 0, 65, gathered) == 0
+    assert rows(1, 4, 512, 65, 9, 72, 1) == lib.gemm_grouped_workspace(1, 4, 512, 65) == 512 * 256
+    slabs = 2 * 64 * (256 + 128)
+    assert grad(2, 3, 65, 64, 3, 64, 0, 72) == lib.gemm_grouped_wgrad_workspace(2, 3, 65, 64, 0) == slabs
+    assert grad(2, 3, 65, 64, 3, 64, 1, 72) == slabs + 3 * 128
+    assert grad(2, 3, 65, 64, 3, 64, 0, 65) == slabs + 3 * 256
+    assert grad(2, 3, 65, 60, 3, 60, 0, 65) == slabs + 3 * (128 + 256)
+    assert grad(2, 1, 65, 60, 1, 60, 0, 65) == slabs
+
+
+def test_rows_of_any_pitch_need_their_workspace(lib):
+    for kw in (dict(), dict(rows=5 * P)):
+        assert _grouped(lib, lda=12, ws=6 * P, bytes=4 * 128 - 1, **kw) == MISALIGNED
+        assert _grouped(lib, lda=12, ws=4 * P, bytes=4 * 128, **kw) == INVALID            # it is C
+        assert _grouped(lib, lda=12, A=2 * P + 8, ws=6 * P, bytes=4 * 128, **kw) == MISALIGNED
+    grad = dict(groups=2, off=P, slots=4, N=8, K=8, A=2 * P, a_rows=4, lda=8, rows=None, dC=3 * P, lddc=12, dW=4 * P,
+                lddw=8, sdw=64, layout=1, ws=7 * P, bytes=2 * 64 * 256 + 4 * 128 - 1)
+    assert lib.gemm_bf16_grouped_wgrad(*grad.values(), None) == MISALIGNED
+    grad["bytes"], grad["dC"] = 2 * 64 * 256 + 4 * 128, 3 * P + 2
+    assert lib.gemm_bf16_grouped_wgrad(*grad.values(), None) == MISALIGNED

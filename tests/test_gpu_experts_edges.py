@@ -189,6 +189,41 @@ def test_weights_of_one_row(K, N, dtype, layout):
     _accept(C, c, s, dtype)
 
 
+# one token; a few rows a group; groups of more than a tile; pairs of tiles
+SIZES = [(1, 4, 2, 67, 41), (23, 5, 2, 133, 90), (300, 3, 2, 515, 131), (700, 2, 1, 90, 333)]
+
+
+@pytest.mark.parametrize("tokens,E,k,K,N", SIZES)
+@pytest.mark.parametrize("dtype,layout", KINDS)
+@pytest.mark.parametrize("gather", [True, False])
+def test_contiguous_rows_of_any_width(tokens, E, k, K, N, dtype, layout, gather):
+    _, _, rows, offsets = _routing(tokens, E, k, 1, empty=(1,) if E > 3 else (), unused=tokens // 9)
+    n = tokens if gather else tokens * k
+    a, w = _normal((n, K), dtype, 2), _normal((E, N, K) if layout else (E, K, N), dtype, 3)
+    if dtype != "e4m3":  # a row that no slot takes touches its neighbours' memory only
+        a[list(set(range(n)) - set(rows[:offsets[-1]] if gather else range(offsets[-1])))] = float("nan")
+    r, off = _dev_order(rows, offsets)
+    C = experts.expert_matmul(a.cuda(), _pitch16(w), off, r if gather else None, layout=layout)
+    c, s = ox.grouped(_np(a.float()), _np(w.float()), offsets, rows if gather else None, layout)
+    _accept(C, c, s, dtype)
+
+
+@pytest.mark.parametrize("tokens,E,k,K,N", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("which", ["A", "dC", "both"])
+def test_weight_gradient_of_contiguous_rows_of_any_width(tokens, E, k, K, N, dtype, layout, gather, which):
+    _, _, rows, offsets = _routing(tokens, E, k, 21, empty=(2,) if E > 3 else (), unused=tokens // 9)
+    a, dc = _normal((tokens if gather else tokens * k, K), dtype, 22), _normal((tokens * k, N), dtype, 23)
+    dc[offsets[-1]:] = float("nan")  # rows of no group
+    r, off = _dev_order(rows, offsets)
+    dw = experts.expert_weight_grad(a.cuda() if which != "dC" else _pitch16(a), dc.cuda() if which != "A" else _pitch16(dc),
+                                    off, r if gather else None, layout=layout)
+    want, s = ox.grouped_wgrad(_np(a), np.nan_to_num(_np(dc)), offsets, rows if gather else None, layout)
+    _accept(dw, want, s, dtype)
+
+
 # ---------------------------------------------------------------- numbers at the ends of their ranges
 
 def test_routing_of_the_most_tokens():
