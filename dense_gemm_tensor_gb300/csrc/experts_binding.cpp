@@ -38,6 +38,7 @@ struct Entries {
   decltype(&gemm_bf16_grouped) bf16_grouped;
   decltype(&gemm_e4m3_grouped) e4m3_grouped;
   decltype(&gemm_grouped_rows_workspace) grouped_rows_workspace;
+  decltype(&gemm_grouped_weights_workspace) grouped_weights_workspace;
   decltype(&gemm_f16_grouped_wgrad) f16_grouped_wgrad;
   decltype(&gemm_bf16_grouped_wgrad) bf16_grouped_wgrad;
   decltype(&gemm_grouped_wgrad_rows_workspace) grouped_wgrad_rows_workspace;
@@ -47,7 +48,7 @@ struct Entries {
 constexpr const char* kNames[] = {
     "gemm_rmsnorm",          "gemm_rmsnorm_backward", "gemm_rmsnorm_backward_workspace", "gemm_route",
     "gemm_route_workspace",  "gemm_route_backward",   "gemm_f16_grouped",                "gemm_bf16_grouped",
-    "gemm_e4m3_grouped",     "gemm_grouped_rows_workspace", "gemm_f16_grouped_wgrad",         "gemm_bf16_grouped_wgrad",
+    "gemm_e4m3_grouped",     "gemm_grouped_rows_workspace", "gemm_grouped_weights_workspace", "gemm_f16_grouped_wgrad",         "gemm_bf16_grouped_wgrad",
     "gemm_grouped_wgrad_rows_workspace", "gemm_combine",   "gemm_combine_backward"};
 constexpr int kEntries = sizeof(kNames) / sizeof(kNames[0]);
 static_assert(sizeof(Entries) == kEntries * sizeof(void*), "one address for each name");
@@ -284,8 +285,9 @@ PyObject* expert_matmul(PyObject* const* a) {
     slots = r.numel();
     rows = vector<int32_t>(r, "rows", at::kInt, slots);
   }
-  const int64_t need = entry.c.grouped_rows_workspace(code, e, slots, K, a_rows, lda, rows != nullptr);
   const int act = static_cast<int>(whole(a[10]));
+  const int64_t need = entry.c.grouped_rows_workspace(code, e, slots, K, a_rows, lda, rows != nullptr) +
+                       entry.c.grouped_weights_workspace(code, e, N, K, w.ld, w.stride, layout, act);
   const int64_t cols = act == GEMM_ACT_SILU_GATED ? N / 2 : N;
   Tensor out;
   int64_t ldc = cols;

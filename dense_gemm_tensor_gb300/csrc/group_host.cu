@@ -58,6 +58,9 @@ void fill_common(const CallContext& ctx, GroupParams& p) {
 // bytes of the destination's pitch past the row are zero):
 //   * `order`: the gathered operand's rows in slot order, order[s] = a[row(s)]
 //   * `order_c`: the other operand's rows c[s], where their pitch is not TMA's
+//   * `mats`: the weights of the groups that have slots, where TMA cannot read them in
+//     place; a row of w_parts parts (the two halves of gated row-major weights) gets each
+//     part on a boundary of its own
 //   * `slab_a`, `slab_c` (the weights' gradient): the last slab of 64 slots of
 //     every group whose count is not a multiple of 64, zeros past its end
 // Bound by memory: one read of the rows (repeats of a token hit L2) and one
@@ -65,23 +68,27 @@ void fill_common(const CallContext& ctx, GroupParams& p) {
 struct StageRows {
   const uint8_t* a;
   const uint8_t* c;
+  const uint8_t* w;
   const int* rows;
   const int* offsets;
   uint8_t* order;
   uint8_t* order_c;
   uint8_t* slab_a;
   uint8_t* slab_c;
-  long long ld_a, ld_c, pitch_a, pitch_c, bytes_a, bytes_c;
-  int a_rows, groups, slots;
+  uint8_t* mats;
+  long long ld_a, ld_c, ld_w, stride_w, pitch_a, pitch_c, pitch_w, bytes_a, bytes_c, bytes_w;  // (_w: of one part)
+  int a_rows, groups, slots, w_rows, w_parts;
 };
 
 constexpr int kSlab = 64;
 
-// A row that starts m bytes past a 16-byte boundary: each piece is shifted
-// together from the two aligned ones that hold it, as long as the second lies
-// whole in the row; the last pieces go byte by byte.
-__device__ __forceinline__ void stage_shifted_row(const uint8_t* from, int m, long long bytes, uint8_t* to,
-                                                  long long pitch, int lane) {
+// A row that starts anywhere: each piece is shifted together from the two
+// aligned ones that hold it, as long as the second lies whole in the row; the last
+// pieces go byte by byte.
+__device__ __forceinline__ void stage_shifted_row(const uint8_t* from, long long bytes, uint8_t* to, long long pitch,
+                                                  int lane) {
+  const int m = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
+  if (from == nullptr) bytes = 0;
   const int pieces = static_cast<int>(pitch / 16), whole = static_cast<int>((m + bytes) / 16) - 1;
   const uint8_t* base = from - m;  // in the matrix, which starts on a boundary
 #pragma unroll 2
@@ -107,11 +114,11 @@ __device__ __forceinline__ void stage_shifted_row(const uint8_t* from, int m, lo
   }
 }
 
+template <bool SHIFTED>
 __device__ __forceinline__ void stage_row(const uint8_t* from, long long bytes, uint8_t* to, long long pitch,
                                           int lane) {
-  const int m = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
-  if (m != 0) {
-    stage_shifted_row(from, m, bytes, to, pitch, lane);
+  if constexpr (SHIFTED) {
+    stage_shifted_row(from, bytes, to, pitch, lane);
     return;
   }
   const int pieces = static_cast<int>(pitch / 16);
@@ -136,23 +143,41 @@ __device__ __forceinline__ void stage_row(const uint8_t* from, long long bytes, 
   }
 }
 
+// SHIFTED: some rows start off 16-byte boundaries, which every copy of dC's rows
+// and of the weights means. (A build of its own: with its registers and branches the
+// rows of a training step's gradient, 16384 x 4096 BF16, took 3 us more.)
+template <bool SHIFTED>
 __global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   auto start = [&](int e) { return e <= 0 ? 0 : min(max(p.offsets[e], 0), p.slots); };
   auto row = [&](int s) { return min(max(p.rows != nullptr ? p.rows[s] : s, 0), p.a_rows - 1); };
   const long long rows_a = p.order != nullptr ? start(p.groups) : 0;
-  const long long used = rows_a + (p.order_c != nullptr ? start(p.groups) : 0);
-  const long long tasks = used + (p.slab_a != nullptr ? 2LL * p.groups * kSlab : 0);
+  long long used = rows_a;
+  if constexpr (SHIFTED) used += p.order_c != nullptr ? start(p.groups) : 0;
+  const long long slabs = used + (p.slab_a != nullptr ? 2LL * p.groups * kSlab : 0);
+  long long tasks = slabs;
+  if constexpr (SHIFTED) tasks += p.mats != nullptr ? static_cast<long long>(p.groups) * p.w_rows * p.w_parts : 0;
   for (long long t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < tasks; t += gridDim.x * 8LL) {
     if (t < rows_a) {
-      stage_row(p.a + row(int(t)) * p.ld_a, p.bytes_a, p.order + t * p.pitch_a, p.pitch_a, lane);
+      stage_row<SHIFTED>(p.a + row(int(t)) * p.ld_a, p.bytes_a, p.order + t * p.pitch_a, p.pitch_a, lane);
       continue;
     }
-    if (t < used) {
-      const long long s = t - rows_a;
-      stage_row(p.c + s * p.ld_c, p.bytes_c, p.order_c + s * p.pitch_c, p.pitch_c, lane);
-      continue;
+    if constexpr (SHIFTED) {
+      if (t < used) {
+        const long long s = t - rows_a;
+        stage_row<SHIFTED>(p.c + s * p.ld_c, p.bytes_c, p.order_c + s * p.pitch_c, p.pitch_c, lane);
+        continue;
+      }
+      if (t >= slabs) {
+        const long long part = t - slabs, r = part / p.w_parts;
+        const int e = int(r / p.w_rows);
+        if (start(e + 1) <= start(e)) continue;
+        stage_row<SHIFTED>(p.w + e * p.stride_w + (r - static_cast<long long>(e) * p.w_rows) * p.ld_w +
+                               (part - r * p.w_parts) * p.bytes_w,
+                           p.bytes_w, p.mats + part * p.pitch_w, p.pitch_w, lane);
+        continue;
+      }
     }
     const int q = int(t - used), e = q / (2 * kSlab), r = (q >> 1) % kSlab;
     const int begin = start(e), end = max(begin, start(e + 1));
@@ -160,9 +185,9 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
     const int s = begin + (end - begin) / kSlab * kSlab + r;
     const long long at = static_cast<long long>(e) * kSlab + r;
     if (q & 1)
-      stage_row(s < end ? p.a + row(s) * p.ld_a : nullptr, p.bytes_a, p.slab_a + at * p.pitch_a, p.pitch_a, lane);
+      stage_row<SHIFTED>(s < end ? p.a + row(s) * p.ld_a : nullptr, p.bytes_a, p.slab_a + at * p.pitch_a, p.pitch_a, lane);
     else
-      stage_row(s < end ? p.c + s * p.ld_c : nullptr, p.bytes_c, p.slab_c + at * p.pitch_c, p.pitch_c, lane);
+      stage_row<SHIFTED>(s < end ? p.c + s * p.ld_c : nullptr, p.bytes_c, p.slab_c + at * p.pitch_c, p.pitch_c, lane);
   }
   grid_launch_dependents();
 }
@@ -172,9 +197,14 @@ int64_t staged_pitch(int64_t cols, int es) { return (cols * es + 127) / 128 * 12
 
 int stage_rows(const CallContext& ctx, const StageRows& p, cudaStream_t stream) {
   const int64_t rows = (p.order != nullptr ? p.slots : 0) + (p.order_c != nullptr ? p.slots : 0) +
-                       (p.slab_a != nullptr ? 2 * int64_t(p.groups) * kSlab : 0);
+                       (p.slab_a != nullptr ? 2 * int64_t(p.groups) * kSlab : 0) +
+                       (p.mats != nullptr ? int64_t(p.groups) * p.w_rows * p.w_parts : 0);
   const int64_t blocks = (rows + 7) / 8, most = int64_t(ctx.sm_count) * 8;
-  const cudaError_t e = launch_dependent(stage_rows_kernel, int(blocks < most ? blocks : most), 256, 0, stream, 1, p);
+  const int grid = int(blocks < most ? blocks : most);
+  const bool shifted = (p.a != nullptr && p.ld_a % 16 != 0) || (p.c != nullptr && p.ld_c % 16 != 0) ||
+                       (p.w != nullptr && (p.ld_w | p.stride_w | (p.w_parts - 1) * p.bytes_w) % 16 != 0);
+  const cudaError_t e = shifted ? launch_dependent(stage_rows_kernel<true>, grid, 256, 0, stream, 1, p)
+                                : launch_dependent(stage_rows_kernel<false>, grid, 256, 0, stream, 1, p);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -202,6 +232,30 @@ constexpr int kGroupRaster = 8;
 int64_t rows_workspace(int es, int64_t groups, int64_t slots, int64_t K, int64_t a_rows, int64_t lda, bool gathered) {
   const bool copied = odd_pitch(row_pitch(a_rows, K, lda, es), es) || (gathered && use_staging(slots, groups));
   return copied ? slots * staged_pitch(K, es) : 0;
+}
+
+// Weights that TMA cannot read where they are: rows or matrices off 16-byte multiples, or a value half that starts off
+// one. They are copied, the groups with slots, in every call (a caller that keeps them aligned saves that: 16 tokens x
+// 4 of 64 experts, gated row-major 2048 x 4090 BF16, 420 us against 113 for 2048 x 4096; 8192 tokens x 2 of 16, 4096 x
+// 4090, 600 against 378. The copy runs at 6.3-6.9 TB/s.)
+struct WeightCopy {
+  int64_t rows, cols, ld;  // of W_e; ld as TMA may take it
+  int parts;               // of a copied row
+  int64_t pitch;           // of a copied part, bytes
+  int64_t bytes;           // of the workspace: 0 where nothing is copied
+};
+WeightCopy weight_copy(int es, int64_t groups, int64_t N, int64_t K, int64_t ldw, int64_t stride_w, bool row_major,
+                       bool gated) {
+  WeightCopy c;
+  c.rows = row_major ? K : N;
+  c.cols = row_major ? N : K;
+  c.ld = row_pitch(c.rows, c.cols, ldw, es);
+  c.parts = gated && row_major ? 2 : 1;
+  c.pitch = staged_pitch(c.cols / c.parts, es);
+  const bool odd = odd_pitch(c.ld, es) || (groups > 1 && odd_pitch(stride_w, es)) ||
+                   (c.parts == 2 && odd_pitch(c.cols / 2, es));
+  c.bytes = odd && K > 0 ? groups * c.rows * c.parts * c.pitch : 0;
+  return c;
 }
 
 int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
@@ -232,21 +286,24 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   }
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
   lda = row_pitch(a_rows, K, lda, es);
-  ldw = row_pitch(w_rows, w_cols, ldw, es);
+  const WeightCopy wc = weight_copy(es, groups, N, K, ldw, stride_w, layout == GEMM_B_ROW_MAJOR, gated);
+  ldw = wc.ld;
   const void* bias = epi != nullptr ? epi->bias : nullptr;
   const bool odd_a = K > 0 && odd_pitch(lda, es);
-  if ((rows == nullptr && !odd_a) || K == 0) workspace = nullptr;
-  if (workspace != nullptr && workspace_bytes < slots * staged_pitch(K, es))
-    return odd_a ? GEMM_ERR_MISALIGNED : GEMM_ERR_INVALID_VALUE;
+  if (K == 0 || (rows == nullptr && !odd_a && wc.bytes == 0)) workspace = nullptr;
+  // A's rows come first in the workspace, then the weights. Named rows are gathered on the way where there is room for
+  // the weights only.
+  const int64_t a_bytes = slots * staged_pitch(K, es);
+  bool copy_a = workspace != nullptr && (rows != nullptr || odd_a);
+  if (wc.bytes > 0 && copy_a && !odd_a && workspace_bytes < a_bytes + wc.bytes) copy_a = false;
+  if (workspace != nullptr && workspace_bytes < (copy_a ? a_bytes : 0) + wc.bytes)
+    return odd_a || wc.bytes > 0 ? GEMM_ERR_MISALIGNED : GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
       misaligned(workspace, 128) ||
       (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
     return GEMM_ERR_MISALIGNED;
-  if (K > 0 && (misaligned(A, 16) || (odd_a && workspace == nullptr) || misaligned(W, 16) || odd_pitch(ldw, es) ||
-                (groups > 1 && (stride_w * es) % 16 != 0)))
+  if (K > 0 && (misaligned(A, 16) || misaligned(W, 16) || (workspace == nullptr && (odd_a || wc.bytes > 0))))
     return GEMM_ERR_MISALIGNED;
-  // the value half of row-major weights is a TMA box of its own
-  if (K > 0 && gated && layout == GEMM_B_ROW_MAJOR && (out_cols * es) % 16 != 0) return GEMM_ERR_MISALIGNED;
   const Range rc = range_of(C, slots, out_cols, ldc, 2);
   if (workspace != nullptr && meet(rc, range_of(workspace, 1, workspace_bytes, 0, 1))) return GEMM_ERR_INVALID_VALUE;
   if (K > 0 && (meet(rc, range_of(A, a_rows, K, lda, es)) ||
@@ -300,25 +357,43 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
 
   const CUtensorMapDataType dt = map_type(kind);
   const uint32_t bk = 128 / es;
+  p.value_at = int(N / 2);
   if (K > 0) {
-    p.gather_a = rows != nullptr;
-    if (workspace != nullptr) {
-      StageRows q = {};
+    p.gather_a = rows != nullptr && !copy_a;
+    StageRows q = {};
+    q.offsets = offsets;
+    q.groups = groups;
+    q.slots = int(slots);
+    if (copy_a) {
       q.a = static_cast<const uint8_t*>(A);
       q.ld_a = lda * es;
       q.bytes_a = K * es;
       q.pitch_a = staged_pitch(K, es);
       q.a_rows = int(a_rows);
       q.rows = rows;
-      q.offsets = offsets;
-      q.groups = groups;
-      q.slots = int(slots);
       q.order = static_cast<uint8_t*>(workspace);
-      st = stage_rows(ctx, q, L.stream);
-      if (st != GEMM_OK) return st;
       A = workspace;
       lda = staged_pitch(K, es) / es;
-      p.gather_a = 0;
+    }
+    int64_t w_cols_read = N;  // of row-major weights
+    if (wc.bytes > 0) {
+      q.w = static_cast<const uint8_t*>(W);
+      q.ld_w = ldw * es;
+      q.stride_w = groups > 1 ? stride_w * es : 0;
+      q.bytes_w = wc.cols / wc.parts * es;
+      q.pitch_w = wc.pitch;
+      q.w_rows = int(wc.rows);
+      q.w_parts = wc.parts;
+      q.mats = static_cast<uint8_t*>(workspace) + (copy_a ? a_bytes : 0);
+      W = q.mats;
+      ldw = wc.parts * wc.pitch / es;
+      stride_w = wc.rows * ldw;
+      if (layout == GEMM_B_ROW_MAJOR) w_cols_read = ldw;
+      if (wc.parts == 2) p.value_at = int(wc.pitch / es);
+    }
+    if (copy_a || wc.bytes > 0) {
+      st = stage_rows(ctx, q, L.stream);
+      if (st != GEMM_OK) return st;
     }
     const bool mapped =
         p.gather_a ? encode_map_2d(&L.tmA2, dt, A, K, a_rows, lda * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B)
@@ -331,7 +406,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
       const uint32_t box = L.pair ? kGroupPairN / 2 : gated ? kGroupSingleN / 2 : kGroupSingleN;
       ok = encode_map_3d(&L.tmB, dt, W, K, N, ldw * es, groups, mat, bk, box, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
-      ok = encode_map_3d(&L.tmB, dt, W, N, K, ldw * es, groups, mat, 128 / es, bk, CU_TENSOR_MAP_SWIZZLE_128B);
+      ok = encode_map_3d(&L.tmB, dt, W, w_cols_read, K, ldw * es, groups, mat, 128 / es, bk, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (!ok) return GEMM_ERR_DRIVER;
   }
@@ -498,6 +573,14 @@ int64_t gemm_grouped_rows_workspace(int type, int groups, int64_t slots, int64_t
                                     int gathered) {
   if (groups < 1 || slots <= 0 || K <= 0) return 0;
   return dgt::rows_workspace(type == GEMM_TYPE_E4M3 ? 1 : 2, groups, slots, K, a_rows, lda, gathered != 0);
+}
+
+int64_t gemm_grouped_weights_workspace(int type, int groups, int64_t N, int64_t K, int64_t ldw, int64_t stride_w,
+                                       int layout, int activation) {
+  if (groups < 1 || N <= 0 || K <= 0) return 0;
+  return dgt::weight_copy(type == GEMM_TYPE_E4M3 ? 1 : 2, groups, N, K, ldw, stride_w, layout == GEMM_B_ROW_MAJOR,
+                          activation == GEMM_ACT_SILU_GATED)
+      .bytes;
 }
 
 int64_t gemm_grouped_wgrad_rows_workspace(int groups, int64_t slots, int64_t N, int64_t K, int64_t a_rows, int64_t lda,

@@ -91,6 +91,7 @@ struct GroupParams {
   const float* row_scale;
   const float* col_scale;
   int gather_a;  // product: rows of A by gather (else boxes by slot)
+  int value_at;  // gated: where the value half starts in W (a column of row-major W, else a row)
   int plain;     // the epilogue is the identity
   int out_cols;  // columns of C (or of dW)
   int out_rows;  // gradient: rows of dW
@@ -510,11 +511,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
               }
               if constexpr (Cf::B_KMAJOR) {
                 if constexpr (PAIR) {
-                  const int n0 = GATED ? int(half) * (p.g.N / 2) + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH;
+                  const int n0 = GATED ? int(half) * p.value_at + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH;
                   tma_load_3d_pair(b_dst, &tmB, fb, x, n0, t.e);
                 } else if constexpr (GATED) {
                   tma_load_3d(b_dst, &tmB, fb, x, t.nb * Cf::OUT_BN, t.e);
-                  tma_load_3d(b_dst + Cf::B_BYTES / 2, &tmB, fb, x, p.g.N / 2 + t.nb * Cf::OUT_BN, t.e);
+                  tma_load_3d(b_dst + Cf::B_BYTES / 2, &tmB, fb, x, p.value_at + t.nb * Cf::OUT_BN, t.e);
                 } else {
                   tma_load_3d(b_dst, &tmB, fb, x, t.nb * BN, t.e);
                 }
@@ -523,12 +524,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                 for (int j = 0; j < Cf::BNH / Cf::BOXN; ++j) {
                   int n0;
                   if constexpr (PAIR) {
-                    n0 = (GATED ? int(half) * (p.g.N / 2) + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH) +
+                    n0 = (GATED ? int(half) * p.value_at + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH) +
                          j * Cf::BOXN;
                     tma_load_3d_pair(b_dst + j * Cf::BOX_BYTES, &tmB, fb, n0, x, t.e);
                   } else {
                     constexpr int HB = Cf::BNH / Cf::BOXN / 2;  // boxes of one half
-                    n0 = GATED ? (j >= HB ? p.g.N / 2 : 0) + t.nb * Cf::OUT_BN + (j >= HB ? j - HB : j) * Cf::BOXN
+                    n0 = GATED ? (j >= HB ? p.value_at : 0) + t.nb * Cf::OUT_BN + (j >= HB ? j - HB : j) * Cf::BOXN
                                : t.nb * BN + j * Cf::BOXN;
                     tma_load_3d(b_dst + j * Cf::BOX_BYTES, &tmB, fb, n0, x, t.e);
                   }

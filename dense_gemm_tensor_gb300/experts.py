@@ -28,8 +28,8 @@ GEMM_ACT_SILU_GATED = 4
 EXPORTS = ("gemm_rmsnorm", "gemm_rmsnorm_backward", "gemm_rmsnorm_backward_workspace", "gemm_route",
            "gemm_route_workspace", "gemm_route_backward", "gemm_f16_grouped", "gemm_bf16_grouped",
            "gemm_e4m3_grouped", "gemm_grouped_workspace", "gemm_f16_grouped_wgrad", "gemm_bf16_grouped_wgrad",
-           "gemm_grouped_wgrad_workspace", "gemm_grouped_rows_workspace", "gemm_grouped_wgrad_rows_workspace",
-           "gemm_combine", "gemm_combine_backward")
+           "gemm_grouped_wgrad_workspace", "gemm_grouped_rows_workspace", "gemm_grouped_weights_workspace",
+           "gemm_grouped_wgrad_rows_workspace", "gemm_combine", "gemm_combine_backward")
 
 ACTIVATIONS = {**gemm.ACTIVATIONS, "silu_gated": GEMM_ACT_SILU_GATED}
 SCORES = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
@@ -95,6 +95,7 @@ def _load():
     sizes = {"gemm_rmsnorm_backward_workspace": [i64, i64], "gemm_route_workspace": [i64, i, i],
              "gemm_grouped_workspace": [i, i, i64, i64], "gemm_grouped_wgrad_workspace": [i, i64, i64, i64, i],
              "gemm_grouped_rows_workspace": [i, i, i64, i64, i64, i64, i],
+             "gemm_grouped_weights_workspace": [i, i, i64, i64, i64, i64, i, i],
              "gemm_grouped_wgrad_rows_workspace": [i, i64, i64, i64, i64, i64, i, i64]}
     for name, args in {**sig, **sizes}.items():
         fn = getattr(lib, name)
@@ -221,7 +222,12 @@ def expert_matmul(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, rows:
     experts x N floats; ``bias``: experts x N of C's dtype; ``activation``: as
     ``gemm.matmul``'s, or "silu_gated" (W holds gate and value halves, C has
     N / 2 columns). Rows of C past offsets[-1] are zero. With the other layout
-    flag the call is the gradient of A (a row per slot)."""
+    flag the call is the gradient of A (a row per slot).
+
+    A and W start on 16-byte boundaries. Rows may have any pitch, but only those
+    (and matrices of W, and the value half of row-major gated weights) that are
+    16-byte multiples apart are read where they are: others are copied first, in
+    every call, so keep weights of an odd width in a padded buffer."""
     if stream is not None:
         return _under(stream, expert_matmul, A, W, offsets, rows, layout=layout, out=out, alpha=alpha, a_scale=a_scale,
                       w_scale=w_scale, bias=bias, activation=activation)
@@ -239,7 +245,9 @@ def expert_weight_grad(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor,
                        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """The gradient of ``expert_matmul``'s W (of its plain product) from
     ``dC`` (slots x N): experts x K x N for ``layout=GEMM_B_ROW_MAJOR``,
-    experts x N x K for ``GEMM_B_K_MAJOR``; zeros for an expert without slots."""
+    experts x N x K for ``GEMM_B_K_MAJOR``; zeros for an expert without slots.
+    A and dC start on 16-byte boundaries; rows that are not 16-byte multiples
+    apart are copied first."""
     if stream is not None:
         return _under(stream, expert_weight_grad, A, dC, offsets, rows, layout=layout, out=out)
     r = (_ext or _binding()).expert_weight_grad(A, dC, offsets, rows, layout, out)

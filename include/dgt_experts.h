@@ -167,21 +167,25 @@ typedef struct gemm_grouped_epilogue {
  * layout flag the same call is the gradient of A: dA = dC . W_e^T, one row a
  * slot. epilogue NULL: C = A . W. 1 <= groups <= 1024; slots, N, K < 2^31;
  * K = 0 gives the epilogue of 0 (an A of no rows takes no row_scale then). A and
- * W must start on 16-byte boundaries, and W's rows and the matrix stride must be
- * 16-byte multiples (GEMM_ERR_MISALIGNED otherwise; a W_e of one row may have any
- * pitch), and with row-major W GEMM_ACT_SILU_GATED's second half must start on
- * one; C may have any alignment that keeps its elements aligned.
+ * W must start on 16-byte boundaries (GEMM_ERR_MISALIGNED otherwise); C may have
+ * any alignment that keeps its elements aligned.
  *
- * workspace: gemm_grouped_rows_workspace bytes, 128-byte aligned, into which A's
- * rows are put in slot order first: rows of a pitch that is not a multiple of 16
- * bytes (GEMM_ERR_MISALIGNED without it; an A of one row may have any pitch), and
- * with `rows` those of groups that have many rows on average. Without it (NULL)
- * named rows are gathered on the way to shared memory (the same results; slower
- * where groups have many rows). gemm_grouped_workspace: the same for A with rows
- * of 16-byte multiples and `rows`.
+ * workspace: 128-byte aligned, gemm_grouped_rows_workspace + gemm_grouped_weights_workspace
+ * bytes. The first are for A's rows, put in slot order before the product: rows of
+ * a pitch that is not a multiple of 16 bytes (an A of one row may have any pitch),
+ * and with `rows` those of groups that have many rows on average; without room
+ * for them named rows are gathered on the way to shared memory (the same
+ * results; slower where groups have many rows). The second are for a copy of W, made in
+ * every call, where its pitch (of a W_e of more than one row) or its matrix
+ * stride is not a multiple of 16 bytes, or where the second half of row-major
+ * gated weights does not start on one: weights kept without these cost
+ * nothing more. GEMM_ERR_MISALIGNED where a copy is needed and there is no room for
+ * it. gemm_grouped_workspace: the first for A with rows of 16-byte multiples and `rows`.
  */
 int64_t gemm_grouped_rows_workspace(int type, int groups, int64_t slots, int64_t K, int64_t a_rows, int64_t lda,
                                     int gathered);
+int64_t gemm_grouped_weights_workspace(int type, int groups, int64_t N, int64_t K, int64_t ldw, int64_t stride_w,
+                                       int layout, int activation);
 int64_t gemm_grouped_workspace(int type, int groups, int64_t slots, int64_t K);
 int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
                      int64_t a_rows, int64_t lda, const int32_t* rows, const uint16_t* W, int64_t ldw,

@@ -55,3 +55,32 @@ def test_rows_of_any_pitch_need_their_workspace(lib):
     assert lib.gemm_bf16_grouped_wgrad(*grad.values(), None) == MISALIGNED
     grad["bytes"], grad["dC"] = 2 * 64 * 256 + 4 * 128, 3 * P + 2
     assert lib.gemm_bf16_grouped_wgrad(*grad.values(), None) == MISALIGNED
+
+
+def test_workspace_of_weights_that_are_copied(lib):
+    def size(type=1, E=3, N=40, K=24, ldw=None, sw=None, layout=1, act=0):
+        w_rows, w_cols = (N, K) if layout else (K, N)
+        ldw = w_cols if ldw is None else ldw
+        return lib.gemm_grouped_weights_workspace(type, E, N, K, ldw, w_rows * ldw if sw is None else sw, layout, act)
+
+    assert size() == size(layout=0) == size(E=1, sw=1) == 0
+    assert size(K=25) == 3 * 40 * 128                        # rows of 50 bytes
+    assert size(layout=0, N=65) == 3 * 24 * 256
+    assert size(sw=40 * 24 + 4) == 3 * 40 * 128              # matrices off 16-byte multiples
+    assert size(K=25, N=1, sw=32) == size(E=1, K=25, N=1) == 0  # one row a matrix
+    assert size(type=3) == 3 * 40 * 128 and size(type=3, K=32) == 0
+    assert size(layout=0, act=4, N=40) == 3 * 24 * 2 * 128   # halves of 40 bytes, each on a boundary of its own
+    assert size(layout=0, act=4, N=32) == size(act=4, N=42) == 0
+    assert size(K=0) == 0
+
+
+def test_copied_weights_need_their_workspace(lib):
+    copied = 2 * 8 * 128
+    for kw in (dict(ldw=12, sw=96), dict(sw=68)):
+        assert _grouped(lib, ws=6 * P, bytes=copied - 1, **kw) == MISALIGNED
+        assert _grouped(lib, ws=4 * P, bytes=copied, **kw) == INVALID                     # it is C
+        assert _grouped(lib, W=3 * P + 8, ws=6 * P, bytes=copied, **kw) == MISALIGNED
+        assert _grouped(lib, lda=12, ws=6 * P, bytes=copied + 4 * 128 - 1, **kw) == MISALIGNED
+    gated = dict(act=4, N=24, ldw=24, sw=192, ldc=12, layout=0)
+    assert _grouped(lib, ws=6 * P, bytes=2 * copied - 1, **gated) == MISALIGNED
+    assert _grouped(lib, ws=4 * P, bytes=2 * copied, **gated) == INVALID

@@ -224,6 +224,63 @@ def test_weight_gradient_of_contiguous_rows_of_any_width(tokens, E, k, K, N, dty
     _accept(dw, want, s, dtype)
 
 
+@pytest.mark.parametrize("tokens,E,k,K,N", SIZES)
+@pytest.mark.parametrize("dtype,layout", KINDS)
+@pytest.mark.parametrize("gather", [True, False])
+def test_contiguous_weights_of_any_width(tokens, E, k, K, N, dtype, layout, gather):
+    _, _, rows, offsets = _routing(tokens, E, k, 31, empty=(1,) if E > 3 else (), unused=tokens // 9)
+    n = tokens if gather else tokens * k
+    a, w = _normal((n, K), dtype, 32), _normal((E, N, K) if layout else (E, K, N), dtype, 33)
+    if E > 3 and dtype != "e4m3":
+        w[1] = float("nan")  # no row goes there
+    r, off = _dev_order(rows, offsets)
+    for rows_of_a in (a.cuda(), _pitch16(a)):
+        C = experts.expert_matmul(rows_of_a, w.cuda(), off, r if gather else None, layout=layout)
+        c, s = ox.grouped(_np(a.float()), np.nan_to_num(_np(w.float())), offsets, rows if gather else None, layout)
+        _accept(C, c, s, dtype)
+
+
+@pytest.mark.parametrize("tokens,E,k,K,F", [(1, 4, 2, 64, 37), (9, 5, 2, 200, 131), (400, 3, 2, 136, 197), (500, 2, 2, 67, 70)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("padded", [True, False])
+def test_gated_row_major_halves_of_any_width(tokens, E, k, K, F, dtype, gather, padded):
+    _, _, rows, offsets = _routing(tokens, E, k, 11, empty=(0,) if E > 3 else ())
+    a, w = _normal((tokens if gather else tokens * k, K), dtype, 12), _normal((E, K, 2 * F), dtype, 13, 0.2)
+    bias = _normal((E, 2 * F), dtype, 14)
+    r, off = _dev_order(rows, offsets)
+    C = experts.expert_matmul(_pitch16(a), _pitch16(w) if padded else w.cuda(), off, r if gather else None, layout=0,
+                              bias=bias.cuda(), activation="silu_gated")
+    c, s = ox.grouped(_np(a), _np(w), offsets, rows if gather else None, 0)
+    e = np.searchsorted(offsets, np.arange(len(rows)), side="right") - 1
+    c, s = c + _np(bias)[e], s + np.abs(_np(bias)[e])
+    g, v = c[:, :F], c[:, F:]
+    silu = g / (1 + np.exp(-g))
+    _accept(C, silu * v, 1.1 * s[:, :F] * (np.abs(v) + 1e-3 * s[:, F:]) + np.abs(silu) * s[:, F:], dtype)
+
+
+@pytest.mark.parametrize("hidden,inner", [(128, 100), (100, 72), (101, 33)])
+def test_block_of_any_width(hidden, inner):
+    """The operators take each other's outputs: the block against its own form with every width padded to whole pieces."""
+    from dense_gemm_tensor_gb300 import moe
+    block = moe.MoeBlock.random(hidden, inner, 4, 2, torch.bfloat16)
+    x, residual, dy = (_normal((50, hidden), "bf16", 40 + i).cuda() for i in range(3))
+    y, saved = block.forward(x, residual)
+    served, grads = block.serve(x, residual), block.backward(dy, saved)
+    assert block.quantize().serve(x, residual).shape == y.shape
+    n = saved.norm
+    ids, w = saved.routing.ids.long(), saved.routing.weights
+    want = n.h.double()
+    for j in range(2):
+        gate, value = torch.einsum("tnh,th->tn", block.up.double()[ids[:, j]], n.y.double()).chunk(2, dim=1)
+        z = torch.einsum("thf,tf->th", block.down.double()[ids[:, j]], torch.nn.functional.silu(gate) * value)
+        want = want + w[:, j:j + 1].double() * z
+    for got in (y, served):  # four roundings to bfloat16 on the way: up, inner, z, y
+        assert (got.double() - want).norm() <= 4 * 2.0 ** -9 * want.norm()
+    for g, p in zip(grads, (x, block.norm, block.router, block.up, block.down)):
+        assert g.shape == p.shape and bool(torch.isfinite(g.float()).all())
+
+
 # ---------------------------------------------------------------- numbers at the ends of their ranges
 
 def test_routing_of_the_most_tokens():
