@@ -127,19 +127,19 @@ __device__ __forceinline__ void stage_row(const uint8_t* from, long long bytes, 
   for (; c + 96 < whole; c += 128) {
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (c + 32 * i) * 16);
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (c + 32 * i) * 16LL);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (c + 32 * i) * 16) = v[i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (c + 32 * i) * 16LL) = v[i];
   }
   for (; c < pieces; c += 32) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (c < whole) {
-      const uint4 v = *reinterpret_cast<const uint4*>(from + c * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(from + c * 16LL);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else if (from != nullptr && c == whole) {
-      for (int i = 0; i < int(bytes - whole * 16LL); ++i) w[i >> 2] |= uint32_t(from[c * 16 + i]) << (8 * (i & 3));
+      for (int i = 0; i < int(bytes - whole * 16LL); ++i) w[i >> 2] |= uint32_t(from[c * 16LL + i]) << (8 * (i & 3));
     }
-    *reinterpret_cast<uint4*>(to + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(to + c * 16LL) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

@@ -240,6 +240,25 @@ def test_contiguous_weights_of_any_width(tokens, E, k, K, N, dtype, layout, gath
         _accept(C, c, s, dtype)
 
 
+def test_rows_longer_than_two_gigabytes():
+    """Sixteen named rows of 2^30 + 64 columns, put in slot order first."""
+    K = (1 << 30) + 64
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("takes 40 GB")
+    a, w = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((1, K), (1, 1, K)))
+    at = torch.tensor([0, 5, (1 << 29) + 3, (1 << 30) - 1, 1 << 30, K - 1], device="cuda")
+    a[0, at] = torch.tensor([1.0, 2, 4, 8, 16, 32], device="cuda").bfloat16()
+    w[0, 0, at] = 1
+    off = torch.tensor([0, 16], dtype=torch.int32, device="cuda")
+    rows = torch.zeros(16, dtype=torch.int32, device="cuda")
+    try:
+        gemm.set_debug(0, 60_000_000_000)  # one CTA walks 16.8 million slabs, some seconds
+        C = experts.expert_matmul(a, w, off, rows, layout=1)
+        assert C.shape == (16, 1) and torch.all(C == 63)
+    finally:
+        gemm.set_debug(0, 0)
+
+
 @pytest.mark.parametrize("tokens,E,k,K,F", [(1, 4, 2, 64, 37), (9, 5, 2, 200, 131), (400, 3, 2, 136, 197), (500, 2, 2, 67, 70)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("gather", [True, False])
