@@ -140,6 +140,17 @@ int64_t whole(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+// A whole number that the C call takes as an int.
+int whole_int(PyObject* o, const char* what) {
+  const int64_t v = whole(o);
+  if (v != static_cast<int>(v)) value_error(std::string(what) + " does not fit 32 bits");
+  return static_cast<int>(v);
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
 double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -220,8 +231,8 @@ PyObject* rms_norm_backward(PyObject* const* a) {
 
 gemm_route_config_t route_config(PyObject* k, PyObject* score, PyObject* groups, PyObject* kept, PyObject* renormalize,
                                  PyObject* scale) {
-  return {static_cast<int>(whole(k)),    static_cast<int>(whole(score)),       static_cast<int>(whole(groups)),
-          static_cast<int>(whole(kept)), PyObject_IsTrue(renormalize) != 0, static_cast<float>(real(scale))};
+  return {whole_int(k, "k"),       whole_int(score, "score"), whole_int(groups, "groups"), whole_int(kept, "kept_groups"),
+          truth(renormalize), static_cast<float>(real(scale))};
 }
 
 // route(logits, k, score, bias, groups, kept_groups, renormalize, scale) -> (ids, weights, slots, rows, offsets)
@@ -231,7 +242,7 @@ PyObject* route(PyObject* const* a) {
   const int64_t ld = matrix(logits, "logits"), tokens = logits.size(0), experts = logits.size(1);
   const gemm_route_config_t cfg = route_config(a[1], a[2], a[4], a[5], a[6], a[7]);
   const float* bias = vector_or_null<float>(a[3], "bias", at::kFloat, experts);
-  const int64_t k = cfg.k > 0 ? cfg.k : 0;
+  const int64_t k = cfg.k > 0 && cfg.k <= experts ? cfg.k : 0;  // (the call refuses others)
   Tensor ids = make({tokens, k}, logits, at::kInt), weights = make({tokens, k}, logits, at::kFloat);
   Tensor slots = make({tokens, k}, logits, at::kInt), rows = make({tokens * k}, logits, at::kInt);
   Tensor offsets = make({experts + 1}, logits, at::kInt);
@@ -252,8 +263,8 @@ PyObject* route_backward(PyObject* const* a) {
   const int64_t ld = matrix(logits, "logits"), tokens = logits.size(0), experts = logits.size(1);
   if (ids.dim() != 2 || ids.size(0) != tokens) value_error("ids must be T x k");
   const int64_t k = ids.size(1);
-  gemm_route_config_t cfg = {static_cast<int>(k > 1 << 20 ? 1 << 20 : k), static_cast<int>(whole(a[3])), 1, 1,
-                             PyObject_IsTrue(a[4]) != 0, static_cast<float>(real(a[5]))};
+  gemm_route_config_t cfg = {static_cast<int>(k > 1 << 20 ? 1 << 20 : k), whole_int(a[3], "score"), 1, 1, truth(a[4]),
+                             static_cast<float>(real(a[5]))};
   const int32_t* i = vector<int32_t>(ids, "ids", at::kInt, tokens * k);
   const float* d = vector<float>(tensor(a[0], "dweights"), "dweights", at::kFloat, tokens * k);
   Tensor out = make({tokens, experts}, logits, logits.scalar_type());
@@ -271,7 +282,7 @@ PyObject* expert_matmul(PyObject* const* a) {
   if (W.scalar_type() != dt) type_error("A and W must have the same dtype");
   const int64_t lda = matrix(A, "A"), a_rows = A.size(0), K = A.size(1);
   const Stack w = stack(W, "W");
-  const int layout = static_cast<int>(whole(a[4]));
+  const int layout = whole_int(a[4], "layout");
   const bool kmajor = layout == GEMM_B_K_MAJOR;
   const int64_t experts = W.size(0), N = W.size(kmajor ? 1 : 2);
   if (W.size(kmajor ? 2 : 1) != K) value_error("W's K dimension does not match A");
@@ -285,7 +296,7 @@ PyObject* expert_matmul(PyObject* const* a) {
     slots = r.numel();
     rows = vector<int32_t>(r, "rows", at::kInt, slots);
   }
-  const int act = static_cast<int>(whole(a[10]));
+  const int act = whole_int(a[10], "activation");
   const int64_t need = entry.c.grouped_rows_workspace(code, e, slots, K, a_rows, lda, rows != nullptr) +
                        entry.c.grouped_weights_workspace(code, e, N, K, w.ld, w.stride, layout, act);
   const int64_t cols = act == GEMM_ACT_SILU_GATED ? N / 2 : N;
@@ -339,7 +350,7 @@ PyObject* expert_weight_grad(PyObject* const* a) {
   const int64_t experts = off.numel() - 1;
   const int32_t* offsets = vector<int32_t>(off, "offsets", at::kInt, experts + 1);
   const int e = experts > (1 << 30) ? 1 << 30 : static_cast<int>(experts);
-  const int layout = static_cast<int>(whole(a[4]));
+  const int layout = whole_int(a[4], "layout");
   const int64_t r0 = layout == GEMM_B_K_MAJOR ? N : K, r1 = layout == GEMM_B_K_MAJOR ? K : N;
   Tensor out;
   if (a[5] != Py_None) {

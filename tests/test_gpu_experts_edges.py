@@ -302,6 +302,20 @@ def test_block_of_any_width(hidden, inner):
 
 # ---------------------------------------------------------------- numbers at the ends of their ranges
 
+def test_numbers_that_do_not_fit_32_bits_are_refused():
+    logits = torch.zeros(4, 8, device="cuda")
+    with pytest.raises(ValueError):
+        experts.route(logits, (1 << 32) + 2)
+    with pytest.raises(ValueError):
+        experts.route(logits, 2, groups=(1 << 32) + 1, kept_groups=(1 << 32) + 1)
+    a, w = torch.zeros(4, 64, device="cuda").bfloat16(), torch.zeros(2, 64, 64, device="cuda").bfloat16()
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        experts.expert_matmul(a, w, off, layout=1 << 32)
+    with pytest.raises(ValueError):
+        experts.expert_weight_grad(a, a, off, layout=(1 << 32) + 1)
+
+
 def test_routing_of_the_most_tokens():
     """tokens * k just below 2^31, whose last block of tokens ends past it."""
     tokens = (1 << 31) - 1
