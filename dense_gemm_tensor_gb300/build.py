@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -27,6 +28,7 @@ LIB = os.path.join(PKG, "libdgt_gemm.so")
 # links torch and takes the library's entry points from the loaded library).
 BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")
 BINDING = os.path.join(PKG, "_experts.so")
+BINDING_STAMP = os.path.join(BUILD, "experts_binding.txt")
 # The checked build: every range check in the kernels compiled in (DGT_CHECKED=1).
 LIB_CHECKED = os.path.join(PKG, "libdgt_gemm_checked.so")
 
@@ -54,13 +56,26 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _torch_root() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _binding_stamp() -> str:
+    """What the binding is built against: it works with this torch and this Python only."""
+    lib = os.path.join(_torch_root(), "lib", "libtorch_python.so")
+    st = os.stat(lib)
+    return f"{lib} {st.st_size} {st.st_mtime_ns} {sys.version}\n"
+
+
 def _build_binding(force: bool = False) -> None:
     deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(BINDING) and \
+    stamp = _binding_stamp()
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP) and \
+            open(BINDING_STAMP).read() == stamp and \
             all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
         return
     import torch
-    root = os.path.dirname(torch.__file__)
+    root = _torch_root()
     libs = os.path.join(root, "lib")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     cxx = shutil.which("g++") or "c++"
@@ -72,6 +87,9 @@ def _build_binding(force: bool = False) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(stamp)
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -1,6 +1,8 @@
 """The mixture-of-experts operators' edges that need no GPU: refusals of the C
 interface, workspace sizes and the build of the compiled binding."""
 
+import subprocess
+
 import pytest
 
 from dense_gemm_tensor_gb300 import build, experts, gemm
@@ -84,3 +86,29 @@ def test_copied_weights_need_their_workspace(lib):
     gated = dict(act=4, N=24, ldw=24, sw=192, ldc=12, layout=0)
     assert _grouped(lib, ws=6 * P, bytes=2 * copied - 1, **gated) == MISALIGNED
     assert _grouped(lib, ws=4 * P, bytes=2 * copied, **gated) == INVALID
+
+
+@pytest.fixture
+def compiled(monkeypatch, tmp_path):
+    """The binding's build with its files in tmp_path and a compiler that only leaves a file; the list of its runs."""
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_experts.so"))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(tmp_path / "b" / "experts_binding.txt"))
+    runs = []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return runs
+
+
+def test_the_binding_is_built_anew_for_another_torch(compiled, monkeypatch):
+    build._build_binding()
+    build._build_binding()
+    assert len(compiled) == 1
+    monkeypatch.setattr(build, "_binding_stamp", lambda: "another torch")
+    build._build_binding()
+    build._build_binding()
+    assert len(compiled) == 2
