@@ -1,5 +1,5 @@
 """Builds the CUDA library ``libdgt_gemm.so`` in-tree with nvcc for sm_103a,
-and with g++ the compiled Python binding ``_experts.so``.
+and with g++, where torch is installed, the compiled Python binding ``_experts.so``.
 
 The translation units compile in parallel into ``_build/`` and link into
 ``dense_gemm_tensor_gb300/libdgt_gemm.so`` (CUDA runtime linked statically, so
@@ -68,6 +68,8 @@ def _binding_stamp() -> str:
 
 
 def _build_binding(force: bool = False) -> None:
+    if importlib.util.find_spec("torch") is None:
+        return  # the C library needs no torch; without it there is nothing to bind
     deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     stamp = _binding_stamp()
     if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP) and \

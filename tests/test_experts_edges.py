@@ -2,6 +2,7 @@
 interface, workspace sizes and the build of the compiled binding."""
 
 import subprocess
+import sys
 
 import pytest
 
@@ -112,3 +113,10 @@ def test_the_binding_is_built_anew_for_another_torch(compiled, monkeypatch):
     build._build_binding()
     build._build_binding()
     assert len(compiled) == 2
+
+
+def test_the_library_is_built_without_torch(compiled, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    build._build_binding()
+    assert compiled == []
