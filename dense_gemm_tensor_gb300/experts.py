@@ -108,8 +108,12 @@ def _binding():
     """The compiled binding, given the loaded library's entry points (once)."""
     global _ext
     if _ext is None:
-        from . import _experts
         lib = _load()
+        try:
+            from . import _experts
+        except ImportError as e:
+            raise RuntimeError(f"the compiled binding _experts.so cannot be loaded ({e}): build it with "
+                               "dense_gemm_tensor_gb300.build.build()") from e
         _experts.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS})
         _ext = _experts
     return _ext

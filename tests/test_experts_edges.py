@@ -5,7 +5,9 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
+import dense_gemm_tensor_gb300
 from dense_gemm_tensor_gb300 import build, experts, gemm
 
 INVALID, MISALIGNED = gemm.GEMM_ERR_INVALID_VALUE, gemm.GEMM_ERR_MISALIGNED
@@ -120,3 +122,17 @@ def test_the_library_is_built_without_torch(compiled, monkeypatch):
     monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
     build._build_binding()
     assert compiled == []
+
+
+def test_an_unbuilt_tree_says_what_to_do(lib, monkeypatch, tmp_path):
+    x = torch.zeros(2, 8)
+    monkeypatch.setattr(experts, "_ext", None)
+    monkeypatch.delattr(dense_gemm_tensor_gb300, "_experts", raising=False)
+    monkeypatch.setitem(sys.modules, "dense_gemm_tensor_gb300._experts", None)
+    with pytest.raises(RuntimeError, match=r"_experts.so .*build\.build\(\)"):
+        experts.route(x, 2)
+    monkeypatch.setattr(experts, "_lib", None)
+    monkeypatch.setattr(gemm, "_lib", None)
+    monkeypatch.setattr(gemm, "_LIB_PATH", str(tmp_path / "none.so"))
+    with pytest.raises(RuntimeError, match=r"none.so is missing: build it"):
+        experts.route(x, 2)
