@@ -327,9 +327,12 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
 
 // The activation of every element. GELU's tanh form is v / (1 + exp(-2 u)) with
 // u = sqrt(2 / pi) (v + 0.044715 v^3); like the gated SiLU it takes the hardware's
-// exponential and reciprocal, both within a few 2^-22 of the value, far inside
-// the 2^-9 (2^-11) to which the result is rounded next (with tanhf the epilogue
-// of a 256-wide tile took about 15000 cycles).
+// exponential and reciprocal. The exponential of x is within 2 + 1.17 |x| units in
+// the last place: 2^-22 near zero, 2^-18 at 20, 1.3e-5 at 88, so the result is within
+// 4e-5 of its value before it is rounded to 16 bits (up to 2^-8, 2^-11 for float16). Where
+// 1 + exp passes 2^126 (gates below -87.3) the quotient is 0 and not the 1e-36 that bfloat16 could
+// hold. (With tanhf, which the dense products' epilogue takes, a 256-wide tile's took
+// about 15000 cycles.)
 __device__ __forceinline__ void group_activate(float (&v)[32], int act) {
   if (act == GEMM_ACT_GELU_TANH) {
 #pragma unroll

@@ -144,7 +144,9 @@ int gemm_route_backward(int type, int64_t tokens, int experts, const void* logit
  * Epilogue of a grouped product, in fp32 from the fp32 accumulator, rounded
  * once: act(alpha * row_scale[row(s)] * col_scale[e][j] * acc + bias[e][j]).
  * row_scale: one per row of A; col_scale: `groups` x N; bias: groups x N of
- * C's type; each may be NULL.
+ * C's type; each may be NULL. GEMM_ACT_GELU_TANH and the gated SiLU take the
+ * hardware's exponential: within 4e-5 of their values before the rounding, and 0
+ * where 1 + exp passes 2^126 (gates below -87.3). The dense calls' tanh form is another.
  */
 typedef struct gemm_grouped_epilogue {
   float alpha;

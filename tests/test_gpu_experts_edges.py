@@ -333,3 +333,31 @@ def test_routing_of_the_most_tokens():
                 want[-1] = last
             assert torch.equal(got, want)
     assert int(r.ids[-1]) == -1 and not bool(r.ids[:-1].any()) and float(r.weights[-1]) == 0
+
+
+# ---------------------------------------------------------------- activations over their range
+
+@pytest.mark.parametrize("tokens", [182, 1500])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu_gated", "gelu_tanh"])
+def test_activations_from_minus_90_to_90(tokens, dtype, act):
+    """Pre-activations that the product gives exactly. The hardware's exponential of x is within 2 + 1.17 |x| units in the
+    last place (2^-23), at most 1.3e-5 up to 88; GELU's argument adds |x| times four roundings (2^-24), 2.1e-5 there; the
+    quotient's and the products' own are a few 2^-22: 4e-5 in all. Where the divisor passes 2^126 the quotient is 0:
+    at most 91 * 2^-126 is lost."""
+    F = 16
+    v = torch.linspace(-90, 90, tokens).to(DT[dtype])
+    a = torch.zeros(tokens, 8, dtype=DT[dtype])
+    a[:, 0], a[:, 1] = v, 1
+    w = torch.zeros(1, 2 * F if act == "silu_gated" else F, 8, dtype=DT[dtype])
+    w[0, :F, 0] = 1
+    w[0, F:, 1] = 1
+    off = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    C = experts.expert_matmul(a.cuda(), w.cuda(), off, layout=1, activation=act)
+    x = _np(v)
+    t = x if act == "silu_gated" else 2 * np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
+    with np.errstate(over="ignore"):
+        want = np.repeat((x / (1 + np.exp(-t)))[:, None], F, axis=1)
+    got = _np(C)
+    allowed = 0.5 * oracle.ulp(want, dtype) + 4e-5 * np.abs(want) + 91 * 2.0 ** -126
+    assert np.all(np.abs(got - want) <= allowed), np.argwhere(np.abs(got - want) > allowed)[:5]
