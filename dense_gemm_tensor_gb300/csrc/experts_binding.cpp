@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <limits>
 #include <string>
 
 #include "dgt_experts.h"
@@ -197,6 +198,10 @@ PyObject* rms_norm(PyObject* const* a) {
   }
   Tensor y = make({rows, cols}, x, q8 ? at::kFloat8_e4m3fn : dt), rstd = make({rows}, x, at::kFloat);
   Tensor scale = q8 ? make({rows}, x, at::kFloat) : Tensor();
+  if (cols == 0) {  // the call writes nothing: the mean of no elements, and the least scale
+    rstd.fill_(std::numeric_limits<double>::quiet_NaN());
+    if (q8) scale.fill_(1e-12 / 448);
+  }
   const int st = entry.c.rmsnorm(code, rows, cols, x.data_ptr(), ldx, residual, ldr, w, static_cast<float>(real(a[3])), ph,
                                  ldh, q8 ? GEMM_TYPE_E4M3 : code, y.data_ptr(), cols,
                                  q8 ? static_cast<float*>(scale.data_ptr()) : nullptr,

@@ -59,7 +59,7 @@ extern "C" {
  * for the other types. h (written only with a residual; may be NULL, or the
  * very buffer and pitch of x or of residual) and rstd (r of each row) may be
  * NULL. y may be the very buffer and pitch of x where their types are the same.
- * cols <= 16384.
+ * cols <= 16384; with no rows or no columns nothing is written.
  */
 int gemm_rmsnorm(int type, int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
                  const void* weight, float eps, void* h, int64_t ldh, int y_type, void* y, int64_t ldy,

@@ -116,6 +116,16 @@ def test_rms_norm_backward_from_several_threads():
     assert not errors, errors
 
 
+def test_rms_norm_of_no_columns():
+    """Every output is written: the mean of no elements is not a number, and the 8-bit scale has its least value."""
+    x, w = torch.zeros(5, 0, device="cuda"), torch.zeros(0, device="cuda")
+    torch.full((64,), 7.0, device="cuda")  # (what freed memory would show)
+    n = experts.rms_norm(x, w, x)
+    assert n.y.shape == n.h.shape == (5, 0) and torch.isnan(n.rstd).all()
+    n = experts.rms_norm(x, w, out_dtype=torch.float8_e4m3fn)
+    assert n.y.shape == (5, 0) and torch.isnan(n.rstd).all() and torch.all(n.scale == 1e-12 / 448)
+
+
 # ---------------------------------------------------------------- no tokens
 
 def test_combine_backward_of_no_tokens():
