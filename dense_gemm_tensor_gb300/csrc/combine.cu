@@ -61,7 +61,8 @@ struct Picks {
 // PIECES of a row a thread, with a token's FLIGHT rows of each in flight: eight
 // loads a thread whatever k is (k <= FLIGHT where a thread has several pieces).
 // 8192 tokens x k x 4096 BF16 with a residual, one piece a thread against several:
-// k 1 79.6 us and 29.2, k 2 83.3 and 40.3 (6.7 TB/s), k 4 90.5 and 61.0.
+// k 1 79.6 us and 29.2, k 2 83.3 and 40.3 (6.7 TB/s), k 4 90.5 and 61.0. 912 tokens, the limit for k 1: k 1 10.7 and
+// 5.0, k 4 12.0 and 7.9; several were ahead below it too (228 tokens: 3.7 and 2.7, 4.4 and 3.8).
 template <int TYPE, int VEC, int FLIGHT, int PIECES>
 __global__ void __launch_bounds__(kThreads, 3) combine_kernel(const CombineParams p) {
   using P = Pack<TYPE, VEC>;
@@ -154,7 +155,8 @@ struct CombineGradParams {
 // the dots' reductions cost it less (one piece each: 24 instructions an element,
 // 55 us for 4099 tokens x 6 x 2048 BF16, 41.7 now), and where k is small PIECES of
 // them at once, so that eight loads are in flight as well: 8192 tokens x k x 4096
-// BF16, one and several at once: k 1 68.8 us and 40.3, k 2 80.9 and 54.4 (6.2 TB/s), k 4 107 and 92.7.
+// BF16, one and several at once: k 1 68.8 us and 40.3, k 2 80.9 and 54.4 (6.2 TB/s), k 4 107 and 92.7; 912 tokens
+// 7.7 and 5.3, 8.6 and 7.3, 10.7 and 10.5.
 template <int TYPE, int VEC, int FLIGHT, int PIECES>
 __global__ void __launch_bounds__(kThreads, 3) combine_grad_kernel(const CombineGradParams p) {
   using P = Pack<TYPE, VEC>;
@@ -617,7 +619,8 @@ int gemm_combine_backward(int type, int64_t tokens, int64_t cols, int k, const v
   const bool flat = !vec && cols >= v && flat_matrix(dy, lddy) && flat_matrix(dz, lddz) &&
                     (dweights == nullptr || flat_matrix(z, ldz));
   const int64_t nvec = vec ? cols / v : flat ? (cols + v - 1) / v + 1 : cols;
-  // four pieces a thread once the tokens fill the GPU's threads that way
+  // four pieces a thread once the tokens fill the GPU's threads that way: one / four, k 8 x 4096 BF16, us: 228 tokens
+  // 7.9 / 9.7, 456 11.0 / 11.8, 912 (the limit) 20.3 / 17.8, 8192 179 / 178
   const int64_t passes = tokens * nvec >= int64_t(ctx.sm_count) * kThreads * 3 * 4 ? 4 : 1;
   const int pieces = pieces_at_once(ctx, vec, k, tokens, nvec);
   CombineGradParams p = {dy, z, slots, weights, used, dz, dweights, (long long)lddy, (long long)ldz, (long long)lddz,

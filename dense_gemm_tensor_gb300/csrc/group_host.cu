@@ -209,7 +209,9 @@ int stage_rows(const CallContext& ctx, const StageRows& p, cudaStream_t stream) 
 }
 
 // The host knows the slots and the groups, not the group sizes, so its rules go by
-// an average group.
+// an average group. A group far above the average pays for that: 64 groups,
+// 2048 x 4096 BF16, 960 rows (gathered) 171 us evenly spread and 213 with 700 in one
+// group; 1100 rows (put in slot order first), 700 in one group, 178.
 int64_t average_group(int64_t slots, int64_t groups) { return slots / (groups < slots ? groups : slots); }
 
 // Named rows are put in slot order first from 16 rows a group on. 16 groups,

@@ -491,7 +491,10 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* part
 // Blocks of the gradient, at most: each leaves one partial row of dw, which
 // costs a write and a read, so wide rows have about three for each of a GB300's
 // 152 SMs (what fits them at 64 registers) and narrow ones, whose blocks are
-// small, more.
+// small, more. (Numbers, since the size of the workspace goes by them, on a machine
+// without a GPU too.) BF16 with dh, 304 / 456 / 608 / 912 blocks, us: 8192 x 1024 19.1 / 18.4 /
+// 17.7 / 22.2, 30000 x 1024 55.3 / 47.8 / 45.0 / 53.3, 8192 x 2048 33.3 / 30.0 / 29.1 / 33.3,
+// 8192 x 4096 60.8 / 52.0 / 48.8 / 56.0, 8192 x 8192 89.7 / 106 / 94 / 98: no one number is best for wide rows.
 int grad_blocks(int64_t cols) { return cols <= 2048 ? 608 : 456; }
 
 bool aligned(const void* p, int64_t ld, int es, int to) {
@@ -632,10 +635,15 @@ int gemm_rmsnorm(int type, int64_t rows, int64_t cols, const void* x, int64_t ld
   NormParams p = {x,   residual, weight, h,   y,         y_scale,   rstd, (long long)ldx, (long long)ldr,
                   (long long)ldh, (long long)ldy, int(rows), int(cols), 0, eps};
   // Eight elements a thread while the rows leave threads to spare (a row's latency is then one load of each
-  // matrix and two reductions), 64 bytes once they fill the GPU (more loads in flight for each reduction).
+  // matrix and two reductions), 64 bytes once they fill the GPU (more loads in flight for each reduction) and past
+  // what 1024 threads hold. BF16 with a residual, eight elements / 64 bytes, us: 608 x 1024 2.6 / 3.0, 1216 x 1024
+  // (the limit) 3.4 / 3.3, 1 x 4096 2.3 / 2.9, 304 x 4096 (the limit) 2.9 / 3.4, 608 x 4096 5.4 / 4.8,
+  // 152 x 7680 3.1 / 3.6, 304 x 7680 5.8 / 4.8.
   const bool few = cols <= 8000 && rows * cols <= int64_t(ctx.sm_count) * 8192;
   p.tpr = threads_per_row(cols, few ? 8 : mode == SINGLE ? 16 : 64 / es, mode, v);
-  // FLAT blocks stage the weights, so they are few and take many rows
+  // FLAT blocks stage the weights, so they are few and take many rows: blocks of 512 / 128 threads, us: 2048 x 4095
+  // 23.3 / 31.7, 8192 x 4095 84 / 103, 8192 x 1023 40.4 / 44.5, 30000 x 515 70 / 82. Others of 32 / 128 / 256 / 512:
+  // 8192 x 1024 12.2 / 10.3 / 10.0 / 10.3, 30000 x 512 20.2 / 19.9 / 20.0 / 20.4, 100 x 512 2.1 / 2.1 / 2.1 / 2.4.
   const int least = mode == FLAT && !few ? 512 : 128;
   const int block = p.tpr < least ? least / p.tpr * p.tpr : p.tpr;
   const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);

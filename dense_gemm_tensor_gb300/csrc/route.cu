@@ -20,7 +20,9 @@
 // 256 experts 12.1 us; comparing each pair with every other 11.1 us.)
 //
 // The bytes are few (one read of the logits); the time is the selection's
-// instructions and, for a serving step, launch latency.
+// instructions and, for a serving step, latency. One launch (CUDA graph, FP32 sigmoid with a bias): 1 token of 32
+// experts, k 1 3.6 us; of 256 6.2; 16 tokens 7.2; k 8 8.2; 4 of 8 groups 10.1. Two launches (BF16
+// softmax): 33 tokens of 16, k 2 6.8 us; 16384 of 32, k 1 11.9; of 128 18.1; k 8 21.6.
 #include <math.h>
 
 #include "elem.cuh"
@@ -32,7 +34,10 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxK = 32;
-constexpr int kMaxBlocks = 152;      // of the two-launch form: one for each SM
+// Blocks of the two-launch form, at most: one for each SM of a GB300 (a number, since the size of the workspace goes by
+// it, on a machine without a GPU too). 76 / 152 / 304 blocks, us: 8192 x 16, k 2 12.6 / 9.3 / 14.1; 16384 x 128, k 8
+// 34.6 / 21.8 / 30.2; 65536 x 128, k 8 120 / 65 / 72.
+constexpr int kMaxBlocks = 152;
 constexpr int kOneBlockTokens = 32;  // a warp each; more go to several blocks (128 tokens of 64 experts: 13.8 us in one)
 constexpr int kMaskWords = 8192;     // of the ranking's bit masks: 32 KB
 

@@ -68,7 +68,7 @@ class MoeBlock:
         return MoeBlock(self.norm, self.router, self.up, self.down, self.k, up8, scale.contiguous())
 
     def serve(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
-        """The block's output for T x H rows; six to eight launches."""
+        """The block's output for T x H rows; six to nine launches."""
         n = experts.rms_norm(x, self.norm, residual)
         r = experts.route(gemm.matmul(n.y, self.router), self.k)
         if self.up8 is None:
@@ -81,7 +81,8 @@ class MoeBlock:
         return experts.combine(z, r.slots, r.weights, residual=n.h)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor):
-        """(output, what ``backward`` needs): the 16-bit block, the gate's product kept."""
+        """(output, what ``backward`` needs): the 16-bit block, the gate's product kept. The activation
+        and its gradient are elementary torch operations in fp32: no operator of this package has them."""
         n = experts.rms_norm(x, self.norm, residual)
         logits = gemm.matmul(n.y, self.router)
         r = experts.route(logits, self.k)
@@ -157,7 +158,7 @@ def main(argv=None) -> None:
     ms = e0.elapsed_time(e1) / max(args.iters, 1)
     flops = 2.0 * args.tokens * args.k * args.hidden * 3 * args.inner * (3 if args.train else 1)
     print(f"{args.dtype} {'training step' if args.train else 'serving pass'}, {args.tokens} tokens x {args.hidden}, "
-          f"{args.k} of {args.experts} experts of inner width {args.inner}: {launches} launches, {ms * 1e3:.1f} us, "
+          f"{args.k} of {args.experts} experts of inner width {args.inner}: {launches} launches of the library, {ms * 1e3:.1f} us, "
           f"{args.tokens / ms * 1e3:.0f} tokens/s, {flops / ms / 1e9:.1f} TFLOP/s in the experts")
 
 

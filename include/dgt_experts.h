@@ -231,8 +231,8 @@ int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, i
  * Weighted sum over a token's slots:
  *   y[t] = residual[t] + sum_j weights[t][j] * z[slots[t][j]]
  * z: nslots x cols; slots and weights tokens x k (a slot outside [0, nslots)
- * adds nothing but keeps a NaN weight's NaN; weights NULL: all 1); residual may be NULL or the
- * very buffer and pitch of y. type F16, BF16 or F32 (z, residual, y); fp32
+ * adds 0 times its weight: nothing, or NaN where that is not finite; weights NULL:
+ * all 1); residual may be NULL or the very buffer and pitch of y. type F16, BF16 or F32 (z, residual, y); fp32
  * sums in the order of j, the residual last. 1 <= k <= 32.
  */
 int gemm_combine(int type, int64_t tokens, int64_t cols, int k, const void* z, int64_t ldz, int64_t nslots,
