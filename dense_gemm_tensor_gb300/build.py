@@ -1,5 +1,6 @@
 """Builds the CUDA library ``libdgt_gemm.so`` in-tree with nvcc for sm_103a,
-and with g++, where torch is installed, the compiled Python binding ``_experts.so``.
+and with g++, where torch is installed, the compiled Python bindings ``_experts.so``
+and ``_feedforward.so``.
 
 The translation units compile in parallel into ``_build/`` and link into
 ``dense_gemm_tensor_gb300/libdgt_gemm.so`` (CUDA runtime linked statically, so
@@ -29,6 +30,10 @@ LIB = os.path.join(PKG, "libdgt_gemm.so")
 BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")
 BINDING = os.path.join(PKG, "_experts.so")
 BINDING_STAMP = os.path.join(BUILD, "experts_binding.txt")
+# The same of the feed-forward operators.
+FF_BINDING_SRC = os.path.join(CSRC, "feedforward_binding.cpp")
+FF_BINDING = os.path.join(PKG, "_feedforward.so")
+FF_BINDING_STAMP = os.path.join(BUILD, "feedforward_binding.txt")
 # The checked build: every range check in the kernels compiled in (DGT_CHECKED=1).
 LIB_CHECKED = os.path.join(PKG, "libdgt_gemm_checked.so")
 
@@ -67,14 +72,17 @@ def _binding_stamp() -> str:
     return f"{lib} {st.st_size} {st.st_mtime_ns} {sys.version}\n"
 
 
-def _build_binding(force: bool = False) -> None:
+def _build_binding(force: bool = False, feedforward: bool = False) -> None:
+    """One of the two bindings: the experts' (the default) or the feed-forward operators'."""
+    source, target, stamp_file = (FF_BINDING_SRC, FF_BINDING, FF_BINDING_STAMP) if feedforward else \
+        (BINDING_SRC, BINDING, BINDING_STAMP)
     if importlib.util.find_spec("torch") is None:
         return  # the C library needs no torch; without it there is nothing to bind
-    deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = [source, os.path.join(CSRC, "binding.h"), os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     stamp = _binding_stamp()
-    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP) and \
-            open(BINDING_STAMP).read() == stamp and \
-            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+    if not force and os.path.exists(target) and os.path.exists(stamp_file) and \
+            open(stamp_file).read() == stamp and \
+            all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps):
         return
     import torch
     root = _torch_root()
@@ -83,14 +91,14 @@ def _build_binding(force: bool = False) -> None:
     cxx = shutil.which("g++") or "c++"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc, "-I", INCLUDE, BINDING_SRC,
-           "-o", BINDING + ".tmp", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}"]
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc, "-I", INCLUDE, source,
+           "-o", target + ".tmp", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(BINDING + ".tmp", BINDING)
-    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
-    with open(BINDING_STAMP, "w") as f:
+        raise RuntimeError(f"g++ failed on {source}:\n{r.stdout}\n{r.stderr}")
+    os.replace(target + ".tmp", target)
+    os.makedirs(os.path.dirname(stamp_file), exist_ok=True)
+    with open(stamp_file, "w") as f:
         f.write(stamp)
 
 
@@ -107,6 +115,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     lib = LIB_CHECKED if checked else LIB
     if not force and up_to_date(lib):
         _build_binding()
+        _build_binding(feedforward=True)
         return lib
     bdir = os.path.join(BUILD, "checked") if checked else BUILD
     os.makedirs(bdir, exist_ok=True)
@@ -126,9 +135,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_build_binding, force)
+        bindings = [ex.submit(_build_binding, force, ff) for ff in (False, True)]
         objs = list(ex.map(compile_one, _sources()))
-        binding.result()
+        for b in bindings:
+            b.result()
     tmp = lib + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

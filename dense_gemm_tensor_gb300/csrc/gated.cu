@@ -1,0 +1,402 @@
+// The dense gated product and its gradient (gemm_gated, gemm_gated_backward).
+//
+//   up = A W + bias;  C = act(up[:, :F]) * up[:, F:]
+//   dup = [dC value act'(gate), dC act(gate)];  dA = dup W^T;  dW = A^T dup;  dbias = sum over rows of dup
+//
+// The products are the grouped kernel's (group_kernel.cuh) with one group: its
+// tiles hold the same columns of both halves, so the forward pass writes C only
+// (and the halves where a backward pass will need them). The gradient's dup is a
+// pass of its own: both of its products read it, one along F and one along the
+// rows, and it is 1/20 of their time (8192 x 4096 -> 2 x 4096).
+#include "elem.cuh"
+#include "group_launch.h"
+
+namespace dgt {
+namespace {
+
+constexpr int kGateThreads = 256;
+constexpr int kBiasBlocks = 152;  // row blocks, at most, that leave partial sums of dbias
+
+struct GateGradParams {
+  const void* dc;
+  const void* up;
+  void* dup;
+  float* partial;  // a row of 2F sums for each row block, or null
+  long long lddc, ldup, lddup;
+  int rows, F, gate;
+  int tx;             // threads across a block's columns
+  int rows_per_block;
+};
+
+// act(x) and act'(x). Beyond +-30 (SiLU: +-88) the slope's second term is below fp32's least part of 1, and the
+// clamp keeps infinities out of it; a NaN passes.
+__device__ __forceinline__ void gate_slope(float x, int gate, float& act, float& slope) {
+  if (gate == GEMM_GATE_SILU) {
+    const float sig = __fdividef(1.0f, 1.0f + __expf(-x));
+    const float xc = x > 88.0f ? 88.0f : x < -88.0f ? -88.0f : x;
+    act = x * sig;
+    slope = sig * (1.0f + xc * (1.0f - sig));
+  } else if (gate == GEMM_GATE_RELU) {
+    act = x < 0.0f ? 0.0f : x;
+    slope = x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
+  } else {
+    const float xc = x > 30.0f ? 30.0f : x < -30.0f ? -30.0f : x;
+    if (gate == GEMM_GATE_GELU) {
+      const float p = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
+      act = x * p;
+      slope = p + xc * 0.3989422804014327f * __expf(-0.5f * xc * xc);
+    } else {
+      // x / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
+      const float u2 = 1.5957691216057308f * (xc + 0.044715f * xc * xc * xc);
+      const float p = __fdividef(1.0f, 1.0f + __expf(-u2));
+      act = x * p;
+      slope = p + xc * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * xc * xc);
+    }
+  }
+}
+
+// VEC 16-bit elements at a time.
+template <int TYPE, int VEC>
+struct Piece {
+  using T = typename Elem<TYPE>::T;
+  alignas(VEC * 2) T v[VEC];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const T* p = static_cast<const T*>(base) + at;
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(p));
+    else if constexpr (VEC == 4)
+      *reinterpret_cast<uint2*>(v) = __ldcs(reinterpret_cast<const uint2*>(p));
+    else if constexpr (VEC == 2)
+      *reinterpret_cast<uint32_t*>(v) = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    else
+      v[0] = *p;
+  }
+  __device__ __forceinline__ void store(void* base, long long at) const {
+    T* p = static_cast<T*>(base) + at;
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    else if constexpr (VEC == 4)
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+    else if constexpr (VEC == 2)
+      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(v);
+    else
+      *p = v[0];
+  }
+};
+
+// A thread owns VEC columns of each half and walks down its block's rows, several in flight; bound by HBM (3 F read
+// and 2 F written a row). BIAS: its columns' sums, then the block's in the order of its threads.
+template <int TYPE, int VEC, bool BIAS>
+__global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const GateGradParams p) {
+  using E = Elem<TYPE>;
+  __shared__ float sums[BIAS ? kGateThreads * 2 * VEC : 1];
+  const int x = threadIdx.x % p.tx, y = threadIdx.x / p.tx, ty = kGateThreads / p.tx;
+  const long long col = (static_cast<long long>(blockIdx.x) * p.tx + x) * VEC;
+  const bool in = col < p.F;
+  float sg[VEC], sv[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) sg[j] = sv[j] = 0.0f;
+  grid_dependency_wait();
+  const int begin = blockIdx.y * p.rows_per_block, end = min(begin + p.rows_per_block, p.rows);
+  if (in) {
+    constexpr int AHEAD = 2;
+    for (int r0 = begin + y; r0 < end; r0 += AHEAD * ty) {
+      Piece<TYPE, VEC> d[AHEAD], g[AHEAD], v[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const long long r = r0 + i * ty;
+        if (r < end) {
+          d[i].load(p.dc, r * p.lddc + col);
+          g[i].load(p.up, r * p.ldup + col);
+          v[i].load(p.up, r * p.ldup + p.F + col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const long long r = r0 + i * ty;
+        if (r < end) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            float act, slope;
+            gate_slope(E::get(g[i].v[j]), p.gate, act, slope);
+            const float dc = E::get(d[i].v[j]);
+            const float dg = dc * E::get(v[i].v[j]) * slope, dv = dc * act;
+            if constexpr (BIAS) {
+              sg[j] += dg;
+              sv[j] += dv;
+            }
+            g[i].v[j] = E::put(dg);
+            v[i].v[j] = E::put(dv);
+          }
+          g[i].store(p.dup, r * p.lddup + col);
+          v[i].store(p.dup, r * p.lddup + p.F + col);
+        }
+      }
+    }
+  }
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      sums[(2 * j) * kGateThreads + threadIdx.x] = sg[j];
+      sums[(2 * j + 1) * kGateThreads + threadIdx.x] = sv[j];
+    }
+    __syncthreads();
+    if (y == 0 && in) {
+      float* out = p.partial + static_cast<long long>(blockIdx.y) * 2 * p.F;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        float a = 0.0f, b = 0.0f;
+        for (int t = 0; t < ty; ++t) {
+          a += sums[(2 * j) * kGateThreads + t * p.tx + x];
+          b += sums[(2 * j + 1) * kGateThreads + t * p.tx + x];
+        }
+        out[col + j] = a;
+        out[p.F + col + j] = b;
+      }
+    }
+  }
+  grid_launch_dependents();
+}
+
+// dbias from the row blocks' partial sums, in their order; 32 columns a block, a warp's share of the rows each.
+template <int TYPE>
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float* partial, int rows, int cols, void* out) {
+  using E = Elem<TYPE>;
+  __shared__ float part[8][32];
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + c;
+  grid_dependency_wait();
+  float s = 0.0f;
+  if (col < cols)
+    for (int r = g; r < rows; r += 8) s += __ldcg(partial + static_cast<long long>(r) * cols + col);
+  part[g][c] = s;
+  __syncthreads();
+  if (g == 0 && col < cols) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][c];
+    static_cast<typename E::T*>(out)[col] = E::put(s);
+  }
+  grid_launch_dependents();
+}
+
+constexpr int64_t kIntLimit = (int64_t(1) << 31) - 1;
+constexpr int64_t kLdLimit = int64_t(1) << 39;
+
+bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
+int64_t dup_pitch(int64_t F) { return (2 * F + 63) / 64 * 64; }
+int64_t padded(int64_t bytes) { return (bytes + 127) / 128 * 128; }
+
+int kind_of(int type) { return type == GEMM_TYPE_F16 ? KIND_F16 : KIND_BF16; }
+
+bool meet(const void* a, int64_t rows_a, int64_t cols_a, int64_t ld_a, const void* b, int64_t rows_b, int64_t cols_b,
+          int64_t ld_b) {
+  if (a == nullptr || b == nullptr || rows_a == 0 || rows_b == 0 || cols_a == 0 || cols_b == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), a1 = a0 + uintptr_t(((rows_a - 1) * ld_a + cols_a) * 2);
+  const uintptr_t b0 = reinterpret_cast<uintptr_t>(b), b1 = b0 + uintptr_t(((rows_b - 1) * ld_b + cols_b) * 2);
+  return a0 < b1 && b0 < a1;
+}
+
+// Row blocks of the gradient's first kernel: what fills the GPU, but for dbias at most kBiasBlocks.
+struct GateGrid {
+  int tx, blocks_x, blocks_y, rows_per_block;
+};
+GateGrid gate_grid(int64_t M, int64_t F, int vec, bool bias) {
+  GateGrid g;
+  const int64_t pieces = (F + vec - 1) / vec;
+  g.tx = 32;
+  while (g.tx < kGateThreads && g.tx < pieces) g.tx *= 2;
+  g.blocks_x = int((pieces + g.tx - 1) / g.tx);
+  const int64_t want = (152 * 8 + g.blocks_x - 1) / g.blocks_x, most = bias && want > kBiasBlocks ? kBiasBlocks : want;
+  const int64_t rows = (M + most - 1) / most, step = kGateThreads / g.tx;
+  g.rows_per_block = int((rows + step - 1) / step * step);
+  g.blocks_y = int((M + g.rows_per_block - 1) / g.rows_per_block);
+  return g;
+}
+
+template <int TYPE, int VEC>
+cudaError_t launch_gate_grad(const GateGradParams& p, const GateGrid& g, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(g.blocks_x, g.blocks_y, 1);
+  cfg.blockDim = dim3(kGateThreads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t launched = p.partial != nullptr ? cudaLaunchKernelEx(&cfg, gate_grad_kernel<TYPE, VEC, true>, p)
+                                                    : cudaLaunchKernelEx(&cfg, gate_grad_kernel<TYPE, VEC, false>, p);
+  const cudaError_t last = cudaGetLastError();
+  const cudaError_t e = launched != cudaSuccess ? launched : last;
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+template <int TYPE>
+cudaError_t launch_gate_grad_type(const GateGradParams& p, int vec, const GateGrid& g, cudaStream_t s) {
+  return vec == 8   ? launch_gate_grad<TYPE, 8>(p, g, s)
+         : vec == 4 ? launch_gate_grad<TYPE, 4>(p, g, s)
+         : vec == 2 ? launch_gate_grad<TYPE, 2>(p, g, s)
+                    : launch_gate_grad<TYPE, 1>(p, g, s);
+}
+
+// Sizes, types and flags that the forward call and the gradient share.
+bool bad_sizes(int type, int64_t M, int64_t F, int64_t K, int layout, int activation) {
+  return (type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16) || M < 0 || F < 0 || K < 0 || M > kIntLimit ||
+         F > kIntLimit / 2 || K > kIntLimit || (layout != GEMM_B_ROW_MAJOR && layout != GEMM_B_K_MAJOR) ||
+         activation < GEMM_GATE_SILU || activation > GEMM_GATE_RELU;
+}
+
+// Parts of the gradient's workspace: dup, the partial sums of dbias, then what the products stage (one after the
+// other, so the larger of the two).
+struct GradSpace {
+  int64_t dup, partial, stage;
+  int64_t total() const { return dup + partial + stage; }
+};
+GradSpace grad_space(int type, int64_t M, int64_t F, int64_t K, int64_t lda, int64_t ldw, int layout, bool da, bool dw,
+                     bool db) {
+  GradSpace s = {};
+  if (M <= 0 || F <= 0 || (!da && !dw && !db)) return s;
+  s.dup = padded(M * dup_pitch(F) * 2);
+  s.partial = db ? padded(int64_t(kBiasBlocks < M ? kBiasBlocks : M) * 2 * F * 4) : 0;
+  int64_t a = 0, w = 0;
+  if (da && K > 0) {
+    a = gemm_grouped_weights_workspace(type, 1, K, 2 * F, ldw, 0,
+                                       layout == GEMM_B_K_MAJOR ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, GEMM_ACT_NONE);
+  }
+  if (dw && K > 0) w = gemm_grouped_wgrad_rows_workspace(1, M, 2 * F, K, M, lda, 0, dup_pitch(F));
+  s.stage = padded(a > w ? a : w);
+  return s;
+}
+
+}  // namespace
+}  // namespace dgt
+
+using namespace dgt;
+
+extern "C" {
+
+int64_t gemm_gated_workspace(int type, int64_t M, int64_t F, int64_t K, int64_t lda, int64_t ldw, int layout) {
+  if (M <= 0 || F <= 0 || K <= 0) return 0;
+  return gemm_grouped_rows_workspace(type, 1, M, K, M, lda, 0) +
+         gemm_grouped_weights_workspace(type, 1, 2 * F, K, ldw, 0, layout, GEMM_ACT_SILU_GATED);
+}
+
+int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
+               int layout, int activation, const void* bias, void* C, int64_t ldc, void* up, int64_t ldup,
+               void* workspace, int64_t workspace_bytes, void* stream) {
+  if (bad_sizes(type, M, F, K, layout, activation)) return GEMM_ERR_INVALID_VALUE;
+  if (M > 0 && F > 0 && bias != nullptr && C != nullptr && meet(C, M, F, ldc, bias, 1, 2 * F, 2 * F))
+    return GEMM_ERR_INVALID_VALUE;
+  const gemm_grouped_epilogue_t epi = {1.0f, nullptr, nullptr, bias, GEMM_ACT_NONE};
+  const DenseProduct dense = {activation, up, ldup};
+  return run_grouped(kind_of(type), 1, nullptr, M, 2 * F, K, A, M, lda, nullptr, W, ldw, 0, C, ldc, layout, &epi,
+                     workspace, workspace_bytes, stream, &dense);
+}
+
+int64_t gemm_gated_backward_workspace(int type, int64_t M, int64_t F, int64_t K, int64_t lda, int64_t ldw, int layout,
+                                      int want_da, int want_dw, int want_dbias) {
+  return grad_space(type, M, F, K, lda, ldw, layout, want_da != 0, want_dw != 0, want_dbias != 0).total();
+}
+
+int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* dC, int64_t lddc, const void* up,
+                        int64_t ldup, const void* A, int64_t lda, const void* W, int64_t ldw, int layout,
+                        int activation, void* dA, int64_t ldda, void* dW, int64_t lddw, void* dbias, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  if (bad_sizes(type, M, F, K, layout, activation)) return GEMM_ERR_INVALID_VALUE;
+  const bool km = layout == GEMM_B_K_MAJOR;
+  const int64_t w_rows = km ? 2 * F : K, w_cols = km ? K : 2 * F;
+  if (M == 0 || K == 0) dA = nullptr;  // (F = 0: dA of no terms is zeros)
+  if (F == 0 || K == 0) dW = nullptr;
+  if (F == 0) dbias = nullptr;
+  if (dA == nullptr && dW == nullptr && dbias == nullptr) return GEMM_OK;
+  const bool terms = M > 0 && F > 0;
+  // what the two products would refuse is refused before anything is launched
+  if (dA != nullptr && (ldda < K || ldda > kLdLimit || (F > 0 && (W == nullptr || ldw < w_cols || ldw > kLdLimit))))
+    return GEMM_ERR_INVALID_VALUE;
+  if (dW != nullptr && (lddw < w_cols || lddw > kLdLimit || (M > 0 && (A == nullptr || lda < K || lda > kLdLimit))))
+    return GEMM_ERR_INVALID_VALUE;
+  if (terms && (dC == nullptr || up == nullptr || lddc < F || ldup < 2 * F || lddc > kLdLimit || ldup > kLdLimit))
+    return GEMM_ERR_INVALID_VALUE;
+  const GradSpace space = grad_space(type, M, F, K, lda, ldw, layout, dA != nullptr, dW != nullptr, dbias != nullptr);
+  if (terms && (workspace == nullptr || workspace_bytes < space.total())) return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(dC, 2) || misaligned(up, 2) || misaligned(dA, 2) || misaligned(dW, 2) || misaligned(dbias, 2) ||
+      misaligned(workspace, 128) || (terms && dA != nullptr && misaligned(W, 16)) ||
+      (terms && dW != nullptr && misaligned(A, 16)))
+    return GEMM_ERR_MISALIGNED;
+  struct Matrix {
+    const void* p;
+    int64_t rows, cols, ld;
+  };
+  const Matrix outs[4] = {{dA, M, K, ldda},
+                          {dW, w_rows, w_cols, lddw},
+                          {dbias, 1, 2 * F, 2 * F},
+                          {terms ? workspace : nullptr, 1, workspace_bytes / 2, workspace_bytes / 2}};
+  const Matrix ins[4] = {{dC, M, F, lddc},
+                         {up, M, 2 * F, ldup},
+                         {dW != nullptr ? A : nullptr, M, K, lda},
+                         {dA != nullptr ? W : nullptr, w_rows, w_cols, ldw}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (meet(outs[i].p, outs[i].rows, outs[i].cols, outs[i].ld, ins[j].p, ins[j].rows, ins[j].cols, ins[j].ld))
+        return GEMM_ERR_INVALID_VALUE;
+    for (int j = 0; j < i; ++j)
+      if (meet(outs[i].p, outs[i].rows, outs[i].cols, outs[i].ld, outs[j].p, outs[j].rows, outs[j].cols, outs[j].ld))
+        return GEMM_ERR_INVALID_VALUE;
+  }
+  CallContext ctx;
+  int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[8] = {dA, dW, dbias, terms ? workspace : nullptr, terms ? dC : nullptr, terms ? up : nullptr,
+                         terms && dW != nullptr ? A : nullptr, terms && dA != nullptr ? W : nullptr};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* dup = ws;
+  const int64_t lddup = dup_pitch(F);
+  if (terms) {
+    // the widest pieces that the rows of all matrices are made of
+    int vec = 8;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(dC) | reinterpret_cast<uintptr_t>(up) | uintptr_t(F * 2) |
+                          uintptr_t(M > 1 ? lddc * 2 : 0) | uintptr_t(M > 1 ? ldup * 2 : 0);
+    while (vec > 1 && all % (vec * 2) != 0) vec /= 2;
+    const GateGrid g = gate_grid(M, F, vec, dbias != nullptr);
+    GateGradParams p = {dC,
+                        up,
+                        ws,
+                        dbias != nullptr ? reinterpret_cast<float*>(ws + space.dup) : nullptr,
+                        (long long)lddc,
+                        (long long)ldup,
+                        (long long)lddup,
+                        int(M),
+                        int(F),
+                        activation,
+                        g.tx,
+                        g.rows_per_block};
+    cudaError_t e = type == GEMM_TYPE_F16 ? launch_gate_grad_type<GEMM_TYPE_F16>(p, vec, g, s)
+                                          : launch_gate_grad_type<GEMM_TYPE_BF16>(p, vec, g, s);
+    if (e == cudaSuccess && dbias != nullptr) {
+      const int cols = int(2 * F), grid = (cols + 31) / 32;
+      e = type == GEMM_TYPE_F16 ? launch_dependent(bias_sum_kernel<GEMM_TYPE_F16>, grid, 256, 0, s, 1, p.partial, g.blocks_y, cols, dbias)
+                                : launch_dependent(bias_sum_kernel<GEMM_TYPE_BF16>, grid, 256, 0, s, 1, p.partial, g.blocks_y, cols, dbias);
+    }
+    if (e != cudaSuccess) return GEMM_ERR_LAUNCH;
+  } else if (dbias != nullptr) {  // no rows
+    if (cudaMemsetAsync(dbias, 0, size_t(2 * F) * 2, s) != cudaSuccess) return GEMM_ERR_LAUNCH;
+  }
+  uint8_t* stage = terms && space.stage > 0 ? ws + space.dup + space.partial : nullptr;
+  if (dA != nullptr) {
+    const DenseProduct dense = {-1, nullptr, 0};
+    st = run_grouped(kind_of(type), 1, nullptr, M, K, 2 * F, dup, M, lddup, nullptr, W, ldw, 0, dA, ldda,
+                     km ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, nullptr, stage, space.stage, stream, &dense);
+    if (st != GEMM_OK) return st;
+  }
+  if (dW != nullptr)
+    st = run_wgrad(kind_of(type), 1, nullptr, M, 2 * F, K, A, M, lda, nullptr, dup, lddup, dW, lddw, 0, layout, stage,
+                   space.stage, stream, true);
+  return st;
+}
+
+}  // extern "C"

@@ -150,7 +150,7 @@ template <bool SHIFTED>
 __global__ void __launch_bounds__(256) stage_rows_kernel(const StageRows p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  auto start = [&](int e) { return e <= 0 ? 0 : min(max(p.offsets[e], 0), p.slots); };
+  auto start = [&](int e) { return e <= 0 ? 0 : p.offsets == nullptr ? p.slots : min(max(p.offsets[e], 0), p.slots); };
   auto row = [&](int s) { return min(max(p.rows != nullptr ? p.rows[s] : s, 0), p.a_rows - 1); };
   const long long rows_a = p.order != nullptr ? start(p.groups) : 0;
   long long used = rows_a;
@@ -260,10 +260,12 @@ WeightCopy weight_copy(int es, int64_t groups, int64_t N, int64_t K, int64_t ldw
   return c;
 }
 
+}  // namespace
+
 int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
                 int64_t a_rows, int64_t lda, const int32_t* rows, const void* W, int64_t ldw, int64_t stride_w, void* C,
                 int64_t ldc, int layout, const gemm_grouped_epilogue_t* epi, void* workspace, int64_t workspace_bytes,
-                void* stream) {
+                void* stream, const DenseProduct* dense) {
   const int es = kind == KIND_E4M3 ? 1 : 2;
   if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
       N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
@@ -272,11 +274,15 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if (kind == KIND_E4M3 && layout != GEMM_B_K_MAJOR) return GEMM_ERR_INVALID_VALUE;
   const int act = epi != nullptr ? epi->activation : GEMM_ACT_NONE;
   if (act < GEMM_ACT_NONE || act > GEMM_ACT_SILU_GATED) return GEMM_ERR_INVALID_VALUE;
-  const bool gated = act == GEMM_ACT_SILU_GATED;
+  const bool gated = act == GEMM_ACT_SILU_GATED || (dense != nullptr && dense->gate >= 0);
   if (gated && N % 2 != 0) return GEMM_ERR_INVALID_VALUE;
   if (slots == 0 || N == 0) return GEMM_OK;
   const int64_t out_cols = gated ? N / 2 : N;
-  if (offsets == nullptr || C == nullptr || ldc < out_cols || ldc > kLdLimit) return GEMM_ERR_INVALID_VALUE;
+  if ((offsets == nullptr && dense == nullptr) || C == nullptr || ldc < out_cols || ldc > kLdLimit)
+    return GEMM_ERR_INVALID_VALUE;
+  void* up = dense != nullptr ? dense->up : nullptr;
+  const int64_t ldup = dense != nullptr ? dense->ldup : 0;
+  if (up != nullptr && (ldup < N || ldup > kLdLimit)) return GEMM_ERR_INVALID_VALUE;
   if (rows == nullptr && a_rows < slots) return GEMM_ERR_INVALID_VALUE;
   // (with K = 0 rows of A may be named that it does not have: nothing of them is read but their scales)
   if (a_rows == 0 && epi != nullptr && epi->row_scale != nullptr) return GEMM_ERR_INVALID_VALUE;
@@ -300,7 +306,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if (wc.bytes > 0 && copy_a && !odd_a && workspace_bytes < a_bytes + wc.bytes) copy_a = false;
   if (workspace != nullptr && workspace_bytes < (copy_a ? a_bytes : 0) + wc.bytes)
     return odd_a || wc.bytes > 0 ? GEMM_ERR_MISALIGNED : GEMM_ERR_INVALID_VALUE;
-  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(bias, 2) ||
+  if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(C, 2) || misaligned(up, 2) || misaligned(bias, 2) ||
       misaligned(workspace, 128) ||
       (epi != nullptr && (misaligned(epi->row_scale, 4) || misaligned(epi->col_scale, 4))))
     return GEMM_ERR_MISALIGNED;
@@ -311,12 +317,19 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if (K > 0 && (meet(rc, range_of(A, a_rows, K, lda, es)) ||
                 meet(rc, range_of(W, w_rows, w_cols, ldw, es, groups, groups > 1 ? stride_w : 0))))
     return GEMM_ERR_INVALID_VALUE;
+  if (up != nullptr) {
+    const Range ru = range_of(up, slots, N, ldup, 2);
+    if (meet(ru, rc) || (workspace != nullptr && meet(ru, range_of(workspace, 1, workspace_bytes, 0, 1))) ||
+        (bias != nullptr && meet(ru, range_of(bias, 1, N, N, 2))) ||
+        (K > 0 && (meet(ru, range_of(A, a_rows, K, lda, es)) || meet(ru, range_of(W, w_rows, w_cols, ldw, es)))))
+      return GEMM_ERR_INVALID_VALUE;
+  }
 
   CallContext ctx;
   int st = begin_call(&ctx);
   if (st != GEMM_OK) return st;
-  if (!on_device(C, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
-      (bias != nullptr && !on_device(bias, ctx.dev)) || (workspace != nullptr && !on_device(workspace, ctx.dev)) || (K > 0 && (!on_device(A, ctx.dev) || !on_device(W, ctx.dev))))
+  if (!on_device(C, ctx.dev) || (offsets != nullptr && !on_device(offsets, ctx.dev)) ||
+      (rows != nullptr && !on_device(rows, ctx.dev)) || (up != nullptr && !on_device(up, ctx.dev)) || (bias != nullptr && !on_device(bias, ctx.dev)) || (workspace != nullptr && !on_device(workspace, ctx.dev)) || (K > 0 && (!on_device(A, ctx.dev) || !on_device(W, ctx.dev))))
     return GEMM_ERR_NOT_DEVICE_MEMORY;
   if (epi != nullptr && ((epi->row_scale != nullptr && !on_device(epi->row_scale, ctx.dev)) ||
                          (epi->col_scale != nullptr && !on_device(epi->col_scale, ctx.dev))))
@@ -417,7 +430,21 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
     return GEMM_ERR_DRIVER;
   cudaError_t e;
   const bool km = layout == GEMM_B_K_MAJOR;
-  if (kind == KIND_E4M3)
+  if (dense != nullptr && gated) {
+    p.gate = dense->gate;
+    if (up != nullptr) {
+      p.up = up;
+      p.ldup = ldup;
+      p.up_gran = store_granularity(up, ldup, 0);
+      p.up_value_gran = store_granularity(static_cast<uint16_t*>(up) + out_cols, ldup, 0);
+      if (p.up_gran == 16 && !encode_map_3d(&L.tmB2, CU_TENSOR_MAP_DATA_TYPE_UINT16, up, N, slots, ldup * 2, 1, 0, 64, 32,
+                                            CU_TENSOR_MAP_SWIZZLE_128B))
+        return GEMM_ERR_DRIVER;
+      if (p.up_gran != 16) p.up_value_gran = p.up_value_gran == 16 ? 8 : p.up_value_gran;  // there is no map
+    }
+    e = kind == KIND_BF16 ? (km ? launch_gated_bf16_km(L) : launch_gated_bf16_rm(L))
+                          : (km ? launch_gated_f16_km(L) : launch_gated_f16_rm(L));
+  } else if (kind == KIND_E4M3)
     e = launch_group_e4m3_km(L);
   else if (kind == KIND_BF16)
     e = km ? launch_group_bf16_km(L) : launch_group_bf16_rm(L);
@@ -426,15 +453,19 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+namespace {
+
 // The slabs, and the rows of A and of dC that are copied whole.
 int64_t wgrad_workspace(int64_t groups, int64_t slots, int64_t N, int64_t K, bool copy_a, bool copy_c = false) {
   return groups * kSlab * (staged_pitch(N, 2) + staged_pitch(K, 2)) + (copy_a ? slots * staged_pitch(K, 2) : 0) +
          (copy_c ? slots * staged_pitch(N, 2) : 0);
 }
 
+}  // namespace
+
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
               int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
-              int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream) {
+              int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream, bool dense) {
   if (groups < 1 || groups > kMaxGroups || slots < 0 || N < 0 || K < 0 || a_rows < 0 || slots > kIntLimit ||
       N > kIntLimit || K > kIntLimit || a_rows > kIntLimit)
     return GEMM_ERR_INVALID_VALUE;
@@ -442,7 +473,7 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   if (N == 0 || K == 0) return GEMM_OK;
   const bool km = layout == GEMM_B_K_MAJOR;
   const int64_t out_rows = km ? N : K, out_cols = km ? K : N;
-  if (offsets == nullptr || dW == nullptr || lddw < out_cols || lddw > kLdLimit || stride_dw < 0 ||
+  if ((offsets == nullptr && !dense) || dW == nullptr || lddw < out_cols || lddw > kLdLimit || stride_dw < 0 ||
       stride_dw > kLdLimit || (groups > 1 && stride_dw < (out_rows - 1) * lddw + out_cols))
     return GEMM_ERR_INVALID_VALUE;
   if (slots > 0 && (A == nullptr || dC == nullptr || a_rows == 0 || lda < K || lddc < N || lda > kLdLimit ||
@@ -469,7 +500,7 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   CallContext ctx;
   int st = begin_call(&ctx);
   if (st != GEMM_OK) return st;
-  if (!on_device(dW, ctx.dev) || !on_device(offsets, ctx.dev) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
+  if (!on_device(dW, ctx.dev) || (offsets != nullptr && !on_device(offsets, ctx.dev)) || (rows != nullptr && !on_device(rows, ctx.dev)) ||
       (workspace != nullptr && !on_device(workspace, ctx.dev)) ||
       (slots > 0 && (!on_device(A, ctx.dev) || !on_device(dC, ctx.dev))))
     return GEMM_ERR_NOT_DEVICE_MEMORY;
@@ -531,7 +562,8 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
       dC = q.order_c;
       lddc = q.pitch_c / 2;
     }
-    st = stage_rows(ctx, q, L.stream);
+    // one group of whole slabs has nothing to stage
+    if (offsets != nullptr || slots % kSlab != 0 || copy_a || copy_c) st = stage_rows(ctx, q, L.stream);
     if (st != GEMM_OK) return st;
     // rows x cols with rows `ld` apart: 64-column blocks as the outer coordinate, two to a box, where the columns are
     // whole blocks (a block past the row's end would be memory past the matrix); else boxes of one block
@@ -557,7 +589,6 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-}  // namespace
 }  // namespace dgt
 
 extern "C" {
@@ -598,7 +629,7 @@ int gemm_f16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t 
                      int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
                      void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, workspace, workspace_bytes, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream, nullptr);
 }
 
 int gemm_bf16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
@@ -606,7 +637,7 @@ int gemm_bf16_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
                       void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, workspace, workspace_bytes, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream, nullptr);
 }
 
 int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint8_t* A,
@@ -614,7 +645,7 @@ int gemm_e4m3_grouped(int groups, const int32_t* offsets, int64_t slots, int64_t
                       int64_t stride_w, uint16_t* C, int64_t ldc, int layout, const gemm_grouped_epilogue_t* epilogue,
                       void* workspace, int64_t workspace_bytes, void* stream) {
   return dgt::run_grouped(dgt::KIND_E4M3, groups, offsets, slots, N, K, A, a_rows, lda, rows, W, ldw, stride_w, C, ldc,
-                          layout, epilogue, workspace, workspace_bytes, stream);
+                          layout, epilogue, workspace, workspace_bytes, stream, nullptr);
 }
 
 int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const uint16_t* A,
@@ -622,7 +653,7 @@ int gemm_f16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, in
                            uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
                            int64_t workspace_bytes, void* stream) {
   return dgt::run_wgrad(dgt::KIND_F16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
-                        stride_dw, layout, workspace, workspace_bytes, stream);
+                        stride_dw, layout, workspace, workspace_bytes, stream, false);
 }
 
 int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K,
@@ -630,7 +661,7 @@ int gemm_bf16_grouped_wgrad(int groups, const int32_t* offsets, int64_t slots, i
                             int64_t lddc, uint16_t* dW, int64_t lddw, int64_t stride_dw, int layout, void* workspace,
                             int64_t workspace_bytes, void* stream) {
   return dgt::run_wgrad(dgt::KIND_BF16, groups, offsets, slots, N, K, A, a_rows, lda, rows, dC, lddc, dW, lddw,
-                        stride_dw, layout, workspace, workspace_bytes, stream);
+                        stride_dw, layout, workspace, workspace_bytes, stream, false);
 }
 
 }  // extern "C"

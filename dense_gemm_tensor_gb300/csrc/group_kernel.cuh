@@ -40,9 +40,12 @@
 // GATED: W's columns are gate and value halves; a tile holds the same BN / 2
 // columns of both (in the pair each CTA loads one of them), and the epilogue
 // stores silu(gate) * value, so the 2 x wider intermediate is never written.
+// GATED_ANY is the dense product's form: any of four activations, and the two
+// halves before it kept on request for a backward pass.
 #pragma once
 
 #include "dgt_experts.h"
+#include "dgt_feedforward.h"
 #include "gemm_kernel.cuh"
 
 namespace dgt {
@@ -79,11 +82,18 @@ enum : int {
   GROUP_WGRAD = 2,  // weight gradient: both operands MN-major (rows of the contraction are slots)
 };
 
+// Gated products.
+enum : int {
+  GATED_NONE = 0,
+  GATED_SILU = 1,  // silu(gate) * value
+  GATED_ANY = 2,   // p.gate(gate) * value, and the halves themselves where p.up is given
+};
+
 struct GroupParams {
   // N, K, C, ldc, stride_c, c_tma, c_gran, num_kb, raster, tiles_m, tiles_n, alpha, act, bias and the launch-wide
   // status fields are used; N is the width of the accumulators' matrix (both halves of a gated product).
   GemmParams g;
-  const int* offsets;
+  const int* offsets;  // null: one group of all slots
   int groups;
   int slots;
   const int* rows;  // row of the gathered operand for each slot, or null: the slot itself
@@ -96,9 +106,22 @@ struct GroupParams {
   int out_cols;  // columns of C (or of dW)
   int out_rows;  // gradient: rows of dW
   int wide_p, wide_q;  // gradient: an operand's map has 64-column blocks as its outer coordinate (two blocks a box)
+  // GATED_ANY: the activation (GEMM_GATE_*), and where both halves before it go (slots x N, or null; the map is tmB2)
+  int gate;
+  void* up;
+  long long ldup;
+  int up_gran, up_value_gran;  // widest stores of the gate's and of the value's half
 };
 
-template <int KIND, int OPS, int BN_, bool PAIR, bool GATED>
+// A matrix that an epilogue warp stores to: 16-bit elements, matrices stride apart, columns before `cols`.
+struct GroupOut {
+  uint16_t* base;
+  long long ld, stride;
+  int tma, gran, cols;
+  int tma_x;  // column of the map that `base` is
+};
+
+template <int KIND, int OPS, int BN_, bool PAIR, int GATED>
 struct GroupCfg {
   using T = typename KindTraits<KIND>::T;
   static constexpr int ES = sizeof(T);
@@ -154,6 +177,7 @@ struct GroupTile {
 // from device memory, so they are kept inside [0, slots].
 __device__ __forceinline__ int group_start(const GroupParams& p, int e) {
   if (e <= 0) return 0;
+  if (p.offsets == nullptr) return p.slots;
   return min(max(p.offsets[e], 0), p.slots);
 }
 
@@ -231,27 +255,27 @@ __device__ __forceinline__ uint32_t stage_chunk(uint32_t stage, int r, int j) {
 }
 
 // Writes the staged 32 x 64 tile to C[row0 .., col0 ..] of matrix z: rows
-// before row_end and columns before p.out_cols only. TMA stores whole 32-row
+// before row_end and columns before o.cols only. TMA stores whole 32-row
 // pieces (CLIP: it clips at the tensor's end; a group's end it does not know, so
 // a piece that crosses it is stored row by row).
 template <bool CLIP>
-__device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensorMap* tmC, uint32_t stage, int lane,
+__device__ __forceinline__ void group_flush(const GroupOut& o, const CUtensorMap* tmC, uint32_t stage, int lane,
                                             int row0, int row_end, int col0, int z) {
-  const bool full_cols = col0 + 64 <= p.out_cols;
-  if (p.g.c_tma && full_cols && (CLIP ? row0 < row_end : row0 + 32 <= row_end)) {
+  const bool full_cols = col0 + 64 <= o.cols;
+  if (o.tma && full_cols && (CLIP ? row0 < row_end : row0 + 32 <= row_end)) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(tmC, stage, col0, row0, z);
+      tma_store_3d(tmC, stage, o.tma_x + col0, row0, z);
       bulk_commit_group();
     }
     return;
   }
   __syncwarp();
-  uint16_t* base = static_cast<uint16_t*>(p.g.C) + z * p.g.stride_c + col0;
-  if (p.g.c_gran == 16) {
+  uint16_t* base = o.base + z * o.stride + col0;
+  if (o.gran == 16) {
     // 8 lanes a row, 16 bytes a lane; the last lane of a ragged row element by element
-    const int l = lane & 7, cols = p.out_cols - col0 - 8 * l;
+    const int l = lane & 7, cols = o.cols - col0 - 8 * l;
 #pragma unroll
     for (int rr = 0; rr < 32; rr += 4) {
       const int r = rr + (lane >> 3);
@@ -261,7 +285,7 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
                    : "r"(stage_chunk(stage, r, l))
                    : "memory");
       if (row0 + r < row_end) {
-        uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 8 * l;
+        uint16_t* dst = base + static_cast<long long>(row0 + r) * o.ld + 8 * l;
         if (cols >= 8) {
           *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
@@ -278,7 +302,7 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
 #pragma unroll
     for (int rr = 0; rr < 32; rr += 4) {
       const int r = rr + (lane >> 3);
-      uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc;
+      uint16_t* dst = base + static_cast<long long>(row0 + r) * o.ld;
       const int m = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 7;  // columns past a 16-byte boundary
       uint32_t w[8];
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -315,10 +339,10 @@ __device__ __forceinline__ void group_flush(const GroupParams& p, const CUtensor
 #pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       const uint32_t v = ld_shared_u32(stage_chunk(stage, r, lane >> 2) + ((lane & 3) << 2));
-      if (row0 + r < row_end && col < p.out_cols) {
-        uint16_t* dst = base + static_cast<long long>(row0 + r) * p.g.ldc + 2 * lane;
+      if (row0 + r < row_end && col < o.cols) {
+        uint16_t* dst = base + static_cast<long long>(row0 + r) * o.ld + 2 * lane;
         dst[0] = static_cast<uint16_t>(v & 0xFFFFu);
-        if (col + 1 < p.out_cols) dst[1] = static_cast<uint16_t>(v >> 16);
+        if (col + 1 < o.cols) dst[1] = static_cast<uint16_t>(v >> 16);
       }
     }
   }
@@ -343,6 +367,18 @@ __device__ __forceinline__ void group_activate(float (&v)[32], int act) {
   } else {
     epi_activate(v, act);
   }
+}
+
+// act(gate) * value of the dense gated product, act by GEMM_GATE_* (the hardware's exponential as above).
+__device__ __forceinline__ void gate_activate(float (&g)[32], const float (&value)[32], int gate) {
+  if (gate == GEMM_GATE_SILU) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) g[k] = __fdividef(g[k], 1.0f + __expf(-g[k])) * value[k];
+    return;
+  }
+  group_activate(g, gate == GEMM_GATE_RELU ? GEMM_ACT_RELU : gate == GEMM_GATE_GELU ? GEMM_ACT_GELU : GEMM_ACT_GELU_TANH);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) g[k] *= value[k];
 }
 
 template <bool PAIR>
@@ -381,7 +417,7 @@ __device__ __forceinline__ void group_scale(const GroupParams& p, int e, int col
   }
 }
 
-template <int KIND, int OPS, int BN, bool PAIR, bool GATED>
+template <int KIND, int OPS, int BN, bool PAIR, int GATED>
 __global__ void __launch_bounds__(kGroupThreads, 1)
     group_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
@@ -665,7 +701,55 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
       if (!WGRAD && p.row_scale != nullptr && !null_group && row0 + lane < t.end)
         scale *= p.row_scale[gathered_row(p, row0 + lane, t.end)];
       if (row0 < t.row_end) {
+        const GroupOut out_c = {static_cast<uint16_t*>(p.g.C), p.g.ldc, p.g.stride_c, p.g.c_tma, p.g.c_gran, p.out_cols, 0};
         for (int c = set * 64; c < Cf::OUT_BN && col0 + c < p.out_cols; c += 128) {
+          if constexpr (GATED == GATED_ANY) {
+            // C's piece, and the halves' pieces where they are kept: the accumulators are read again for each
+            const GroupOut out_g = {static_cast<uint16_t*>(p.up), p.ldup, 0, p.up_gran == 16, p.up_gran, p.out_cols, 0};
+            const GroupOut out_v = {out_g.base + p.out_cols, p.ldup, 0, p.up_value_gran == 16, p.up_value_gran, p.out_cols,
+                                    p.out_cols};
+            for (int out = 0; out < (p.up != nullptr ? 3 : 1); ++out) {
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                const int cc = c + 32 * h;
+                uint32_t acc[2][32];
+                if (t.kbs > 0) {
+                  __syncwarp();
+                  tmem_ld_32x32b_x32(taddr + cc, acc[0]);
+                  tmem_ld_32x32b_x32(taddr + BN / 2 + cc, acc[1]);
+                  tmem_wait_ld_into(acc[0]);
+                  tmem_wait_ld_into(acc[1]);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) acc[0][k] = acc[1][k] = 0u;
+                }
+                float v[32], u[32];
+                if (out < 2) group_scale<KIND>(p, t.e, col0 + cc, lane, 1.0f, acc[0], v);
+                if (out != 1) group_scale<KIND>(p, t.e, p.out_cols + col0 + cc, lane, 1.0f, acc[1], u);
+                if (out == 0) gate_activate(v, u, p.gate);
+                if (out == 2) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] = u[k];
+                }
+                uint32_t words[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  words[j] = pack2<KindTraits<KIND>::out>(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
+                if (h == 0) {
+                  // the tile's last TMA store has read it
+                  if (lane == 0) bulk_wait_read_all();
+                  __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  st_shared_v4(stage_chunk(stage, lane, 4 * h + j), words[4 * j], words[4 * j + 1], words[4 * j + 2],
+                               words[4 * j + 3]);
+              }
+              group_flush<false>(out == 0 ? out_c : out == 1 ? out_g : out_v, out == 0 ? &tmC : &tmB2, stage, lane, row0,
+                                 t.row_end, col0 + c, z);
+            }
+            continue;
+          }
           uint32_t acc[2][32];
           if (t.kbs == 0) {
             // nothing was accumulated (K = 0, an empty group's gradient, the slots past the last group)
@@ -719,7 +803,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
               st_shared_v4(stage_chunk(stage, lane, 4 * h + j), words[4 * j], words[4 * j + 1], words[4 * j + 2],
                            words[4 * j + 3]);
           }
-          group_flush<WGRAD>(p, &tmC, stage, lane, row0, t.row_end, col0 + c, z);
+          group_flush<WGRAD>(out_c, &tmC, stage, lane, row0, t.row_end, col0 + c, z);
         }
       }
       if (t.kbs == 0) continue;

@@ -9,7 +9,7 @@ namespace dgt {
 
 struct GroupLaunch {
   CUtensorMap tmA, tmA2;  // the MMA's A operand: boxes; gathered rows (product) or the groups' ragged slabs (gradient)
-  CUtensorMap tmB, tmB2;  // its B operand: boxes; ragged slabs (gradient)
+  CUtensorMap tmB, tmB2;  // its B operand: boxes; ragged slabs (gradient), or the kept halves (dense gated product)
   CUtensorMap tmC;        // valid when p.g.c_tma
   GroupParams p;
   bool pair, gated;
@@ -25,9 +25,30 @@ cudaError_t launch_group_f16_rm(const GroupLaunch& L);
 cudaError_t launch_group_f16_km(const GroupLaunch& L);
 cudaError_t launch_group_f16_wgrad(const GroupLaunch& L);
 cudaError_t launch_group_e4m3_km(const GroupLaunch& L);
+cudaError_t launch_gated_bf16_rm(const GroupLaunch& L);
+cudaError_t launch_gated_bf16_km(const GroupLaunch& L);
+cudaError_t launch_gated_f16_rm(const GroupLaunch& L);
+cudaError_t launch_gated_f16_km(const GroupLaunch& L);
+
+// What a dense product adds to a grouped one: one group of all rows, without offsets on the device; and a gated one's
+// activation (GEMM_GATE_*; -1: not gated) and kept halves.
+struct DenseProduct {
+  int gate;
+  void* up;  // slots x N, or null
+  int64_t ldup;
+};
+// The grouped product and weight gradient behind the C entry points (group_host.cu). dense: null for groups on the
+// device; offsets and rows are null where it is given.
+int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
+                int64_t a_rows, int64_t lda, const int32_t* rows, const void* W, int64_t ldw, int64_t stride_w, void* C,
+                int64_t ldc, int layout, const gemm_grouped_epilogue_t* epi, void* workspace, int64_t workspace_bytes,
+                void* stream, const DenseProduct* dense);
+int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
+              int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
+              int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream, bool dense);
 
 // Sets the kernel's dynamic shared-memory limit once per device, then launches.
-template <int KIND, int OPS, int BN, bool PAIR, bool GATED>
+template <int KIND, int OPS, int BN, bool PAIR, int GATED>
 cudaError_t launch_group_variant(const GroupLaunch& L) {
   using Cf = GroupCfg<KIND, OPS, BN, PAIR, GATED>;
   static int configured[64] = {};
@@ -48,15 +69,22 @@ constexpr int kGroupSingleN = 128;
 #define DGT_DEFINE_GROUP(name, KIND, OPS)                                                            \
   cudaError_t launch_group_##name(const GroupLaunch& L) {                                            \
     if (L.pair)                                                                                      \
-      return L.gated ? launch_group_variant<KIND, OPS, kGroupPairN, true, true>(L)                   \
-                     : launch_group_variant<KIND, OPS, kGroupPairN, true, false>(L);                 \
-    return L.gated ? launch_group_variant<KIND, OPS, kGroupSingleN, false, true>(L)                  \
-                   : launch_group_variant<KIND, OPS, kGroupSingleN, false, false>(L);                \
+      return L.gated ? launch_group_variant<KIND, OPS, kGroupPairN, true, GATED_SILU>(L)             \
+                     : launch_group_variant<KIND, OPS, kGroupPairN, true, GATED_NONE>(L);            \
+    return L.gated ? launch_group_variant<KIND, OPS, kGroupSingleN, false, GATED_SILU>(L)            \
+                   : launch_group_variant<KIND, OPS, kGroupSingleN, false, GATED_NONE>(L);           \
+  }
+
+// The dense gated product.
+#define DGT_DEFINE_GATED(name, KIND, OPS)                                                            \
+  cudaError_t launch_gated_##name(const GroupLaunch& L) {                                            \
+    return L.pair ? launch_group_variant<KIND, OPS, kGroupPairN, true, GATED_ANY>(L)                 \
+                  : launch_group_variant<KIND, OPS, kGroupSingleN, false, GATED_ANY>(L);             \
   }
 
 #define DGT_DEFINE_GROUP_WGRAD(name, KIND)                                                           \
   cudaError_t launch_group_##name(const GroupLaunch& L) {                                            \
-    return launch_group_variant<KIND, GROUP_WGRAD, kGroupPairN, true, false>(L);                     \
+    return launch_group_variant<KIND, GROUP_WGRAD, kGroupPairN, true, GATED_NONE>(L);                  \
   }
 
 }  // namespace dgt

@@ -1,0 +1,629 @@
+// Layer norm with the residual's addition and an optional 8-bit output, and its
+// gradient (gemm_layernorm, gemm_layernorm_backward).
+//
+//   h = round(x + residual);  m = mean(h);  r = (mean((h - m)^2) + eps)^-1/2;  y = (h - m) r w + b
+//   xhat = (h - m) r,  g = dy w:  dx = r (g - mean(g)) - r mean(g xhat) xhat + dh
+//   dw = sum over rows of dy xhat,  db = sum over rows of dy
+//
+// Both are bound by HBM: each matrix is read or written once. As in the
+// root-mean-square norm a row stays in its threads' registers, here between three
+// reductions: the mean, the squares of what is left of it (two passes over
+// registers: mean(h^2) - m^2 would cancel where the mean is large), and the 8-bit
+// scale. The ways to reach memory are in row.cuh.
+#include "row.cuh"
+
+#include "dgt_feedforward.h"
+
+namespace dgt {
+namespace {
+
+struct LayerParams {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  const void* bias;
+  void* h;
+  void* y;
+  float* scale;
+  float* mean;
+  float* rstd;
+  long long ldx, ldr, ldh, ldy;
+  int rows, cols, tpr;
+  float eps;
+};
+
+// Column j of piece i is one of the row's (pieces past the row's end, and of the
+// rows around it where they are FLAT, are held as zeros and must not count as h - m).
+template <int MODE, int VEC>
+__device__ __forceinline__ bool column(const Row<MODE, VEC>& r, int i, int j) {
+  if constexpr (MODE == FLAT) return r.lo(i) + j >= 0 && r.lo(i) + j < r.cols;
+  return r.whole(i);
+}
+
+template <int TYPE, int MODE, int EPT, bool Q8>
+__global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EPT> == 512 ? 2 : 1)
+    layernorm_kernel(const LayerParams p) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = MODE == SINGLE ? 1 : 16 / sizeof(T);
+  using P = Pack<TYPE, VEC>;
+  constexpr int NV = EPT / VEC;
+  __shared__ float red[2][3][32];
+  extern __shared__ uint4 dynamic[];
+  T* shared_w = reinterpret_cast<T*>(dynamic);
+  T* shared_b = shared_w + (MODE == FLAT ? (p.cols + VEC - 1) / VEC * VEC : 0);
+  const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
+  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const RowWarps row_warps(p.tpr, sub);
+  grid_dependency_wait();
+  if constexpr (MODE == FLAT) {
+    if (p.bias != nullptr) stage_weights<TYPE, VEC>(shared_b, p.bias, p.cols);
+    stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
+  }
+  int turn = 0;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows;
+       r0 += static_cast<long long>(gridDim.x) * per_block, turn ^= 1) {
+    const long long row = r0 + sub;
+    const bool in = row < p.rows;
+    r.at(row);
+    P h[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in);
+    if (p.residual != nullptr) {
+      P a[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[j] = h[i].get(j) + a[i].get(j);
+        h[i].set(x);
+        if (p.h != nullptr) r.store(h[i], p.h, row, p.ldh, i, in);
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s += h[i].get(j);
+    const float mean = row_warps.sum(s, red[turn][0]) / static_cast<float>(p.cols);
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float d = column(r, i, j) ? h[i].get(j) - mean : 0.0f;
+        s = fmaf(d, d, s);
+      }
+    const float rstd = 1.0f / sqrtf(row_warps.sum(s, red[turn][1]) / static_cast<float>(p.cols) + p.eps);
+    if (in && r.tid == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    // the output of piece i, before its rounding
+    auto norm = [&](float(&w)[VEC], int i) {
+      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = (h[i].get(j) - mean) * rstd * w[j];
+      if (p.bias != nullptr) {
+        float b[VEC];
+        load_weights<MODE, TYPE, VEC>(b, r, p.bias, shared_b, i);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] += b[j];
+      }
+    };
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float y[VEC];
+        norm(y, i);
+        P o;
+        o.set(y);
+        r.store(o, p.y, row, p.ldy, i, in);
+      }
+    } else {
+      // |y| compared by bit pattern: a NaN is above every number and reaches the scale
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float y[VEC];
+        norm(y, i);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (column(r, i, j)) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+      }
+      const float amax = __uint_as_float(row_warps.max_bits(top, red[turn][2]));
+      const float scale = (amax < 1e-12f ? 1e-12f : amax) / kE4M3Max;
+      const float inv = 1.0f / scale;
+      if (in && r.tid == 0) p.scale[row] = scale;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float y[VEC];
+        norm(y, i);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) y[j] *= inv;
+        r.store_q8(y, p.y, row, p.ldy, i, in);
+      }
+    }
+  }
+  grid_launch_dependents();
+}
+
+constexpr int kGradEpt = 16;  // elements of a row per thread of the gradient
+
+struct LayerGradParams {
+  const void* dy;
+  const void* h;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  const void* dh;
+  void* dx;
+  float* partial;  // a row of `cols` sums of dw and one of db per block
+  long long lddy, ldh, lddh, lddx;
+  int rows, cols, tpr;
+};
+
+// Two sums over a row's warps at once: one barrier for both.
+__device__ __forceinline__ float2 sum_two(const RowWarps& w, float2 v, float2* red) {
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  if (w.warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < w.warps ? red[w.w0 + lane] : make_float2(0.0f, 0.0f);
+  return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+// A thread owns the same columns of every row (ALIGNED, SINGLE) and adds dw and db
+// up in registers; FLAT rows move against the threads, and both are in shared
+// memory, where a column meets one thread a row and the rows' reductions separate
+// them. ALIGNED with AHEAD: each thread copies its pieces of the next row to its
+// own places in shared memory (cp.async) before it works on this one, so that
+// loads are in flight during the reduction and the stores, and reads a piece from
+// its place once for the sums and once for the output, so that registers hold one
+// piece at a time beside the 32 sums. THREADS: what the block has at most; up to
+// 512 leave a thread 128 registers, and the sums stay in them.
+template <int TYPE, int MODE, bool AHEAD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) layernorm_grad_kernel(const LayerGradParams p) {
+  constexpr int EPT = kGradEpt;
+  using T = typename Elem<TYPE>::T;
+  constexpr int VEC = MODE == SINGLE ? 1 : 16 / sizeof(T);
+  using P = Pack<TYPE, VEC>;
+  constexpr int NV = EPT / VEC;
+  __shared__ float2 red[2][32];
+  extern __shared__ uint4 dynamic[];
+  // ALIGNED, SINGLE: (rows of the block - 1) x 2 x cols partial sums; FLAT: dw and db of each row of the block, then
+  // the weights
+  float* sums = reinterpret_cast<float*>(dynamic);
+  const int places = (p.cols + VEC - 1) / VEC * VEC;
+  const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
+  T* shared_w = reinterpret_cast<T*>(sums + 2 * per_block * places);
+  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const RowWarps row_warps(p.tpr, sub);
+  const long long step = static_cast<long long>(gridDim.x) * per_block;
+  // AHEAD: piece i of h, dy or dh (m = 0, 1, 2) of stage s
+  auto cell = [&](int s, int m, int i) { return dynamic + ((s * 3 + m) * NV + i) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](long long row, int s) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (r.whole(i)) {
+        if (row < p.rows) {
+          copy16(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i));
+          copy16(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i));
+          if (p.dh != nullptr) copy16(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i));
+        } else if (per_block > 1) {  // a row past the last one counts as zeros
+          *cell(s, 0, i) = *cell(s, 1, i) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const long long start = static_cast<long long>(blockIdx.x) * per_block + sub;
+  grid_dependency_wait();
+  if constexpr (AHEAD) {
+    // zeros where no copy lands: past the last column, and dh where there is none
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      for (int c = 0; c < 6; ++c)
+        if (!r.whole(i) || (c % 3 == 2 && p.dh == nullptr)) *cell(c / 3, c % 3, i) = make_uint4(0u, 0u, 0u, 0u);
+    fetch(start, 0);
+  }
+  // a row past the last one has dy = 0, mean = rstd = 0: it adds nothing
+  auto statistics = [&](long long row) {
+    return row < p.rows ? make_float2(p.mean[row], p.rstd[row]) : make_float2(0.0f, 0.0f);
+  };
+  float2 next = AHEAD ? statistics(start) : make_float2(0.0f, 0.0f);
+  constexpr int SUMS = MODE == FLAT ? 1 : EPT;
+  float dw[SUMS], db[SUMS];
+  if constexpr (MODE == FLAT) {
+    for (int i = threadIdx.x; i < 2 * per_block * places; i += blockDim.x) sums[i] = 0.0f;
+    stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
+  } else {
+#pragma unroll
+    for (int e = 0; e < SUMS; ++e) dw[e] = db[e] = 0.0f;
+  }
+  int turn = 0;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows; r0 += step, turn ^= 1) {
+    const long long row = r0 + sub;
+    const bool in = row < p.rows;
+    r.at(row);
+    P h[NV], dy[NV], dh[NV];
+    float2 stat;
+    if constexpr (AHEAD) {
+      fetch(row + step, turn ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row's pieces have landed
+      stat = next;
+      next = statistics(row + step);
+    } else {
+      stat = statistics(row);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        r.load(h[i], p.h, row, p.ldh, i, in);
+        r.load(dy[i], p.dy, row, p.lddy, i, in);
+      }
+      if (p.dh != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dh[i].zero();
+      }
+    }
+    const float mean = stat.x, rstd = stat.y;
+    // AHEAD: a piece from its place, once for each use: registers hold one piece at a time, not the row's
+    auto take = [&](P(&v)[NV], int m, int i) {
+      if constexpr (AHEAD) v[i].load(reinterpret_cast<const T*>(cell(turn, m, i)));
+    };
+    // sums of g and of g xhat (outside the row dy is 0, and so is what is added)
+    float2 dots = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float w[VEC];
+      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      take(h, 0, i);
+      take(dy, 1, i);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float xhat = (h[i].get(j) - mean) * rstd, d = dy[i].get(j), g = d * w[j];
+        if constexpr (MODE == FLAT) {
+          if (in && column(r, i, j)) {
+            dots.x += g;
+            dots.y = fmaf(g, xhat, dots.y);
+            float* at = sums + 2 * sub * places + r.place(i, j);
+            at[0] += d * xhat;
+            at[places] += d;
+          }
+        } else {
+          dots.x += g;
+          dots.y = fmaf(g, xhat, dots.y);
+          dw[i * VEC + j] = fmaf(d, xhat, dw[i * VEC + j]);
+          db[i * VEC + j] += d;
+        }
+      }
+    }
+    dots = sum_two(row_warps, dots, red[turn]);
+    const float mean_g = dots.x / static_cast<float>(p.cols), back = rstd * (dots.y / static_cast<float>(p.cols));
+    if (MODE == FLAT && p.tpr <= 32) __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float w[VEC];
+      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      take(h, 0, i);
+      take(dy, 1, i);
+      take(dh, 2, i);
+      P o;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        w[j] = fmaf(fmaf(dy[i].get(j), w[j], -mean_g), rstd, fmaf((h[i].get(j) - mean) * rstd, -back, dh[i].get(j)));
+      o.set(w);
+      r.store(o, p.dx, row, p.lddx, i, in);
+    }
+  }
+  if constexpr (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+  if constexpr (MODE == FLAT) {
+    __syncthreads();
+    const int per = places / VEC;
+    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+      float s = 0.0f, t = 0.0f;
+      for (int i = 0; i < per_block; ++i) {
+        const float* at = sums + 2 * i * places + (c % VEC) * per + c / VEC;
+        s += at[0];
+        t += at[places];
+      }
+      out[c] = s;
+      out[p.cols + c] = t;
+    }
+  } else {
+    // the block's sums over its rows, in row order; four columns a store
+    constexpr int RUN = VEC < 4 ? 1 : 4;
+    auto each = [&](auto use) {
+#pragma unroll
+      for (int e = 0; e < EPT; e += RUN)
+        if (r.whole(e / VEC)) use(r.lo(e / VEC) + e % VEC, e);
+    };
+    auto store = [&](float* to, const float* from) {
+      if constexpr (RUN == 1)
+        *to = *from;
+      else
+        *reinterpret_cast<float4*>(to) = make_float4(from[0], from[1], from[2], from[3]);
+    };
+    if (per_block > 1) {
+      __syncthreads();
+      if (sub > 0)
+        each([&](int c, int e) {
+          store(sums + 2 * (sub - 1) * p.cols + c, dw + e);
+          store(sums + (2 * (sub - 1) + 1) * p.cols + c, db + e);
+        });
+      __syncthreads();
+      if (sub == 0)
+        for (int s = 0; s + 1 < per_block; ++s)
+          each([&](int c, int e) {
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+              dw[e + k] += sums[2 * s * p.cols + c + k];
+              db[e + k] += sums[(2 * s + 1) * p.cols + c + k];
+            }
+          });
+    }
+    if (sub == 0)
+      each([&](int c, int e) {
+        store(out + c, dw + e);
+        store(out + p.cols + c, db + e);
+      });
+  }
+  grid_launch_dependents();
+}
+
+// dw and db from the blocks' partial rows (2 x cols each): 32 columns a block, 32
+// threads a column, each a fixed share of the rows, added in order of the threads.
+template <int TYPE>
+__global__ void __launch_bounds__(1024) layer_weight_sum_kernel(const float* partial, int rows, int cols, void* dw,
+                                                                void* db) {
+  using E = Elem<TYPE>;
+  __shared__ float part[32][33];
+  grid_dependency_wait();
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + c;
+  float s = 0.0f;
+  if (col < 2 * cols) {
+#pragma unroll 8
+    for (int r = g; r < rows; r += 32) s += __ldcg(partial + static_cast<long long>(r) * 2 * cols + col);
+  }
+  part[g][c] = s;
+  __syncthreads();
+  // warp g adds up column g of the block
+  s = warp_sum(part[c][g]);
+  const int mine = blockIdx.x * 32 + g;
+  if (c == 0 && mine < 2 * cols) {
+    void* to = mine < cols ? dw : db;
+    if (to != nullptr) static_cast<typename E::T*>(to)[mine < cols ? mine : mine - cols] = E::put(s);
+  }
+  grid_launch_dependents();
+}
+
+// Blocks of the gradient, at most: each leaves two partial rows. (Numbers, since
+// the size of the workspace goes by them, on a machine without a GPU too.)
+int grad_blocks(int64_t cols) { return cols <= 2048 ? 608 : 304; }
+
+template <int TYPE, int MODE, int EPT>
+cudaError_t launch_layer_mode(const LayerParams& p, bool q8, int grid, int block, size_t smem, cudaStream_t s) {
+  return q8 ? launch_dependent(layernorm_kernel<TYPE, MODE, EPT, true>, grid, block, smem, s, 1, p)
+            : launch_dependent(layernorm_kernel<TYPE, MODE, EPT, false>, grid, block, smem, s, 1, p);
+}
+
+// Most columns of a FLAT row whose weights and bias fit the 48 KB that a launch may take without asking.
+template <int TYPE>
+constexpr int64_t kFlatCols = TYPE == GEMM_TYPE_F32 ? 6000 : kMaxFlatCols;
+
+template <int TYPE>
+cudaError_t launch_layer(const LayerParams& p, int mode, bool few, bool q8, int grid, int block, cudaStream_t s) {
+  const size_t smem = mode == FLAT ? 2 * size_t(p.cols + 8) * sizeof(typename Elem<TYPE>::T) : 0;
+  if (mode == ALIGNED)
+    return few ? launch_layer_mode<TYPE, ALIGNED, 8>(p, q8, grid, block, smem, s)
+               : launch_layer_mode<TYPE, ALIGNED, kFullEpt<TYPE, ALIGNED>>(p, q8, grid, block, smem, s);
+  if (mode == FLAT)
+    return few ? launch_layer_mode<TYPE, FLAT, 8>(p, q8, grid, block, smem, s)
+               : launch_layer_mode<TYPE, FLAT, kFullEpt<TYPE, FLAT>>(p, q8, grid, block, smem, s);
+  return few ? launch_layer_mode<TYPE, SINGLE, 8>(p, q8, grid, block, smem, s)
+             : launch_layer_mode<TYPE, SINGLE, kFullEpt<TYPE, SINGLE>>(p, q8, grid, block, smem, s);
+}
+
+// Dynamic shared memory of the gradient's kernel.
+size_t grad_smem(const LayerGradParams& p, int mode, bool ahead, int block, int es) {
+  if (mode == FLAT) return size_t(p.cols + 8) * (2 * size_t(block / p.tpr) * sizeof(float) + es);
+  const size_t sums = 2 * size_t(block / p.tpr - 1) * size_t(p.cols) * sizeof(float);
+  const size_t stages = ahead ? size_t(2 * 3) * kGradEpt * es * size_t(block) : 0;
+  return sums > stages ? sums : stages;
+}
+
+// Most dynamic shared memory that a launch of the gradient takes: AHEAD goes up to here, and a FLAT row of
+// kMaxFlatCols has 132 KB.
+constexpr size_t kGradSmem = 200 * 1024;
+
+// Launches one build of the gradient's kernel. Its limit is a property of the kernel, not of the launch, so it is set
+// once, to the most that any launch takes: other host threads may be launching it with other sizes.
+template <int TYPE, int MODE, bool AHEAD, int THREADS>
+cudaError_t launch_layer_grad_mode(const LayerGradParams& p, int dev, int grid, int block, size_t smem,
+                                   cudaStream_t s) {
+  static int configured[64] = {};
+  auto kern = layernorm_grad_kernel<TYPE, MODE, AHEAD, THREADS>;
+  if (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGradSmem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+  }
+  return launch_dependent(kern, grid, block, smem, s, 1, p);
+}
+
+template <int TYPE, int THREADS>
+cudaError_t launch_layer_grad_threads(const LayerGradParams& p, int mode, bool ahead, int dev, int grid, int block,
+                                      cudaStream_t s) {
+  const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
+  if (mode == ALIGNED)
+    return ahead ? launch_layer_grad_mode<TYPE, ALIGNED, true, THREADS>(p, dev, grid, block, smem, s)
+                 : launch_layer_grad_mode<TYPE, ALIGNED, false, THREADS>(p, dev, grid, block, smem, s);
+  return mode == FLAT ? launch_layer_grad_mode<TYPE, FLAT, false, THREADS>(p, dev, grid, block, smem, s)
+                      : launch_layer_grad_mode<TYPE, SINGLE, false, THREADS>(p, dev, grid, block, smem, s);
+}
+
+template <int TYPE>
+cudaError_t launch_layer_grad(const LayerGradParams& p, int mode, bool ahead, int dev, int grid, int block, void* dw,
+                              void* db, cudaStream_t s) {
+  const cudaError_t e = block <= 512 ? launch_layer_grad_threads<TYPE, 512>(p, mode, ahead, dev, grid, block, s)
+                                     : launch_layer_grad_threads<TYPE, 1024>(p, mode, ahead, dev, grid, block, s);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(layer_weight_sum_kernel<TYPE>, (2 * p.cols + 31) / 32, 1024, 0, s, 1, p.partial, grid, p.cols,
+                          dw, db);
+}
+
+}  // namespace
+}  // namespace dgt
+
+using namespace dgt;
+
+extern "C" {
+
+int gemm_layernorm(int type, int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                   const void* weight, const void* bias, float eps, void* h, int64_t ldh, int y_type, void* y,
+                   int64_t ldy, float* y_scale, float* mean, float* rstd, void* stream) {
+  if (bad_type(type) || (y_type != type && y_type != GEMM_TYPE_E4M3) || rows < 0 || cols < 0 || cols > kMaxCols ||
+      rows >= (int64_t(1) << 31))
+    return GEMM_ERR_INVALID_VALUE;
+  const bool q8 = y_type == GEMM_TYPE_E4M3;
+  if ((y_scale != nullptr) != q8 && rows > 0 && cols > 0) return GEMM_ERR_INVALID_VALUE;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (x == nullptr || weight == nullptr || y == nullptr || bad_ld(ldx, cols) || bad_ld(ldy, cols) ||
+      (residual != nullptr && bad_ld(ldr, cols)))
+    return GEMM_ERR_INVALID_VALUE;
+  if (residual == nullptr) h = nullptr;  // h is x itself
+  if (h != nullptr && bad_ld(ldh, cols)) return GEMM_ERR_INVALID_VALUE;
+  const int es = type_bytes(type), eo = type_bytes(y_type);
+  if (misaligned(x, es) || misaligned(residual, es) || misaligned(weight, es) || misaligned(bias, es) ||
+      misaligned(h, es) || misaligned(y, eo) || misaligned(y_scale, 4) || misaligned(mean, 4) || misaligned(rstd, 4))
+    return GEMM_ERR_MISALIGNED;
+  // an output may be an input's very buffer (each element is read, then written, by one thread), or apart from it
+  auto clash = [&](const void* o, int64_t ldo, int e_o, const void* i, int64_t ldi) {
+    if (o == nullptr || i == nullptr || (o == i && ldo == ldi && e_o == es)) return false;
+    return meet(o, rows, cols, ldo, e_o, i, rows, cols, ldi, es);
+  };
+  auto on_row = [&](const void* o, int64_t ldo, int e_o, const void* v) {  // o meets the weights or the bias
+    return o != nullptr && v != nullptr && meet(o, rows, cols, ldo, e_o, v, 1, cols, cols, es);
+  };
+  auto on_vector = [&](const void* o, int64_t ldo, int e_o, const void* v) {  // o meets a number for each row
+    return o != nullptr && v != nullptr && meet(o, rows, cols, ldo, e_o, v, 1, rows, rows, 4);
+  };
+  if (clash(h, ldh, es, x, ldx) || clash(h, ldh, es, residual, ldr) || clash(y, ldy, eo, x, ldx) ||
+      (residual != nullptr && meet(y, rows, cols, ldy, eo, residual, rows, cols, ldr, es)) ||
+      (h != nullptr && meet(y, rows, cols, ldy, eo, h, rows, cols, ldh, es)) || on_row(y, ldy, eo, weight) ||
+      on_row(y, ldy, eo, bias) || on_row(h, ldh, es, weight) || on_row(h, ldh, es, bias))
+    return GEMM_ERR_INVALID_VALUE;
+  for (const float* v : {y_scale, mean, rstd})
+    if (on_vector(x, ldx, es, v) || on_vector(residual, ldr, es, v) || on_vector(h, ldh, es, v) ||
+        on_vector(y, ldy, eo, v))
+      return GEMM_ERR_INVALID_VALUE;
+  CallContext ctx;
+  const int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[9] = {x, weight, y, residual, bias, h, y_scale, mean, rstd};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  const int v = 16 / es;
+  int mode = SINGLE;
+  if (cols % v == 0 && aligned(x, ldx, es, 16) && aligned(weight, 0, es, 16) && aligned(bias, 0, es, 16) &&
+      (residual == nullptr || aligned(residual, ldr, es, 16)) && (h == nullptr || aligned(h, ldh, es, 16)) &&
+      aligned(y, ldy, eo, v * eo))
+    mode = ALIGNED;
+  else if (cols <= (es == 4 ? kFlatCols<GEMM_TYPE_F32> : kFlatCols<GEMM_TYPE_BF16>) && flat(x, ldx, cols, 16) &&
+           (residual == nullptr || flat(residual, ldr, cols, 16)) && (h == nullptr || flat(h, ldh, cols, 16)) &&
+           flat(y, ldy, cols, v * eo))
+    mode = FLAT;
+  LayerParams p = {x,       residual, weight,  bias,    h,         y,         y_scale, mean, rstd, (long long)ldx,
+                   (long long)ldr, (long long)ldh, (long long)ldy, int(rows), int(cols), 0, eps};
+  // Eight elements a thread while the rows leave threads to spare, 64 bytes' worth once they fill the GPU and past
+  // what 1024 threads hold (the root-mean-square norm's rule: its loads and reductions are these).
+  const bool few = cols <= 8000 && rows * cols <= int64_t(ctx.sm_count) * 8192;
+  p.tpr = threads_per_row(cols, few ? 8 : mode == SINGLE ? 16 : 64 / es, mode, v);
+  const int least = mode == FLAT && !few ? 512 : 128;  // FLAT blocks stage the weights: few that take many rows
+  const int block = p.tpr < least ? least / p.tpr * p.tpr : p.tpr;
+  const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
+  const int64_t most = int64_t(ctx.sm_count) * (mode == FLAT ? 1024 / block + 1 : 2048 / block);
+  const int grid = int(need < most ? need : most);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_layer<GEMM_TYPE_F16>(p, mode, few, q8, grid, block, s)
+                        : type == GEMM_TYPE_BF16 ? launch_layer<GEMM_TYPE_BF16>(p, mode, few, q8, grid, block, s)
+                                                 : launch_layer<GEMM_TYPE_F32>(p, mode, few, q8, grid, block, s);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int64_t gemm_layernorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols > kMaxCols) return 0;
+  return (rows < grad_blocks(cols) ? rows : grad_blocks(cols)) * 2 * cols * int64_t(sizeof(float));
+}
+
+int gemm_layernorm_backward(int type, int64_t rows, int64_t cols, const void* dy, int64_t lddy, const void* h,
+                            int64_t ldh, const void* weight, const float* mean, const float* rstd, const void* dh,
+                            int64_t lddh, void* dx, int64_t lddx, void* dw, void* db, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  if (bad_type(type) || rows < 0 || cols < 0 || cols > kMaxCols || rows >= (int64_t(1) << 31))
+    return GEMM_ERR_INVALID_VALUE;
+  if (cols == 0) return GEMM_OK;
+  const int es = type_bytes(type);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CallContext ctx;
+  if (dw == nullptr) return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(dw, es) || misaligned(db, es)) return GEMM_ERR_MISALIGNED;
+  if (db != nullptr && meet(dw, 1, cols, cols, es, db, 1, cols, cols, es)) return GEMM_ERR_INVALID_VALUE;
+  if (rows == 0) {  // no rows: dw = db = 0
+    const int st = begin_call(&ctx);
+    if (st != GEMM_OK) return st;
+    if (!on_device(dw, ctx.dev) || (db != nullptr && !on_device(db, ctx.dev))) return GEMM_ERR_NOT_DEVICE_MEMORY;
+    if (cudaMemsetAsync(dw, 0, size_t(cols) * es, s) != cudaSuccess) return GEMM_ERR_LAUNCH;
+    return db == nullptr || cudaMemsetAsync(db, 0, size_t(cols) * es, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+  }
+  if (dy == nullptr || h == nullptr || weight == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr ||
+      workspace == nullptr || bad_ld(lddy, cols) || bad_ld(ldh, cols) || bad_ld(lddx, cols) ||
+      (dh != nullptr && bad_ld(lddh, cols)) || workspace_bytes < gemm_layernorm_backward_workspace(rows, cols))
+    return GEMM_ERR_INVALID_VALUE;
+  if (misaligned(dy, es) || misaligned(h, es) || misaligned(weight, es) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+      misaligned(dh, es) || misaligned(dx, es) || misaligned(workspace, 16))
+    return GEMM_ERR_MISALIGNED;
+  auto clash = [&](const void* i, int64_t ldi) {
+    if (i == nullptr || (i == dx && ldi == lddx)) return false;
+    return meet(dx, rows, cols, lddx, es, i, rows, cols, ldi, es);
+  };
+  auto on_dx = [&](const void* v, int64_t n, int e_v) {
+    return v != nullptr && meet(dx, rows, cols, lddx, es, v, 1, n, n, e_v);
+  };
+  if (clash(dy, lddy) || clash(dh, lddh) || clash(h, ldh) || on_dx(weight, cols, es) || on_dx(dw, cols, es) ||
+      on_dx(db, cols, es) || on_dx(mean, rows, 4) || on_dx(rstd, rows, 4))
+    return GEMM_ERR_INVALID_VALUE;
+  const int st = begin_call(&ctx);
+  if (st != GEMM_OK) return st;
+  const void* ptrs[10] = {dy, h, weight, mean, rstd, dx, dw, db, workspace, dh};
+  for (const void* q : ptrs)
+    if (q != nullptr && !on_device(q, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+  const int v = 16 / es;
+  int mode = SINGLE;
+  if (cols % v == 0 && aligned(dy, lddy, es, 16) && aligned(h, ldh, es, 16) && aligned(weight, 0, es, 16) &&
+      aligned(dx, lddx, es, 16) && (dh == nullptr || aligned(dh, lddh, es, 16)))
+    mode = ALIGNED;
+  else if (cols <= kMaxFlatCols && flat(dy, lddy, cols, 16) && flat(h, ldh, cols, 16) && flat(dx, lddx, cols, 16) &&
+           (dh == nullptr || flat(dh, lddh, cols, 16)))
+    mode = FLAT;
+  LayerGradParams p = {dy,   h,      weight, mean, rstd, dh, dx, static_cast<float*>(workspace), (long long)lddy,
+                       (long long)ldh, (long long)lddh, (long long)lddx, int(rows), int(cols), 0};
+  p.tpr = threads_per_row(cols, kGradEpt, mode, v);
+  const int block = p.tpr >= 256 ? p.tpr : 256 / p.tpr * p.tpr;
+  const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= kGradSmem;
+  const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
+  const int grid = int(need < grad_blocks(cols) ? need : grad_blocks(cols));
+  const cudaError_t e =
+      type == GEMM_TYPE_F16    ? launch_layer_grad<GEMM_TYPE_F16>(p, mode, ahead, ctx.dev, grid, block, dw, db, s)
+      : type == GEMM_TYPE_BF16 ? launch_layer_grad<GEMM_TYPE_BF16>(p, mode, ahead, ctx.dev, grid, block, dw, db, s)
+                               : launch_layer_grad<GEMM_TYPE_F32>(p, mode, ahead, ctx.dev, grid, block, dw, db, s);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // extern "C"
