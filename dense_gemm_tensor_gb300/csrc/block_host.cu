@@ -2,8 +2,7 @@
 // (gemm_e4m3_blocks): argument checks, tensor maps, the choice of tile and split.
 #include <cstring>
 
-#include "block_kernel.cuh"
-#include "host.h"
+#include "block_launch.h"
 
 namespace dgt {
 namespace {
@@ -24,17 +23,24 @@ bool meet(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // Sets the kernel's dynamic shared-memory limit once per device, then launches.
 template <int BN, bool COLS, bool SWAP>
-cudaError_t launch_block(const CUtensorMap& tmP, const CUtensorMap& tmQ, const BlockParams& p, int dev, int grid,
-                         cudaStream_t s) {
+cudaError_t launch_block(const BlockLaunch& L) {
   using Cf = BlockCfg<BN>;
   static int configured[64] = {};
   auto kern = block_kernel<BN, COLS, SWAP>;
-  if (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+  if (L.dev >= 64 || !__atomic_load_n(&configured[L.dev], __ATOMIC_ACQUIRE)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if (dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    if (L.dev < 64) __atomic_store_n(&configured[L.dev], 1, __ATOMIC_RELEASE);
   }
-  return launch_dependent(kern, grid, kBlockThreads, Cf::SMEM_BYTES, s, p.splits, tmP, tmQ, p);
+  return launch_dependent(kern, L.grid, kBlockThreads, Cf::SMEM_BYTES, L.stream, L.p.splits, L.tmP, L.tmQ, L.p);
+}
+
+// Columns of a CTA pair's tile, or 0 for single CTAs: the widest whose tiles give most pairs one.
+int pair_width(int64_t M, int64_t N, int sms) {
+  const int64_t rows = (M + 255) / 256, units = sms / 2;
+  for (int bn : {256, 128})
+    if (rows * ((N + bn - 1) / bn) * 4 >= units * 3) return bn;
+  return 0;
 }
 
 }  // namespace
@@ -80,8 +86,9 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
   if (M == 1) lda = (K + 15) / 16 * 16;
   if (N == 1) ldb = (K + 15) / 16 * 16;
   const bool swap = M <= 64;
-  BlockParams p;
-  memset(&p, 0, sizeof(p));
+  BlockLaunch L;
+  memset(&L, 0, sizeof(L));
+  BlockParams& p = L.p;
   p.g.status = ctx.status;
   p.g.epoch = ctx.epoch;
   p.g.debug = ctx.debug;
@@ -89,36 +96,49 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
   p.g.C = C;
   p.g.ldc = ldc;
   p.g.num_kb = int(blocks);
+  p.g.raster = 8;
   const BlockScales sa = {a_scale, as_row, as_block, 0}, sb = {b_scale, bs_row, bs_block, b_rows == 1 ? 0 : 7};
   p.ps = swap ? sb : sa;
   p.qs = swap ? sa : sb;
   p.p_rows = int(swap ? N : M);
   p.q_rows = int(swap ? M : N);
-  const int bn = !swap ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  p.g.tiles_m = (p.p_rows + 127) / 128;
+  L.dev = ctx.dev;
+  L.stream = s;
+  const int pair_bn = swap ? 0 : pair_width(M, N, ctx.sm_count);
+  const int bn = pair_bn > 0 ? pair_bn : !swap ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int bm = pair_bn > 0 ? 256 : 128;
+  p.g.tiles_m = (p.p_rows + bm - 1) / bm;
   p.g.tiles_n = (p.q_rows + bn - 1) / bn;
-  p.g.raster = 8;
   const int64_t tiles = int64_t(p.g.tiles_m) * p.g.tiles_n;
-  // a tile is split while the GPU (two CTAs to an SM) has room for twice the CTAs and each would keep four blocks
+  if (tiles > kIntLimit / 8) return GEMM_ERR_INVALID_VALUE;
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * ctx.sm_count && blocks >= p.splits * 8) p.splits *= 2;
-  if (tiles * p.splits > kIntLimit) return GEMM_ERR_INVALID_VALUE;
+  if (pair_bn > 0) {
+    const int64_t units = ctx.sm_count / 2;
+    L.grid = int(2 * (tiles < units ? tiles : units));
+    const uint64_t v = uint64_t(reinterpret_cast<uintptr_t>(C)) | uint64_t(ldc * 2);
+    p.g.c_gran = v % 16 == 0 ? 16 : v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
+    p.g.c_tma = p.g.c_gran == 16;
+    if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, C, N, M, ldc * 2, 1, 0, 64, 32,
+                                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return GEMM_ERR_DRIVER;
+  } else {
+    // a tile is split while the GPU (two CTAs to an SM) has room for twice the CTAs and each would keep four blocks
+    while (p.splits < 8 && tiles * p.splits * 2 <= 2 * ctx.sm_count && blocks >= p.splits * 8) p.splits *= 2;
+    L.grid = int(tiles * p.splits);
+  }
   const void* P = swap ? static_cast<const void*>(B) : A;
   const void* Q = swap ? static_cast<const void*>(A) : B;
-  CUtensorMap tmP, tmQ;
-  if (!encode_map_3d(&tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, P, K, p.p_rows, swap ? ldb : lda, 1, 0, kBlockK, 128,
+  if (!encode_map_3d(&L.tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, P, K, p.p_rows, swap ? ldb : lda, 1, 0, kBlockK, 128,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map_3d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, Q, K, p.q_rows, swap ? lda : ldb, 1, 0, kBlockK, bn,
-                     CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_map_3d(&L.tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, Q, K, p.q_rows, swap ? lda : ldb, 1, 0, kBlockK,
+                     pair_bn > 0 ? bn / 2 : bn, CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_ERR_DRIVER;
-  const int grid = int(tiles * p.splits);
   cudaError_t e;
-  if (swap)
-    e = bn == 16   ? launch_block<16, true, true>(tmP, tmQ, p, ctx.dev, grid, s)
-        : bn == 32 ? launch_block<32, true, true>(tmP, tmQ, p, ctx.dev, grid, s)
-                   : launch_block<64, true, true>(tmP, tmQ, p, ctx.dev, grid, s);
+  if (pair_bn > 0)
+    e = launch_block_pair(L, bn, b_rows == 1);
+  else if (swap)
+    e = bn == 16 ? launch_block<16, true, true>(L) : bn == 32 ? launch_block<32, true, true>(L) : launch_block<64, true, true>(L);
   else
-    e = b_rows == 1 ? launch_block<128, true, false>(tmP, tmQ, p, ctx.dev, grid, s)
-                    : launch_block<128, false, false>(tmP, tmQ, p, ctx.dev, grid, s);
+    e = b_rows == 1 ? launch_block<128, true, false>(L) : launch_block<128, false, false>(L);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
