@@ -9,8 +9,10 @@
 // warps to a scheduler). So the sums are held two to a register pair, a load is in
 // flight while the one before it is added, the accumulator is handed back as soon
 // as its last load has landed, and the epilogue warps have most of the register
-// file (setmaxnreg): 128 sums a thread stay in registers. COLS (a scale for each
-// row of the column operand) has two instructions for one.
+// file (setmaxnreg): 128 sums a thread stay in registers. The scales come through
+// shared memory, loaded by warps of their own, whose arrivals count for the same
+// barrier as the tensor cores': a block costs the epilogue one wait. COLS (a scale
+// for each row of the column operand) has two instructions for one.
 #pragma once
 
 #include "block_kernel.cuh"
@@ -18,7 +20,7 @@
 
 namespace dgt {
 
-constexpr int kPairThreads = 384;  // warps 0-3 and 8-11 epilogue, 4 producer, 5 MMA, 6 column scales, 7 idle
+constexpr int kPairThreads = 384;  // warps 0-3 and 8-11 epilogue, 4 producer, 5 MMA, 6 column scales, 7 row scales
 
 template <int BN_>
 struct BlockPairCfg {
@@ -32,15 +34,18 @@ struct BlockPairCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int EPI_TILE = 32 * 128;
   static constexpr int EPI_STAGING = 8 * EPI_TILE;
-  static constexpr int SCALE_BYTES = kScaleRing * BN * 4;
+  // a block's scales: of the 128 rows (times each 128 columns' one, unless COLS), and of the columns (COLS)
+  static constexpr int ROW_SCALES = 2 * BM;
+  static constexpr int SCALE_BYTES = ACCS * (ROW_SCALES + BN) * 4;
   static constexpr int BAR_BYTES = 512;
   static constexpr int SMEM_LIMIT = 232448;
   static constexpr int STAGES_FIT = (SMEM_LIMIT - 1024 - EPI_STAGING - SCALE_BYTES - BAR_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_STAGING + SCALE_BYTES + BAR_BYTES;
   static constexpr int COLS_PER_SET = BN / 2;  // columns of an epilogue warp
+  static constexpr int BLOCKS = BN / 128;      // scales of the column operand without COLS
   static_assert(BN == 256 || BN == 128, "tile width");
-  static_assert((2 * STAGES + 2 * ACCS + 1 + 2 * kScaleRing) * 8 + 16 <= BAR_BYTES, "barrier area");
+  static_assert((2 * STAGES + 3 * ACCS + 1) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(2 * BM >> 4) << 24);
 };
 
@@ -95,9 +100,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t empty0 = full0 + 8 * S;
   const uint32_t accf0 = empty0 + 8 * S;
   const uint32_t acce0 = accf0 + 8 * Cf::ACCS;
-  const uint32_t scf0 = acce0 + 8 * Cf::ACCS;
-  const uint32_t sce0 = scf0 + 8 * kScaleRing;
-  const uint32_t drain_bar = sce0 + 8 * kScaleRing;
+  const uint32_t sce0 = acce0 + 8 * Cf::ACCS;  // this CTA's epilogue has read a block's scales
+  const uint32_t drain_bar = sce0 + 8 * Cf::ACCS;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + (drain_bar + 8 - sbase));
   volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot) + 1;
   volatile int* consumed_slot = issued_slot + 1;
@@ -124,12 +128,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < Cf::ACCS; ++b) {
-      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(accf0 + 8 * b, COLS ? 3 : 2);  // the tensor cores, and the scales
       mbar_init(acce0 + 8 * b, 16);
-    }
-    for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(scf0 + 8 * i, 1);
-      mbar_init(sce0 + 8 * i, 8);
+      mbar_init(sce0 + 8 * b, 8);
     }
     mbar_init(drain_bar, 1);
     *issued_slot = 0;
@@ -208,38 +209,66 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       if (lane == 0) wait_phase_drain(p.g, drain_bar, 0);
       __syncwarp();
-    } else if (warp == 6 && COLS) {
-      // -------------------------------------------------------------- column scales (each CTA all BN)
-      constexpr int PER = BN / 32;
+    } else if (warp == 7 || (warp == 6 && COLS)) {
+      // -------------------------------------------------------------- scales (each CTA)
+      // A lane has entries lane, lane + 32, ... of the block's scales; two blocks ahead in registers. The arrival for
+      // a block comes after the epilogue has read the slot's last one, and so after that phase of the barrier.
+      const bool rows = warp == 7;
+      constexpr int PER = BN / 32 > 4 + Cf::BLOCKS ? BN / 32 : 4 + Cf::BLOCKS;
       int it = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += nunits) {
         int p0, q0;
         place(t, p0, q0);
-        // one block ahead in registers; a lane has columns lane, lane + 32, ...
-        float next[PER];
-        auto load = [&](int kb) {
+        float next[2][PER];
+        auto load = [&](float(&v)[PER], int kb) {
 #pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const int c = q0 + lane + 32 * j;
-            next[j] = kb < kbs && c < p.q_rows ? p.qs.at(c, kb) : 0.0f;
+          for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+          if (kb >= kbs) return;
+          if (rows) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = p.ps.at(min(p0 + lane + 32 * j, p.p_rows - 1), kb);
+            if constexpr (!COLS) {
+#pragma unroll
+              for (int j = 0; j < Cf::BLOCKS; ++j) v[4 + j] = p.qs.at(min(q0 + 128 * j, p.q_rows - 1), kb);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < BN / 32; ++j) {
+              const int c = q0 + lane + 32 * j;
+              if (c < p.q_rows) v[j] = p.qs.at(c, kb);
+            }
           }
         };
-        load(0);
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-          const int i = it % kScaleRing;
-          float now[PER];
+        load(next[0], 0);
+        load(next[1], 1);
+        for (int kb0 = 0; ok && kb0 < kbs; kb0 += 2) {
 #pragma unroll
-          for (int j = 0; j < PER; ++j) now[j] = next[j];
-          load(kb + 1);
-          if (!group_wait(p.g, sce0 + 8 * i, ((it / kScaleRing) & 1) ^ 1, ROLE_COPY | (i << 8))) {
-            ok = false;
-            break;
+          for (int i = 0; i < 2; ++i) {
+            if (kb0 + i >= kbs) break;
+            float now[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) now[j] = next[i][j];
+            load(next[i], kb0 + i + 2);
+            const int b = it % Cf::ACCS;
+            if (!group_wait(p.g, sce0 + 8 * b, ((it / Cf::ACCS) & 1) ^ 1, ROLE_COPY | (b << 8))) {
+              ok = false;
+              break;
+            }
+            float* to = scales + b * (Cf::ROW_SCALES + BN);
+            if (rows) {
+#pragma unroll
+              for (int k = 0; k < (COLS ? 1 : Cf::BLOCKS); ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[k * Cf::BM + lane + 32 * j] = COLS ? now[j] : now[j] * now[4 + k];
+            } else {
+#pragma unroll
+              for (int j = 0; j < BN / 32; ++j) to[Cf::ROW_SCALES + lane + 32 * j] = now[j];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(accf0 + 8 * b);
+            ++it;
           }
-#pragma unroll
-          for (int j = 0; j < PER; ++j) scales[i * BN + lane + 32 * j] = now[j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scf0 + 8 * i);
         }
       }
     }
@@ -258,73 +287,49 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int p0, q0;
       place(t, p0, q0);
       const int row0 = p0 + q * 32, col0 = q0 + set * NC;
-      const int srow = min(row0 + lane, p.p_rows - 1);
-      const int scol = min(col0, p.q_rows - 1);
       float2 acc[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-      float next[4], next_q[COLS ? 1 : 4];
-      auto load = [&](int kb) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          next[i] = kb + i < kbs ? p.ps.at(srow, kb + i) : 0.0f;
-          if (!COLS) next_q[i] = kb + i < kbs ? p.qs.at(scol, kb + i) : 0.0f;
+      for (int kb = 0; kb < kbs; ++kb, ++it) {
+        const int b = it % Cf::ACCS;
+        if (!group_wait(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8))) {
+          ok = false;
+          break;
         }
-      };
-      load(0);
-      for (int kb0 = 0; ok && kb0 < kbs; kb0 += 4) {
-        float now[4];
+        tc_fence_after();
+        const uint32_t from = taddr + b * BN;
+        const float* scale = scales + b * (Cf::ROW_SCALES + BN);
+        uint32_t r[2][32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(from, r[0]);
+        const float f1 = scale[(COLS ? 0 : (set * NC) / 128 * Cf::BM) + q * 32 + lane];
+        const float2 f = make_float2(f1, f1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) now[i] = COLS ? next[i] : next[i] * next_q[COLS ? 0 : i];
-        load(kb0 + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kb0 + i >= kbs) break;
-          const int b = it % Cf::ACCS, si = it % kScaleRing;
-          if (COLS && !group_wait(p.g, scf0 + 8 * si, (it / kScaleRing) & 1, ROLE_EPILOGUE | (0x90u << 8))) {
-            ok = false;
-            break;
-          }
-          if (!group_wait(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t from = taddr + b * BN;
-          const float2 f = make_float2(now[i], now[i]);
-          uint32_t r[2][16];
-          __syncwarp();
-          tmem_ld_x16(from, r[0]);
-#pragma unroll
-          for (int c = 0; c < NC / 16; ++c) {
-            tmem_wait_ld_x16(r[c & 1]);
-            if (c + 1 < NC / 16) {
-              tmem_ld_x16(from + 16 * (c + 1), r[(c + 1) & 1]);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(lead_acce0 + 8 * b);
-            }
-            const float4* cs = reinterpret_cast<const float4*>(scales + si * BN + set * NC + 16 * c);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
-              float2 y = make_float2(__uint_as_float(r[c & 1][2 * j + 2]), __uint_as_float(r[c & 1][2 * j + 3]));
-              if constexpr (COLS) {
-                const float4 s4 = cs[j / 2];
-                x = __fmul2_rn(x, make_float2(s4.x, s4.y));
-                y = __fmul2_rn(y, make_float2(s4.z, s4.w));
-              }
-              acc[8 * c + j] = __ffma2_rn(x, f, acc[8 * c + j]);
-              acc[8 * c + j + 1] = __ffma2_rn(y, f, acc[8 * c + j + 1]);
-            }
-          }
-          if (COLS) {
+        for (int c = 0; c < NC / 32; ++c) {
+          tmem_wait_ld_into(r[c & 1]);
+          if (c + 1 < NC / 32) {
+            tmem_ld_32x32b_x32(from + 32 * (c + 1), r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sce0 + 8 * si);
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_acce0 + 8 * b);
           }
-          ++it;
+          const float4* cs = reinterpret_cast<const float4*>(scale + Cf::ROW_SCALES + set * NC + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
+            float2 y = make_float2(__uint_as_float(r[c & 1][2 * j + 2]), __uint_as_float(r[c & 1][2 * j + 3]));
+            if constexpr (COLS) {
+              const float4 s4 = cs[j / 2];
+              x = __fmul2_rn(x, make_float2(s4.x, s4.y));
+              y = __fmul2_rn(y, make_float2(s4.z, s4.w));
+            }
+            acc[16 * c + j] = __ffma2_rn(x, f, acc[16 * c + j]);
+            acc[16 * c + j + 1] = __ffma2_rn(y, f, acc[16 * c + j + 1]);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sce0 + 8 * b);
       }
       if (!ok) break;
       if (row0 < p.p_rows) {
