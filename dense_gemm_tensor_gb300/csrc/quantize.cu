@@ -2,10 +2,9 @@
 //
 //   s = max(max |t| over the block, 1e-12) / 448,  q = e4m3(t (1 / s)),  t = x or x^T
 //
-// Bound by HBM: x is read once, into registers or shared memory, and q written
-// once. Three kernels: blocks of 1 x 128 along x's rows (a part of a warp has a
-// block), blocks of 128 x 128 or blocks along x's columns (a thread block has a
-// 128 x 128 tile in shared memory), plain or transposed.
+// Bound by HBM: x is read once, into registers, and q written once. Two kernels:
+// blocks of 1 x 128 along x's rows (a part of a warp has a block), and tiles of
+// 128 x 128 (blocks of a whole tile, or along x's columns), plain or transposed.
 #include "elem.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -26,6 +25,7 @@ struct QuantParams {
   int rows, cols;      // of x
   int tall, transpose;
   int tiles_x;         // tiles across x's columns
+  int shares;          // thread blocks that share a group of rows
 };
 
 // The scale of a block whose largest |t| has these bits (a NaN is above every number), and its reciprocal.
@@ -38,44 +38,60 @@ __device__ __forceinline__ float block_scale(uint32_t top, float& inv) {
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// Four values to E4M3 bytes, the first lowest.
+__device__ __forceinline__ uint32_t four_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
 __device__ __forceinline__ uint8_t to_e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
 
-// Blocks along x's rows. A row's block is LANES lanes of VEC elements, 128 in all; rows by block row, blocks of a
-// row next to each other. (VEC = 4 takes any row: elements one by one where the row does not allow more.)
+// Blocks along x's rows. A row's block is LANES lanes of VEC elements, 128 in all; a warp has neighbouring rows of
+// the same block column, so that their scales, block by block, lie together; a thread block walks along its rows with
+// the next block's elements in flight. WIDE: rows in 16-byte pieces; else elements one by one.
 template <int TYPE, int VEC, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
   using E = Elem<TYPE>;
   using T = typename E::T;
   constexpr int LANES = kBlock / VEC;
-  grid_dependency_wait();
+  constexpr int ROWS = 256 / LANES;  // of a thread block
+  constexpr int PER = 16 / sizeof(T), PIECES = WIDE ? VEC / PER : 1;
+  using P = Pack<TYPE, WIDE ? PER : 1>;
   const int blocks = (p.cols + kBlock - 1) / kBlock;
-  const long long tasks = static_cast<long long>(p.rows) * blocks;
   const int lane = threadIdx.x % LANES;
-  const long long per_grid = static_cast<long long>(gridDim.x) * (256 / LANES);
-  // (whole warps go round together: the shuffles below need all lanes)
-  const long long first = static_cast<long long>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  const long long warp_first = first - (threadIdx.x % 32) / LANES;
-  for (long long t0 = warp_first, t = first; t0 < tasks; t0 += per_grid, t += per_grid) {
-    const bool in = t < tasks;
-    const long long row = in ? t / blocks : 0;
-    const int b = in ? static_cast<int>(t - row * blocks) : 0;
+  // blockIdx.x: a group of rows and a share of their blocks
+  const long long group = blockIdx.x / p.shares;
+  const int share = static_cast<int>(blockIdx.x % p.shares);
+  const int b0 = static_cast<int>(static_cast<long long>(blocks) * share / p.shares);
+  const int b1 = static_cast<int>(static_cast<long long>(blocks) * (share + 1) / p.shares);
+  const long long row = group * ROWS + threadIdx.x / LANES;
+  const bool in = row < p.rows;
+  const T* src = static_cast<const T*>(p.x) + row * p.ldx;
+  grid_dependency_wait();
+  P next[WIDE ? PIECES : VEC];
+  auto load = [&](int b) {
     const int c0 = b * kBlock + lane * VEC;
-    float v[VEC];
-    const T* src = static_cast<const T*>(p.x) + row * p.ldx + c0;
     if constexpr (WIDE) {
-      Pack<TYPE, 16 / int(sizeof(T))> w[VEC * sizeof(T) / 16];
-      constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-      for (int i = 0; i < int(VEC * sizeof(T) / 16); ++i) {
-        w[i].zero();
-        if (in && c0 + i * PER < p.cols) w[i].stream(src + i * PER);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) v[i * PER + j] = w[i].get(j);
+      for (int i = 0; i < PIECES; ++i) {
+        next[i].zero();
+        if (in && b < b1 && c0 + i * PER < p.cols) next[i].stream(src + c0 + i * PER);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = in && c0 + j < p.cols ? E::get(src[j]) : 0.0f;
+      for (int j = 0; j < VEC; ++j) {
+        next[j].zero();
+        if (in && b < b1 && c0 + j < p.cols) next[j].load(src + c0 + j);
+      }
     }
+  };
+  load(b0);
+  for (int b = b0; b < b1; ++b) {
+    float v[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = WIDE ? next[j / PER].get(j % PER) : next[WIDE ? 0 : j].get(0);
+    load(b + 1);
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) top = max(top, magnitude(v[j]));
@@ -87,20 +103,15 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
     if (lane == 0) p.scale[row * p.s_row + b * p.s_block] = scale;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] *= inv;
+    const int c0 = b * kBlock + lane * VEC;
     uint8_t* dst = p.q + row * p.ldq + c0;
     if constexpr (WIDE) {
       if (c0 < p.cols) {
         uint32_t w[VEC / 4];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
-          w[i] = lo | (hi << 16);
-        }
-        if constexpr (VEC == 16)
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        for (int i = 0; i < VEC / 4; ++i) w[i] = four_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        static_assert(VEC == 16, "a 16-byte store");
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     } else {
 #pragma unroll
@@ -111,121 +122,130 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
   grid_launch_dependents();
 }
 
-// A 128 x 128 tile of x in shared memory: blocks of the whole tile (tall) or along x's columns (transposed, not
-// tall), written as they lie or transposed. The tile's columns are one apart from a power of two, so that threads
-// walking down a column meet other banks.
+// A 128 x 128 tile of x: blocks of the whole tile (tall) or along x's columns (transposed, not tall). A thread holds
+// 8 x 8 elements in registers; the transposed q goes through shared memory, 8 rows of a column (8 bytes) at a time, in
+// an order in which 16 threads meet 16 places: piece k of column c sits at k ^ (c / 8).
 template <int TYPE, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantParams p) {
   using E = Elem<TYPE>;
   using T = typename E::T;
-  constexpr int PER = 16 / sizeof(T);
-  constexpr int LD = kBlock + 4 / int(sizeof(T)) * 1;  // a word more than the tile's row
-  extern __shared__ uint4 dynamic[];
-  T* tile = reinterpret_cast<T*>(dynamic);
-  __shared__ uint32_t tops[8];
-  __shared__ uint32_t col_top[2][kBlock];
+  constexpr int PER = WIDE ? 16 / sizeof(T) : 1, PIECES = 8 / PER;
+  using P = Pack<TYPE, PER>;
+  __shared__ uint32_t tops[16][kBlock];
   __shared__ float col_inv[kBlock];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint2 tile[kBlock][16];
+  const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
   const int r0 = static_cast<int>(blockIdx.x / p.tiles_x) * kBlock, c0 = static_cast<int>(blockIdx.x % p.tiles_x) * kBlock;
   const int nr = min(kBlock, p.rows - r0), nc = min(kBlock, p.cols - c0);
-  const T* src = static_cast<const T*>(p.x) + static_cast<long long>(r0) * p.ldx + c0;
+  const T* src = static_cast<const T*>(p.x) + static_cast<long long>(r0 + rg * 8) * p.ldx + c0 + cg * 8;
   grid_dependency_wait();
-  uint32_t top = 0;
-  if constexpr (WIDE) {
-    constexpr int PIECES = kBlock / PER;
-    for (int i = tid; i < kBlock * PIECES; i += 256) {
-      const int r = i / PIECES, c = (i % PIECES) * PER;
-      Pack<TYPE, PER> w;
-      w.zero();
-      if (r < nr && c < nc) w.stream(src + static_cast<long long>(r) * p.ldx + c);
+  P x[8][PIECES];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        tile[r * LD + c + j] = w.v[j];
-        top = max(top, magnitude(w.get(j)));
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      x[i][k].zero();
+      if (rg * 8 + i < nr && cg * 8 + k * PER < nc) x[i][k].stream(src + i * p.ldx + k * PER);
+    }
+  auto at = [&](int i, int j) { return x[i][j / PER].get(j % PER); };
+  const int rb = r0 / kBlock, cb = c0 / kBlock;
+  float inv[8];
+  if (p.tall > 1) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, magnitude(at(i, j)));
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31) == 0) tops[0][tid >> 5] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xFFFFFFFFu, tops[0][tid & 7]);
+    const float scale = block_scale(top, inv[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) inv[j] = inv[0];
+    if (tid == 0) p.scale[(p.transpose ? cb : rb) * p.s_row + (p.transpose ? rb : cb) * p.s_block] = scale;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, magnitude(at(i, j)));
+      tops[rg][cg * 8 + j] = top;
+    }
+    __syncthreads();
+    if (tid < kBlock) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, tops[i][tid]);
+      float one;
+      const float scale = block_scale(top, one);
+      col_inv[tid] = one;
+      if (tid < nc) p.scale[static_cast<long long>(c0 + tid) * p.s_row + rb * p.s_block] = scale;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) inv[j] = col_inv[cg * 8 + j];
+  }
+  if (!p.transpose) {
+    // (tall) 8 neighbouring elements of a row of q a thread
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = rg * 8 + i;
+      if (r >= nr || cg * 8 >= nc) continue;
+      uint8_t* dst = p.q + static_cast<long long>(r0 + r) * p.ldq + c0 + cg * 8;
+      if (cg * 8 + 8 <= nc && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(four_e4m3(at(i, 0) * inv[0], at(i, 1) * inv[1], at(i, 2) * inv[2], at(i, 3) * inv[3]),
+                       four_e4m3(at(i, 4) * inv[4], at(i, 5) * inv[5], at(i, 6) * inv[6], at(i, 7) * inv[7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (cg * 8 + j < nc) dst[j] = to_e4m3(at(i, j) * inv[j]);
       }
     }
   } else {
-    for (int i = tid; i < kBlock * kBlock; i += 256) {
-      const int r = i / kBlock, c = i % kBlock;
-      const T v = r < nr && c < nc ? src[static_cast<long long>(r) * p.ldx + c] : E::put(0.0f);
-      tile[r * LD + c] = v;
-      top = max(top, magnitude(E::get(v)));
-    }
-  }
-  float inv = 0.0f;
-  const int rb = r0 / kBlock, cb = c0 / kBlock;
-  if (p.tall > 1) {
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xFFFFFFFFu, tops[lane & 7]);
-    const float scale = block_scale(top, inv);
-    if (tid == 0) p.scale[(p.transpose ? cb : rb) * p.s_row + (p.transpose ? rb : cb) * p.s_block] = scale;
-  } else {
-    // a column's block: two threads a column, half the rows each
-    __syncthreads();
-    const int c = tid & (kBlock - 1), half = tid / kBlock;
-    top = 0;
-#pragma unroll 8
-    for (int r = half * (kBlock / 2); r < (half + 1) * (kBlock / 2); ++r) top = max(top, magnitude(E::get(tile[r * LD + c])));
-    col_top[half][c] = top;
-    __syncthreads();
-    if (half == 0) {
-      float one;
-      const float scale = block_scale(max(col_top[0][c], col_top[1][c]), one);
-      col_inv[c] = one;
-      if (c < nc) p.scale[static_cast<long long>(c0 + c) * p.s_row + rb * p.s_block] = scale;
-    }
-    __syncthreads();
-  }
-  // four neighbouring elements of a row of q a thread
-  const int out_rows = p.transpose ? nc : nr, out_cols = p.transpose ? nr : nc;
-  const long long q0 = static_cast<long long>(p.transpose ? c0 : r0) * p.ldq + (p.transpose ? r0 : c0);
-  for (int i = tid; i < kBlock * (kBlock / 4); i += 256) {
-    const int r = i / (kBlock / 4), c = (i % (kBlock / 4)) * 4;
-    if (r >= out_rows || c >= out_cols) continue;
-    float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = E::get(p.transpose ? tile[(c + j) * LD + r] : tile[r * LD + c + j]);
-    const float f = p.tall > 1 ? inv : col_inv[r];
+    for (int j = 0; j < 8; ++j)
+      tile[cg * 8 + j][rg ^ cg] =
+          make_uint2(four_e4m3(at(0, j) * inv[j], at(1, j) * inv[j], at(2, j) * inv[j], at(3, j) * inv[j]),
+                     four_e4m3(at(4, j) * inv[j], at(5, j) * inv[j], at(6, j) * inv[j], at(7, j) * inv[j]));
+    __syncthreads();
+    // 16 neighbouring elements of a row of q a thread, eight threads a row
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= f;
-    uint8_t* dst = p.q + q0 + static_cast<long long>(r) * p.ldq + c;
-    if (c + 4 <= out_cols && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
-      store_e4m3<4>(dst, v);
-    } else {
+    for (int k = 0; k < 4; ++k) {
+      const int c = k * 32 + (tid >> 3), r = (tid & 7) * 16;
+      if (c >= nc || r >= nr) continue;
+      const uint2 lo = tile[c][(2 * (tid & 7)) ^ (c >> 3)], hi = tile[c][(2 * (tid & 7) + 1) ^ (c >> 3)];
+      uint8_t* dst = p.q + static_cast<long long>(c0 + c) * p.ldq + r0 + r;
+      if (r + 16 <= nr && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c + j < out_cols) dst[j] = to_e4m3(v[j]);
+        for (int e = 0; e < 16; ++e)
+          if (r + e < nr) dst[e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+      }
     }
   }
   grid_launch_dependents();
 }
 
 template <int TYPE>
-cudaError_t launch_quantize(const QuantParams& p, bool wide_x, bool wide_q, int dev, int sms, cudaStream_t s) {
-  using T = typename Elem<TYPE>::T;
-  constexpr int VEC = 16;
+cudaError_t launch_quantize(QuantParams p, bool wide_x, bool wide_q, int sms, cudaStream_t s) {
   if (p.tall == 1 && !p.transpose) {
-    const int64_t tasks = int64_t(p.rows) * ((p.cols + kBlock - 1) / kBlock);
-    const int64_t per = wide_x && wide_q ? 256 / (kBlock / VEC) : 256 / (kBlock / 4);
-    const int64_t need = (tasks + per - 1) / per, most = int64_t(sms) * 8;
-    const int grid = int(need < most ? need : most);
-    return wide_x && wide_q ? launch_dependent(quantize_rows_kernel<TYPE, VEC, true>, grid, 256, 0, s, 1, p)
-                            : launch_dependent(quantize_rows_kernel<TYPE, 4, false>, grid, 256, 0, s, 1, p);
+    const bool wide = wide_x && wide_q;
+    const int rows = wide ? 256 / (kBlock / 16) : 256 / (kBlock / 4);  // of a thread block
+    const int64_t groups = (int64_t(p.rows) + rows - 1) / rows, blocks = (p.cols + kBlock - 1) / kBlock;
+    // as many thread blocks as fit the GPU at once, in equal shares of the rows' blocks
+    const int64_t want = int64_t(sms) * 8 / groups;
+    p.shares = int(want < 1 ? 1 : want < blocks ? want : blocks);
+    const int grid = int(groups * p.shares);
+    return wide ? launch_dependent(quantize_rows_kernel<TYPE, 16, true>, grid, 256, 0, s, 1, p)
+                : launch_dependent(quantize_rows_kernel<TYPE, 4, false>, grid, 256, 0, s, 1, p);
   }
   const int64_t tiles = int64_t(p.tiles_x) * ((p.rows + kBlock - 1) / kBlock);
-  constexpr size_t smem = size_t(kBlock) * (kBlock + 4 / sizeof(T)) * sizeof(T);
-  static int configured[64] = {};
-  if (smem > 48 * 1024 && (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE))) {
-    cudaError_t e = cudaFuncSetAttribute(quantize_tile_kernel<TYPE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(quantize_tile_kernel<TYPE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    if (dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
-  }
-  return wide_x ? launch_dependent(quantize_tile_kernel<TYPE, true>, int(tiles), 256, smem, s, 1, p)
-                : launch_dependent(quantize_tile_kernel<TYPE, false>, int(tiles), 256, smem, s, 1, p);
+  return wide_x ? launch_dependent(quantize_tile_kernel<TYPE, true>, int(tiles), 256, 0, s, 1, p)
+                : launch_dependent(quantize_tile_kernel<TYPE, false>, int(tiles), 256, 0, s, 1, p);
 }
 
 bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
@@ -276,10 +296,10 @@ extern "C" int gemm_quantize_blocks(int type, int64_t rows, int64_t cols, const 
   const bool wide_x = cols % (16 / es) == 0 && !misaligned(x, 16) && (rows == 1 || (ldx * es) % 16 == 0);
   const bool wide_q = cols % 16 == 0 && !misaligned(q, 16) && (rows == 1 || ldq % 16 == 0);
   QuantParams p = {x,          q,         scale,          (long long)ldx, (long long)ldq, (long long)s_row, (long long)s_block,
-                   int(rows),  int(cols), block_rows,     transpose,      int((cols + kBlock - 1) / kBlock)};
+                   int(rows),  int(cols), block_rows,     transpose,      int((cols + kBlock - 1) / kBlock), 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_quantize<GEMM_TYPE_F16>(p, wide_x, wide_q, ctx.dev, ctx.sm_count, s)
-                        : type == GEMM_TYPE_BF16 ? launch_quantize<GEMM_TYPE_BF16>(p, wide_x, wide_q, ctx.dev, ctx.sm_count, s)
-                                                 : launch_quantize<GEMM_TYPE_F32>(p, wide_x, wide_q, ctx.dev, ctx.sm_count, s);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_quantize<GEMM_TYPE_F16>(p, wide_x, wide_q, ctx.sm_count, s)
+                        : type == GEMM_TYPE_BF16 ? launch_quantize<GEMM_TYPE_BF16>(p, wide_x, wide_q, ctx.sm_count, s)
+                                                 : launch_quantize<GEMM_TYPE_F32>(p, wide_x, wide_q, ctx.sm_count, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
