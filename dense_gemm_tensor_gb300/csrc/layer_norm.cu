@@ -81,35 +81,66 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
         if (p.h != nullptr) r.store(h[i], p.h, row, p.ldh, i, in);
       }
     }
+    // (two elements to an instruction where a piece has two)
     float s = 0.0f;
+    float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (VEC > 1) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s += h[i].get(j);
-    const float mean = row_warps.sum(s, red[turn][0]) / static_cast<float>(p.cols);
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = column(r, i, j) ? h[i].get(j) - mean : 0.0f;
-        s = fmaf(d, d, s);
+        for (int j = 0; j < VEC; j += 2) s2 = __fadd2_rn(s2, h[i].two(j));
+      } else {
+        s += h[i].get(0);
       }
-    const float rstd = 1.0f / sqrtf(row_warps.sum(s, red[turn][1]) / static_cast<float>(p.cols) + p.eps);
+    }
+    const float mean = row_warps.sum(s + (s2.x + s2.y), red[turn][0]) / static_cast<float>(p.cols);
+    const float2 less = make_float2(-mean, -mean);
+    s = 0.0f;
+    s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (MODE == ALIGNED) {
+        if (r.whole(i)) {
+#pragma unroll
+          for (int j = 0; j < VEC; j += 2) {
+            const float2 d = __fadd2_rn(h[i].two(j), less);
+            s2 = __ffma2_rn(d, d, s2);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float d = column(r, i, j) ? h[i].get(j) - mean : 0.0f;
+          s = fmaf(d, d, s);
+        }
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_warps.sum(s + (s2.x + s2.y), red[turn][1]) / static_cast<float>(p.cols) + p.eps);
+    const float2 by = make_float2(rstd, rstd);
     if (in && r.tid == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
     // the output of piece i, before its rounding
-    auto norm = [&](float(&w)[VEC], int i) {
+    auto norm = [&](float* y, int i) {
+      float w[VEC], b[VEC];
       load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) w[j] = (h[i].get(j) - mean) * rstd * w[j];
       if (p.bias != nullptr) {
-        float b[VEC];
         load_weights<MODE, TYPE, VEC>(b, r, p.bias, shared_b, i);
+      } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] += b[j];
+        for (int j = 0; j < VEC; ++j) b[j] = 0.0f;
+      }
+      if constexpr (VEC > 1) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 xhat = __fmul2_rn(__fadd2_rn(h[i].two(j), less), by);
+          const float2 v = __ffma2_rn(xhat, make_float2(w[j], w[j + 1]), make_float2(b[j], b[j + 1]));
+          y[j] = v.x;
+          y[j + 1] = v.y;
+        }
+      } else {
+        y[0] = fmaf((h[i].get(0) - mean) * rstd, w[0], b[0]);
       }
     };
     if constexpr (!Q8) {
@@ -122,15 +153,16 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
         r.store(o, p.y, row, p.ldy, i, in);
       }
     } else {
-      // |y| compared by bit pattern: a NaN is above every number and reaches the scale
+      // the row's outputs take the registers of h. |y| is compared by bit pattern: a NaN is above every number and
+      // reaches the scale
+      float y[EPT];
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float y[VEC];
-        norm(y, i);
+        norm(y + i * VEC, i);
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-          if (column(r, i, j)) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+          if (column(r, i, j)) top = max(top, __float_as_uint(y[i * VEC + j]) & 0x7FFFFFFFu);
       }
       const float amax = __uint_as_float(row_warps.max_bits(top, red[turn][2]));
       const float scale = (amax < 1e-12f ? 1e-12f : amax) / kE4M3Max;
@@ -138,11 +170,10 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
       if (in && r.tid == 0) p.scale[row] = scale;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float y[VEC];
-        norm(y, i);
+        float q[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) y[j] *= inv;
-        r.store_q8(y, p.y, row, p.ldy, i, in);
+        for (int j = 0; j < VEC; ++j) q[j] = y[i * VEC + j] * inv;
+        r.store_q8(q, p.y, row, p.ldy, i, in);
       }
     }
   }
@@ -164,16 +195,25 @@ struct LayerGradParams {
   int rows, cols, tpr;
 };
 
-// Two sums over a row's warps at once: one barrier for both.
+// Two sums over a row's warps at once, with one barrier. After the first exchange the lower half of a warp adds up
+// the first sum and the upper half the second, so that both take the steps of one.
 __device__ __forceinline__ float2 sum_two(const RowWarps& w, float2 v, float2* red) {
-  v.x = warp_sum(v.x);
-  v.y = warp_sum(v.y);
-  if (w.warps == 1) return v;
   const int lane = threadIdx.x & 31;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < w.warps ? red[w.w0 + lane] : make_float2(0.0f, 0.0f);
-  return make_float2(warp_sum(v.x), warp_sum(v.y));
+  const bool up = lane & 16;
+  auto fold = [&](float2 t) {
+    float s = (up ? t.y : t.x) + __shfl_xor_sync(0xFFFFFFFFu, up ? t.x : t.y, 16);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    return s;
+  };
+  float s = fold(v);
+  if (w.warps > 1) {
+    float* r = reinterpret_cast<float*>(red);
+    if ((lane & 15) == 0) r[2 * (threadIdx.x >> 5) + (lane >> 4)] = s;
+    __syncthreads();
+    s = fold(lane < w.warps ? red[w.w0 + lane] : make_float2(0.0f, 0.0f));
+  }
+  return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
 }
 
 // A thread owns the same columns of every row (ALIGNED, SINGLE) and adds dw and db
@@ -183,10 +223,9 @@ __device__ __forceinline__ float2 sum_two(const RowWarps& w, float2 v, float2* r
 // own places in shared memory (cp.async) before it works on this one, so that
 // loads are in flight during the reduction and the stores, and reads a piece from
 // its place once for the sums and once for the output, so that registers hold one
-// piece at a time beside the 32 sums. THREADS: what the block has at most; up to
-// 512 leave a thread 128 registers, and the sums stay in them.
-template <int TYPE, int MODE, bool AHEAD, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) layernorm_grad_kernel(const LayerGradParams p) {
+// piece at a time beside the 32 sums.
+template <int TYPE, int MODE, bool AHEAD>
+__global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_kernel(const LayerGradParams p) {
   constexpr int EPT = kGradEpt;
   using T = typename Elem<TYPE>::T;
   constexpr int VEC = MODE == SINGLE ? 1 : 16 / sizeof(T);
@@ -235,7 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_grad_kernel(const LayerG
   };
   float2 next = AHEAD ? statistics(start) : make_float2(0.0f, 0.0f);
   constexpr int SUMS = MODE == FLAT ? 1 : EPT;
-  float dw[SUMS], db[SUMS];
+  alignas(8) float dw[SUMS], db[SUMS];
   if constexpr (MODE == FLAT) {
     for (int i = threadIdx.x; i < 2 * per_block * places; i += blockDim.x) sums[i] = 0.0f;
     stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
@@ -275,33 +314,49 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_grad_kernel(const LayerG
     auto take = [&](P(&v)[NV], int m, int i) {
       if constexpr (AHEAD) v[i].load(reinterpret_cast<const T*>(cell(turn, m, i)));
     };
-    // sums of g and of g xhat (outside the row dy is 0, and so is what is added)
-    float2 dots = make_float2(0.0f, 0.0f);
+    // sums of g and of g xhat (outside the row dy is 0, and so is what is added); ALIGNED takes two elements to an
+    // instruction
+    float2 dots = make_float2(0.0f, 0.0f), gs = dots, gx = dots;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float w[VEC];
       load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
       take(h, 0, i);
       take(dy, 1, i);
+      if constexpr (MODE == ALIGNED) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float xhat = (h[i].get(j) - mean) * rstd, d = dy[i].get(j), g = d * w[j];
-        if constexpr (MODE == FLAT) {
-          if (in && column(r, i, j)) {
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 xhat = __fmul2_rn(__fadd2_rn(h[i].two(j), make_float2(-mean, -mean)), make_float2(rstd, rstd));
+          const float2 d = dy[i].two(j), g = __fmul2_rn(d, make_float2(w[j], w[j + 1]));
+          gs = __fadd2_rn(gs, g);
+          gx = __ffma2_rn(g, xhat, gx);
+          float2& sw = *reinterpret_cast<float2*>(dw + i * VEC + j);
+          float2& sb = *reinterpret_cast<float2*>(db + i * VEC + j);
+          sw = __ffma2_rn(d, xhat, sw);
+          sb = __fadd2_rn(sb, d);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float xhat = (h[i].get(j) - mean) * rstd, d = dy[i].get(j), g = d * w[j];
+          if constexpr (MODE == FLAT) {
+            if (in && column(r, i, j)) {
+              dots.x += g;
+              dots.y = fmaf(g, xhat, dots.y);
+              float* at = sums + 2 * sub * places + r.place(i, j);
+              at[0] += d * xhat;
+              at[places] += d;
+            }
+          } else {
             dots.x += g;
             dots.y = fmaf(g, xhat, dots.y);
-            float* at = sums + 2 * sub * places + r.place(i, j);
-            at[0] += d * xhat;
-            at[places] += d;
+            dw[i * VEC + j] = fmaf(d, xhat, dw[i * VEC + j]);
+            db[i * VEC + j] += d;
           }
-        } else {
-          dots.x += g;
-          dots.y = fmaf(g, xhat, dots.y);
-          dw[i * VEC + j] = fmaf(d, xhat, dw[i * VEC + j]);
-          db[i * VEC + j] += d;
         }
       }
     }
+    if constexpr (MODE == ALIGNED) dots = make_float2(gs.x + gs.y, gx.x + gx.y);
     dots = sum_two(row_warps, dots, red[turn]);
     const float mean_g = dots.x / static_cast<float>(p.cols), back = rstd * (dots.y / static_cast<float>(p.cols));
     if (MODE == FLAT && p.tpr <= 32) __syncwarp();
@@ -313,9 +368,20 @@ __global__ void __launch_bounds__(THREADS, 1) layernorm_grad_kernel(const LayerG
       take(dy, 1, i);
       take(dh, 2, i);
       P o;
+      if constexpr (MODE == ALIGNED) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        w[j] = fmaf(fmaf(dy[i].get(j), w[j], -mean_g), rstd, fmaf((h[i].get(j) - mean) * rstd, -back, dh[i].get(j)));
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 xhat = __fmul2_rn(__fadd2_rn(h[i].two(j), make_float2(-mean, -mean)), make_float2(rstd, rstd));
+          const float2 g = __ffma2_rn(dy[i].two(j), make_float2(w[j], w[j + 1]), make_float2(-mean_g, -mean_g));
+          const float2 v = __ffma2_rn(g, make_float2(rstd, rstd), __ffma2_rn(xhat, make_float2(-back, -back), dh[i].two(j)));
+          w[j] = v.x;
+          w[j + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          w[j] = fmaf(fmaf(dy[i].get(j), w[j], -mean_g), rstd, fmaf((h[i].get(j) - mean) * rstd, -back, dh[i].get(j)));
+      }
       o.set(w);
       r.store(o, p.dx, row, p.lddx, i, in);
     }
@@ -403,9 +469,16 @@ __global__ void __launch_bounds__(1024) layer_weight_sum_kernel(const float* par
   grid_launch_dependents();
 }
 
-// Blocks of the gradient, at most: each leaves two partial rows. (Numbers, since
-// the size of the workspace goes by them, on a machine without a GPU too.)
-int grad_blocks(int64_t cols) { return cols <= 2048 ? 608 : 304; }
+// Blocks of the gradient, at most: what an SM holds at 64 registers a thread, for each of a GB300's 152 (a number,
+// since the size of the workspace goes by it, on a machine without a GPU too). BF16 with dh, 304 / 456 / 608 blocks, us:
+// 4097 x 5120 (320 threads) 46.4 / 45.1 / 51.8, 8192 x 4096 (256) 77.7 / 64.0 / 59.4, 8192 x 8192 (512) 108 / 127 / 118,
+// 30000 x 1024 68.5 / 56.7 / 52.9. (One block an SM with as many rows side by side, each with a barrier of its own, and
+// so a third of the partial rows: 45.5, 60.6, 114, 57.7.)
+constexpr int kGradThreads = 256;  // of a block, at least
+int64_t grad_blocks(int64_t cols) {
+  const int tpr = threads_per_row(cols, kGradEpt, ALIGNED, 8), fit = 1024 / (tpr < kGradThreads ? kGradThreads : tpr);
+  return int64_t(152) * (fit < 1 ? 1 : fit);
+}
 
 template <int TYPE, int MODE, int EPT>
 cudaError_t launch_layer_mode(const LayerParams& p, bool q8, int grid, int block, size_t smem, cudaStream_t s) {
@@ -444,11 +517,11 @@ constexpr size_t kGradSmem = 200 * 1024;
 
 // Launches one build of the gradient's kernel. Its limit is a property of the kernel, not of the launch, so it is set
 // once, to the most that any launch takes: other host threads may be launching it with other sizes.
-template <int TYPE, int MODE, bool AHEAD, int THREADS>
+template <int TYPE, int MODE, bool AHEAD>
 cudaError_t launch_layer_grad_mode(const LayerGradParams& p, int dev, int grid, int block, size_t smem,
                                    cudaStream_t s) {
   static int configured[64] = {};
-  auto kern = layernorm_grad_kernel<TYPE, MODE, AHEAD, THREADS>;
+  auto kern = layernorm_grad_kernel<TYPE, MODE, AHEAD>;
   if (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGradSmem));
     if (e != cudaSuccess) return e;
@@ -457,22 +530,15 @@ cudaError_t launch_layer_grad_mode(const LayerGradParams& p, int dev, int grid, 
   return launch_dependent(kern, grid, block, smem, s, 1, p);
 }
 
-template <int TYPE, int THREADS>
-cudaError_t launch_layer_grad_threads(const LayerGradParams& p, int mode, bool ahead, int dev, int grid, int block,
-                                      cudaStream_t s) {
-  const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
-  if (mode == ALIGNED)
-    return ahead ? launch_layer_grad_mode<TYPE, ALIGNED, true, THREADS>(p, dev, grid, block, smem, s)
-                 : launch_layer_grad_mode<TYPE, ALIGNED, false, THREADS>(p, dev, grid, block, smem, s);
-  return mode == FLAT ? launch_layer_grad_mode<TYPE, FLAT, false, THREADS>(p, dev, grid, block, smem, s)
-                      : launch_layer_grad_mode<TYPE, SINGLE, false, THREADS>(p, dev, grid, block, smem, s);
-}
-
 template <int TYPE>
 cudaError_t launch_layer_grad(const LayerGradParams& p, int mode, bool ahead, int dev, int grid, int block, void* dw,
                               void* db, cudaStream_t s) {
-  const cudaError_t e = block <= 512 ? launch_layer_grad_threads<TYPE, 512>(p, mode, ahead, dev, grid, block, s)
-                                     : launch_layer_grad_threads<TYPE, 1024>(p, mode, ahead, dev, grid, block, s);
+  const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
+  const cudaError_t e = mode == ALIGNED
+                            ? (ahead ? launch_layer_grad_mode<TYPE, ALIGNED, true>(p, dev, grid, block, smem, s)
+                                     : launch_layer_grad_mode<TYPE, ALIGNED, false>(p, dev, grid, block, smem, s))
+                        : mode == FLAT ? launch_layer_grad_mode<TYPE, FLAT, false>(p, dev, grid, block, smem, s)
+                                       : launch_layer_grad_mode<TYPE, SINGLE, false>(p, dev, grid, block, smem, s);
   if (e != cudaSuccess) return e;
   return launch_dependent(layer_weight_sum_kernel<TYPE>, (2 * p.cols + 31) / 32, 1024, 0, s, 1, p.partial, grid, p.cols,
                           dw, db);
@@ -615,7 +681,7 @@ int gemm_layernorm_backward(int type, int64_t rows, int64_t cols, const void* dy
   LayerGradParams p = {dy,   h,      weight, mean, rstd, dh, dx, static_cast<float*>(workspace), (long long)lddy,
                        (long long)ldh, (long long)lddh, (long long)lddx, int(rows), int(cols), 0};
   p.tpr = threads_per_row(cols, kGradEpt, mode, v);
-  const int block = p.tpr >= 256 ? p.tpr : 256 / p.tpr * p.tpr;
+  const int block = p.tpr >= kGradThreads ? p.tpr : kGradThreads / p.tpr * p.tpr;
   const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= kGradSmem;
   const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
   const int grid = int(need < grad_blocks(cols) ? need : grad_blocks(cols));
