@@ -1,23 +1,28 @@
 // Products of E4M3 matrices with a scale for each block of 128 along K
-// (gemm_e4m3_blocks), for sm_103a.
+// (gemm_e4m3_blocks), for sm_103a: what its kernels share, and the one for few rows.
 //
 //   C[i][j] = sum over blocks b of sa[i][b] sb[j][b] (sum over k of block b of A[i][k] B[j][k])
 //
 // A stage of the pipeline is one block (128 bytes of K), so the tensor cores sum a
 // block into an accumulator of its own in tensor memory, and the epilogue warps
 // take it from there, scale it and add it to the tile's sums, which they hold in
-// registers. Warps: 0-3 epilogue, 4 TMA producer, 5 tcgen05.mma, 6 the column
-// scales (through a ring in shared memory).
+// registers.
 //
-// One CTA computes 128 rows of a "row operand" P against BN rows of a "column
-// operand" Q. With many rows P is A and Q is B; with few (SWAP) P is B, so that
-// 128 lanes are 128 columns of C and a narrow tile wastes nothing. Where the tiles
-// do not fill the GPU a cluster of `splits` CTAs shares a tile: each takes a run of
-// blocks, and they add their sums through distributed shared memory, in order.
+// Few rows of A are bound by reading B. So B is the MMA's 128-row operand P, and A
+// the narrow one Q (BN = 16, 32 or 64 of its rows): 128 lanes are 128 columns of C,
+// and a narrow tile wastes nothing on rows that are not there. A tile's blocks are
+// shared by a cluster of `splits` CTAs, and those add their sums through
+// distributed shared memory, in order. Warps: 0-3 epilogue, 4 TMA producer, 5
+// tcgen05.mma, 6 the scales of A's rows, 7 those of B's; these run up to
+// kScaleRing blocks ahead (loaded as they were needed, four blocks at a time, each
+// four cost a trip to memory).
 #pragma once
+
+#include <type_traits>
 
 #include "dgt_feedforward.h"
 #include "gemm_kernel.cuh"
+#include "split_join.cuh"
 
 namespace dgt {
 
@@ -39,7 +44,7 @@ struct BlockParams {
 };
 
 constexpr int kBlockThreads = 256;
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 16;
 
 template <int BN_>
 struct BlockCfg {
@@ -48,46 +53,22 @@ struct BlockCfg {
   static constexpr int P_BYTES = BM * 128;
   static constexpr int Q_BYTES = BN * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = BN >= 128 ? 3 : 5;  // two CTAs to an SM
-  static constexpr int ACCS = BN >= 128 ? 2 : 4;    // accumulators in tensor memory
-  static constexpr int TMEM_COLS = ACCS * BN < 64 ? 64 : ACCS * BN;
-  static constexpr int SUM_LD = BM + 1;             // a column of the shared sums (free of bank conflicts either way)
-  static constexpr int SCALE_BYTES = kScaleRing * BN * 4;
-  static constexpr int BAR_BYTES = 256;
+  static constexpr int SCALE_BYTES = kScaleRing * (BN + BM) * 4;
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int SMEM_LIMIT = 113 * 1024;  // two CTAs to an SM
+  static constexpr int STAGES = (SMEM_LIMIT - 1024 - SCALE_BYTES - BAR_BYTES) / STAGE_BYTES;
+  static constexpr int ACCS = 4;                 // accumulators in tensor memory
+  static constexpr int TMEM_COLS = ACCS * BN;
+  static constexpr int SUM_LD = BM + 1;          // a column of the shared sums (free of bank conflicts either way)
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SCALE_BYTES + BAR_BYTES;
-  static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "tile width");
+  static_assert(BN == 16 || BN == 32 || BN == 64, "tile width");
   static_assert(BN * SUM_LD * 4 <= STAGES * STAGE_BYTES, "the sums reuse the stages");
   static_assert((2 * STAGES + 2 * ACCS + 1 + 2 * kScaleRing) * 8 + 16 <= BAR_BYTES, "barrier area");
   // D fp32, E4M3 operands, both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
 };
 
-// Loads BN_ (16 or 32) columns of the warp's 32 accumulator rows.
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 32) {
-    tmem_ld_32x32b_x32(taddr, r);
-    tmem_wait_ld_into(r);
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-  }
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-// COLS: the column operand has a scale for each row of it, else one for the tile (its 128 rows' block).
-template <int BN, bool COLS, bool SWAP>
+template <int BN>
 __global__ void __launch_bounds__(kBlockThreads)
     block_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                  const __grid_constant__ BlockParams p) {
@@ -135,7 +116,7 @@ __global__ void __launch_bounds__(kBlockThreads)
       mbar_init(acce0 + 8 * b, 4);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(scf0 + 8 * i, 1);
+      mbar_init(scf0 + 8 * i, 2);
       mbar_init(sce0 + 8 * i, 4);
     }
     mbar_init(drain_bar, 1);
@@ -162,7 +143,7 @@ __global__ void __launch_bounds__(kBlockThreads)
       int it = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const int s = it % S;
-        if (!warp_wait_phase(p.g, empty0 + 8 * s, ((it / S) & 1) ^ 1, ROLE_PRODUCER | (s << 8))) break;
+        if (!warp_wait_short(p.g, empty0 + 8 * s, ((it / S) & 1) ^ 1, ROLE_PRODUCER | (s << 8))) break;
         if (elect_one()) {
           const uint32_t fb = full0 + 8 * s;
           mbar_arrive_expect_tx(fb, Cf::STAGE_BYTES);
@@ -173,14 +154,15 @@ __global__ void __launch_bounds__(kBlockThreads)
       }
       if (lane == 0) *issued_slot = it;
     }
+    grid_launch_dependents();
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA issuer
     const uint64_t p_desc = sdesc(sP, 16, 1024, SWZ_128B), q_desc = sdesc(sQ, 16, 1024, SWZ_128B);
     int it = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
       const int s = it % S, b = it % Cf::ACCS;
-      if (!warp_wait_phase(p.g, acce0 + 8 * b, ((it / Cf::ACCS) & 1) ^ 1, ROLE_MMA | (0x80u << 8))) break;
-      if (!warp_wait_phase(p.g, full0 + 8 * s, (it / S) & 1, ROLE_MMA | (s << 8))) break;
+      if (!warp_wait_short(p.g, acce0 + 8 * b, ((it / Cf::ACCS) & 1) ^ 1, ROLE_MMA | (0x80u << 8))) break;
+      if (!warp_wait_short(p.g, full0 + 8 * s, (it / S) & 1, ROLE_MMA | (s << 8))) break;
       tc_fence_after();
       const uint64_t ps = p_desc + static_cast<uint32_t>(s) * (Cf::P_BYTES / 16);
       const uint64_t qs = q_desc + static_cast<uint32_t>(s) * (Cf::Q_BYTES / 16);
@@ -198,107 +180,110 @@ __global__ void __launch_bounds__(kBlockThreads)
     __syncwarp();
     if (lane == 0) wait_phase_drain(p.g, drain_bar, 0);
     __syncwarp();
-  } else if (warp == 6) {
-    // ---------------------------------------------------------------- column scales
-    if constexpr (COLS) {
-      // four blocks' scales ahead in registers, a lane has columns lane, lane + 32, ...
-      constexpr int PER = (BN + 31) / 32;
-      float next[kScaleRing][PER];
-      auto load = [&](int kb) {
+  } else if (warp >= 6) {
+    // ---------------------------------------------------------------- scales: of A's rows (warp 6), of B's (warp 7)
+    int it = 0;
+    // hands the scales of the next block over: entries lane, lane + 32, ... of n
+    auto put = [&](int at, int n, auto value) {
+      const int slot = it % kScaleRing;
+      if (!warp_wait_short(p.g, sce0 + 8 * slot, ((it / kScaleRing) & 1) ^ 1, ROLE_COPY | (slot << 8))) return false;
+      float* to = scales + slot * (BN + Cf::BM) + at;
 #pragma unroll
-        for (int i = 0; i < kScaleRing; ++i)
+      for (int j = 0; j < Cf::BM / 32; ++j)
+        if (lane + 32 * j < n) to[lane + 32 * j] = value(j);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(scf0 + 8 * slot);
+      ++it;
+      return true;
+    };
+    // `per` entries a lane, AHEAD blocks ahead in registers
+    auto stream = [&](const BlockScales& from, int first, int rows, int at, auto per_, auto ahead_) {
+      constexpr int PER = decltype(per_)::value, AHEAD = decltype(ahead_)::value;
+      const float* src[PER];
 #pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const int c = lane + 32 * j;
-            next[i][j] = kb + i < kb1 && c < BN && q0 + c < p.q_rows ? p.qs.at(q0 + c, kb + i) : 0.0f;
+      for (int j = 0; j < PER; ++j) src[j] = from.s + min(first + lane + 32 * j, rows - 1) * from.row + kb0 * from.block;
+      float next[AHEAD][PER];
+      int loaded = kb0;
+      auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (loaded + i < kb1) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+              next[i][j] = __ldg(src[j]);
+              src[j] += from.block;
+            }
           }
+        loaded += AHEAD;
       };
-      load(kb0);
-      bool ok = true;
-      for (int kb = kb0, round = 0; ok && kb < kb1; kb += kScaleRing, ++round) {
-        float now[kScaleRing][PER];
+      load();
+      for (int kb = kb0; kb < kb1; kb += AHEAD) {
+        float now[AHEAD][PER];
 #pragma unroll
-        for (int i = 0; i < kScaleRing; ++i)
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
           for (int j = 0; j < PER; ++j) now[i][j] = next[i][j];
-        load(kb + kScaleRing);
+        load();
 #pragma unroll
-        for (int i = 0; i < kScaleRing; ++i) {
-          if (!ok || kb + i >= kb1) break;
-          ok = warp_wait_phase(p.g, sce0 + 8 * i, (round & 1) ^ 1, ROLE_COPY | (i << 8));
-          if (!ok) break;
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (lane + 32 * j < BN) scales[i * BN + lane + 32 * j] = now[i][j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scf0 + 8 * i);
+        for (int i = 0; i < AHEAD; ++i)
+          if (kb + i < kb1 && !put(at, at == 0 ? BN : Cf::BM, [&](int j) { return now[i][j < PER ? j : 0]; })) return;
+      }
+    };
+    using std::integral_constant;
+    if (warp == 6) {
+      stream(p.qs, q0, p.q_rows, 0, integral_constant<int, BN == 64 ? 2 : 1>(), integral_constant<int, 8>());
+    } else if (p.ps.shift == 0) {
+      stream(p.ps, p0, p.p_rows, BN, integral_constant<int, 4>(), integral_constant<int, 4>());
+    } else {
+      // one scale for the tile's 128 rows: a lane has a block's
+      auto load = [&](int kb) { return kb + lane < kb1 ? p.ps.at(p0, kb + lane) : 0.0f; };
+      float next = load(kb0);
+      bool ok = true;
+      for (int kb = kb0; ok && kb < kb1; kb += 32) {
+        const float now = next;
+        next = load(kb + 32);
+        for (int i = 0; ok && i < 32 && kb + i < kb1; ++i) {
+          const float f = __shfl_sync(0xFFFFFFFFu, now, i);
+          ok = put(BN, Cf::BM, [&](int) { return f; });
         }
       }
     }
-  } else if (warp < 4) {
+  } else {
     // ---------------------------------------------------------------- epilogue: lane = row of P
-    const int row = p0 + warp * 32 + lane;
-    const int srow = min(row, p.p_rows - 1);
     constexpr int CH = BN < 32 ? BN : 32;
     float acc[BN];
 #pragma unroll
     for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
-    float next[4];
-    auto load = [&](int kb) {
+    int it = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int b = it % Cf::ACCS, slot = it % kScaleRing;
+      if (!warp_wait_short(p.g, scf0 + 8 * slot, (it / kScaleRing) & 1, ROLE_EPILOGUE | (0x90u << 8))) break;
+      if (!warp_wait_short(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8))) break;
+      tc_fence_after();
+      const float* scale = scales + slot * (BN + Cf::BM);
+      const float f = scale[BN + warp * 32 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        next[i] = kb + i < kb1 ? p.ps.at(srow, kb + i) : 0.0f;
-        if (!COLS && kb + i < kb1) next[i] *= p.qs.at(q0, kb + i);
-      }
-    };
-    load(kb0);
-    bool ok = true;
-    for (int kb = kb0; ok && kb < kb1; kb += 4) {
-      float now[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) now[i] = next[i];
-      load(kb + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kb + i >= kb1) break;
-        const int it = kb + i - kb0, b = it % Cf::ACCS;
-        if (COLS) {
-          ok = warp_wait_phase(p.g, scf0 + 8 * i, (it / kScaleRing) & 1, ROLE_EPILOGUE | (0x90u << 8));
-          if (!ok) break;
-        }
-        ok = warp_wait_phase(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8));
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < BN; c += CH) {
-          uint32_t r[CH];
+      for (int c = 0; c < BN; c += CH) {
+        uint32_t r[CH];
+        __syncwarp();
+        tmem_ld_cols<CH>(tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * BN + c, r);
+        if (c + CH == BN) {
+          tc_fence_before();
           __syncwarp();
-          tmem_ld_cols<CH>(tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * BN + c, r);
-          if (c + CH == BN) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acce0 + 8 * b);
-          }
-          if constexpr (COLS) {
-            const float4* cs = reinterpret_cast<const float4*>(scales + i * BN + c);
-#pragma unroll
-            for (int j = 0; j < CH; j += 4) {
-              const float4 f = cs[j / 4];
-              acc[c + j] = fmaf(__uint_as_float(r[j]) * f.x, now[i], acc[c + j]);
-              acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]) * f.y, now[i], acc[c + j + 1]);
-              acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]) * f.z, now[i], acc[c + j + 2]);
-              acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]) * f.w, now[i], acc[c + j + 3]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < CH; ++j) acc[c + j] = fmaf(__uint_as_float(r[j]), now[i], acc[c + j]);
-          }
+          if (lane == 0) mbar_arrive(acce0 + 8 * b);
         }
-        if (COLS) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sce0 + 8 * i);
+        const float4* cs = reinterpret_cast<const float4*>(scale + c);
+#pragma unroll
+        for (int j = 0; j < CH; j += 4) {
+          const float4 s4 = cs[j / 4];
+          acc[c + j] = fmaf(__uint_as_float(r[j]) * s4.x, f, acc[c + j]);
+          acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]) * s4.y, f, acc[c + j + 1]);
+          acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]) * s4.z, f, acc[c + j + 2]);
+          acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]) * s4.w, f, acc[c + j + 3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sce0 + 8 * slot);
     }
     // every MMA has read its stages (the last accumulator was waited for): the sums take their place
 #pragma unroll
@@ -313,27 +298,15 @@ __global__ void __launch_bounds__(kBlockThreads)
   else
     __syncthreads();
   {
-    // this CTA's share: columns of the tile (SWAP: C's rows), or rows of it
-    const uint32_t local = smem_u32(sums);
-    const int outer = SWAP ? BN : Cf::BM, inner = SWAP ? Cf::BM : BN;
-    const int o0 = outer * split / p.splits, o1 = outer * (split + 1) / p.splits;
-    for (int e = threadIdx.x; e < (o1 - o0) * inner; e += kBlockThreads) {
-      const int o = o0 + e / inner, i = e % inner;
-      const int r = SWAP ? i : o, c = SWAP ? o : i;
+    // this CTA's share of the tile's rows of C
+    const int o0 = BN * split / p.splits, o1 = BN * (split + 1) / p.splits;
+    for (int e = threadIdx.x; e < (o1 - o0) * Cf::BM; e += kBlockThreads) {
+      const int c = o0 + e / Cf::BM, r = e % Cf::BM;
       if (p0 + r >= p.p_rows || q0 + c >= p.q_rows) continue;
-      const uint32_t at = static_cast<uint32_t>((c * Cf::SUM_LD + r) * 4);
-      float v;
-      if (p.splits == 1) {
-        v = sums[c * Cf::SUM_LD + r];
-      } else {
-        v = 0.0f;
-        for (int z = 0; z < p.splits; ++z) v += ld_cluster_f32(mapa_shared(local + at, z));
-      }
-      const long long crow = SWAP ? q0 + c : p0 + r, ccol = SWAP ? p0 + r : q0 + c;
-      static_cast<__nv_bfloat16*>(p.g.C)[crow * p.g.ldc + ccol] = __float2bfloat16_rn(v);
+      const float v = joined_sum(sums, c * Cf::SUM_LD + r, p.splits);
+      static_cast<__nv_bfloat16*>(p.g.C)[static_cast<long long>(q0 + c) * p.g.ldc + p0 + r] = __float2bfloat16_rn(v);
     }
   }
-  grid_launch_dependents();
 
   // ------------------------------------------------------------------ teardown
   // loads issued but not consumed exist only when the launch was aborted: let them land

@@ -22,11 +22,11 @@ Range range_of(const void* p, int64_t elems, int es) {
 bool meet(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // Sets the kernel's dynamic shared-memory limit once per device, then launches.
-template <int BN, bool COLS, bool SWAP>
+template <int BN>
 cudaError_t launch_block(const BlockLaunch& L) {
   using Cf = BlockCfg<BN>;
   static int configured[64] = {};
-  auto kern = block_kernel<BN, COLS, SWAP>;
+  auto kern = block_kernel<BN>;
   if (L.dev >= 64 || !__atomic_load_n(&configured[L.dev], __ATOMIC_ACQUIRE)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -35,12 +35,19 @@ cudaError_t launch_block(const BlockLaunch& L) {
   return launch_dependent(kern, L.grid, kBlockThreads, Cf::SMEM_BYTES, L.stream, L.p.splits, L.tmP, L.tmQ, L.p);
 }
 
-// Columns of a CTA pair's tile, or 0 for single CTAs: the widest whose tiles give most pairs one.
-int pair_width(int64_t M, int64_t N, int sms) {
+constexpr int kFewRows = 64;  // up to here always the kernel for few rows
+
+// Columns of a CTA pair's tile, or 0 for the kernel for few rows. Up to 64 rows, and where the tiles are so few that
+// eight CTAs can share each and have work enough: us with it / with pairs, K = 4096: 65 x 512 6.4 / 10.6, 65 x 2048
+// 8.7 / 10.7, 512 x 512 9.4 / 10.9, 1024 x 512 (beyond the limit) 12.0 / 11.2, 512 x 2048 18.0 / 13.5; K = 1024: 65 x
+// 512 6.2 / 5.0. A pair's 256-wide tile takes about one and a half times a 128-wide one's time: 512 x 4096 x 4096
+// (one round of either) 17.3 / 14.0 us, 1024 x 8192 x 4096 (two rounds or four) 32.3 / 37.9.
+int pair_width(int64_t M, int64_t N, int64_t blocks, int sms) {
+  const int64_t few = (M + 63) / 64 * ((N + 127) / 128);
+  if (M <= kFewRows || (blocks >= 16 && few * 8 <= 2 * sms)) return 0;
   const int64_t rows = (M + 255) / 256, units = sms / 2;
-  for (int bn : {256, 128})
-    if (rows * ((N + bn - 1) / bn) * 4 >= units * 3) return bn;
-  return 0;
+  const int64_t wide = (rows * ((N + 255) / 256) + units - 1) / units, narrow = (rows * ((N + 127) / 128) + units - 1) / units;
+  return wide * 3 <= narrow * 2 ? 256 : 128;
 }
 
 }  // namespace
@@ -85,7 +92,8 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
   // (the pitch of a matrix of one row says nothing)
   if (M == 1) lda = (K + 15) / 16 * 16;
   if (N == 1) ldb = (K + 15) / 16 * 16;
-  const bool swap = M <= 64;
+  const int pair_bn = pair_width(M, N, blocks, ctx.sm_count);
+  const bool few = pair_bn == 0;
   BlockLaunch L;
   memset(&L, 0, sizeof(L));
   BlockParams& p = L.p;
@@ -98,21 +106,20 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
   p.g.num_kb = int(blocks);
   p.g.raster = 8;
   const BlockScales sa = {a_scale, as_row, as_block, 0}, sb = {b_scale, bs_row, bs_block, b_rows == 1 ? 0 : 7};
-  p.ps = swap ? sb : sa;
-  p.qs = swap ? sa : sb;
-  p.p_rows = int(swap ? N : M);
-  p.q_rows = int(swap ? M : N);
+  p.ps = few ? sb : sa;
+  p.qs = few ? sa : sb;
+  p.p_rows = int(few ? N : M);
+  p.q_rows = int(few ? M : N);
   L.dev = ctx.dev;
   L.stream = s;
-  const int pair_bn = swap ? 0 : pair_width(M, N, ctx.sm_count);
-  const int bn = pair_bn > 0 ? pair_bn : !swap ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int bn = pair_bn > 0 ? pair_bn : !few ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
   const int bm = pair_bn > 0 ? 256 : 128;
   p.g.tiles_m = (p.p_rows + bm - 1) / bm;
   p.g.tiles_n = (p.q_rows + bn - 1) / bn;
   const int64_t tiles = int64_t(p.g.tiles_m) * p.g.tiles_n;
   if (tiles > kIntLimit / 8) return GEMM_ERR_INVALID_VALUE;
   p.splits = 1;
-  if (pair_bn > 0) {
+  if (!few) {
     const int64_t units = ctx.sm_count / 2;
     L.grid = int(2 * (tiles < units ? tiles : units));
     const uint64_t v = uint64_t(reinterpret_cast<uintptr_t>(C)) | uint64_t(ldc * 2);
@@ -122,23 +129,20 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
                                     CU_TENSOR_MAP_SWIZZLE_128B))
       return GEMM_ERR_DRIVER;
   } else {
-    // a tile is split while the GPU (two CTAs to an SM) has room for twice the CTAs and each would keep four blocks
-    while (p.splits < 8 && tiles * p.splits * 2 <= 2 * ctx.sm_count && blocks >= p.splits * 8) p.splits *= 2;
+    p.splits = choose_splits(tiles, blocks, 2 * ctx.sm_count);
     L.grid = int(tiles * p.splits);
   }
-  const void* P = swap ? static_cast<const void*>(B) : A;
-  const void* Q = swap ? static_cast<const void*>(A) : B;
-  if (!encode_map_3d(&L.tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, P, K, p.p_rows, swap ? ldb : lda, 1, 0, kBlockK, 128,
+  const void* P = few ? static_cast<const void*>(B) : A;
+  const void* Q = few ? static_cast<const void*>(A) : B;
+  if (!encode_map_3d(&L.tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, P, K, p.p_rows, few ? ldb : lda, 1, 0, kBlockK, 128,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map_3d(&L.tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, Q, K, p.q_rows, swap ? lda : ldb, 1, 0, kBlockK,
-                     pair_bn > 0 ? bn / 2 : bn, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_map_3d(&L.tmQ, CU_TENSOR_MAP_DATA_TYPE_UINT8, Q, K, p.q_rows, few ? lda : ldb, 1, 0, kBlockK,
+                     few ? bn : bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_ERR_DRIVER;
   cudaError_t e;
-  if (pair_bn > 0)
+  if (!few)
     e = launch_block_pair(L, bn, b_rows == 1);
-  else if (swap)
-    e = bn == 16 ? launch_block<16, true, true>(L) : bn == 32 ? launch_block<32, true, true>(L) : launch_block<64, true, true>(L);
   else
-    e = b_rows == 1 ? launch_block<128, true, false>(L) : launch_block<128, false, false>(L);
+    e = bn == 16 ? launch_block<16>(L) : bn == 32 ? launch_block<32>(L) : launch_block<64>(L);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }

@@ -2,7 +2,7 @@
 // and the pair kernels' unit (block_pair.cu).
 #pragma once
 
-#include "block_kernel.cuh"
+#include "block_few.cuh"
 #include "host.h"
 
 namespace dgt {

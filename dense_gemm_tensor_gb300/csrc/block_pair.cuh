@@ -1,4 +1,4 @@
-// The products with a scale for each block of 128 (block_kernel.cuh) on CTA pairs,
+// The products with a scale for each block of 128 (block_few.cuh) on CTA pairs,
 // for matrices that fill the GPU with 256-row tiles.
 //
 // A pair (cta_group::2) computes 256 x BN, each CTA 128 rows of it; persistent, a
@@ -15,7 +15,7 @@
 // for each row of the column operand) has two instructions for one.
 #pragma once
 
-#include "block_kernel.cuh"
+#include "block_few.cuh"
 #include "group_kernel.cuh"
 
 namespace dgt {
@@ -65,22 +65,6 @@ __device__ __forceinline__ void registers_down() {
 // for every block: 8192^3 took 1144 us with it.)
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// 16 columns of the warp's 32 accumulator rows, and the wait for them.
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld_x16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
 }
 
 template <int BN, bool COLS>
@@ -299,24 +283,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t from = taddr + b * BN;
         const float* scale = scales + b * (Cf::ROW_SCALES + BN);
-        uint32_t r[2][32];
         __syncwarp();
-        tmem_ld_32x32b_x32(from, r[0]);
         const float f1 = scale[(COLS ? 0 : (set * NC) / 128 * Cf::BM) + q * 32 + lane];
         const float2 f = make_float2(f1, f1);
+        // the next CH columns are on their way while these are added
+        constexpr int CH = 32;
+        uint32_t r[2][CH];
+        tmem_ld_32x32b_x32(from, r[0]);
 #pragma unroll
-        for (int c = 0; c < NC / 32; ++c) {
+        for (int c = 0; c < NC / CH; ++c) {
           tmem_wait_ld_into(r[c & 1]);
-          if (c + 1 < NC / 32) {
-            tmem_ld_32x32b_x32(from + 32 * (c + 1), r[(c + 1) & 1]);
+          if (c + 1 < NC / CH) {
+            tmem_ld_32x32b_x32(from + CH * (c + 1), r[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(lead_acce0 + 8 * b);
           }
-          const float4* cs = reinterpret_cast<const float4*>(scale + Cf::ROW_SCALES + set * NC + 32 * c);
+          const float4* cs = reinterpret_cast<const float4*>(scale + Cf::ROW_SCALES + set * NC + CH * c);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < CH / 2; j += 2) {
             float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
             float2 y = make_float2(__uint_as_float(r[c & 1][2 * j + 2]), __uint_as_float(r[c & 1][2 * j + 3]));
             if constexpr (COLS) {
@@ -324,8 +310,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               x = __fmul2_rn(x, make_float2(s4.x, s4.y));
               y = __fmul2_rn(y, make_float2(s4.z, s4.w));
             }
-            acc[16 * c + j] = __ffma2_rn(x, f, acc[16 * c + j]);
-            acc[16 * c + j + 1] = __ffma2_rn(y, f, acc[16 * c + j + 1]);
+            acc[CH / 2 * c + j] = __ffma2_rn(x, f, acc[CH / 2 * c + j]);
+            acc[CH / 2 * c + j + 1] = __ffma2_rn(y, f, acc[CH / 2 * c + j + 1]);
           }
         }
         __syncwarp();

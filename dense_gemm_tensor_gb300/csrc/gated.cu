@@ -8,12 +8,16 @@
 // (and the halves where a backward pass will need them). The gradient's dup is a
 // pass of its own: both of its products read it, one along F and one along the
 // rows, and it is 1/20 of their time (8192 x 4096 -> 2 x 4096).
+#include <cstring>
+
 #include "elem.cuh"
+#include "gated_few.h"
 #include "group_launch.h"
 
 namespace dgt {
 namespace {
 
+constexpr int kFewRows = 64;  // up to here gemm_gated takes the kernel for few rows; and beyond while its tiles are one a SM
 constexpr int kGateThreads = 256;
 constexpr int kBiasBlocks = 152;  // row blocks, at most, that leave partial sums of dbias
 
@@ -180,6 +184,46 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float* partial, int
   grid_launch_dependents();
 }
 
+// The value half of row-major weights that starts off a 16-byte boundary (m bytes past one), in rows that start on
+// them: 16 bytes a thread, shifted together from the two aligned pieces that hold them; a row's last ones element by
+// element. Bound by memory, and a second launch: 1000 x 3000 FP16 about 4 us. (Copied with the gate half, a warp a row,
+// it took 14.)
+struct HalfParams {
+  const uint8_t* w;
+  uint8_t* to;
+  long long ld, pitch;  // bytes
+  int rows, F, pieces;  // pieces of a row
+};
+__global__ void __launch_bounds__(256) copy_half_kernel(const HalfParams p) {
+  grid_dependency_wait();
+  const long long at = blockIdx.x * 256LL + threadIdx.x;
+  const int row = static_cast<int>(at / p.pieces), i = static_cast<int>(at - static_cast<long long>(row) * p.pieces);
+  if (row < p.rows) {
+    const uint8_t* src = p.w + row * p.ld;
+    const long long begin = 2LL * p.F + 16LL * i, end = 4LL * p.F;  // of this piece, and of the row
+    const int m = static_cast<int>(begin & 15);
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (begin - m + 32 <= end) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(src + begin - m), hi = *reinterpret_cast<const uint4*>(src + begin - m + 16);
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      uint32_t a[6], b[5];
+#pragma unroll
+      for (int k = 0; k < 6; ++k) a[k] = m & 8 ? w[k + 2] : w[k];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) b[k] = m & 4 ? a[k + 1] : a[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(b[k], b[k + 1], (m & 3) * 8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (begin + 2 * k < end)
+          o[k >> 1] |= uint32_t(*reinterpret_cast<const uint16_t*>(src + begin + 2 * k)) << (16 * (k & 1));
+    }
+    *reinterpret_cast<uint4*>(p.to + row * p.pitch + 16LL * i) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  grid_launch_dependents();
+}
+
 constexpr int64_t kIntLimit = (int64_t(1) << 31) - 1;
 constexpr int64_t kLdLimit = int64_t(1) << 39;
 
@@ -241,6 +285,63 @@ cudaError_t launch_gate_grad_type(const GateGradParams& p, int vec, const GateGr
                     : launch_gate_grad<TYPE, 1>(p, g, s);
 }
 
+// Bytes of the copy of row-major weights' value half, where that is all of W that TMA cannot read in place.
+int64_t half_bytes(int64_t F, int64_t K, int64_t ldw, int layout) {
+  const bool off = layout == GEMM_B_ROW_MAJOR && F % 8 != 0 && K > 0 && (K == 1 || ldw % 8 == 0);
+  return off ? K * padded(2 * F) : 0;
+}
+
+int copy_half(const void* W, int64_t ldw, int64_t K, int64_t F, void* to, int64_t ld, cudaStream_t stream) {
+  const HalfParams h = {static_cast<const uint8_t*>(W), static_cast<uint8_t*>(to), (long long)ldw * 2, (long long)ld * 2,
+                        int(K), int(F), int((2 * F + 15) / 16)};
+  const int64_t blocks = (K * h.pieces + 255) / 256;
+  if (blocks > kIntLimit) return GEMM_ERR_INVALID_VALUE;
+  return launch_dependent(copy_half_kernel, int(blocks), 256, 0, stream, 1, h) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+// The product of few rows, where TMA reads both operands in place. All arguments have been checked.
+int run_few(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
+            bool row_major, const void* value, int64_t ldv, int gate, const void* bias, void* C, int64_t ldc, void* up,
+            int64_t ldup, const CallContext& ctx, cudaStream_t s) {
+  GatedFewLaunch L;
+  memset(&L, 0, sizeof(L));
+  GatedFewParams& p = L.p;
+  p.g.status = ctx.status;
+  p.g.epoch = ctx.epoch;
+  p.g.debug = ctx.debug;
+  p.g.wait_limit_ns = ctx.wait_limit_ns;
+  p.g.C = C;
+  p.g.ldc = ldc;
+  p.g.bias = bias;
+  p.g.num_kb = int((K + 63) / 64);
+  p.M = int(M);
+  p.F = int(F);
+  p.value_at = value != nullptr ? 0 : int(F);
+  p.gate = gate;
+  p.up = up;
+  p.ldup = ldup;
+  L.row_major = row_major;
+  L.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  L.dev = ctx.dev;
+  L.stream = s;
+  p.tiles_t = int((M + L.bn - 1) / L.bn);
+  const int64_t tiles = (F + 63) / 64 * p.tiles_t;
+  L.deep = tiles <= ctx.sm_count;
+  p.splits = choose_splits(tiles, p.g.num_kb, L.deep ? ctx.sm_count : 2 * ctx.sm_count);
+  L.grid = int(tiles * p.splits);
+  const CUtensorMapDataType dt = type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const bool ok =
+      (row_major ? encode_map_3d(&L.tmW, dt, W, 2 * F, K, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                 : encode_map_3d(&L.tmW, dt, W, K, 2 * F, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) &&
+      encode_map_3d(&L.tmA, dt, A, K, M, lda * 2, 1, 0, 64, L.bn, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return GEMM_ERR_DRIVER;
+  L.tmV = L.tmW;
+  if (value != nullptr && !encode_map_3d(&L.tmV, dt, value, F, K, ldv * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return GEMM_ERR_DRIVER;
+  const cudaError_t e = type == GEMM_TYPE_F16 ? launch_gated_few_f16(L) : launch_gated_few_bf16(L);
+  return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
 // Sizes, types and flags that the forward call and the gradient share.
 bool bad_sizes(int type, int64_t M, int64_t F, int64_t K, int layout, int activation) {
   return (type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16) || M < 0 || F < 0 || K < 0 || M > kIntLimit ||
@@ -279,8 +380,9 @@ extern "C" {
 
 int64_t gemm_gated_workspace(int type, int64_t M, int64_t F, int64_t K, int64_t lda, int64_t ldw, int layout) {
   if (M <= 0 || F <= 0 || K <= 0) return 0;
+  const int64_t half = half_bytes(F, K, ldw, layout);
   return gemm_grouped_rows_workspace(type, 1, M, K, M, lda, 0) +
-         gemm_grouped_weights_workspace(type, 1, 2 * F, K, ldw, 0, layout, GEMM_ACT_SILU_GATED);
+         (half > 0 ? half : gemm_grouped_weights_workspace(type, 1, 2 * F, K, ldw, 0, layout, GEMM_ACT_SILU_GATED));
 }
 
 int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
@@ -290,7 +392,24 @@ int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t
   if (M > 0 && F > 0 && bias != nullptr && C != nullptr && meet(C, M, F, ldc, bias, 1, 2 * F, 2 * F))
     return GEMM_ERR_INVALID_VALUE;
   const gemm_grouped_epilogue_t epi = {1.0f, nullptr, nullptr, bias, GEMM_ACT_NONE};
-  const DenseProduct dense = {activation, up, ldup};
+  // us with the kernel for few rows / with the grouped products' kernel, BF16, K = 4096: 65 x F 512 10.1 / 23.7, 128 x
+  // 4096 21.0 / 25.4, 256 x 2048 20.7 / 24.8, 256 x 4096 (beyond the limit) 25.1 / 25.4, 512 x 4096 48.0 / 26.9;
+  // K = 1024: 65 x 512 7.2 / 10.3, 128 x 4096 9.5 / 12.5.
+  const bool few = M <= kFewRows || (M + 63) / 64 * ((F + 63) / 64) <= 152;
+  DenseProduct dense = {activation, up, ldup, nullptr, 0, nullptr, few ? run_few : nullptr};
+  const int64_t half = M > 0 && F > 0 ? half_bytes(F, K, ldw, layout) : 0;
+  if (half > 0 && W != nullptr && C != nullptr && ldw >= 2 * F && ldw <= kLdLimit && !misaligned(W, 16)) {
+    const int64_t rest = workspace_bytes - half;
+    if (workspace == nullptr || rest < 0 || misaligned(workspace, 128)) return GEMM_ERR_MISALIGNED;
+    if (meet(C, M, F, ldc, workspace, 1, half / 2, half / 2) || meet(up, M, 2 * F, ldup, workspace, 1, half / 2, half / 2) ||
+        meet(W, K, 2 * F, ldw, workspace, 1, half / 2, half / 2) || meet(A, M, K, lda, workspace, 1, half / 2, half / 2))
+      return GEMM_ERR_INVALID_VALUE;
+    dense.copy = copy_half;
+    dense.value = workspace;
+    dense.ldv = padded(2 * F) / 2;
+    workspace = rest > 0 ? static_cast<uint8_t*>(workspace) + half : nullptr;
+    workspace_bytes = rest;
+  }
   return run_grouped(kind_of(type), 1, nullptr, M, 2 * F, K, A, M, lda, nullptr, W, ldw, 0, C, ldc, layout, &epi,
                      workspace, workspace_bytes, stream, &dense);
 }
@@ -388,7 +507,7 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
   }
   uint8_t* stage = terms && space.stage > 0 ? ws + space.dup + space.partial : nullptr;
   if (dA != nullptr) {
-    const DenseProduct dense = {-1, nullptr, 0};
+    const DenseProduct dense = {-1, nullptr, 0, nullptr, 0, nullptr, nullptr};
     st = run_grouped(kind_of(type), 1, nullptr, M, K, 2 * F, dup, M, lddup, nullptr, W, ldw, 0, dA, ldda,
                      km ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, nullptr, stage, space.stage, stream, &dense);
     if (st != GEMM_OK) return st;

@@ -246,6 +246,8 @@ struct WeightCopy {
   int64_t pitch;           // of a copied part, bytes
   int64_t bytes;           // of the workspace: 0 where nothing is copied
 };
+//
+// The dense gated product copies the value half alone where that is all that is off (gated.cu).
 WeightCopy weight_copy(int es, int64_t groups, int64_t N, int64_t K, int64_t ldw, int64_t stride_w, bool row_major,
                        bool gated) {
   WeightCopy c;
@@ -294,7 +296,9 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   }
   if ((slots / 128 + groups + 1) * ((out_cols + 63) / 64) > kIntLimit) return GEMM_ERR_INVALID_VALUE;
   lda = row_pitch(a_rows, K, lda, es);
-  const WeightCopy wc = weight_copy(es, groups, N, K, ldw, stride_w, layout == GEMM_B_ROW_MAJOR, gated);
+  const void* value = dense != nullptr ? dense->value : nullptr;  // (checked by the caller)
+  const WeightCopy wc =
+      weight_copy(es, groups, N, K, ldw, stride_w, layout == GEMM_B_ROW_MAJOR, gated && value == nullptr);
   ldw = wc.ld;
   const void* bias = epi != nullptr ? epi->bias : nullptr;
   const bool odd_a = K > 0 && odd_pitch(lda, es);
@@ -334,6 +338,15 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
   if (epi != nullptr && ((epi->row_scale != nullptr && !on_device(epi->row_scale, ctx.dev)) ||
                          (epi->col_scale != nullptr && !on_device(epi->col_scale, ctx.dev))))
     return GEMM_ERR_NOT_DEVICE_MEMORY;
+  if (value != nullptr) {
+    if (!on_device(value, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
+    st = dense->copy(W, ldw, K, out_cols, dense->value, dense->ldv, static_cast<cudaStream_t>(stream));
+    if (st != GEMM_OK) return st;
+  }
+  if (dense != nullptr && dense->few != nullptr && K > 0 && workspace == nullptr)
+    return dense->few(kind == KIND_F16 ? GEMM_TYPE_F16 : GEMM_TYPE_BF16, slots, out_cols, K, A, lda, W, ldw,
+                      layout == GEMM_B_ROW_MAJOR, value, dense->ldv, dense->gate, bias, C, ldc, up, ldup, ctx,
+                      static_cast<cudaStream_t>(stream));
   GroupLaunch L;
   memset(&L, 0, sizeof(L));
   GroupParams& p = L.p;
@@ -424,6 +437,14 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
       ok = encode_map_3d(&L.tmB, dt, W, w_cols_read, K, ldw * es, groups, mat, 128 / es, bk, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (!ok) return GEMM_ERR_DRIVER;
+    if (dense != nullptr && gated) {
+      L.tmA2 = L.tmB;
+      if (value != nullptr) {
+        p.value_at = 0;
+        if (!encode_map_3d(&L.tmA2, dt, value, out_cols, K, dense->ldv * es, 1, 0, 128 / es, bk, CU_TENSOR_MAP_SWIZZLE_128B))
+          return GEMM_ERR_DRIVER;
+      }
+    }
   }
   if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, C, out_cols, slots, ldc * 2, 1, 0, 64, 32,
                                   CU_TENSOR_MAP_SWIZZLE_128B))

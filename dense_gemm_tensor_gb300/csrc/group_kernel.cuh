@@ -40,8 +40,9 @@
 // GATED: W's columns are gate and value halves; a tile holds the same BN / 2
 // columns of both (in the pair each CTA loads one of them), and the epilogue
 // stores silu(gate) * value, so the 2 x wider intermediate is never written.
-// GATED_ANY is the dense product's form: any of four activations, and the two
-// halves before it kept on request for a backward pass.
+// GATED_ANY is the dense product's form: any of four activations, the two halves
+// before it kept on request for a backward pass, and a map of its own (tmA2) for the
+// value half, which may be elsewhere.
 #pragma once
 
 #include "dgt_experts.h"
@@ -389,6 +390,14 @@ __device__ __forceinline__ void wgrad_load(uint32_t dst, const CUtensorMap* map,
     tma_load_3d(dst, map, bar, x, y, z);
 }
 
+template <int KIND>
+__device__ __forceinline__ float bias_at(const GroupParams& p, long long at) {
+  if constexpr (KindTraits<KIND>::out == KIND_F16)
+    return __half2float(static_cast<const __half*>(p.g.bias)[at]);
+  else
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p.g.bias)[at]);
+}
+
 // The scaled and biased pre-activation of 32 accumulator columns from
 // column `col` of group e: v = scale * col_scale[col] * acc + bias[col]. Each
 // lane loads one column's scale and bias, and shuffles hand them to every lane.
@@ -551,10 +560,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
               if constexpr (Cf::B_KMAJOR) {
                 if constexpr (PAIR) {
                   const int n0 = GATED ? int(half) * p.value_at + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH;
-                  tma_load_3d_pair(b_dst, &tmB, fb, x, n0, t.e);
+                  tma_load_3d_pair(b_dst, GATED == GATED_ANY && half ? &tmA2 : &tmB, fb, x, n0, t.e);
                 } else if constexpr (GATED) {
                   tma_load_3d(b_dst, &tmB, fb, x, t.nb * Cf::OUT_BN, t.e);
-                  tma_load_3d(b_dst + Cf::B_BYTES / 2, &tmB, fb, x, p.value_at + t.nb * Cf::OUT_BN, t.e);
+                  tma_load_3d(b_dst + Cf::B_BYTES / 2, GATED == GATED_ANY ? &tmA2 : &tmB, fb, x, p.value_at + t.nb * Cf::OUT_BN, t.e);
                 } else {
                   tma_load_3d(b_dst, &tmB, fb, x, t.nb * BN, t.e);
                 }
@@ -565,12 +574,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                   if constexpr (PAIR) {
                     n0 = (GATED ? int(half) * p.value_at + t.nb * Cf::OUT_BN : t.nb * BN + int(half) * Cf::BNH) +
                          j * Cf::BOXN;
-                    tma_load_3d_pair(b_dst + j * Cf::BOX_BYTES, &tmB, fb, n0, x, t.e);
+                    tma_load_3d_pair(b_dst + j * Cf::BOX_BYTES, GATED == GATED_ANY && half ? &tmA2 : &tmB, fb, n0, x, t.e);
                   } else {
                     constexpr int HB = Cf::BNH / Cf::BOXN / 2;  // boxes of one half
                     n0 = GATED ? (j >= HB ? p.value_at : 0) + t.nb * Cf::OUT_BN + (j >= HB ? j - HB : j) * Cf::BOXN
                                : t.nb * BN + j * Cf::BOXN;
-                    tma_load_3d(b_dst + j * Cf::BOX_BYTES, &tmB, fb, n0, x, t.e);
+                    tma_load_3d(b_dst + j * Cf::BOX_BYTES, GATED == GATED_ANY && j >= HB ? &tmA2 : &tmB, fb, n0, x, t.e);
                   }
                 }
               }
@@ -686,6 +695,21 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
       const GroupTile t = next_tile(p.g, schf0, sche0, ring, n, ROLE_EPILOGUE | (0x80u << 8));
       if (t.kbs < 0) break;
       const int b = tc & 1;
+      // GATED_ANY: the biases of this warp's one piece, a column of either half a lane, asked for ahead of the wait
+      float bias[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+      if constexpr (GATED == GATED_ANY) {
+        static_assert(Cf::OUT_BN <= 128, "one piece a warp");
+        if (p.g.bias != nullptr) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = t.nb * Cf::OUT_BN + set * 64 + 32 * h + lane;
+            if (col < p.out_cols) {
+              bias[0][h] = bias_at<KIND>(p, col);
+              bias[1][h] = bias_at<KIND>(p, p.out_cols + static_cast<long long>(col));
+            }
+          }
+        }
+      }
       if (t.kbs > 0) {
         if (!warp_wait_phase(p.g, accf0 + 8 * b, (tc >> 1) & 1, ROLE_EPILOGUE | (b << 8))) break;
         ++tc;
@@ -704,47 +728,62 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
         const GroupOut out_c = {static_cast<uint16_t*>(p.g.C), p.g.ldc, p.g.stride_c, p.g.c_tma, p.g.c_gran, p.out_cols, 0};
         for (int c = set * 64; c < Cf::OUT_BN && col0 + c < p.out_cols; c += 128) {
           if constexpr (GATED == GATED_ANY) {
-            // C's piece, and the halves' pieces where they are kept: the accumulators are read again for each
             const GroupOut out_g = {static_cast<uint16_t*>(p.up), p.ldup, 0, p.up_gran == 16, p.up_gran, p.out_cols, 0};
             const GroupOut out_v = {out_g.base + p.out_cols, p.ldup, 0, p.up_value_gran == 16, p.up_value_gran, p.out_cols,
                                     p.out_cols};
-            for (int out = 0; out < (p.up != nullptr ? 3 : 1); ++out) {
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                const int cc = c + 32 * h;
-                uint32_t acc[2][32];
-                if (t.kbs > 0) {
-                  __syncwarp();
-                  tmem_ld_32x32b_x32(taddr + cc, acc[0]);
-                  tmem_ld_32x32b_x32(taddr + BN / 2 + cc, acc[1]);
-                  tmem_wait_ld_into(acc[0]);
-                  tmem_wait_ld_into(acc[1]);
-                } else {
+            // words of 2 x 32 columns of C, and of both halves where they are kept
+            uint32_t words[3][2][16];
+            auto pack = [&](uint32_t(&w)[16], const float(&v)[32]) {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) acc[0][k] = acc[1][k] = 0u;
-                }
-                float v[32], u[32];
-                if (out < 2) group_scale<KIND>(p, t.e, col0 + cc, lane, 1.0f, acc[0], v);
-                if (out != 1) group_scale<KIND>(p, t.e, p.out_cols + col0 + cc, lane, 1.0f, acc[1], u);
-                if (out == 0) gate_activate(v, u, p.gate);
-                if (out == 2) {
+              for (int j = 0; j < 16; ++j)
+                w[j] = pack2<KindTraits<KIND>::out>(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
+            };
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) v[k] = u[k];
-                }
-                uint32_t words[16];
+            for (int h = 0; h < 2; ++h) {
+              const int cc = c + 32 * h;
+              uint32_t acc[2][32];
+              if (t.kbs > 0) {
+                __syncwarp();
+                tmem_ld_32x32b_x32(taddr + cc, acc[0]);
+                tmem_ld_32x32b_x32(taddr + BN / 2 + cc, acc[1]);
+                tmem_wait_ld_into(acc[0]);
+                tmem_wait_ld_into(acc[1]);
+              } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  words[j] = pack2<KindTraits<KIND>::out>(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
-                if (h == 0) {
-                  // the tile's last TMA store has read it
-                  if (lane == 0) bulk_wait_read_all();
-                  __syncwarp();
+                for (int k = 0; k < 32; ++k) acc[0][k] = acc[1][k] = 0u;
+              }
+              float v[32], u[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                v[k] = __uint_as_float(acc[0][k]);
+                u[k] = __uint_as_float(acc[1][k]);
+              }
+              if (p.g.bias != nullptr) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  v[k] += __shfl_sync(0xFFFFFFFFu, bias[0][h], k);
+                  u[k] += __shfl_sync(0xFFFFFFFFu, bias[1][h], k);
                 }
+              }
+              if (p.up != nullptr) {
+                pack(words[1][h], v);
+                pack(words[2][h], u);
+              }
+              gate_activate(v, u, p.gate);
+              pack(words[0][h], v);
+            }
+#pragma unroll
+            for (int out = 0; out < 3; ++out) {
+              if (out > 0 && p.up == nullptr) break;
+              // the tile's last TMA store has read it
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  st_shared_v4(stage_chunk(stage, lane, 4 * h + j), words[4 * j], words[4 * j + 1], words[4 * j + 2],
-                               words[4 * j + 3]);
-              }
+                  st_shared_v4(stage_chunk(stage, lane, 4 * h + j), words[out][h][4 * j], words[out][h][4 * j + 1],
+                               words[out][h][4 * j + 2], words[out][h][4 * j + 3]);
               group_flush<false>(out == 0 ? out_c : out == 1 ? out_g : out_v, out == 0 ? &tmC : &tmB2, stage, lane, row0,
                                  t.row_end, col0 + c, z);
             }

@@ -8,7 +8,9 @@
 namespace dgt {
 
 struct GroupLaunch {
-  CUtensorMap tmA, tmA2;  // the MMA's A operand: boxes; gathered rows (product) or the groups' ragged slabs (gradient)
+  // the MMA's A operand: boxes; gathered rows (product), the groups' ragged slabs (gradient) or W's value half (dense
+  // gated product)
+  CUtensorMap tmA, tmA2;
   CUtensorMap tmB, tmB2;  // its B operand: boxes; ragged slabs (gradient), or the kept halves (dense gated product)
   CUtensorMap tmC;        // valid when p.g.c_tma
   GroupParams p;
@@ -36,6 +38,14 @@ struct DenseProduct {
   int gate;
   void* up;  // slots x N, or null
   int64_t ldup;
+  // Where the value half of row-major weights goes that TMA cannot read in place (or null), and what copies it there.
+  void* value;
+  int64_t ldv;
+  int (*copy)(const void* W, int64_t ldw, int64_t K, int64_t F, void* to, int64_t ld, cudaStream_t stream);
+  // A kernel of its own for few rows (or null), taken where TMA reads A and W in place.
+  int (*few)(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
+             bool row_major, const void* value, int64_t ldv, int gate, const void* bias, void* C, int64_t ldc, void* up,
+             int64_t ldup, const CallContext& ctx, cudaStream_t stream);
 };
 // The grouped product and weight gradient behind the C entry points (group_host.cu). dense: null for groups on the
 // device; offsets and rows are null where it is given.

@@ -177,7 +177,7 @@ def test_gated_workspaces(lib):
     assert size(1, 4, 8, 8, 8, 8, 1) == size(1, 4, 8, 8, 8, 16, 0) == size(1, 0, 8, 8, 8, 8, 1) == 0
     assert size(1, 4, 8, 9, 9, 16, 1) == 4 * 128                          # rows of A of 18 bytes
     assert size(1, 4, 8, 9, 16, 9, 1) == 16 * 128                         # of W
-    assert size(1, 4, 12, 8, 8, 24, 0) == 8 * 2 * 128                     # halves of 24 bytes, each on a boundary
+    assert size(1, 4, 12, 8, 8, 24, 0) == 8 * 128                         # a value half of 24 bytes, off a boundary
     slabs = 64 * (128 + 128)
     assert grad(1, 4, 8, 8, 8, 8, 1, 1, 0, 0) == 4 * 128                  # dup
     assert grad(1, 4, 8, 8, 8, 8, 1, 0, 0, 1) == 4 * 128 + 4 * 2 * 8 * 4  # and partial sums of dbias
