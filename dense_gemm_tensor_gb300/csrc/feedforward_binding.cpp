@@ -255,14 +255,13 @@ PyObject* quantize_blocks(PyObject* const* a) {
   const int64_t out_rows = transpose ? cols : rows, out_cols = transpose ? rows : cols;
   const int64_t blocks = (out_cols + kBlock - 1) / kBlock, runs = tall == 1 ? out_rows : (out_rows + kBlock - 1) / kBlock;
   // q's rows start on 16-byte boundaries, as the product wants them; scales of single rows lie block by block
-  const int64_t ldq = (out_cols + 15) / 16 * 16;
-  Tensor q = make({out_rows, ldq}, x, at::kFloat8_e4m3fn);
-  Tensor scale = make({tall == 1 ? blocks : runs, tall == 1 ? runs : blocks}, x, at::kFloat);
+  const int64_t ldq = (out_cols + 15) / 16 * 16, s_row = tall == 1 ? 1 : blocks, s_block = tall == 1 ? runs : 1;
+  Tensor q = make_strided({out_rows, out_cols}, {ldq, 1}, x, at::kFloat8_e4m3fn);
+  Tensor scale = make_strided({runs, blocks}, {s_row, s_block}, x, at::kFloat);
   const int st = entry.c.quantize_blocks(code, rows, cols, x.data_ptr(), ldx, tall, transpose,
                                          static_cast<uint8_t*>(q.data_ptr()), ldq, static_cast<float*>(scale.data_ptr()),
-                                         tall == 1 ? 1 : blocks, tall == 1 ? runs : 1, stream_of(x));
-  if (st != GEMM_OK) return PyLong_FromLong(st);
-  return tuple_of(ldq == out_cols ? q : q.narrow(1, 0, out_cols), tall == 1 ? scale.t() : scale);
+                                         s_row, s_block, stream_of(x));
+  return st != GEMM_OK ? PyLong_FromLong(st) : tuple_of(q, scale);
 }
 
 bool is_bound() { return entry.address[0] != nullptr; }
