@@ -366,7 +366,7 @@ GradSpace grad_space(int type, int64_t M, int64_t F, int64_t K, int64_t lda, int
     a = gemm_grouped_weights_workspace(type, 1, K, 2 * F, ldw, 0,
                                        layout == GEMM_B_K_MAJOR ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, GEMM_ACT_NONE);
   }
-  if (dw && K > 0) w = gemm_grouped_wgrad_rows_workspace(1, M, 2 * F, K, M, lda, 0, dup_pitch(F));
+  if (dw && K > 0) w = dense_wgrad_workspace(M, 2 * F, K, lda, dup_pitch(F));
   s.stage = padded(a > w ? a : w);
   return s;
 }

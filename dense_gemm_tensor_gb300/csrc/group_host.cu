@@ -484,6 +484,11 @@ int64_t wgrad_workspace(int64_t groups, int64_t slots, int64_t N, int64_t K, boo
 
 }  // namespace
 
+int64_t dense_wgrad_workspace(int64_t slots, int64_t N, int64_t K, int64_t lda, int64_t lddc) {
+  return (odd_pitch(row_pitch(slots, K, lda, 2), 2) ? slots * staged_pitch(K, 2) : 0) +
+         (odd_pitch(row_pitch(slots, N, lddc, 2), 2) ? slots * staged_pitch(N, 2) : 0);
+}
+
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
               int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
               int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream, bool dense) {
@@ -503,15 +508,15 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
   if (((out_rows + 255) / 256) * ((out_cols + 255) / 256) > kIntLimit / groups) return GEMM_ERR_INVALID_VALUE;
   lda = row_pitch(a_rows, K, lda, 2);
   lddc = row_pitch(slots, N, lddc, 2);
-  if (slots == 0) workspace = nullptr;
-  if (slots > 0 && (workspace == nullptr ||
-                    workspace_bytes < wgrad_workspace(groups, slots, N, K, rows != nullptr)))
+  const bool copy_a = rows != nullptr || odd_pitch(lda, 2), copy_c = odd_pitch(lddc, 2);
+  if (slots == 0 || (dense && !copy_a && !copy_c)) workspace = nullptr;
+  if (slots > 0 && !dense &&
+      (workspace == nullptr || workspace_bytes < wgrad_workspace(groups, slots, N, K, rows != nullptr)))
     return GEMM_ERR_INVALID_VALUE;
   if (misaligned(offsets, 4) || misaligned(rows, 4) || misaligned(dW, 2) || misaligned(workspace, 128))
     return GEMM_ERR_MISALIGNED;
-  const bool copy_a = rows != nullptr || odd_pitch(lda, 2), copy_c = odd_pitch(lddc, 2);
-  if (slots > 0 && (misaligned(A, 16) || misaligned(dC, 16) ||
-                    workspace_bytes < wgrad_workspace(groups, slots, N, K, copy_a, copy_c)))
+  const int64_t need = dense ? dense_wgrad_workspace(slots, N, K, lda, lddc) : wgrad_workspace(groups, slots, N, K, copy_a, copy_c);
+  if (slots > 0 && (misaligned(A, 16) || misaligned(dC, 16) || (need > 0 && (workspace == nullptr || workspace_bytes < need))))
     return GEMM_ERR_MISALIGNED;
   const Range rw = range_of(dW, out_rows, out_cols, lddw, 2, groups, groups > 1 ? stride_dw : 0);
   if (workspace != nullptr && meet(rw, range_of(workspace, 1, workspace_bytes, 0, 1))) return GEMM_ERR_INVALID_VALUE;
@@ -569,9 +574,12 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
     q.offsets = offsets;
     q.groups = groups;
     q.slots = int(slots);
-    q.slab_c = static_cast<uint8_t*>(workspace);
-    q.slab_a = q.slab_c + int64_t(groups) * kSlab * q.pitch_c;
-    uint8_t* next = q.slab_a + int64_t(groups) * kSlab * q.pitch_a;
+    uint8_t* next = static_cast<uint8_t*>(workspace);
+    if (!dense) {  // (rows past a single group's end are past the tensors', where TMA reads zeros)
+      q.slab_c = next;
+      q.slab_a = q.slab_c + int64_t(groups) * kSlab * q.pitch_c;
+      next = q.slab_a + int64_t(groups) * kSlab * q.pitch_a;
+    }
     if (copy_a) {
       q.order = next;
       next += slots * q.pitch_a;
@@ -583,8 +591,7 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
       dC = q.order_c;
       lddc = q.pitch_c / 2;
     }
-    // one group of whole slabs has nothing to stage
-    if (offsets != nullptr || slots % kSlab != 0 || copy_a || copy_c) st = stage_rows(ctx, q, L.stream);
+    if (!dense || copy_a || copy_c) st = stage_rows(ctx, q, L.stream);
     if (st != GEMM_OK) return st;
     // rows x cols with rows `ld` apart: 64-column blocks as the outer coordinate, two to a box, where the columns are
     // whole blocks (a block past the row's end would be memory past the matrix); else boxes of one block
@@ -599,8 +606,8 @@ int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64
     };
     const bool ok = operand(km ? &L.tmA : &L.tmB, dC, N, slots, lddc * 2, km ? &p.wide_p : &p.wide_q) &&
                     operand(km ? &L.tmB : &L.tmA, A, K, slots, lda * 2, km ? &p.wide_q : &p.wide_p) &&
-                    slabs(km ? &L.tmA2 : &L.tmB2, q.slab_c, q.pitch_c) &&
-                    slabs(km ? &L.tmB2 : &L.tmA2, q.slab_a, q.pitch_a);
+                    (dense || (slabs(km ? &L.tmA2 : &L.tmB2, q.slab_c, q.pitch_c) &&
+                               slabs(km ? &L.tmB2 : &L.tmA2, q.slab_a, q.pitch_a)));
     if (!ok) return GEMM_ERR_DRIVER;
   }
   if (p.g.c_tma && !encode_map_3d(&L.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT16, dW, out_cols, out_rows, lddw * 2, groups,

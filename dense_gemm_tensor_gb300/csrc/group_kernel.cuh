@@ -592,9 +592,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                 tma_gather4(a_dst + lane * 512, &tmA2, fb, kb * Cf::BK, r0, r1, r2, r3);
             }
           } else {
-            // the group's last slab, where ragged, comes from its zero-padded copy: 64 rows for each group
+            // the group's last slab, where ragged, comes from its zero-padded copy: 64 rows for each group (a single
+            // group without offsets ends where the tensors do, and TMA reads zeros there)
             const int s0 = t.begin + kb * Cf::BK;
-            const bool ragged = s0 + Cf::BK > t.end;
+            const bool ragged = p.offsets != nullptr && s0 + Cf::BK > t.end;
             const int y = ragged ? t.e * Cf::BK : s0;
             const CUtensorMap* map_p = ragged ? &tmA2 : &tmA;
             const CUtensorMap* map_q = ragged ? &tmB2 : &tmB;

@@ -56,6 +56,8 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
 int run_wgrad(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
               int64_t a_rows, int64_t lda, const int32_t* rows, const void* dC, int64_t lddc, void* dW, int64_t lddw,
               int64_t stride_dw, int layout, void* workspace, int64_t workspace_bytes, void* stream, bool dense);
+// Bytes of workspace that run_wgrad takes for a dense product: copies of rows whose pitch is not TMA's.
+int64_t dense_wgrad_workspace(int64_t slots, int64_t N, int64_t K, int64_t lda, int64_t lddc);
 
 // Sets the kernel's dynamic shared-memory limit once per device, then launches.
 template <int KIND, int OPS, int BN, bool PAIR, int GATED>
