@@ -17,7 +17,12 @@
 namespace dgt {
 namespace {
 
-constexpr int kFewRows = 64;  // up to here gemm_gated takes the kernel for few rows; and beyond while its tiles are one a SM
+// Whether a product of M rows and N columns, `per` of them a tile, takes the kernel for few rows: up to 64 rows, and
+// beyond while its tiles are one an SM. Gated, BF16, us with it / with the grouped products' kernel, K = 4096: 65 x F
+// 512 10.1 / 23.7, 128 x 4096 21.0 / 25.4, 256 x 2048 20.7 / 24.8, 256 x 4096 (beyond the limit) 25.1 / 25.4, 512 x
+// 4096 48.0 / 26.9; K = 1024: 65 x 512 7.2 / 10.3, 128 x 4096 9.5 / 12.5.
+bool few_rows(int64_t M, int64_t N, int per) { return M <= 64 || (M + 63) / 64 * ((N + per - 1) / per) <= 152; }
+
 constexpr int kGateThreads = 256;
 constexpr int kBiasBlocks = 152;  // row blocks, at most, that leave partial sums of dbias
 
@@ -299,7 +304,8 @@ int copy_half(const void* W, int64_t ldw, int64_t K, int64_t F, void* to, int64_
   return launch_dependent(copy_half_kernel, int(blocks), 256, 0, stream, 1, h) == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-// The product of few rows, where TMA reads both operands in place. All arguments have been checked.
+// The product of few rows, where TMA reads both operands in place; F columns of C (gate -1: W has them alone). All
+// arguments have been checked.
 int run_few(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
             bool row_major, const void* value, int64_t ldv, int gate, const void* bias, void* C, int64_t ldc, void* up,
             int64_t ldup, const CallContext& ctx, cudaStream_t s) {
@@ -316,7 +322,8 @@ int run_few(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t ld
   p.g.num_kb = int((K + 63) / 64);
   p.M = int(M);
   p.F = int(F);
-  p.value_at = value != nullptr ? 0 : int(F);
+  const bool plain = gate < 0;
+  p.value_at = plain ? 64 : value != nullptr ? 0 : int(F);
   p.gate = gate;
   p.up = up;
   p.ldup = ldup;
@@ -325,14 +332,14 @@ int run_few(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t ld
   L.dev = ctx.dev;
   L.stream = s;
   p.tiles_t = int((M + L.bn - 1) / L.bn);
-  const int64_t tiles = (F + 63) / 64 * p.tiles_t;
+  const int64_t tiles = (plain ? (F + 127) / 128 : (F + 63) / 64) * p.tiles_t;
   L.deep = tiles <= ctx.sm_count;
   p.splits = choose_splits(tiles, p.g.num_kb, L.deep ? ctx.sm_count : 2 * ctx.sm_count);
   L.grid = int(tiles * p.splits);
   const CUtensorMapDataType dt = type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const bool ok =
-      (row_major ? encode_map_3d(&L.tmW, dt, W, 2 * F, K, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
-                 : encode_map_3d(&L.tmW, dt, W, K, 2 * F, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) &&
+      (row_major ? encode_map_3d(&L.tmW, dt, W, plain ? F : 2 * F, K, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                 : encode_map_3d(&L.tmW, dt, W, K, plain ? F : 2 * F, ldw * 2, 1, 0, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) &&
       encode_map_3d(&L.tmA, dt, A, K, M, lda * 2, 1, 0, 64, L.bn, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return GEMM_ERR_DRIVER;
   L.tmV = L.tmW;
@@ -392,11 +399,7 @@ int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t
   if (M > 0 && F > 0 && bias != nullptr && C != nullptr && meet(C, M, F, ldc, bias, 1, 2 * F, 2 * F))
     return GEMM_ERR_INVALID_VALUE;
   const gemm_grouped_epilogue_t epi = {1.0f, nullptr, nullptr, bias, GEMM_ACT_NONE};
-  // us with the kernel for few rows / with the grouped products' kernel, BF16, K = 4096: 65 x F 512 10.1 / 23.7, 128 x
-  // 4096 21.0 / 25.4, 256 x 2048 20.7 / 24.8, 256 x 4096 (beyond the limit) 25.1 / 25.4, 512 x 4096 48.0 / 26.9;
-  // K = 1024: 65 x 512 7.2 / 10.3, 128 x 4096 9.5 / 12.5.
-  const bool few = M <= kFewRows || (M + 63) / 64 * ((F + 63) / 64) <= 152;
-  DenseProduct dense = {activation, up, ldup, nullptr, 0, nullptr, few ? run_few : nullptr};
+  DenseProduct dense = {activation, up, ldup, nullptr, 0, nullptr, few_rows(M, F, 64) ? run_few : nullptr};
   const int64_t half = M > 0 && F > 0 ? half_bytes(F, K, ldw, layout) : 0;
   if (half > 0 && W != nullptr && C != nullptr && ldw >= 2 * F && ldw <= kLdLimit && !misaligned(W, 16)) {
     const int64_t rest = workspace_bytes - half;
@@ -507,7 +510,7 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
   }
   uint8_t* stage = terms && space.stage > 0 ? ws + space.dup + space.partial : nullptr;
   if (dA != nullptr) {
-    const DenseProduct dense = {-1, nullptr, 0, nullptr, 0, nullptr, nullptr};
+    const DenseProduct dense = {-1, nullptr, 0, nullptr, 0, nullptr, few_rows(M, K, 128) ? run_few : nullptr};
     st = run_grouped(kind_of(type), 1, nullptr, M, K, 2 * F, dup, M, lddup, nullptr, W, ldw, 0, dA, ldda,
                      km ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, nullptr, stage, space.stage, stream, &dense);
     if (st != GEMM_OK) return st;

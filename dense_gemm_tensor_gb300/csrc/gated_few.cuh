@@ -11,6 +11,8 @@
 // meet. DEEP: one CTA to an SM, with all of its shared memory for loads in flight;
 // else two, for more tiles than SMs. Warps: 0-3 take the sums out of tensor memory,
 // 4 loads by TMA, 5 issues tcgen05.mma.
+// The plain product (gate < 0; the gradient of A) is the same with 128 neighbouring
+// columns to a tile.
 #pragma once
 
 #include "dgt_feedforward.h"
@@ -21,9 +23,9 @@ namespace dgt {
 
 struct GatedFewParams {
   GemmParams g;  // C, ldc, bias, num_kb and the launch-wide status fields
-  int M, F;
-  int value_at;  // where the value half starts in its map (a column of row-major W, else a row)
-  int gate;
+  int M, F;      // rows of A; columns of C
+  int value_at;  // where the value half starts in its map (a column of row-major W, else a row); plain: 64
+  int gate;      // GEMM_GATE_*, or -1: no gate
   void* up;
   long long ldup;
   int splits;
@@ -100,7 +102,8 @@ __global__ void __launch_bounds__(kFewThreads)
   const int split = static_cast<int>(blockIdx.x % p.splits);
   // (tiles of the same weights are neighbours)
   const int tile = static_cast<int>(blockIdx.x / p.splits);
-  const int n0 = tile / p.tiles_t * 64, row0 = tile % p.tiles_t * BN;
+  const bool plain = p.gate < 0;
+  const int n0 = tile / p.tiles_t * (plain ? 128 : 64), row0 = tile % p.tiles_t * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(p.g.num_kb) * split / p.splits);
   const int kb1 = static_cast<int>(static_cast<long long>(p.g.num_kb) * (split + 1) / p.splits);
 
@@ -199,7 +202,14 @@ __global__ void __launch_bounds__(kFewThreads)
   {
     // this CTA's share of the rows of A
     const int left = min(BN, p.M - row0), c0 = min(BN * split / p.splits, left), c1 = min(BN * (split + 1) / p.splits, left);
-    for (int e = threadIdx.x; e < (c1 - c0) * 64; e += kFewThreads) {
+    if (plain) {
+      for (int e = threadIdx.x; e < (c1 - c0) * 128; e += kFewThreads) {
+        const int c = c0 + e / 128, r = e % 128, j = n0 + r;
+        if (j < p.F)
+          to16<KIND>(p.g.C, static_cast<long long>(row0 + c) * p.g.ldc + j, joined_sum(sums, c * Cf::SUM_LD + r, p.splits));
+      }
+    }
+    for (int e = threadIdx.x; !plain && e < (c1 - c0) * 64; e += kFewThreads) {
       const int c = c0 + e / 64, r = e % 64, j = n0 + r;
       if (j >= p.F) continue;
       const int at = c * Cf::SUM_LD + r;
