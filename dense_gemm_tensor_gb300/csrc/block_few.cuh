@@ -33,7 +33,8 @@ struct BlockScales {
   const float* s;
   long long row, block;
   int shift;
-  __device__ __forceinline__ float at(int r, int b) const { return __ldg(s + (r >> shift) * row + b * block); }
+  // (plain loads: the previous kernel on the stream, which this one's start overlaps, may be what writes the scales)
+  __device__ __forceinline__ float at(int r, int b) const { return s[(r >> shift) * row + b * block]; }
 };
 
 struct BlockParams {
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kBlockThreads)
           if (loaded + i < kb1) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-              next[i][j] = __ldg(src[j]);
+              next[i][j] = *src[j];
               src[j] += from.block;
             }
           }

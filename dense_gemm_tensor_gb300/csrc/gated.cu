@@ -106,10 +106,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const GateGradP
 #pragma unroll
   for (int j = 0; j < VEC; ++j) sg[j] = sv[j] = 0.0f;
   grid_dependency_wait();
-  const int begin = blockIdx.y * p.rows_per_block, end = min(begin + p.rows_per_block, p.rows);
+  const long long begin = static_cast<long long>(blockIdx.y) * p.rows_per_block;
+  const long long end = min(begin + p.rows_per_block, static_cast<long long>(p.rows));
   if (in) {
     constexpr int AHEAD = 2;
-    for (int r0 = begin + y; r0 < end; r0 += AHEAD * ty) {
+    for (long long r0 = begin + y; r0 < end; r0 += AHEAD * ty) {
       Piece<TYPE, VEC> d[AHEAD], g[AHEAD], v[AHEAD];
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {

@@ -563,3 +563,132 @@ def test_refusals_on_the_device():
     host = torch.zeros(64, dtype=torch.bfloat16)
     code = ff._load().gemm_quantize_blocks(1, 2, 32, host.data_ptr(), 32, 1, 0, q.q.data_ptr(), 32, one.data_ptr(), 1, 2, None)
     assert code == gemm.GEMM_ERR_NOT_DEVICE_MEMORY
+
+
+# ---------------------------------------------------------------- at the edges
+
+# slabs (or blocks) that clusters of one to eight CTAs share, and tiles that leave no room for a cluster
+@pytest.mark.parametrize("slabs", [1, 2, 3, 4, 6, 8, 10, 12, 14, 16, 17])
+@pytest.mark.parametrize("M", [3, 20, 40])
+def test_few_rows_by_every_split(M, slabs):
+    K, F = 64 * slabs - 5, 70
+    a, w, ad, wd = _gated_case(M, K, F, "bf16", slabs % 2, 120)
+    want, up, s = of.gated(_np(a), _np(w), None, "silu")
+    r = ff.gated_matmul(ad, wd, layout=slabs % 2, keep=True)
+    _accept(r.c, want, _gated_s(up, s, "silu"), "bf16")
+    _accept(r.up, up, s, "bf16")
+    K = 128 * slabs - 9
+    a, sa = _operand(M, K, 1, 122)
+    b, sb = _operand(150, K, 128 if slabs % 2 else 1, 124)
+    want, s = of.matmul_blocks(_np(a.float()), _np(b.float()), _np(sa), _np(sb), 128 if slabs % 2 else 1)
+    _accept(ff.matmul_blocks(_pitch16(a), _pitch16(b), sa.cuda(), sb.cuda()), want, s, "bf16")
+
+
+@pytest.mark.parametrize("M,F", [(5, 10100), (40, 20000), (70, 9000), (150, 4200)])
+def test_few_rows_of_many_tiles(M, F):
+    """More tiles than SMs, and than twice as many; tiles along the rows too."""
+    a, w, ad, wd = _gated_case(M, 136, F, "bf16", 1, 130)
+    want, up, s = of.gated(_np(a), _np(w), None, "relu")
+    _accept(ff.gated_matmul(ad, wd, layout=1, activation="relu").c, want, _gated_s(up, s, "relu"), "bf16")
+    dc = _normal((M, F), "bf16", 132)
+    up = _normal((M, 2 * F), "bf16", 133)
+    dup = of.gated_grad(_np(dc), _np(up), "relu")  # products of 16-bit numbers: dup is rounded once
+    got = ff.gated_matmul_backward(dc.cuda(), ad, wd, up.cuda(), layout=1, activation="relu", weights=False).dA
+    bad = ~(np.abs(_np(got) - dup @ _np(w).T) <=
+            oracle.allowed_error(dup @ _np(w).T, np.abs(dup) @ np.abs(_np(w)).T, "bf16") + HALF["bf16"] * np.abs(dup) @ np.abs(_np(w)).T)
+    assert not bad.any()
+
+
+# pairs of CTAs: a round of 256-wide tiles, of 128-wide ones, several rounds, ragged ends on both sides
+@pytest.mark.parametrize("M,N,K", [(1000, 9000, 300), (2100, 2300, 520), (4100, 4000, 130), (515, 4001, 1027), (257, 9999, 129)])
+@pytest.mark.parametrize("b_rows", [1, 128])
+def test_matmul_blocks_of_many_rows(M, N, K, b_rows):
+    a, sa = _operand(M, K, 1, 140)
+    b, sb = _operand(N, K, b_rows, 142)
+    want, s = of.matmul_blocks(_np(a.float()), _np(b.float()), _np(sa), _np(sb), b_rows)
+    for extra in (0, 3):
+        buf = torch.full((M + 1, N + extra), 7.0, dtype=torch.bfloat16, device="cuda")
+        C = ff.matmul_blocks(_pitch16(a), _pitch16(b), sa.t().contiguous().cuda().t(), sb.cuda(), out=buf[:M, :N])
+        _accept(C, want, s, "bf16")
+        assert torch.all(buf[M:] == 7.0) and torch.all(buf[:, N:] == 7.0)
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 elements: their last rows against the same rows alone (enough of them that both take
+    the same kernel: those for few rows add up in another order)."""
+    M, K, F, tail_rows = (1 << 31) // 1024 + 40, 16, 1024, 10000
+    a = torch.randn((M, K), device="cuda").bfloat16()
+    w = _normal((2 * F, K), "bf16", 150).cuda()
+    one = ff.gated_matmul(a, w, layout=1, keep=True)
+    few = ff.gated_matmul(a[-tail_rows:].contiguous(), w, layout=1, keep=True)
+    assert torch.equal(one.c[-tail_rows:], few.c) and torch.equal(one.up[-tail_rows:], few.up)
+    big = ff.gated_matmul_backward(one.c, a, w, one.up, layout=1, weights=False).dA
+    small = ff.gated_matmul_backward(few.c, a[-tail_rows:].contiguous(), w, few.up, layout=1, weights=False).dA
+    assert torch.equal(big[-tail_rows:], small)
+    q, tail = ff.quantize_blocks(one.c), ff.quantize_blocks(few.c)
+    assert torch.equal(q.q[-tail_rows:].view(torch.uint8), tail.q.view(torch.uint8)) and torch.equal(q.scale[-tail_rows:], tail.scale)
+    t = ff.quantize_blocks(one.c, rows=128, transpose=True)
+    first = one.c[M - M % 128 if M % 128 else M - 128:].float().abs()
+    assert t.q.shape == (F, M)
+    want = torch.from_numpy(of.block_scales(_np(first.t()), 128)).float()
+    assert torch.allclose(t.scale[:, -1:].cpu(), want, rtol=1e-6)
+    b = ff.quantize_blocks(_normal((64, F), "bf16", 151).cuda())
+    c = ff.matmul_blocks(q.q, b.q, q.scale, b.scale)
+    assert torch.equal(c[-tail_rows:], ff.matmul_blocks(tail.q, b.q, tail.scale, b.scale))
+    del t, c
+    n = ff.layer_norm(one.c, torch.ones(F, device="cuda").bfloat16())
+    assert torch.equal(n.y[-tail_rows:], ff.layer_norm(few.c, torch.ones(F, device="cuda").bfloat16()).y)
+
+
+def test_from_several_threads():
+    """The calls from host threads at once, each on its own stream."""
+    import threading
+    cases, errors = [], []
+    for i in range(4):
+        args = _block_inputs(100 + 60 * i, 128 + 64 * i, 136 + 40 * i)
+        qa, qw = ff.quantize_blocks(args[0]), ff.quantize_blocks(args[4], rows=128)
+        y, n, g = _block(*args)
+        grads = _block_backward(y, n, g, args[2], args[4], args[5])
+        cases.append((args, qa, qw, y, grads, ff.matmul_blocks(qa.q, qw.q, qa.scale, qw.scale)))
+    torch.cuda.synchronize()
+
+    def work(args, qa, qw, y0, grads0, c0):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    y, n, g = _block(*args)
+                    grads = _block_backward(y, n, g, args[2], args[4], args[5])
+                    c = ff.matmul_blocks(qa.q, qw.q, qa.scale, qw.scale)
+                    torch.cuda.current_stream().synchronize()
+                    if not (torch.equal(y, y0) and torch.equal(c, c0) and all(torch.equal(a, b) for a, b in zip(grads, grads0))):
+                        errors.append("another result")
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[:2]
+
+
+def test_two_graphs_replayed_in_turn():
+    """Graphs that hold the same calls on other inputs keep their own scratch."""
+    graphs = []
+    for seed in (0, 1):
+        args = [t + seed for t in _block_inputs(70)]
+        y, n, g = _block(*args)
+        want = (y, *_block_backward(y, n, g, args[2], args[4], args[5]))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, n, g = _block(*args)
+            got = (y, *_block_backward(y, n, g, args[2], args[4], args[5]))
+        graphs.append((graph, got, want, args))
+    for _ in range(3):
+        for graph, _, _, _ in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _ in graphs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
