@@ -9,7 +9,7 @@
 // root-mean-square norm a row stays in its threads' registers, here between three
 // reductions: the mean, the squares of what is left of it (two passes over
 // registers: mean(h^2) - m^2 would cancel where the mean is large), and the 8-bit
-// scale. The ways to reach memory are in row.cuh.
+// scale. The ways to reach memory are row.cuh's; FLAT rows go by their shift.
 #include "row.cuh"
 
 #include "dgt_feedforward.h"
@@ -32,12 +32,131 @@ struct LayerParams {
   float eps;
 };
 
-// Column j of piece i is one of the row's (pieces past the row's end, and of the
-// rows around it where they are FLAT, are held as zeros and must not count as h - m).
+// A row as the thread's pieces, as in row.cuh, but for FLAT rows: a block has rows of one shift only (rows `VEC` apart
+// start at the same offset in their first piece), so that a thread's columns, its weights and its sums stay the same
+// from row to row, and all that sets these rows apart is a mask on the first and the last piece. (With any row in any
+// block, and weights and sums looked up by column, 8192 x 1023 BF16 took 53 us and its gradient 51; 8192 x 1024 11
+// and 22.)
 template <int MODE, int VEC>
-__device__ __forceinline__ bool column(const Row<MODE, VEC>& r, int i, int j) {
-  if constexpr (MODE == FLAT) return r.lo(i) + j >= 0 && r.lo(i) + j < r.cols;
-  return r.whole(i);
+struct Pieces {
+  int tid, tpr, cols, shift;
+
+  __device__ __forceinline__ int lo(int i) const { return (i * tpr + tid) * VEC - shift; }
+  __device__ __forceinline__ int place(int i) const { return (i * tpr + tid) * VEC; }  // in an array of the row's pieces
+  __device__ __forceinline__ bool whole(int i) const {
+    return MODE == FLAT ? lo(i) >= 0 && lo(i) + VEC <= cols : lo(i) < cols;
+  }
+  __device__ __forceinline__ bool any(int i) const { return (MODE != FLAT || lo(i) + VEC > 0) && lo(i) < cols; }
+  __device__ __forceinline__ bool has(int i, int j) const { return lo(i) + j >= 0 && lo(i) + j < cols; }
+  // what is not the row's is zero
+  template <int TYPE>
+  __device__ __forceinline__ void mask(Pack<TYPE, VEC>& v, int i) const {
+    if constexpr (MODE == FLAT)
+      if (!whole(i)) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (!has(i, j)) v.v[j] = Elem<TYPE>::put(0.0f);
+      }
+  }
+  // `last`: the matrix's last row, whose last piece may reach past its end. (The neighbours' elements that a piece
+  // brings along may be on their way out of another block, where an output takes the place of its input: they are
+  // masked, whatever they are.)
+  template <int TYPE>
+  __device__ __forceinline__ void load(Pack<TYPE, VEC>& v, const void* base, long long row, long long ld, int i, bool in,
+                                       bool last) const {
+    using T = typename Pack<TYPE, VEC>::T;
+    v.zero();
+    if (!in || !any(i)) return;
+    const T* p = static_cast<const T*>(base) + row * ld;
+    if (MODE == FLAT && last && lo(i) + VEC > cols) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (has(i, j)) v.v[j] = p[lo(i) + j];
+    } else {
+      v.stream(p + lo(i));
+      mask(v, i);
+    }
+  }
+  template <int TYPE>
+  __device__ __forceinline__ void store(const Pack<TYPE, VEC>& v, void* base, long long row, long long ld, int i,
+                                        bool in) const {
+    using T = typename Pack<TYPE, VEC>::T;
+    if (!in) return;
+    T* p = static_cast<T*>(base) + row * ld;
+    if (whole(i)) {
+      v.store(p + lo(i));
+    } else if constexpr (MODE == FLAT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (has(i, j)) p[lo(i) + j] = v.v[j];
+    }
+  }
+  __device__ __forceinline__ void store_q8(const float (&x)[VEC], void* base, long long row, long long ld, int i,
+                                           bool in) const {
+    if (!in) return;
+    uint8_t* p = static_cast<uint8_t*>(base) + row * ld;
+    if (whole(i)) {
+      store_e4m3<VEC>(p + lo(i), x);
+    } else if constexpr (MODE == FLAT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (has(i, j)) p[lo(i) + j] = __nv_cvt_float_to_fp8(x[j], __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+  // Columns' weights as fp32, zeros past the row: from memory (L1 holds them), or from the block's copy in the order
+  // of its pieces (FLAT).
+  template <int TYPE>
+  __device__ __forceinline__ void weights(float (&w)[VEC], const void* weight, const typename Elem<TYPE>::T* shared,
+                                          int i) const {
+    Pack<TYPE, VEC> v;
+    v.zero();
+    if constexpr (MODE == FLAT) {
+      if (any(i)) v.load(shared + place(i));
+    } else {
+      if (whole(i)) v.load(static_cast<const typename Elem<TYPE>::T*>(weight) + lo(i));
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = v.get(j);
+  }
+};
+
+// The rows of a block: all of them in turn, or those of one shift (FLAT).
+template <int MODE, int VEC>
+struct BlockRows {
+  int cls, first, blocks;
+  long long count;
+  __device__ __forceinline__ BlockRows(int rows) {
+    constexpr int CLASSES = MODE == FLAT ? VEC : 1;
+    cls = blockIdx.x % CLASSES;
+    first = blockIdx.x / CLASSES;
+    blocks = max(static_cast<int>(gridDim.x) / CLASSES, 1);  // (fewer rows than classes have a block each)
+    count = rows <= cls ? 0 : (static_cast<long long>(rows) - cls + CLASSES - 1) / CLASSES;
+  }
+  __device__ __forceinline__ long long row(long long q) const { return MODE == FLAT ? cls + VEC * q : q; }
+};
+
+// Pieces of a FLAT row of any shift.
+__host__ __device__ constexpr int flat_places(int cols, int vec) { return (cols + vec - 1 + vec - 1) / vec * vec; }
+
+// FLAT: weights in the order of the pieces, zeros around them.
+template <int TYPE, int VEC>
+__device__ __forceinline__ void stage_pieces(typename Elem<TYPE>::T* shared, const void* weight, int cols, int shift) {
+  using E = Elem<TYPE>;
+  const int n = flat_places(cols, VEC);
+  // (eight loads in flight: one at a time took 2.5 us)
+  for (int e0 = threadIdx.x; e0 < n; e0 += 8 * blockDim.x) {
+    typename E::T v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = e0 + k * static_cast<int>(blockDim.x) - shift;
+      v[k] = c >= 0 && c < cols ? static_cast<const typename E::T*>(weight)[c] : E::put(0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = e0 + k * static_cast<int>(blockDim.x);
+      if (e < n) shared[e] = v[k];
+    }
+  }
 }
 
 template <int TYPE, int MODE, int EPT, bool Q8>
@@ -50,28 +169,30 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
   __shared__ float red[2][3][32];
   extern __shared__ uint4 dynamic[];
   T* shared_w = reinterpret_cast<T*>(dynamic);
-  T* shared_b = shared_w + (MODE == FLAT ? (p.cols + VEC - 1) / VEC * VEC : 0);
+  T* shared_b = shared_w + (MODE == FLAT ? flat_places(p.cols, VEC) : 0);
   const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
-  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const BlockRows<MODE, VEC> rows(p.rows);
+  const Pieces<MODE, VEC> r = {static_cast<int>(threadIdx.x) - sub * p.tpr, p.tpr, p.cols,
+                               MODE == FLAT ? static_cast<int>(static_cast<long long>(rows.cls) * p.cols % VEC) : 0};
   const RowWarps row_warps(p.tpr, sub);
   grid_dependency_wait();
   if constexpr (MODE == FLAT) {
-    if (p.bias != nullptr) stage_weights<TYPE, VEC>(shared_b, p.bias, p.cols);
-    stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
+    stage_pieces<TYPE, VEC>(shared_w, p.weight, p.cols, r.shift);
+    if (p.bias != nullptr) stage_pieces<TYPE, VEC>(shared_b, p.bias, p.cols, r.shift);
+    __syncthreads();
   }
   int turn = 0;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows;
-       r0 += static_cast<long long>(gridDim.x) * per_block, turn ^= 1) {
-    const long long row = r0 + sub;
-    const bool in = row < p.rows;
-    r.at(row);
+  for (long long q0 = static_cast<long long>(rows.first) * per_block; q0 < rows.count;
+       q0 += static_cast<long long>(rows.blocks) * per_block, turn ^= 1) {
+    const long long row = rows.row(q0 + sub);
+    const bool in = q0 + sub < rows.count, last = row == p.rows - 1;
     P h[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in);
+    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in, last);
     if (p.residual != nullptr) {
       P a[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in);
+      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in, last);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float x[VEC];
@@ -99,18 +220,19 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
     s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (MODE == ALIGNED) {
-        if (r.whole(i)) {
+      if constexpr (MODE == SINGLE) {
+        const float d = r.whole(i) ? h[i].get(0) - mean : 0.0f;
+        s = fmaf(d, d, s);
+      } else if (r.whole(i)) {
 #pragma unroll
-          for (int j = 0; j < VEC; j += 2) {
-            const float2 d = __fadd2_rn(h[i].two(j), less);
-            s2 = __ffma2_rn(d, d, s2);
-          }
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 d = __fadd2_rn(h[i].two(j), less);
+          s2 = __ffma2_rn(d, d, s2);
         }
-      } else {
+      } else if constexpr (MODE == FLAT) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float d = column(r, i, j) ? h[i].get(j) - mean : 0.0f;
+          const float d = r.has(i, j) ? h[i].get(j) - mean : 0.0f;
           s = fmaf(d, d, s);
         }
       }
@@ -124,9 +246,9 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
     // the output of piece i, before its rounding
     auto norm = [&](float* y, int i) {
       float w[VEC], b[VEC];
-      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      r.template weights<TYPE>(w, p.weight, shared_w, i);
       if (p.bias != nullptr) {
-        load_weights<MODE, TYPE, VEC>(b, r, p.bias, shared_b, i);
+        r.template weights<TYPE>(b, p.bias, shared_b, i);
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) b[j] = 0.0f;
@@ -162,7 +284,7 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
         norm(y + i * VEC, i);
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-          if (column(r, i, j)) top = max(top, __float_as_uint(y[i * VEC + j]) & 0x7FFFFFFFu);
+          if (MODE == FLAT ? r.has(i, j) : r.whole(i)) top = max(top, __float_as_uint(y[i * VEC + j]) & 0x7FFFFFFFu);
       }
       const float amax = __uint_as_float(row_warps.max_bits(top, red[turn][2]));
       const float scale = (amax < 1e-12f ? 1e-12f : amax) / kE4M3Max;
@@ -181,6 +303,11 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
 }
 
 constexpr int kGradEpt = 16;  // elements of a row per thread of the gradient
+
+// cp.async of 16 bytes, of which `bytes` come from memory and the rest are zero.
+__device__ __forceinline__ void copy16_part(uint4* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 
 struct LayerGradParams {
   const void* dy;
@@ -216,14 +343,10 @@ __device__ __forceinline__ float2 sum_two(const RowWarps& w, float2 v, float2* r
   return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
 }
 
-// A thread owns the same columns of every row (ALIGNED, SINGLE) and adds dw and db
-// up in registers; FLAT rows move against the threads, and both are in shared
-// memory, where a column meets one thread a row and the rows' reductions separate
-// them. ALIGNED with AHEAD: each thread copies its pieces of the next row to its
-// own places in shared memory (cp.async) before it works on this one, so that
-// loads are in flight during the reduction and the stores, and reads a piece from
-// its place once for the sums and once for the output, so that registers hold one
-// piece at a time beside the 32 sums.
+// A thread owns the same columns of each of its rows and adds dw and db up in registers. AHEAD: each thread copies its
+// pieces of the next row to its own places in shared memory (cp.async) before it works on this one, so that loads are
+// in flight during the reduction and the stores, and reads a piece from its place once for the sums and once for the
+// output, so that registers hold one piece at a time beside the 32 sums.
 template <int TYPE, int MODE, bool AHEAD>
 __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_kernel(const LayerGradParams p) {
   constexpr int EPT = kGradEpt;
@@ -233,77 +356,83 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
   constexpr int NV = EPT / VEC;
   __shared__ float2 red[2][32];
   extern __shared__ uint4 dynamic[];
-  // ALIGNED, SINGLE: (rows of the block - 1) x 2 x cols partial sums; FLAT: dw and db of each row of the block, then
-  // the weights
-  float* sums = reinterpret_cast<float*>(dynamic);
-  const int places = (p.cols + VEC - 1) / VEC * VEC;
+  // FLAT: the weights; then the copies ahead, whose place (rows of the block - 1) x 2 rows of sums take at the end
+  T* shared_w = reinterpret_cast<T*>(dynamic);
+  uint4* stages = dynamic + (MODE == FLAT ? flat_places(p.cols, VEC) / VEC : 0);
+  float* sums = reinterpret_cast<float*>(stages);
+  const int places = MODE == FLAT ? flat_places(p.cols, VEC) : p.cols;
   const int per_block = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr;
-  T* shared_w = reinterpret_cast<T*>(sums + 2 * per_block * places);
-  Row<MODE, VEC> r(threadIdx.x - sub * p.tpr, p.tpr, p.cols);
+  const BlockRows<MODE, VEC> rows(p.rows);
+  const Pieces<MODE, VEC> r = {static_cast<int>(threadIdx.x) - sub * p.tpr, p.tpr, p.cols,
+                               MODE == FLAT ? static_cast<int>(static_cast<long long>(rows.cls) * p.cols % VEC) : 0};
   const RowWarps row_warps(p.tpr, sub);
-  const long long step = static_cast<long long>(gridDim.x) * per_block;
+  const long long step = static_cast<long long>(rows.blocks) * per_block;
   // AHEAD: piece i of h, dy or dh (m = 0, 1, 2) of stage s
-  auto cell = [&](int s, int m, int i) { return dynamic + ((s * 3 + m) * NV + i) * blockDim.x + threadIdx.x; };
-  auto fetch = [&](long long row, int s) {
+  auto cell = [&](int s, int m, int i) { return stages + ((s * 3 + m) * NV + i) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](long long q, int s) {
+    const long long row = rows.row(q);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (r.whole(i)) {
-        if (row < p.rows) {
-          copy16(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i));
-          copy16(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i));
-          if (p.dh != nullptr) copy16(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i));
+      if (r.any(i)) {
+        if (q < rows.count) {
+          // (the last piece of the last row may reach past the matrix: the copy reads what there is)
+          const bool cut = MODE == FLAT && row == p.rows - 1 && r.lo(i) + VEC > p.cols;
+          const int bytes = cut ? (p.cols - r.lo(i)) * int(sizeof(T)) : 16;
+          copy16_part(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i), bytes);
+          copy16_part(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i), bytes);
+          if (p.dh != nullptr) copy16_part(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i), bytes);
         } else if (per_block > 1) {  // a row past the last one counts as zeros
           *cell(s, 0, i) = *cell(s, 1, i) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const long long start = static_cast<long long>(blockIdx.x) * per_block + sub;
+  const long long start = static_cast<long long>(rows.first) * per_block + sub;
   grid_dependency_wait();
   if constexpr (AHEAD) {
     // zeros where no copy lands: past the last column, and dh where there is none
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       for (int c = 0; c < 6; ++c)
-        if (!r.whole(i) || (c % 3 == 2 && p.dh == nullptr)) *cell(c / 3, c % 3, i) = make_uint4(0u, 0u, 0u, 0u);
+        if (!r.any(i) || (c % 3 == 2 && p.dh == nullptr)) *cell(c / 3, c % 3, i) = make_uint4(0u, 0u, 0u, 0u);
     fetch(start, 0);
   }
+  if constexpr (MODE == FLAT) {
+    stage_pieces<TYPE, VEC>(shared_w, p.weight, p.cols, r.shift);
+    __syncthreads();
+  }
   // a row past the last one has dy = 0, mean = rstd = 0: it adds nothing
-  auto statistics = [&](long long row) {
-    return row < p.rows ? make_float2(p.mean[row], p.rstd[row]) : make_float2(0.0f, 0.0f);
+  auto statistics = [&](long long q) {
+    if (q >= rows.count) return make_float2(0.0f, 0.0f);
+    const long long row = rows.row(q);
+    return make_float2(p.mean[row], p.rstd[row]);
   };
   float2 next = AHEAD ? statistics(start) : make_float2(0.0f, 0.0f);
-  constexpr int SUMS = MODE == FLAT ? 1 : EPT;
-  alignas(8) float dw[SUMS], db[SUMS];
-  if constexpr (MODE == FLAT) {
-    for (int i = threadIdx.x; i < 2 * per_block * places; i += blockDim.x) sums[i] = 0.0f;
-    stage_weights<TYPE, VEC>(shared_w, p.weight, p.cols);
-  } else {
+  alignas(8) float dw[EPT], db[EPT];
 #pragma unroll
-    for (int e = 0; e < SUMS; ++e) dw[e] = db[e] = 0.0f;
-  }
+  for (int e = 0; e < EPT; ++e) dw[e] = db[e] = 0.0f;
   int turn = 0;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * per_block; r0 < p.rows; r0 += step, turn ^= 1) {
-    const long long row = r0 + sub;
-    const bool in = row < p.rows;
-    r.at(row);
+  for (long long q0 = static_cast<long long>(rows.first) * per_block; q0 < rows.count; q0 += step, turn ^= 1) {
+    const long long row = rows.row(q0 + sub);
+    const bool in = q0 + sub < rows.count;
     P h[NV], dy[NV], dh[NV];
     float2 stat;
     if constexpr (AHEAD) {
-      fetch(row + step, turn ^ 1);
+      fetch(q0 + sub + step, turn ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");  // this row's pieces have landed
       stat = next;
-      next = statistics(row + step);
+      next = statistics(q0 + sub + step);
     } else {
-      stat = statistics(row);
+      stat = statistics(q0 + sub);
+      const bool last = row == p.rows - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        r.load(h[i], p.h, row, p.ldh, i, in);
-        r.load(dy[i], p.dy, row, p.lddy, i, in);
+        r.load(h[i], p.h, row, p.ldh, i, in, last);
+        r.load(dy[i], p.dy, row, p.lddy, i, in, last);
       }
       if (p.dh != nullptr) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in);
+        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in, last);
       } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) dh[i].zero();
@@ -314,16 +443,18 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
     auto take = [&](P(&v)[NV], int m, int i) {
       if constexpr (AHEAD) v[i].load(reinterpret_cast<const T*>(cell(turn, m, i)));
     };
-    // sums of g and of g xhat (outside the row dy is 0, and so is what is added); ALIGNED takes two elements to an
-    // instruction
+    // sums of g and of g xhat (outside the row dy is 0, and so is what is added); two elements to an instruction where
+    // a piece has two
     float2 dots = make_float2(0.0f, 0.0f), gs = dots, gx = dots;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if (!r.any(i)) continue;
       float w[VEC];
-      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      r.template weights<TYPE>(w, p.weight, shared_w, i);
       take(h, 0, i);
       take(dy, 1, i);
-      if constexpr (MODE == ALIGNED) {
+      if constexpr (AHEAD) r.mask(dy[i], i);
+      if constexpr (VEC > 1) {
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
           const float2 xhat = __fmul2_rn(__fadd2_rn(h[i].two(j), make_float2(-mean, -mean)), make_float2(rstd, rstd));
@@ -336,39 +467,25 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
           sb = __fadd2_rn(sb, d);
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xhat = (h[i].get(j) - mean) * rstd, d = dy[i].get(j), g = d * w[j];
-          if constexpr (MODE == FLAT) {
-            if (in && column(r, i, j)) {
-              dots.x += g;
-              dots.y = fmaf(g, xhat, dots.y);
-              float* at = sums + 2 * sub * places + r.place(i, j);
-              at[0] += d * xhat;
-              at[places] += d;
-            }
-          } else {
-            dots.x += g;
-            dots.y = fmaf(g, xhat, dots.y);
-            dw[i * VEC + j] = fmaf(d, xhat, dw[i * VEC + j]);
-            db[i * VEC + j] += d;
-          }
-        }
+        const float xhat = (h[i].get(0) - mean) * rstd, d = dy[i].get(0), g = d * w[0];
+        dots.x += g;
+        dots.y = fmaf(g, xhat, dots.y);
+        dw[i] = fmaf(d, xhat, dw[i]);
+        db[i] += d;
       }
     }
-    if constexpr (MODE == ALIGNED) dots = make_float2(gs.x + gs.y, gx.x + gx.y);
+    if constexpr (VEC > 1) dots = make_float2(gs.x + gs.y, gx.x + gx.y);
     dots = sum_two(row_warps, dots, red[turn]);
     const float mean_g = dots.x / static_cast<float>(p.cols), back = rstd * (dots.y / static_cast<float>(p.cols));
-    if (MODE == FLAT && p.tpr <= 32) __syncwarp();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float w[VEC];
-      load_weights<MODE, TYPE, VEC>(w, r, p.weight, shared_w, i);
+      r.template weights<TYPE>(w, p.weight, shared_w, i);
       take(h, 0, i);
       take(dy, 1, i);
       take(dh, 2, i);
       P o;
-      if constexpr (MODE == ALIGNED) {
+      if constexpr (VEC > 1) {
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
           const float2 xhat = __fmul2_rn(__fadd2_rn(h[i].two(j), make_float2(-mean, -mean)), make_float2(rstd, rstd));
@@ -378,9 +495,7 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
           w[j + 1] = v.y;
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          w[j] = fmaf(fmaf(dy[i].get(j), w[j], -mean_g), rstd, fmaf((h[i].get(j) - mean) * rstd, -back, dh[i].get(j)));
+        w[0] = fmaf(fmaf(dy[i].get(0), w[0], -mean_g), rstd, fmaf((h[i].get(0) - mean) * rstd, -back, dh[i].get(0)));
       }
       o.set(w);
       r.store(o, p.dx, row, p.lddx, i, in);
@@ -388,57 +503,53 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
   }
   if constexpr (AHEAD) asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
-  if constexpr (MODE == FLAT) {
+  // the block's sums over its rows, in row order; four columns at a time
+  constexpr int RUN = VEC < 4 ? 1 : 4;
+  auto each = [&](auto use) {
+#pragma unroll
+    for (int e = 0; e < EPT; e += RUN)
+      if (r.any(e / VEC)) use(r.place(e / VEC) + e % VEC, e);
+  };
+  auto store = [&](float* to, const float* from) {
+    if constexpr (RUN == 1)
+      *to = *from;
+    else
+      *reinterpret_cast<float4*>(to) = make_float4(from[0], from[1], from[2], from[3]);
+  };
+  if (per_block > 1) {
     __syncthreads();
-    const int per = places / VEC;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-      float s = 0.0f, t = 0.0f;
-      for (int i = 0; i < per_block; ++i) {
-        const float* at = sums + 2 * i * places + (c % VEC) * per + c / VEC;
-        s += at[0];
-        t += at[places];
-      }
-      out[c] = s;
-      out[p.cols + c] = t;
-    }
-  } else {
-    // the block's sums over its rows, in row order; four columns a store
-    constexpr int RUN = VEC < 4 ? 1 : 4;
-    auto each = [&](auto use) {
-#pragma unroll
-      for (int e = 0; e < EPT; e += RUN)
-        if (r.whole(e / VEC)) use(r.lo(e / VEC) + e % VEC, e);
-    };
-    auto store = [&](float* to, const float* from) {
-      if constexpr (RUN == 1)
-        *to = *from;
-      else
-        *reinterpret_cast<float4*>(to) = make_float4(from[0], from[1], from[2], from[3]);
-    };
-    if (per_block > 1) {
-      __syncthreads();
-      if (sub > 0)
-        each([&](int c, int e) {
-          store(sums + 2 * (sub - 1) * p.cols + c, dw + e);
-          store(sums + (2 * (sub - 1) + 1) * p.cols + c, db + e);
-        });
-      __syncthreads();
-      if (sub == 0)
-        for (int s = 0; s + 1 < per_block; ++s)
-          each([&](int c, int e) {
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-              dw[e + k] += sums[2 * s * p.cols + c + k];
-              db[e + k] += sums[(2 * s + 1) * p.cols + c + k];
-            }
-          });
-    }
-    if (sub == 0)
-      each([&](int c, int e) {
-        store(out + c, dw + e);
-        store(out + p.cols + c, db + e);
+    if (sub > 0)
+      each([&](int at, int e) {
+        store(sums + 2 * (sub - 1) * places + at, dw + e);
+        store(sums + (2 * (sub - 1) + 1) * places + at, db + e);
       });
+    __syncthreads();
+    if (sub == 0)
+      for (int s = 0; s + 1 < per_block; ++s)
+        each([&](int at, int e) {
+#pragma unroll
+          for (int k = 0; k < RUN; ++k) {
+            dw[e + k] += sums[2 * s * places + at + k];
+            db[e + k] += sums[(2 * s + 1) * places + at + k];
+          }
+        });
   }
+  if (sub == 0)
+    each([&](int at, int e) {
+      if constexpr (MODE == FLAT) {
+#pragma unroll
+        for (int k = 0; k < RUN; ++k) {
+          const int c = at + k - r.shift;
+          if (c >= 0 && c < p.cols) {
+            out[c] = dw[e + k];
+            out[p.cols + c] = db[e + k];
+          }
+        }
+      } else {
+        store(out + at, dw + e);
+        store(out + p.cols + at, db + e);
+      }
+    });
   grid_launch_dependents();
 }
 
@@ -480,39 +591,65 @@ int64_t grad_blocks(int64_t cols) {
   return int64_t(152) * (fit < 1 ? 1 : fit);
 }
 
-template <int TYPE, int MODE, int EPT>
-cudaError_t launch_layer_mode(const LayerParams& p, bool q8, int grid, int block, size_t smem, cudaStream_t s) {
-  return q8 ? launch_dependent(layernorm_kernel<TYPE, MODE, EPT, true>, grid, block, smem, s, 1, p)
-            : launch_dependent(layernorm_kernel<TYPE, MODE, EPT, false>, grid, block, smem, s, 1, p);
+// Blocks of `per` rows for `rows` of them, `most` at most. FLAT: as many for each of the v shifts that rows have.
+int grid_of(int mode, int v, int64_t rows, int per, int64_t most) {
+  const int64_t classes = mode != FLAT ? 1 : rows < v ? rows : v;
+  const int64_t need = ((rows + classes - 1) / classes + per - 1) / per, fit = most / classes < 1 ? 1 : most / classes;
+  return int(classes * (need < fit ? need : fit));
 }
 
-// Most columns of a FLAT row whose weights and bias fit the 48 KB that a launch may take without asking.
+template <int TYPE, int MODE, int EPT, bool Q8>
+cudaError_t launch_layer_build(const LayerParams& p, int dev, int grid, int block, size_t smem, cudaStream_t s) {
+  auto kern = layernorm_kernel<TYPE, MODE, EPT, Q8>;
+  if constexpr (MODE == FLAT) {  // weights and bias of the widest rows are more than a launch may take without asking
+    static int configured[64] = {};
+    if (dev >= 64 || !__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+      constexpr int es = sizeof(typename Elem<TYPE>::T);
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 2 * flat_places(kMaxFlatCols, 16 / es) * es);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    }
+  }
+  return launch_dependent(kern, grid, block, smem, s, 1, p);
+}
+template <int TYPE, int MODE, int EPT>
+cudaError_t launch_layer_mode(const LayerParams& p, bool q8, int dev, int grid, int block, size_t smem, cudaStream_t s) {
+  return q8 ? launch_layer_build<TYPE, MODE, EPT, true>(p, dev, grid, block, smem, s)
+            : launch_layer_build<TYPE, MODE, EPT, false>(p, dev, grid, block, smem, s);
+}
+
+// Elements a thread holds of a FLAT row: 32 bytes' worth, or 64 of rows of 12000 bytes and more. us with 32 / 64: BF16
+// 30000 x 77 34 / 64, 8192 x 1023 34 / 42, 2048 x 4095 30 / 36, 8192 x 8191 234 / 188; FP32 30000 x 77 20 / 34, 2048 x
+// 4095 54 / 42.
 template <int TYPE>
-constexpr int64_t kFlatCols = TYPE == GEMM_TYPE_F32 ? 6000 : kMaxFlatCols;
+constexpr int kFlatEpt = 32 / int(sizeof(typename Elem<TYPE>::T));
+bool wide_flat(int64_t cols, int es) { return cols * es > 12000; }
 
 template <int TYPE>
-cudaError_t launch_layer(const LayerParams& p, int mode, bool few, bool q8, int grid, int block, cudaStream_t s) {
-  const size_t smem = mode == FLAT ? 2 * size_t(p.cols + 8) * sizeof(typename Elem<TYPE>::T) : 0;
+cudaError_t launch_layer(const LayerParams& p, int mode, bool few, bool q8, int dev, int grid, int block, cudaStream_t s) {
+  constexpr int es = sizeof(typename Elem<TYPE>::T);
+  const size_t smem = mode == FLAT ? 2 * size_t(flat_places(p.cols, 16 / es)) * es : 0;
   if (mode == ALIGNED)
-    return few ? launch_layer_mode<TYPE, ALIGNED, 8>(p, q8, grid, block, smem, s)
-               : launch_layer_mode<TYPE, ALIGNED, kFullEpt<TYPE, ALIGNED>>(p, q8, grid, block, smem, s);
+    return few ? launch_layer_mode<TYPE, ALIGNED, 8>(p, q8, dev, grid, block, smem, s)
+               : launch_layer_mode<TYPE, ALIGNED, kFullEpt<TYPE, ALIGNED>>(p, q8, dev, grid, block, smem, s);
   if (mode == FLAT)
-    return few ? launch_layer_mode<TYPE, FLAT, 8>(p, q8, grid, block, smem, s)
-               : launch_layer_mode<TYPE, FLAT, kFullEpt<TYPE, FLAT>>(p, q8, grid, block, smem, s);
-  return few ? launch_layer_mode<TYPE, SINGLE, 8>(p, q8, grid, block, smem, s)
-             : launch_layer_mode<TYPE, SINGLE, kFullEpt<TYPE, SINGLE>>(p, q8, grid, block, smem, s);
+    return few                        ? launch_layer_mode<TYPE, FLAT, 8>(p, q8, dev, grid, block, smem, s)
+           : wide_flat(p.cols, es)    ? launch_layer_mode<TYPE, FLAT, kFullEpt<TYPE, FLAT>>(p, q8, dev, grid, block, smem, s)
+                                      : launch_layer_mode<TYPE, FLAT, kFlatEpt<TYPE>>(p, q8, dev, grid, block, smem, s);
+  return few ? launch_layer_mode<TYPE, SINGLE, 8>(p, q8, dev, grid, block, smem, s)
+             : launch_layer_mode<TYPE, SINGLE, kFullEpt<TYPE, SINGLE>>(p, q8, dev, grid, block, smem, s);
 }
 
 // Dynamic shared memory of the gradient's kernel.
 size_t grad_smem(const LayerGradParams& p, int mode, bool ahead, int block, int es) {
-  if (mode == FLAT) return size_t(p.cols + 8) * (2 * size_t(block / p.tpr) * sizeof(float) + es);
-  const size_t sums = 2 * size_t(block / p.tpr - 1) * size_t(p.cols) * sizeof(float);
+  const size_t places = mode == FLAT ? flat_places(p.cols, 16 / es) : p.cols;
+  const size_t sums = 2 * size_t(block / p.tpr - 1) * places * sizeof(float);
   const size_t stages = ahead ? size_t(2 * 3) * kGradEpt * es * size_t(block) : 0;
-  return sums > stages ? sums : stages;
+  return (mode == FLAT ? places * es : 0) + (sums > stages ? sums : stages);
 }
 
-// Most dynamic shared memory that a launch of the gradient takes: AHEAD goes up to here, and a FLAT row of
-// kMaxFlatCols has 132 KB.
+// Most dynamic shared memory that a launch of the gradient takes: AHEAD goes up to here.
 constexpr size_t kGradSmem = 200 * 1024;
 
 // Launches one build of the gradient's kernel. Its limit is a property of the kernel, not of the launch, so it is set
@@ -534,11 +671,12 @@ template <int TYPE>
 cudaError_t launch_layer_grad(const LayerGradParams& p, int mode, bool ahead, int dev, int grid, int block, void* dw,
                               void* db, cudaStream_t s) {
   const size_t smem = grad_smem(p, mode, ahead, block, sizeof(typename Elem<TYPE>::T));
-  const cudaError_t e = mode == ALIGNED
-                            ? (ahead ? launch_layer_grad_mode<TYPE, ALIGNED, true>(p, dev, grid, block, smem, s)
-                                     : launch_layer_grad_mode<TYPE, ALIGNED, false>(p, dev, grid, block, smem, s))
-                        : mode == FLAT ? launch_layer_grad_mode<TYPE, FLAT, false>(p, dev, grid, block, smem, s)
-                                       : launch_layer_grad_mode<TYPE, SINGLE, false>(p, dev, grid, block, smem, s);
+  const cudaError_t e =
+      mode == ALIGNED ? (ahead ? launch_layer_grad_mode<TYPE, ALIGNED, true>(p, dev, grid, block, smem, s)
+                               : launch_layer_grad_mode<TYPE, ALIGNED, false>(p, dev, grid, block, smem, s))
+      : mode == FLAT  ? (ahead ? launch_layer_grad_mode<TYPE, FLAT, true>(p, dev, grid, block, smem, s)
+                               : launch_layer_grad_mode<TYPE, FLAT, false>(p, dev, grid, block, smem, s))
+                      : launch_layer_grad_mode<TYPE, SINGLE, false>(p, dev, grid, block, smem, s);
   if (e != cudaSuccess) return e;
   return launch_dependent(layer_weight_sum_kernel<TYPE>, (2 * p.cols + 31) / 32, 1024, 0, s, 1, p.partial, grid, p.cols,
                           dw, db);
@@ -601,7 +739,7 @@ int gemm_layernorm(int type, int64_t rows, int64_t cols, const void* x, int64_t 
       (residual == nullptr || aligned(residual, ldr, es, 16)) && (h == nullptr || aligned(h, ldh, es, 16)) &&
       aligned(y, ldy, eo, v * eo))
     mode = ALIGNED;
-  else if (cols <= (es == 4 ? kFlatCols<GEMM_TYPE_F32> : kFlatCols<GEMM_TYPE_BF16>) && flat(x, ldx, cols, 16) &&
+  else if (cols <= kMaxFlatCols && flat(x, ldx, cols, 16) &&
            (residual == nullptr || flat(residual, ldr, cols, 16)) && (h == nullptr || flat(h, ldh, cols, 16)) &&
            flat(y, ldy, cols, v * eo))
     mode = FLAT;
@@ -610,16 +748,13 @@ int gemm_layernorm(int type, int64_t rows, int64_t cols, const void* x, int64_t 
   // Eight elements a thread while the rows leave threads to spare, 64 bytes' worth once they fill the GPU and past
   // what 1024 threads hold (the root-mean-square norm's rule: its loads and reductions are these).
   const bool few = cols <= 8000 && rows * cols <= int64_t(ctx.sm_count) * 8192;
-  p.tpr = threads_per_row(cols, few ? 8 : mode == SINGLE ? 16 : 64 / es, mode, v);
-  const int least = mode == FLAT && !few ? 512 : 128;  // FLAT blocks stage the weights: few that take many rows
-  const int block = p.tpr < least ? least / p.tpr * p.tpr : p.tpr;
-  const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
-  const int64_t most = int64_t(ctx.sm_count) * (mode == FLAT ? 1024 / block + 1 : 2048 / block);
-  const int grid = int(need < most ? need : most);
+  p.tpr = threads_per_row(cols, few ? 8 : mode == SINGLE ? 16 : mode == FLAT && !wide_flat(cols, es) ? 32 / es : 64 / es, mode, v);
+  const int block = p.tpr < 128 ? 128 / p.tpr * p.tpr : p.tpr;
+  const int grid = grid_of(mode, v, rows, block / p.tpr, int64_t(ctx.sm_count) * (2048 / block));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_layer<GEMM_TYPE_F16>(p, mode, few, q8, grid, block, s)
-                        : type == GEMM_TYPE_BF16 ? launch_layer<GEMM_TYPE_BF16>(p, mode, few, q8, grid, block, s)
-                                                 : launch_layer<GEMM_TYPE_F32>(p, mode, few, q8, grid, block, s);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_layer<GEMM_TYPE_F16>(p, mode, few, q8, ctx.dev, grid, block, s)
+                        : type == GEMM_TYPE_BF16 ? launch_layer<GEMM_TYPE_BF16>(p, mode, few, q8, ctx.dev, grid, block, s)
+                                                 : launch_layer<GEMM_TYPE_F32>(p, mode, few, q8, ctx.dev, grid, block, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -682,9 +817,8 @@ int gemm_layernorm_backward(int type, int64_t rows, int64_t cols, const void* dy
                        (long long)ldh, (long long)lddh, (long long)lddx, int(rows), int(cols), 0};
   p.tpr = threads_per_row(cols, kGradEpt, mode, v);
   const int block = p.tpr >= kGradThreads ? p.tpr : kGradThreads / p.tpr * p.tpr;
-  const bool ahead = mode == ALIGNED && grad_smem(p, mode, true, block, es) <= kGradSmem;
-  const int64_t need = (rows + block / p.tpr - 1) / (block / p.tpr);
-  const int grid = int(need < grad_blocks(cols) ? need : grad_blocks(cols));
+  const bool ahead = mode != SINGLE && grad_smem(p, mode, true, block, es) <= kGradSmem;
+  const int grid = grid_of(mode, v, rows, block / p.tpr, rows < grad_blocks(cols) ? rows : grad_blocks(cols));
   const cudaError_t e =
       type == GEMM_TYPE_F16    ? launch_layer_grad<GEMM_TYPE_F16>(p, mode, ahead, ctx.dev, grid, block, dw, db, s)
       : type == GEMM_TYPE_BF16 ? launch_layer_grad<GEMM_TYPE_BF16>(p, mode, ahead, ctx.dev, grid, block, dw, db, s)
