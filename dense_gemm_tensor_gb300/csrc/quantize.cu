@@ -26,6 +26,7 @@ struct QuantParams {
   int tall, transpose;
   int tiles_x;         // tiles across x's columns
   int shares;          // thread blocks that share a group of rows
+  int wide_q;          // q's rows start on 16-byte boundaries
 };
 
 // The scale of a block whose largest |t| has these bits (a NaN is above every number), and its reciprocal.
@@ -47,17 +48,55 @@ __device__ __forceinline__ uint32_t four_e4m3(float a, float b, float c, float d
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
 
-// Blocks along x's rows. A row's block is LANES lanes of VEC elements, 128 in all; a warp has neighbouring rows of
-// the same block column, so that their scales, block by block, lie together; a thread block walks along its rows with
-// the next block's elements in flight. WIDE: rows in 16-byte pieces; else elements one by one.
-template <int TYPE, int VEC, bool WIDE>
+// 16 bytes of a row from `src` on, of which `valid` elements are the row's; the others are zero. SHIFT: src is
+// anywhere. 16-bit elements are then shifted together from the two aligned pieces that hold them (the second is read
+// where it holds some of the row's: an aligned piece with a byte of the matrix is in its memory); FP32 ones are read
+// one by one. (2048 x 4095 BF16 8.6 us shifted, 11.8 one by one; FP32 14.2 and 13.2.)
+template <int TYPE, bool SHIFT>
+__device__ __forceinline__ void load_piece(Pack<TYPE, 16 / int(sizeof(typename Elem<TYPE>::T))>& v,
+                                           const typename Elem<TYPE>::T* src, int valid) {
+  using T = typename Elem<TYPE>::T;
+  constexpr int PER = 16 / sizeof(T);
+  v.zero();
+  if (valid <= 0) return;
+  if constexpr (!SHIFT) {
+    v.stream(src);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (j < valid) v.v[j] = src[j];
+  } else {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+    const int m = static_cast<int>(at & 15);
+    const uint4 lo = *reinterpret_cast<const uint4*>(at - m);
+    uint4 hi = make_uint4(0u, 0u, 0u, 0u);
+    if (m + valid * int(sizeof(T)) > 16) hi = *reinterpret_cast<const uint4*>(at - m + 16);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t a[6], b[5], o[4];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) a[k] = m & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) b[k] = m & 4 ? a[k + 1] : a[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(b[k], b[k + 1], (m & 3) * 8);
+    *reinterpret_cast<uint4*>(v.v) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (valid < PER) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (j >= valid) v.v[j] = Elem<TYPE>::put(0.0f);
+  }
+}
+
+// Blocks along x's rows. Eight lanes have a row's block, 16 elements each; a warp has neighbouring rows of the same
+// block column, so that their scales, block by block, lie together; a thread block walks along its rows with the next
+// block's elements in flight.
+template <int TYPE, bool SHIFT>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
   using E = Elem<TYPE>;
   using T = typename E::T;
-  constexpr int LANES = kBlock / VEC;
-  constexpr int ROWS = 256 / LANES;  // of a thread block
-  constexpr int PER = 16 / sizeof(T), PIECES = WIDE ? VEC / PER : 1;
-  using P = Pack<TYPE, WIDE ? PER : 1>;
+  constexpr int VEC = 16, LANES = kBlock / VEC, ROWS = 256 / LANES;
+  constexpr int PER = 16 / sizeof(T), PIECES = VEC / PER;
   const int blocks = (p.cols + kBlock - 1) / kBlock;
   const int lane = threadIdx.x % LANES;
   // blockIdx.x: a group of rows and a share of their blocks
@@ -69,28 +108,18 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
   const bool in = row < p.rows;
   const T* src = static_cast<const T*>(p.x) + row * p.ldx;
   grid_dependency_wait();
-  P next[WIDE ? PIECES : VEC];
+  Pack<TYPE, PER> next[PIECES];
   auto load = [&](int b) {
     const int c0 = b * kBlock + lane * VEC;
-    if constexpr (WIDE) {
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        next[i].zero();
-        if (in && b < b1 && c0 + i * PER < p.cols) next[i].stream(src + c0 + i * PER);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        next[j].zero();
-        if (in && b < b1 && c0 + j < p.cols) next[j].load(src + c0 + j);
-      }
-    }
+    for (int i = 0; i < PIECES; ++i)
+      load_piece<TYPE, SHIFT>(next[i], src + c0 + i * PER, in && b < b1 ? p.cols - c0 - i * PER : 0);
   };
   load(b0);
   for (int b = b0; b < b1; ++b) {
     float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = WIDE ? next[j / PER].get(j % PER) : next[WIDE ? 0 : j].get(0);
+    for (int j = 0; j < VEC; ++j) v[j] = next[j / PER].get(j % PER);
     load(b + 1);
     uint32_t top = 0;
 #pragma unroll
@@ -105,14 +134,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
     for (int j = 0; j < VEC; ++j) v[j] *= inv;
     const int c0 = b * kBlock + lane * VEC;
     uint8_t* dst = p.q + row * p.ldq + c0;
-    if constexpr (WIDE) {
-      if (c0 < p.cols) {
-        uint32_t w[VEC / 4];
+    if (p.wide_q && c0 + VEC <= p.cols) {
+      uint32_t w[VEC / 4];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) w[i] = four_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        static_assert(VEC == 16, "a 16-byte store");
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int i = 0; i < VEC / 4; ++i) w[i] = four_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
@@ -125,11 +151,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
 // A 128 x 128 tile of x: blocks of the whole tile (tall) or along x's columns (transposed, not tall). A thread holds
 // 8 x 8 elements in registers; the transposed q goes through shared memory, 8 rows of a column (8 bytes) at a time, in
 // an order in which 16 threads meet 16 places: piece k of column c sits at k ^ (c / 8).
-template <int TYPE, bool WIDE>
+template <int TYPE, bool SHIFT>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantParams p) {
   using E = Elem<TYPE>;
   using T = typename E::T;
-  constexpr int PER = WIDE ? 16 / sizeof(T) : 1, PIECES = 8 / PER;
+  constexpr int PER = 16 / sizeof(T), PIECES = 8 / PER;
   using P = Pack<TYPE, PER>;
   __shared__ uint32_t tops[16][kBlock];
   __shared__ float col_inv[kBlock];
@@ -143,10 +169,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantParams p)
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int k = 0; k < PIECES; ++k) {
-      x[i][k].zero();
-      if (rg * 8 + i < nr && cg * 8 + k * PER < nc) x[i][k].stream(src + i * p.ldx + k * PER);
-    }
+    for (int k = 0; k < PIECES; ++k)
+      load_piece<TYPE, SHIFT>(x[i][k], src + i * p.ldx + k * PER, rg * 8 + i < nr ? nc - cg * 8 - k * PER : 0);
   auto at = [&](int i, int j) { return x[i][j / PER].get(j % PER); };
   const int rb = r0 / kBlock, cb = c0 / kBlock;
   float inv[8];
@@ -231,10 +255,9 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantParams p)
 }
 
 template <int TYPE>
-cudaError_t launch_quantize(QuantParams p, bool wide_x, bool wide_q, cudaStream_t s) {
+cudaError_t launch_quantize(QuantParams p, bool shift, cudaStream_t s) {
   if (p.tall == 1 && !p.transpose) {
-    const bool wide = wide_x && wide_q;
-    const int rows = wide ? 256 / (kBlock / 16) : 256 / (kBlock / 4);  // of a thread block
+    constexpr int rows = 256 / (kBlock / 16);  // of a thread block
     const int64_t groups = (int64_t(p.rows) + rows - 1) / rows, blocks = (p.cols + kBlock - 1) / kBlock;
     // about eight blocks of a row each, or as many thread blocks as keep the GPU busy. 8192 x 8192 BF16, shares of a
     // row's 64 blocks 2 / 4 / 8 / 16 / 64: 36.2 / 35.4 / 31.4 / 33.9 / 45.4 us; 8192 x 1024, 1 / 2 / 4 / 8: 6.8 / 5.3 /
@@ -242,12 +265,12 @@ cudaError_t launch_quantize(QuantParams p, bool wide_x, bool wide_q, cudaStream_
     const int64_t fill = (512 + groups - 1) / groups, want = fill > blocks / 8 ? fill : blocks / 8;
     p.shares = int(want < blocks ? want : blocks);
     const int grid = int(groups * p.shares);
-    return wide ? launch_dependent(quantize_rows_kernel<TYPE, 16, true>, grid, 256, 0, s, 1, p)
-                : launch_dependent(quantize_rows_kernel<TYPE, 4, false>, grid, 256, 0, s, 1, p);
+    return shift ? launch_dependent(quantize_rows_kernel<TYPE, true>, grid, 256, 0, s, 1, p)
+                 : launch_dependent(quantize_rows_kernel<TYPE, false>, grid, 256, 0, s, 1, p);
   }
   const int64_t tiles = int64_t(p.tiles_x) * ((p.rows + kBlock - 1) / kBlock);
-  return wide_x ? launch_dependent(quantize_tile_kernel<TYPE, true>, int(tiles), 256, 0, s, 1, p)
-                : launch_dependent(quantize_tile_kernel<TYPE, false>, int(tiles), 256, 0, s, 1, p);
+  return shift ? launch_dependent(quantize_tile_kernel<TYPE, true>, int(tiles), 256, 0, s, 1, p)
+               : launch_dependent(quantize_tile_kernel<TYPE, false>, int(tiles), 256, 0, s, 1, p);
 }
 
 bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) % size) != 0; }
@@ -294,14 +317,13 @@ extern "C" int gemm_quantize_blocks(int type, int64_t rows, int64_t cols, const 
   const int st = begin_call(&ctx);
   if (st != GEMM_OK) return st;
   if (!on_device(x, ctx.dev) || !on_device(q, ctx.dev) || !on_device(scale, ctx.dev)) return GEMM_ERR_NOT_DEVICE_MEMORY;
-  // 16-byte pieces, where every row of x starts on one and is made of them; q's rows in pieces of 16 elements
-  const bool wide_x = cols % (16 / es) == 0 && !misaligned(x, 16) && (rows == 1 || (ldx * es) % 16 == 0);
-  const bool wide_q = cols % 16 == 0 && !misaligned(q, 16) && (rows == 1 || ldq % 16 == 0);
+  const bool shift = misaligned(x, 16) || (rows > 1 && (ldx * es) % 16 != 0);
+  const bool wide_q = !misaligned(q, 16) && (rows == 1 || ldq % 16 == 0);
   QuantParams p = {x,          q,         scale,          (long long)ldx, (long long)ldq, (long long)s_row, (long long)s_block,
-                   int(rows),  int(cols), block_rows,     transpose,      int((cols + kBlock - 1) / kBlock), 1};
+                   int(rows),  int(cols), block_rows,     transpose,      int((cols + kBlock - 1) / kBlock), 1, wide_q};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_quantize<GEMM_TYPE_F16>(p, wide_x, wide_q, s)
-                        : type == GEMM_TYPE_BF16 ? launch_quantize<GEMM_TYPE_BF16>(p, wide_x, wide_q, s)
-                                                 : launch_quantize<GEMM_TYPE_F32>(p, wide_x, wide_q, s);
+  const cudaError_t e = type == GEMM_TYPE_F16    ? launch_quantize<GEMM_TYPE_F16>(p, shift, s)
+                        : type == GEMM_TYPE_BF16 ? launch_quantize<GEMM_TYPE_BF16>(p, shift, s)
+                                                 : launch_quantize<GEMM_TYPE_F32>(p, shift, s);
   return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
