@@ -12,7 +12,8 @@
 // else two, for more tiles than SMs. Warps: 0-3 take the sums out of tensor memory,
 // 4 loads by TMA, 5 issues tcgen05.mma.
 // The plain product (gate < 0; the gradient of A) is the same with 128 neighbouring
-// columns to a tile.
+// columns to a tile. 16 x 4096 -> 2 x 8192 BF16 24.8 us (5.4 TB/s; the bytes 19.8,
+// the rest is the launch, the first loads and the join), -> 2 x 2048 9.7.
 #pragma once
 
 #include "dgt_feedforward.h"

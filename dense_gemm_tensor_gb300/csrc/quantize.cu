@@ -5,6 +5,8 @@
 // Bound by HBM: x is read once, into registers, and q written once. Two kernels:
 // blocks of 1 x 128 along x's rows (a part of a warp has a block), and tiles of
 // 128 x 128 (blocks of a whole tile, or along x's columns), plain or transposed.
+// 8192 x 8192 BF16 32 us in every form (6.2 TB/s), FP32 54-57 (6.0), 4099 x 5120 BF16
+// transposed 11.3 (5.6).
 #include "elem.cuh"
 #include "host.h"
 #include "ptx.cuh"
