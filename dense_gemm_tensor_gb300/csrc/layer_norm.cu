@@ -38,7 +38,7 @@ struct LayerParams {
 // A row as the thread's pieces, as in row.cuh, but for FLAT rows: a block has rows of one shift only (rows `VEC` apart
 // start at the same offset in their first piece), so that a thread's columns, its weights and its sums stay the same
 // from row to row, and all that sets these rows apart is a mask on the first and the last piece. (With any row in any
-// block, and weights and sums looked up by column, 8192 x 1023 BF16 took 53 us and its gradient 51; 8192 x 1024 11
+// block, and weights and sums looked up by column, 8192 x 1023 BF16 took 53 us and its gradient 51, now 34 and 33; 8192 x 1024 11
 // and 22.)
 template <int MODE, int VEC>
 struct Pieces {
@@ -51,27 +51,30 @@ struct Pieces {
   }
   __device__ __forceinline__ bool any(int i) const { return (MODE != FLAT || lo(i) + VEC > 0) && lo(i) < cols; }
   __device__ __forceinline__ bool has(int i, int j) const { return lo(i) + j >= 0 && lo(i) + j < cols; }
-  // what is not the row's is zero
+  // what is not the row's is `fill`
   template <int TYPE>
-  __device__ __forceinline__ void mask(Pack<TYPE, VEC>& v, int i) const {
+  __device__ __forceinline__ void mask(Pack<TYPE, VEC>& v, int i, float fill = 0.0f) const {
     if constexpr (MODE == FLAT)
       if (!whole(i)) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-          if (!has(i, j)) v.v[j] = Elem<TYPE>::put(0.0f);
+          if (!has(i, j)) v.v[j] = Elem<TYPE>::put(fill);
       }
   }
-  // `last`: the matrix's last row, whose last piece may reach past its end. (The neighbours' elements that a piece
-  // brings along may be on their way out of another block, where an output takes the place of its input: they are
-  // masked, whatever they are.)
+  // Elements from a row's start to the matrix's end, where a FLAT piece of it may reach past that end.
+  __device__ __forceinline__ int left(long long row, int rows) const {
+    return static_cast<int>(min(static_cast<long long>(rows) - row, static_cast<long long>(VEC))) * cols;
+  }
+  // (The neighbours' elements that a piece brings along may be on their way out of another block, where an output takes
+  // the place of its input: they are masked, whatever they are.)
   template <int TYPE>
   __device__ __forceinline__ void load(Pack<TYPE, VEC>& v, const void* base, long long row, long long ld, int i, bool in,
-                                       bool last) const {
+                                       int left) const {
     using T = typename Pack<TYPE, VEC>::T;
     v.zero();
     if (!in || !any(i)) return;
     const T* p = static_cast<const T*>(base) + row * ld;
-    if (MODE == FLAT && last && lo(i) + VEC > cols) {
+    if (MODE == FLAT && lo(i) + VEC > left) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
         if (has(i, j)) v.v[j] = p[lo(i) + j];
@@ -188,14 +191,15 @@ __global__ void __launch_bounds__(kNormThreads<TYPE, EPT>, kNormThreads<TYPE, EP
   for (long long q0 = static_cast<long long>(rows.first) * per_block; q0 < rows.count;
        q0 += static_cast<long long>(rows.blocks) * per_block, turn ^= 1) {
     const long long row = rows.row(q0 + sub);
-    const bool in = q0 + sub < rows.count, last = row == p.rows - 1;
+    const bool in = q0 + sub < rows.count;
+    const int left = r.left(row, p.rows);
     P h[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in, last);
+    for (int i = 0; i < NV; ++i) r.load(h[i], p.x, row, p.ldx, i, in, left);
     if (p.residual != nullptr) {
       P a[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in, last);
+      for (int i = 0; i < NV; ++i) r.load(a[i], p.residual, row, p.ldr, i, in, left);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float x[VEC];
@@ -378,9 +382,9 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
     for (int i = 0; i < NV; ++i)
       if (r.any(i)) {
         if (q < rows.count) {
-          // (the last piece of the last row may reach past the matrix: the copy reads what there is)
-          const bool cut = MODE == FLAT && row == p.rows - 1 && r.lo(i) + VEC > p.cols;
-          const int bytes = cut ? (p.cols - r.lo(i)) * int(sizeof(T)) : 16;
+          // (a piece that reaches past the matrix: the copy reads what there is)
+          const int most = r.left(row, p.rows) - r.lo(i);
+          const int bytes = MODE == FLAT && most < VEC ? most * int(sizeof(T)) : 16;
           copy16_part(cell(s, 0, i), static_cast<const T*>(p.h) + row * p.ldh + r.lo(i), bytes);
           copy16_part(cell(s, 1, i), static_cast<const T*>(p.dy) + row * p.lddy + r.lo(i), bytes);
           if (p.dh != nullptr) copy16_part(cell(s, 2, i), static_cast<const T*>(p.dh) + row * p.lddh + r.lo(i), bytes);
@@ -427,15 +431,15 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
       next = statistics(q0 + sub + step);
     } else {
       stat = statistics(q0 + sub);
-      const bool last = row == p.rows - 1;
+      const int left = r.left(row, p.rows);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        r.load(h[i], p.h, row, p.ldh, i, in, last);
-        r.load(dy[i], p.dy, row, p.lddy, i, in, last);
+        r.load(h[i], p.h, row, p.ldh, i, in, left);
+        r.load(dy[i], p.dy, row, p.lddy, i, in, left);
       }
       if (p.dh != nullptr) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in, last);
+        for (int i = 0; i < NV; ++i) r.load(dh[i], p.dh, row, p.lddh, i, in, left);
       } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) dh[i].zero();
@@ -456,6 +460,7 @@ __global__ void __launch_bounds__(int(kMaxCols) / kGradEpt, 1) layernorm_grad_ke
       r.template weights<TYPE>(w, p.weight, shared_w, i);
       take(h, 0, i);
       take(dy, 1, i);
+      r.mask(h[i], i, mean);  // (0 times a neighbour's infinity, or what -mean rstd may pass, is not 0)
       if constexpr (AHEAD) r.mask(dy[i], i);
       if constexpr (VEC > 1) {
 #pragma unroll

@@ -180,6 +180,54 @@ def test_layer_norm_backward(rows, cols, dtype, pad, path):
     _close(db, want[2], np.abs(_np(dy)).sum(0), dtype)
 
 
+@pytest.mark.parametrize("rows,cols", [(47, 1), (30, 2), (44, 3), (20, 7), (50, 33), (40, 1023), (9, 2050), (50, 40)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_layer_norm_rows_stay_apart(rows, cols, dtype, bad):
+    """What a row holds, and what lies behind the matrix, reaches no other row: the others are the same bit for bit."""
+    def behind(t):  # the same matrix with `bad` right behind it
+        if t.dtype == torch.float32 and t.dim() == 1:
+            return t.cuda()
+        return torch.cat((t.flatten(), torch.full((64,), bad, dtype=t.dtype))).cuda()[:t.numel()].view(t.shape)
+
+    ts = [_normal((rows, cols), dtype, 900 + i) for i in range(5)]
+    w, b = _normal(cols, dtype, 906), _normal(cols, dtype, 907)
+
+    def run(x, res, dy, dh, h, **kw):
+        outs = []
+        for q in (None, E4M3):
+            n = ff.layer_norm(behind(x), behind(w), behind(b), behind(res), out_dtype=q)
+            outs += [n.y.view(torch.uint8) if q else n.y, n.mean, n.rstd] + ([n.scale] if q else [])
+        n = ff.layer_norm(behind(h), behind(w), behind(b))
+        outs += [n.y]
+        return outs + [ff.layer_norm_backward(behind(dy), behind(h), behind(w), n.mean, n.rstd, dh=behind(dh))[0]]
+
+    want = run(*ts)
+    assert not any(torch.isnan(t.float()).any() for t in want)
+    at = rows // 2
+    poisoned = [t.clone() for t in ts]
+    for t in poisoned:
+        t[at] = bad
+    rest = [i for i in range(rows) if i != at]
+    for got, ref in zip(run(*poisoned), want):
+        assert torch.equal(got[rest].float(), ref[rest].float())
+
+
+@pytest.mark.parametrize("cols", [40, 33, 1023])
+def test_layer_norm_backward_of_huge_constant_rows(cols):
+    """h - mean is 0 and rstd eps^-1/2: no step of any path may pass fp32's range."""
+    h = torch.full((20, cols), 2.0 ** 123, dtype=torch.bfloat16, device="cuda")
+    dy = _normal((20, cols), "bf16", 911).cuda()
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    mean = torch.full((20,), 2.0 ** 123, device="cuda")
+    rstd = torch.full((20,), 316.0, device="cuda")
+    dx, dw, db = ff.layer_norm_backward(dy, h, w, mean, rstd)
+    g = dy.double()
+    want = 316.0 * (g - g.mean(1, keepdim=True))
+    assert ((dx.double() - want).abs() <= want.abs() * 2.0 ** -8 + 316.0 * 1e-5 * (g.abs() + g.abs().mean(1, keepdim=True))).all()
+    assert (dw == 0).all() and not torch.isnan(db.float()).any()
+
+
 def test_layer_norm_backward_of_no_rows():
     z, v = torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(0, device="cuda")
     dx, dw, db = ff.layer_norm_backward(z, z, torch.ones(64, device="cuda", dtype=torch.bfloat16), v, v)
