@@ -35,7 +35,8 @@ struct BlockScales {
   long long row, block;
   int shift;
   // (plain loads: the previous kernel on the stream, which this one's start overlaps, may be what writes the scales)
-  __device__ __forceinline__ float at(int r, int b) const { return s[(r >> shift) * row + b * block]; }
+  __device__ __forceinline__ const float* from(int r, int b) const { return s + ((r >> shift) * row + b * block); }
+  __device__ __forceinline__ float at(int r, int b) const { return *from(r, b); }
 };
 
 struct BlockParams {

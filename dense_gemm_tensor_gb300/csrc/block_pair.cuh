@@ -10,10 +10,12 @@
 // flight while the one before it is added, the accumulator is handed back as soon
 // as its last load has landed, and the epilogue warps have most of the register
 // file (setmaxnreg): 128 sums a thread stay in registers. The scales come through
-// shared memory, loaded by warps of their own, whose arrivals count for the same
-// barrier as the tensor cores': a block costs the epilogue one wait. COLS (a scale
-// for each row of the column operand) has two instructions for one. 8192^3: 357-363
-// us (3.03 PFLOP/s; 424 at the power limit), COLS 579-597, bound by the FP32 pipe.
+// shared memory, copied by warps of their own some blocks ahead. COLS (a scale for
+// each row of the column operand) has two instructions for one. 8192^3: 357-364 us
+// (3.0 PFLOP/s; about 415 at the power limit), COLS 500. Cycles a block of a 256-wide
+// tile (128-wide), at 2070 MHz: 690 (490), COLS 1100 (600), and with an epilogue that
+// waits and hands back but reads nothing 546 (455), which is what loads of 24 and 32
+// KB a block and CTA allow; the rest is the epilogue's loads and, COLS, the FP32 pipe.
 #pragma once
 
 #include "block_few.cuh"
@@ -35,9 +37,10 @@ struct BlockPairCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int EPI_TILE = 32 * 128;
   static constexpr int EPI_STAGING = 8 * EPI_TILE;
-  // a block's scales: of the 128 rows (times each 128 columns' one, unless COLS), and of the columns (COLS)
-  static constexpr int ROW_SCALES = 2 * BM;
-  static constexpr int SCALE_BYTES = ACCS * (ROW_SCALES + BN) * 4;
+  // a block's scales: of the 128 rows, then of the columns (COLS) or of each 128 of them
+  static constexpr int SCALE_RING = 8;
+  static constexpr int SCALES = BM + BN;
+  static constexpr int SCALE_BYTES = SCALE_RING * SCALES * 4;
   static constexpr int BAR_BYTES = 512;
   static constexpr int SMEM_LIMIT = 232448;
   static constexpr int STAGES_FIT = (SMEM_LIMIT - 1024 - EPI_STAGING - SCALE_BYTES - BAR_BYTES) / STAGE_BYTES;
@@ -46,7 +49,7 @@ struct BlockPairCfg {
   static constexpr int COLS_PER_SET = BN / 2;  // columns of an epilogue warp
   static constexpr int BLOCKS = BN / 128;      // scales of the column operand without COLS
   static_assert(BN == 256 || BN == 128, "tile width");
-  static_assert((2 * STAGES + 3 * ACCS + 1) * 8 + 16 <= BAR_BYTES, "barrier area");
+  static_assert((2 * STAGES + 2 * ACCS + 2 * SCALE_RING + 1) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(2 * BM >> 4) << 24);
 };
 
@@ -68,6 +71,21 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on the barrier (one of its expected count) once this thread's copies so far have landed.
+__device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A wait of each lane by itself: the warp agrees on the outcome now and then (a vote at each wait held back what it
+// releases: 8192^3 364 us, COLS 522, where it takes 360 and 500).
+__device__ __forceinline__ bool lane_wait(const GemmParams& g, uint32_t bar, uint32_t parity, uint32_t code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_phase(g, bar, parity, code);
+}
+
 template <int BN, bool COLS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     block_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
@@ -85,8 +103,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t empty0 = full0 + 8 * S;
   const uint32_t accf0 = empty0 + 8 * S;
   const uint32_t acce0 = accf0 + 8 * Cf::ACCS;
-  const uint32_t sce0 = acce0 + 8 * Cf::ACCS;  // this CTA's epilogue has read a block's scales
-  const uint32_t drain_bar = sce0 + 8 * Cf::ACCS;
+  const uint32_t scf0 = acce0 + 8 * Cf::ACCS;  // a block's scales have landed
+  const uint32_t sce0 = scf0 + 8 * Cf::SCALE_RING;  // this CTA's epilogue has read them
+  const uint32_t drain_bar = sce0 + 8 * Cf::SCALE_RING;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + (drain_bar + 8 - sbase));
   volatile int* issued_slot = reinterpret_cast<volatile int*>(tmem_slot) + 1;
   volatile int* consumed_slot = issued_slot + 1;
@@ -113,8 +132,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < Cf::ACCS; ++b) {
-      mbar_init(accf0 + 8 * b, COLS ? 3 : 2);  // the tensor cores, and the scales
+      mbar_init(accf0 + 8 * b, 1);
       mbar_init(acce0 + 8 * b, 16);
+    }
+    for (int b = 0; b < Cf::SCALE_RING; ++b) {
+      mbar_init(scf0 + 8 * b, COLS ? 64 : 32);
       mbar_init(sce0 + 8 * b, 8);
     }
     mbar_init(drain_bar, 1);
@@ -196,66 +218,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
     } else if (warp == 7 || (warp == 6 && COLS)) {
       // -------------------------------------------------------------- scales (each CTA)
-      // A lane has entries lane, lane + 32, ... of the block's scales; two blocks ahead in registers. The arrival for
-      // a block comes after the epilogue has read the slot's last one, and so after that phase of the barrier.
+      // Copied by each lane (entries lane, lane + 32, ...), up to SCALE_RING blocks ahead. (With two blocks ahead
+      // in registers their latency held COLS back: 8192^3 579 us, 522 with the copies.)
       const bool rows = warp == 7;
-      constexpr int PER = BN / 32 > 4 + Cf::BLOCKS ? BN / 32 : 4 + Cf::BLOCKS;
+      const uint32_t to0 = smem_u32(scales) + 4 * lane;
       int it = 0;
       bool ok = true;
       for (int t = unit; ok && t < tiles; t += nunits) {
         int p0, q0;
         place(t, p0, q0);
-        float next[2][PER];
-        auto load = [&](float(&v)[PER], int kb) {
-#pragma unroll
-          for (int j = 0; j < PER; ++j) v[j] = 0.0f;
-          if (kb >= kbs) return;
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const int b = it % Cf::SCALE_RING;
+          if (!group_wait(p.g, sce0 + 8 * b, ((it / Cf::SCALE_RING) & 1) ^ 1, ROLE_COPY | (b << 8))) {
+            ok = false;
+            break;
+          }
+          const uint32_t to = to0 + b * Cf::SCALES * 4;
           if (rows) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = p.ps.at(min(p0 + lane + 32 * j, p.p_rows - 1), kb);
-            if constexpr (!COLS) {
-#pragma unroll
-              for (int j = 0; j < Cf::BLOCKS; ++j) v[4 + j] = p.qs.at(min(q0 + 128 * j, p.q_rows - 1), kb);
-            }
+            for (int j = 0; j < 4; ++j) copy4(to + 128 * j, p.ps.from(min(p0 + lane + 32 * j, p.p_rows - 1), kb));
+            if (!COLS && lane < Cf::BLOCKS) copy4(to + 512, p.qs.from(min(q0 + 128 * lane, p.q_rows - 1), kb));
           } else {
 #pragma unroll
-            for (int j = 0; j < BN / 32; ++j) {
-              const int c = q0 + lane + 32 * j;
-              if (c < p.q_rows) v[j] = p.qs.at(c, kb);
-            }
+            for (int j = 0; j < BN / 32; ++j) copy4(to + 512 + 128 * j, p.qs.from(min(q0 + lane + 32 * j, p.q_rows - 1), kb));
           }
-        };
-        load(next[0], 0);
-        load(next[1], 1);
-        for (int kb0 = 0; ok && kb0 < kbs; kb0 += 2) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (kb0 + i >= kbs) break;
-            float now[PER];
-#pragma unroll
-            for (int j = 0; j < PER; ++j) now[j] = next[i][j];
-            load(next[i], kb0 + i + 2);
-            const int b = it % Cf::ACCS;
-            if (!group_wait(p.g, sce0 + 8 * b, ((it / Cf::ACCS) & 1) ^ 1, ROLE_COPY | (b << 8))) {
-              ok = false;
-              break;
-            }
-            float* to = scales + b * (Cf::ROW_SCALES + BN);
-            if (rows) {
-#pragma unroll
-              for (int k = 0; k < (COLS ? 1 : Cf::BLOCKS); ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) to[k * Cf::BM + lane + 32 * j] = COLS ? now[j] : now[j] * now[4 + k];
-            } else {
-#pragma unroll
-              for (int j = 0; j < BN / 32; ++j) to[Cf::ROW_SCALES + lane + 32 * j] = now[j];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(accf0 + 8 * b);
-            ++it;
-          }
+          mbar_arrive_copies(scf0 + 8 * b);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---------------------------------------------------------------- epilogue: lane = row of P
@@ -276,21 +266,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
       for (int kb = 0; kb < kbs; ++kb, ++it) {
-        const int b = it % Cf::ACCS;
-        if (!group_wait(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8))) {
-          ok = false;
-          break;
-        }
+        const int b = it % Cf::ACCS, sb = it % Cf::SCALE_RING;
+        if (!lane_wait(p.g, scf0 + 8 * sb, (it / Cf::SCALE_RING) & 1, ROLE_EPILOGUE | (sb << 8))) ok = false;
+        if (!lane_wait(p.g, accf0 + 8 * b, (it / Cf::ACCS) & 1, ROLE_EPILOGUE | (b << 8))) ok = false;
         tc_fence_after();
         const uint32_t from = taddr + b * BN;
-        const float* scale = scales + b * (Cf::ROW_SCALES + BN);
         __syncwarp();
-        const float f1 = scale[(COLS ? 0 : (set * NC) / 128 * Cf::BM) + q * 32 + lane];
-        const float2 f = make_float2(f1, f1);
         // the next CH columns are on their way while these are added
         constexpr int CH = 32;
         uint32_t r[2][CH];
         tmem_ld_32x32b_x32(from, r[0]);
+        const float* scale = scales + sb * Cf::SCALES;
+        const float f1 = COLS ? scale[q * 32 + lane] : scale[q * 32 + lane] * scale[Cf::BM + (set * NC) / 128];
+        const float2 f = make_float2(f1, f1);
 #pragma unroll
         for (int c = 0; c < NC / CH; ++c) {
           tmem_wait_ld_into(r[c & 1]);
@@ -301,7 +289,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(lead_acce0 + 8 * b);
           }
-          const float4* cs = reinterpret_cast<const float4*>(scale + Cf::ROW_SCALES + set * NC + CH * c);
+          const float4* cs = reinterpret_cast<const float4*>(scale + Cf::BM + set * NC + CH * c);
 #pragma unroll
           for (int j = 0; j < CH / 2; j += 2) {
             float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
@@ -316,8 +304,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(sce0 + 8 * b);
+        if (lane == 0) mbar_arrive(sce0 + 8 * sb);
+        if (kb % 64 == 63 && !__all_sync(0xFFFFFFFFu, ok)) break;
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (row0 < p.p_rows) {
 #pragma unroll
