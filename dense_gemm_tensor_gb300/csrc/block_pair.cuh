@@ -12,7 +12,7 @@
 // file (setmaxnreg): 128 sums a thread stay in registers. The scales come through
 // shared memory, copied by warps of their own some blocks ahead. COLS (a scale for
 // each row of the column operand) has two instructions for one. 8192^3: 357-364 us
-// (3.0 PFLOP/s; about 415 at the power limit), COLS 500. Cycles a block of a 256-wide
+// (3.0 PFLOP/s; 422 at the power limit), COLS 500. Cycles a block of a 256-wide
 // tile (128-wide), at 2070 MHz: 690 (490), COLS 1100 (600), and with an epilogue that
 // waits and hands back but reads nothing 546 (455), which is what loads of 24 and 32
 // KB a block and CTA allow; the rest is the epilogue's loads and, COLS, the FP32 pipe.
