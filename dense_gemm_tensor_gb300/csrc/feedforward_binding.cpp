@@ -67,6 +67,15 @@ T* vector_on(PyObject* o, const char* what, at::ScalarType dt, int64_t n, const 
   return p;
 }
 
+// Part `i` of a buffer of vectors of `n` floats. (An allocation costs twice what another tensor on its memory does.)
+Tensor part(const Tensor& buffer, int64_t i, int64_t n) {
+  c10::Storage storage = buffer.storage();
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(std::move(storage), buffer.key_set(), buffer.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  t.unsafeGetTensorImpl()->set_storage_offset(buffer.storage_offset() + i * n);
+  return t;
+}
+
 // layer_norm(x, weight, bias, residual, eps, 8-bit rows, h_out) -> (y, h, mean, rstd, scale)
 PyObject* layer_norm(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x");
@@ -94,8 +103,9 @@ PyObject* layer_norm(PyObject* const* a) {
   } else if (a[6] != Py_None) {
     value_error("h_out is given without a residual: h is x");
   }
-  Tensor y = make({rows, cols}, x, q8 ? at::kFloat8_e4m3fn : dt), mean = make({rows}, x, at::kFloat);
-  Tensor rstd = make({rows}, x, at::kFloat), scale = q8 ? make({rows}, x, at::kFloat) : Tensor();
+  Tensor y = make({rows, cols}, x, q8 ? at::kFloat8_e4m3fn : dt);
+  const Tensor vectors = make({(q8 ? 3 : 2) * rows}, x, at::kFloat);
+  Tensor mean = part(vectors, 0, rows), rstd = part(vectors, 1, rows), scale = q8 ? part(vectors, 2, rows) : Tensor();
   if (cols == 0) {  // the call writes nothing: the mean of no elements, and the least scale
     mean.fill_(std::numeric_limits<double>::quiet_NaN());
     rstd.fill_(std::numeric_limits<double>::quiet_NaN());
