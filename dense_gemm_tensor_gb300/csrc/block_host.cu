@@ -41,13 +41,15 @@ constexpr int kFewRows = 64;  // up to here always the kernel for few rows
 // eight CTAs can share each and have work enough: us with it / with pairs, K = 4096: 65 x 512 6.4 / 10.6, 65 x 2048
 // 8.7 / 10.7, 512 x 512 9.4 / 10.9, 1024 x 512 (beyond the limit) 12.0 / 11.2, 512 x 2048 18.0 / 13.5; K = 1024: 65 x
 // 512 6.2 / 5.0. A pair's 256-wide tile takes about one and a half times a 128-wide one's time: 512 x 4096 x 4096
-// (one round of either) 17.3 / 14.0 us, 1024 x 8192 x 4096 (two rounds or four) 32.3 / 37.9.
-int pair_width(int64_t M, int64_t N, int64_t blocks, int sms) {
+// (one round of either) 16.8 / 12.6 us, 2048 x 4096 x 4096 (two rounds or four) 30.6 / 37.7. With a scale for each row of
+// B (`cols`) the columns weigh more, and it takes 1.8 times: 4096 x 4096 x 4096 (four or seven) 77.7 / 76.5, 4096 x 5120
+// x 4099 (five or nine) 101.7 / 101.0, 8192 x 8192 x 8192 (14 or 27) 503 / 541.
+int pair_width(int64_t M, int64_t N, int64_t blocks, bool cols, int sms) {
   const int64_t few = (M + 63) / 64 * ((N + 127) / 128);
   if (M <= kFewRows || (blocks >= 16 && few * 8 <= 2 * sms)) return 0;
   const int64_t rows = (M + 255) / 256, units = sms / 2;
   const int64_t wide = (rows * ((N + 255) / 256) + units - 1) / units, narrow = (rows * ((N + 127) / 128) + units - 1) / units;
-  return wide * 3 <= narrow * 2 ? 256 : 128;
+  return (cols ? wide * 9 <= narrow * 5 : wide * 3 <= narrow * 2) ? 256 : 128;
 }
 
 }  // namespace
@@ -92,7 +94,7 @@ extern "C" int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* 
   // (the pitch of a matrix of one row says nothing)
   if (M == 1) lda = (K + 15) / 16 * 16;
   if (N == 1) ldb = (K + 15) / 16 * 16;
-  const int pair_bn = pair_width(M, N, blocks, ctx.sm_count);
+  const int pair_bn = pair_width(M, N, blocks, b_rows == 1, ctx.sm_count);
   const bool few = pair_bn == 0;
   BlockLaunch L;
   memset(&L, 0, sizeof(L));

@@ -82,7 +82,7 @@ class MoeBlock:
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor):
         """(output, what ``backward`` needs): the 16-bit block, the gate's product kept. The activation
-        and its gradient are elementary torch operations in fp32: no operator of this package has them."""
+        and its gradient are elementary torch operations in fp32: no operator of this package has them for groups."""
         n = experts.rms_norm(x, self.norm, residual)
         logits = gemm.matmul(n.y, self.router)
         r = experts.route(logits, self.k)
