@@ -553,6 +553,68 @@ def test_in_a_cuda_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,K,F", [(5, 100, 70), (70, 333, 65), (300, 200, 136), (600, 77, 201)])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gated_rows_and_columns_stay_apart(M, K, F, layout, bad):
+    a, w, ad, wd = _gated_case(M, K, F, "bf16", layout, 160)
+    dc = _normal((M, F), "bf16", 163).cuda()
+
+    def run(a, w, dc):
+        r = ff.gated_matmul(a, w, layout=layout, keep=True)
+        return r.c, r.up, ff.gated_matmul_backward(dc, a, w, r.up, layout=layout, weights=False).dA
+
+    # (a clone drops the pitch, and another pitch may take another kernel, with another order of sums: both are clones)
+    want = run(ad.clone(), wd, dc)
+    at, rest = M // 2, [i for i in range(M) if i != M // 2]
+    ad2, dc2 = ad.clone(), dc.clone()
+    ad2[at] = bad
+    dc2[at] = bad
+    for got, ref in zip(run(ad2, wd, dc2), want):
+        assert torch.equal(got[rest], ref[rest])
+    col, others = F // 3, [j for j in range(F) if j != F // 3]
+    wd2 = wd.clone()
+    if layout:
+        wd2[F + col] = bad
+    else:
+        wd2[:, F + col] = bad
+    got, ref = (ff.gated_matmul(ad, t, layout=layout).c for t in (wd2, wd.clone()))
+    assert torch.equal(got[:, others], ref[:, others])
+
+
+def test_in_inference_mode():
+    args = _block_inputs(40)
+    y, n, g = _block(*args)
+    q = ff.layer_norm(args[0], args[2], args[3], args[1], out_dtype=E4M3)
+    with torch.inference_mode():
+        y2, n2, g2 = _block(*args)
+        q2 = ff.layer_norm(args[0], args[2], args[3], args[1], out_dtype=E4M3)
+        blocks = ff.quantize_blocks(args[0])
+        assert q2.scale.is_inference() and n2.mean.is_inference() and blocks.q.is_inference()
+        doubled = (n2.mean * 2).cpu()
+    assert torch.equal(y, y2) and torch.equal(g.c, g2.c)
+    for a, b in ((n.mean, n2.mean), (n.rstd, n2.rstd), (q.mean, q2.mean), (q.rstd, q2.rstd), (q.scale, q2.scale)):
+        assert a.is_contiguous() and torch.equal(a, b)
+    assert torch.equal(doubled, n.mean.cpu() * 2)
+    n.mean.zero_()  # the statistics share memory, and no element of it
+    q.rstd.zero_()
+    assert torch.equal(n.rstd, n2.rstd) and torch.equal(q.mean, q2.mean) and torch.equal(q.scale, q2.scale)
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 64), (3, 0), (0, 0)])
+def test_layer_norm_of_nothing(rows, cols):
+    x, w = torch.empty(rows, cols, device="cuda").bfloat16(), torch.empty(cols, device="cuda").bfloat16()
+    for kw in ({}, {"out_dtype": E4M3}):
+        n = ff.layer_norm(x, w, residual=x, **kw)
+        assert n.y.shape == n.h.shape == x.shape and n.mean.shape == n.rstd.shape == (rows,)
+        assert n.scale is None or n.scale.shape == (rows,)
+        if cols == 0:
+            assert torch.isnan(n.mean).all() and torch.isnan(n.rstd).all()
+            assert n.scale is None or (n.scale == torch.tensor(1e-12 / 448, device="cuda")).all()
+    dx, dw, db = ff.layer_norm_backward(x, x, w, n.mean, n.rstd)
+    assert dx.shape == x.shape and not dw.any() and not db.any()
+
+
 def test_a_stalled_product_reports_a_timeout():
     """A producer that loads nothing: the kernel gives up within its limit and says so in the status word."""
     a, w = _normal((300, 64), "bf16", 98).cuda(), _normal((128, 64), "bf16", 99).cuda()
