@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float* partial, int
 
 // The value half of row-major weights that starts off a 16-byte boundary (m bytes past one), in rows that start on
 // them: 16 bytes a thread, shifted together from the two aligned pieces that hold them; a row's last ones element by
-// element. Bound by memory, and a second launch: 1000 x 3000 FP16 adds about 5 us. (Copied with the gate half, a warp a row,
-// it took 14.)
+// element. Bound by memory, and a second launch: 1000 x 3000 FP16 adds about 5 us. (Copied with the gate half, a warp a
+// row, it took 14.)
 struct HalfParams {
   const uint8_t* w;
   uint8_t* to;
