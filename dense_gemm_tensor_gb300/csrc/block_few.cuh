@@ -275,14 +275,15 @@ __global__ void __launch_bounds__(kBlockThreads)
           __syncwarp();
           if (lane == 0) mbar_arrive(acce0 + 8 * b);
         }
+        // (the scales' product first: a block's sum times one of them may pass fp32's range where that does not)
         const float4* cs = reinterpret_cast<const float4*>(scale + c);
 #pragma unroll
         for (int j = 0; j < CH; j += 4) {
           const float4 s4 = cs[j / 4];
-          acc[c + j] = fmaf(__uint_as_float(r[j]) * s4.x, f, acc[c + j]);
-          acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]) * s4.y, f, acc[c + j + 1]);
-          acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]) * s4.z, f, acc[c + j + 2]);
-          acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]) * s4.w, f, acc[c + j + 3]);
+          acc[c + j] = fmaf(__uint_as_float(r[j]), s4.x * f, acc[c + j]);
+          acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), s4.y * f, acc[c + j + 1]);
+          acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), s4.z * f, acc[c + j + 2]);
+          acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), s4.w * f, acc[c + j + 3]);
         }
       }
       __syncwarp();

@@ -42,8 +42,8 @@ constexpr int kFewRows = 64;  // up to here always the kernel for few rows
 // 8.7 / 10.7, 512 x 512 9.4 / 10.9, 1024 x 512 (beyond the limit) 12.0 / 11.2, 512 x 2048 18.0 / 13.5; K = 1024: 65 x
 // 512 6.2 / 5.0. A pair's 256-wide tile takes about one and a half times a 128-wide one's time: 512 x 4096 x 4096
 // (one round of either) 16.8 / 12.6 us, 2048 x 4096 x 4096 (two rounds or four) 30.6 / 37.7. With a scale for each row of
-// B (`cols`) the columns weigh more, and it takes 1.8 times: 4096 x 4096 x 4096 (four or seven) 77.7 / 76.5, 4096 x 5120
-// x 4099 (five or nine) 101.7 / 101.0, 8192 x 8192 x 8192 (14 or 27) 503 / 541.
+// B (`cols`) the columns weigh more, and it takes 1.8 times: 4096 x 4096 x 4096 (four or seven) 83.5 / 80.0, 4096 x 5120
+// x 4096 (five or nine) 101.2 / 101.3, 8192 x 8192 x 8192 (14 or 27) 531 / 572.
 int pair_width(int64_t M, int64_t N, int64_t blocks, bool cols, int sms) {
   const int64_t few = (M + 63) / 64 * ((N + 127) / 128);
   if (M <= kFewRows || (blocks >= 16 && few * 8 <= 2 * sms)) return 0;

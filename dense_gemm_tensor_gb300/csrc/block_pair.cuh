@@ -11,11 +11,13 @@
 // as its last load has landed, and the epilogue warps have most of the register
 // file (setmaxnreg): 128 sums a thread stay in registers. The scales come through
 // shared memory, copied by warps of their own some blocks ahead. COLS (a scale for
-// each row of the column operand) has two instructions for one. 8192^3: 357-364 us
-// (3.0 PFLOP/s; 422 at the power limit), COLS 500. Cycles a block of a 256-wide
-// tile (128-wide), at 2070 MHz: 690 (490), COLS 1100 (600), and with an epilogue that
-// waits and hands back but reads nothing 546 (455), which is what loads of 24 and 32
-// KB a block and CTA allow; the rest is the epilogue's loads and, COLS, the FP32 pipe.
+// each row of the column operand) has two instructions for one, the product of a
+// value's scales and the addition. 8192^3: 357-364 us (3.0 PFLOP/s; 422 at the power
+// limit), COLS 530 (500 with the sum times one scale first, which passes fp32's range
+// where the two scales are far apart). Cycles a block of a 256-wide tile (128-wide),
+// at 2070 MHz: 690 (490), COLS 1100 (600), and with an epilogue that waits and hands
+// back but reads nothing 546 (455), which is what loads of 24 and 32 KB a block and
+// CTA allow; the rest is the epilogue's loads and, COLS, the FP32 pipe.
 #pragma once
 
 #include "block_few.cuh"
@@ -292,15 +294,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const float4* cs = reinterpret_cast<const float4*>(scale + Cf::BM + set * NC + CH * c);
 #pragma unroll
           for (int j = 0; j < CH / 2; j += 2) {
-            float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
-            float2 y = make_float2(__uint_as_float(r[c & 1][2 * j + 2]), __uint_as_float(r[c & 1][2 * j + 3]));
+            const float2 x = make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1]));
+            const float2 y = make_float2(__uint_as_float(r[c & 1][2 * j + 2]), __uint_as_float(r[c & 1][2 * j + 3]));
+            // COLS: the scales' product first (a block's sum times one of them may pass fp32's range where that does not)
+            float2 fx = f, fy = f;
             if constexpr (COLS) {
               const float4 s4 = cs[j / 2];
-              x = __fmul2_rn(x, make_float2(s4.x, s4.y));
-              y = __fmul2_rn(y, make_float2(s4.z, s4.w));
+              fx = __fmul2_rn(f, make_float2(s4.x, s4.y));
+              fy = __fmul2_rn(f, make_float2(s4.z, s4.w));
             }
-            acc[CH / 2 * c + j] = __ffma2_rn(x, f, acc[CH / 2 * c + j]);
-            acc[CH / 2 * c + j + 1] = __ffma2_rn(y, f, acc[CH / 2 * c + j + 1]);
+            acc[CH / 2 * c + j] = __ffma2_rn(x, fx, acc[CH / 2 * c + j]);
+            acc[CH / 2 * c + j + 1] = __ffma2_rn(y, fy, acc[CH / 2 * c + j + 1]);
           }
         }
         __syncwarp();

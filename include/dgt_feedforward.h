@@ -125,8 +125,8 @@ int64_t gemm_gated_backward_workspace(int type, int64_t M, int64_t F, int64_t K,
  * boundaries and their pitches are multiples of 16 (but for a matrix of one row):
  * GEMM_ERR_MISALIGNED otherwise. A scale that is not finite reaches the entries
  * that it belongs to, also where the block's sum is 0 (as NaN). A block's two
- * scales and its sum are multiplied in either order: the product of the scales
- * has to be within fp32's range.
+ * scales are multiplied with each other, then with its sum: their product has to
+ * be within fp32's normal range, and each of them may be anywhere in it.
  */
 int gemm_e4m3_blocks(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const float* a_scale,
                      int64_t as_row, int64_t as_block, const uint8_t* B, int64_t ldb, const float* b_scale,
