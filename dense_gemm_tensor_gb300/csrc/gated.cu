@@ -19,14 +19,10 @@
 namespace dgt {
 namespace {
 
-// Whether a product of M rows and N columns, `per` of them a tile, takes the kernel for few rows: up to 64 rows, and
-// beyond while its tiles are one an SM. Gated, BF16, us with it / with the grouped products' kernel, K = 4096: 65 x F
-// 512 10.1 / 23.7, 128 x 4096 21.0 / 25.4, 256 x 2048 20.7 / 24.8, 256 x 4096 (beyond the limit) 25.1 / 25.4, 512 x
-// 4096 48.0 / 26.9; K = 1024: 65 x 512 7.2 / 10.3, 128 x 4096 9.5 / 12.5.
-bool few_rows(int64_t M, int64_t N, int per) { return M <= 64 || (M + 63) / 64 * ((N + per - 1) / per) <= 152; }
-
 constexpr int kGateThreads = 256;
-constexpr int kBiasBlocks = 152;  // row blocks, at most, that leave partial sums of dbias
+// Row blocks, at most, that leave partial sums of dbias (a number: the size of the workspace goes by it, on a machine
+// without a GPU too).
+constexpr int kBiasBlocks = 152;
 
 struct GateGradParams {
   const void* dc;
@@ -253,13 +249,13 @@ bool meet(const void* a, int64_t rows_a, int64_t cols_a, int64_t ld_a, const voi
 struct GateGrid {
   int tx, blocks_x, blocks_y, rows_per_block;
 };
-GateGrid gate_grid(int64_t M, int64_t F, int vec, bool bias) {
+GateGrid gate_grid(int64_t M, int64_t F, int vec, bool bias, int sms) {
   GateGrid g;
   const int64_t pieces = (F + vec - 1) / vec;
   g.tx = 32;
   while (g.tx < kGateThreads && g.tx < pieces) g.tx *= 2;
   g.blocks_x = int((pieces + g.tx - 1) / g.tx);
-  const int64_t want = (152 * 8 + g.blocks_x - 1) / g.blocks_x, most = bias && want > kBiasBlocks ? kBiasBlocks : want;
+  const int64_t want = (sms * 8 + g.blocks_x - 1) / g.blocks_x, most = bias && want > kBiasBlocks ? kBiasBlocks : want;
   const int64_t rows = (M + most - 1) / most, step = kGateThreads / g.tx;
   g.rows_per_block = int((rows + step - 1) / step * step);
   g.blocks_y = int((M + g.rows_per_block - 1) / g.rows_per_block);
@@ -402,7 +398,7 @@ int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t
   if (M > 0 && F > 0 && bias != nullptr && C != nullptr && meet(C, M, F, ldc, bias, 1, 2 * F, 2 * F))
     return GEMM_ERR_INVALID_VALUE;
   const gemm_grouped_epilogue_t epi = {1.0f, nullptr, nullptr, bias, GEMM_ACT_NONE};
-  DenseProduct dense = {activation, up, ldup, nullptr, 0, nullptr, few_rows(M, F, 64) ? run_few : nullptr};
+  DenseProduct dense = {activation, up, ldup, nullptr, 0, nullptr, run_few, 64};
   const int64_t half = M > 0 && F > 0 ? half_bytes(F, K, ldw, layout) : 0;
   if (half > 0 && W != nullptr && C != nullptr && ldw >= 2 * F && ldw <= kLdLimit && !misaligned(W, 16)) {
     const int64_t rest = workspace_bytes - half;
@@ -487,7 +483,7 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
     const uintptr_t all = reinterpret_cast<uintptr_t>(dC) | reinterpret_cast<uintptr_t>(up) | uintptr_t(F * 2) |
                           uintptr_t(M > 1 ? lddc * 2 : 0) | uintptr_t(M > 1 ? ldup * 2 : 0);
     while (vec > 1 && all % (vec * 2) != 0) vec /= 2;
-    const GateGrid g = gate_grid(M, F, vec, dbias != nullptr);
+    const GateGrid g = gate_grid(M, F, vec, dbias != nullptr, ctx.sm_count);
     GateGradParams p = {dC,
                         up,
                         ws,
@@ -513,7 +509,7 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
   }
   uint8_t* stage = terms && space.stage > 0 ? ws + space.dup + space.partial : nullptr;
   if (dA != nullptr) {
-    const DenseProduct dense = {-1, nullptr, 0, nullptr, 0, nullptr, few_rows(M, K, 128) ? run_few : nullptr};
+    const DenseProduct dense = {-1, nullptr, 0, nullptr, 0, nullptr, run_few, 128};
     st = run_grouped(kind_of(type), 1, nullptr, M, K, 2 * F, dup, M, lddup, nullptr, W, ldw, 0, dA, ldda,
                      km ? GEMM_B_ROW_MAJOR : GEMM_B_K_MAJOR, nullptr, stage, space.stage, stream, &dense);
     if (st != GEMM_OK) return st;

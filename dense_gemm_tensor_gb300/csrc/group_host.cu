@@ -246,8 +246,7 @@ struct WeightCopy {
   int64_t pitch;           // of a copied part, bytes
   int64_t bytes;           // of the workspace: 0 where nothing is copied
 };
-//
-// The dense gated product copies the value half alone where that is all that is off (gated.cu).
+// (The dense gated product copies the value half alone where that is all that is off: gated.cu.)
 WeightCopy weight_copy(int es, int64_t groups, int64_t N, int64_t K, int64_t ldw, int64_t stride_w, bool row_major,
                        bool gated) {
   WeightCopy c;
@@ -343,7 +342,7 @@ int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int
     st = dense->copy(W, ldw, K, out_cols, dense->value, dense->ldv, static_cast<cudaStream_t>(stream));
     if (st != GEMM_OK) return st;
   }
-  if (dense != nullptr && dense->few != nullptr && K > 0 && workspace == nullptr)
+  if (dense != nullptr && K > 0 && workspace == nullptr && few_rows(slots, out_cols, dense->few_columns, ctx.sm_count))
     return dense->few(kind == KIND_F16 ? GEMM_TYPE_F16 : GEMM_TYPE_BF16, slots, out_cols, K, A, lda, W, ldw,
                       layout == GEMM_B_ROW_MAJOR, value, dense->ldv, dense->gate, bias, C, ldc, up, ldup, ctx,
                       static_cast<cudaStream_t>(stream));

@@ -42,11 +42,19 @@ struct DenseProduct {
   void* value;
   int64_t ldv;
   int (*copy)(const void* W, int64_t ldw, int64_t K, int64_t F, void* to, int64_t ld, cudaStream_t stream);
-  // A kernel of its own for few rows (or null), taken where TMA reads A and W in place.
+  // The kernel for few rows, taken by few_rows where TMA reads A and W in place, and the columns of C in its tile.
   int (*few)(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
              bool row_major, const void* value, int64_t ldv, int gate, const void* bias, void* C, int64_t ldc, void* up,
              int64_t ldup, const CallContext& ctx, cudaStream_t stream);
+  int few_columns;
 };
+// Whether a product of M rows and N columns, `per` of them a tile, takes the kernel for few rows: up to 64 rows, and
+// beyond while its tiles are one an SM. Gated, BF16, us with it / with the grouped products' kernel, K = 4096: 65 x F
+// 512 10.1 / 23.7, 128 x 4096 21.0 / 25.4, 256 x 2048 20.7 / 24.8, 256 x 4096 (beyond the limit) 25.1 / 25.4, 512 x
+// 4096 48.0 / 26.9; K = 1024: 65 x 512 7.2 / 10.3, 128 x 4096 9.5 / 12.5.
+inline bool few_rows(int64_t M, int64_t N, int per, int sms) {
+  return M <= 64 || (M + 63) / 64 * ((N + per - 1) / per) <= sms;
+}
 // The grouped product and weight gradient behind the C entry points (group_host.cu). dense: null for groups on the
 // device; offsets and rows are null where it is given.
 int run_grouped(int kind, int groups, const int32_t* offsets, int64_t slots, int64_t N, int64_t K, const void* A,
