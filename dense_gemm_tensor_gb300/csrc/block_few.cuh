@@ -16,7 +16,7 @@
 // tcgen05.mma, 6 the scales of A's rows, 7 those of B's; these run up to
 // kScaleRing blocks ahead (loaded as they were needed, four blocks at a time, each
 // four cost a trip to memory). 16 x 8192 x 8192 15.4 us (4.4 TB/s; the bytes 9.9,
-// the rest is the launch, the first loads and the join), 128 rows 23.7.
+// the rest is the launch, the first loads and the join).
 #pragma once
 
 #include <type_traits>

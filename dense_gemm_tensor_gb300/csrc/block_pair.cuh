@@ -14,10 +14,13 @@
 // each row of the column operand) has two instructions for one, the product of a
 // value's scales and the addition. 8192^3: 357-364 us (3.0 PFLOP/s; 422 at the power
 // limit), COLS 530 (500 with the sum times one scale first, which passes fp32's range
-// where the two scales are far apart). Cycles a block of a 256-wide tile (128-wide),
-// at 2070 MHz: 690 (490), COLS 1100 (600), and with an epilogue that waits and hands
-// back but reads nothing 546 (455), which is what loads of 24 and 32 KB a block and
-// CTA allow; the rest is the epilogue's loads and, COLS, the FP32 pipe.
+// where the two scales are far apart); 128 x 8192 x 8192, half of each tile empty, 23.7.
+// Cycles a block of a 256-wide tile (128-wide), at 2070 MHz: 690-730 (490-500), COLS
+// 1180 (650), and with an epilogue that waits and hands back but reads nothing 546
+// (455), which is what loads of 24 and 32 KB a block and CTA allow. The rest is the
+// epilogue, and of it no one unit is full: COLS of 256 columns has 46% of the issue
+// slots, 23% of the FMA pipe, 42% of the shared-memory data pipe (every lane reads
+// every column's scale: two wavefronts an LDS.128) and 42% of the tensor pipe.
 #pragma once
 
 #include "block_few.cuh"
@@ -82,7 +85,7 @@ __device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
 }
 
 // A wait of each lane by itself: the warp agrees on the outcome now and then (a vote at each wait held back what it
-// releases: 8192^3 364 us, COLS 522, where it takes 360 and 500).
+// releases: 8192^3 364 us, COLS 522, and 360 and 500 without, when the sum met one scale first).
 __device__ __forceinline__ bool lane_wait(const GemmParams& g, uint32_t bar, uint32_t parity, uint32_t code) {
   if (mbar_try_wait(bar, parity)) return true;
   return wait_phase(g, bar, parity, code);

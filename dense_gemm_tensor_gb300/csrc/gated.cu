@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const GateGradP
               sg[j] += dg;
               sv[j] += dv;
             }
+            // (rounded to 16 bits, as the tensor cores take both products' operands; FP16 past 65504 is infinite)
             g[i].v[j] = E::put(dg);
             v[i].v[j] = E::put(dv);
           }
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float* partial, int
 }
 
 // The value half of row-major weights that starts off a 16-byte boundary (m bytes past one), in rows that start on
-// them: 16 bytes a thread, shifted together from the two aligned pieces that hold them; a row's last ones element by
+// them: a tiled TMA copy has to start on such a boundary, its innermost coordinate as well as its address (an
+// illegal instruction otherwise), so the half cannot be read at column F of W's own map. 16 bytes a thread, shifted together from the two aligned pieces that hold them; a row's last ones element by
 // element. Bound by memory, and a second launch: 1000 x 3000 FP16 adds about 5 us. (Copied with the gate half, a warp a
 // row, it took 14.)
 struct HalfParams {

@@ -1,5 +1,6 @@
 // What the kernels share whose tiles are split along K over a cluster of CTAs: each
-// CTA leaves its sums in its shared memory, and one of them adds them up in order.
+// CTA leaves its sums in its shared memory, and adds up a share of the tile's rows
+// from all of them, in the CTAs' order.
 #pragma once
 
 #include "gemm_kernel.cuh"
@@ -58,9 +59,12 @@ __device__ __forceinline__ float joined_sum(const float* sums, int at, int split
   return s;
 }
 
-// CTAs of a tile's cluster, 1 to 8: as many as all fit the GPU at once (`slots` CTAs), each with two slabs or more.
-// (More of them, in turns, spend their time on starting and joining: 16 rows x 4096 -> 2 x 8192 BF16, 128 tiles on 152
-// SMs, 25.4 us with one CTA a tile and 38.6 us with seven.)
+// CTAs of a tile's cluster, 1 to 8: as many as there are places for (`slots` CTAs), each with two slabs or more. (More
+// of them, in turns, spend their time on starting and joining: 16 rows x 4096 -> 2 x 8192 BF16, 128 tiles on 152 SMs,
+// 25.4 us with one CTA a tile and 38.6 us with seven.) Places are counted, not what a GPC can hold of clusters, so that
+// at some tile counts the last clusters wait for a second round. Gated, 16 x 4096 -> 2 x F BF16, us at 15 tiles 7.3, 16
+// to 21 (splits of 8 and 7) 12.5 to 12.8, 22 and 23 8.3 and 8.7, 24 and 25 14.0, 26 to 28 8.7 to 9.4, 29 and 30 15.0, 31
+// to 36 9.4 to 10.1, 37 and 38 16.8; blocks, 16 rows, K = 8192: 33 tiles 10.5, 37 15.8, 41 17.2, 45 12.2, 49 18.9, 53 13.4.
 inline int choose_splits(int64_t tiles, int64_t slabs, int64_t slots) {
   int64_t s = slots / tiles;
   if (s > slabs / 2) s = slabs / 2;

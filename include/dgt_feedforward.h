@@ -81,13 +81,16 @@ int64_t gemm_layernorm_backward_workspace(int64_t rows, int64_t cols);
  * NULL) receives the rounded sums that gemm_gated_backward takes; C is computed
  * from the fp32 ones. SiLU and GELU's tanh form take the hardware's exponential:
  * within 4e-5 of their values before the rounding, and 0 where 1 + exp passes
- * 2^126 (gates below -87.3). M, 2F, K < 2^31; K = 0 gives the products of no
+ * 2^126 (gates below -87.3). GELU's other form is 1 + erf in fp32: within 2e-7 of
+ * the gate's size, which leaves few digits of its tail below about -4. M, 2F, K < 2^31; K = 0 gives the products of no
  * terms. A and W start on 16-byte boundaries (GEMM_ERR_MISALIGNED otherwise); C
  * and up may have any alignment that keeps their elements aligned.
  * workspace: gemm_gated_workspace bytes (0 for most), 128-byte aligned: where
  * the pitch of A or W is not a multiple of 16 bytes, or the value half of
  * row-major weights does not start on one, they are copied there first, in
- * every call.
+ * every call. A few rows take a kernel of their own only where A and W are read in
+ * place; it adds up in another order, so that the same numbers at another pitch may
+ * give another last bit.
  */
 int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const void* W, int64_t ldw,
                int layout, int activation, const void* bias, void* C, int64_t ldc, void* up, int64_t ldup,
