@@ -588,12 +588,13 @@ __global__ void __launch_bounds__(1024) layer_weight_sum_kernel(const float* par
   grid_launch_dependents();
 }
 
-// Blocks of the gradient, at most: what an SM holds of 16-bit rows at 64 registers a thread, for each of a GB300's 152 (a number,
-// since the size of the workspace goes by it, on a machine without a GPU too). BF16 with dh, 304 / 456 / 608 blocks, us:
-// 4097 x 5120 (320 threads) 46.4 / 45.1 / 51.8, 8192 x 4096 (256) 77.7 / 64.0 / 59.4, 8192 x 8192 (512) 108 / 127 / 118,
-// 30000 x 1024 68.5 / 56.7 / 52.9. FP32 rows take the same number, of which a half or a third fit at a time (their
-// stages are twice as large): 4097 x 5120 90 us, 8192 x 4096 123, 8192 x 8192 260, 30000 x 1024 109. (One block an SM with as many rows side by side, each with a barrier of its own, and
-// so a third of the partial rows: 45.5, 60.6, 114, 57.7.)
+// Blocks of the gradient, at most: what an SM holds of 16-bit rows at 64 registers a thread, for each of a GB300's 152
+// (a number, since the size of the workspace goes by it, on a machine without a GPU too). BF16 with dh, 304 / 456 /
+// 608 blocks, us: 4097 x 5120 (320 threads) 46.4 / 45.1 / 51.8, 8192 x 4096 (256) 77.7 / 64.0 / 59.4, 8192 x 8192
+// (512) 108 / 127 / 118, 30000 x 1024 68.5 / 56.7 / 52.9. FP32 rows take the same number, of which a half or a third
+// fit at a time (their stages are twice as large): 4097 x 5120 90 us, 8192 x 4096 123, 8192 x 8192 260, 30000 x 1024
+// 109. (One block an SM with as many rows side by side, each with a barrier of its own, and so a third of the partial
+// rows: 45.5, 60.6, 114, 57.7.)
 constexpr int kGradThreads = 256;  // of a block, at least
 int64_t grad_blocks(int64_t cols) {
   const int tpr = threads_per_row(cols, kGradEpt, ALIGNED, 8), fit = 1024 / (tpr < kGradThreads ? kGradThreads : tpr);
